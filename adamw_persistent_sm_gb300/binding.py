@@ -61,6 +61,9 @@ MT_VIEW_EXPERT_IN = 17
 MT_VIEW_FINAL_NORM = 18
 MT_VIEW_DX = 19
 
+MT_DT_FP32 = 0
+MT_DT_BF16 = 1
+
 MT_OP_ATTN_FWD = 1
 MT_OP_ATTN_BWD = 2
 MT_OP_ROUTER = 3
@@ -102,7 +105,14 @@ class mt_view(C.Structure):
     _fields_ = [("ptr", C.c_void_p), ("numel", C.c_int64), ("elem_bytes", C.c_int32)]
 
 
+class mt_mat8(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64),
+                ("ld", C.c_int64), ("lds", C.c_int64), ("block_rows", C.c_int32), ("batch", C.c_int32),
+                ("halves", C.c_int32), ("reserved0", C.c_int32)]
+
+
 _P = C.c_void_p
+_I, _L, _M8 = C.c_int32, C.c_int64, C.POINTER(mt_mat8)
 _SIGNATURES = {
     "mt_param_count": (C.c_int64, [C.POINTER(mt_hparams)]),
     "mt_param_layout": (C.c_int32, [C.POINTER(mt_hparams), C.POINTER(mt_tensor_desc), C.c_int32]),
@@ -119,6 +129,21 @@ _SIGNATURES = {
                                  C.c_int64, _P]),
     "mt_debug_gemm": (C.c_int32, [_P, C.c_int32, _P, C.c_int32, _P, C.c_int32, C.c_int32, C.c_int32,
                                   C.c_int32, _P, C.c_int32, C.c_int32, C.c_int32, _P, C.c_int64, _P]),
+    # stand-alone operators of the expert layer
+    "mt_route_rows": (_L, [_L, _I, _I]),
+    "mt_route_ws_bytes": (_L, [_L, _I, _I]),
+    "mt_route_order": (_I, [_P, _L, _I, _I, _P, _P, _P, _P, _L, _P, _P]),
+    "mt_dispatch": (_I, [_P, _I, _L, _L, _L, _I, _I, _P, _P, _P, _L, _P, _L, _P]),
+    "mt_dispatch8": (_I, [_P, _I, _L, _L, _I, _I, _P, _P, _P, _M8, _P]),
+    "mt_combine": (_I, [_P, _I, _L, _L, _P, _P, _L, _I, _L, _P, _L, _P]),
+    "mt_combine_bwd": (_I, [_P, _I, _L, _P, _L, _P, _P, _P, _L, _P, _L, _I, _I, _L, _P, _L, _P, _P]),
+    "mt_quant8": (_I, [_P, _I, _L, _P, _M8, _P]),
+    "mt_quant8_t": (_I, [_P, _I, _L, _M8, _P, _M8, _P]),
+    "mt_dequant8": (_I, [_M8, _P, _P, _I, _L, _P]),
+    "mt_gemm8": (_I, [_M8, _M8, _P, _I, _P, _I, _L, _I, _P, _P]),
+    "mt_gemm8_reduce": (_I, [_M8, _M8, _P, _I, _P, _L, _I, _P, _P]),
+    "mt_swiglu8": (_I, [_P, _I, _L, _P, _M8, _M8, _P]),
+    "mt_swiglu8_bwd": (_I, [_P, _I, _L, _M8, _P, _P, _L, _P, _L, _P]),
 }
 
 _lib = None

@@ -1,0 +1,171 @@
+// ops8.cuh - what the stand-alone expert operators share: 8-element row
+// accesses, the 8-bit quantiser's arithmetic and the host-side checks.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/moe_train.h"
+
+#define OPS_MAX_ROWS (1LL << 30)
+
+// ---------------------------------------------------------------------------
+// device
+// ---------------------------------------------------------------------------
+// n_rows of the C ABI: rows below *p (clamped), or all of them
+__device__ __forceinline__ long long ops_row_limit(const int* p, long long rows) {
+  if (!p) return rows;
+  const long long v = *p;
+  return v < 0 ? 0 : v < rows ? v : rows;
+}
+
+// Elements c..c+7 of a row, zeros from column n on.  VEC: row start and c are
+// 16-byte aligned.
+template <bool VEC>
+__device__ __forceinline__ void ops_ld8(const float* p, long long c, long long n, float* v) {
+  if (VEC && c + 8 <= n) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p + c)), b = __ldg(reinterpret_cast<const float4*>(p + c + 4));
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = c + i < n ? __ldg(p + c + i) : 0.f;
+}
+__device__ __forceinline__ float ops_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float ops_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+template <bool VEC>
+__device__ __forceinline__ void ops_ld8(const __nv_bfloat16* p, long long c, long long n, float* v) {
+  if (VEC && c + 8 <= n) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p + c));
+    v[0] = ops_lo(u.x); v[1] = ops_hi(u.x); v[2] = ops_lo(u.y); v[3] = ops_hi(u.y);
+    v[4] = ops_lo(u.z); v[5] = ops_hi(u.z); v[6] = ops_lo(u.w); v[7] = ops_hi(u.w);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = c + i < n ? __bfloat162float(p[c + i]) : 0.f;
+}
+__device__ __forceinline__ uint32_t ops_bf2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <bool VEC>
+__device__ __forceinline__ void ops_st8(float* p, long long c, long long n, const float* v) {
+  if (VEC && c + 8 <= n) {
+    *reinterpret_cast<float4*>(p + c) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(p + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < n) p[c + i] = v[i];
+}
+template <bool VEC>
+__device__ __forceinline__ void ops_st8(__nv_bfloat16* p, long long c, long long n, const float* v) {
+  if (VEC && c + 8 <= n) {
+    *reinterpret_cast<uint4*>(p + c) =
+        make_uint4(ops_bf2(v[0], v[1]), ops_bf2(v[2], v[3]), ops_bf2(v[4], v[5]), ops_bf2(v[6], v[7]));
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < n) p[c + i] = __float2bfloat16_rn(v[i]);
+}
+// Eight codes; `v8`: the address is 8-byte aligned.
+__device__ __forceinline__ void ops_st_codes(uint8_t* p, long long c, long long n, uint2 q, bool v8) {
+  if (v8 && c + 8 <= n) {
+    *reinterpret_cast<uint2*>(p + c) = q;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < n) p[c + i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+}
+__device__ __forceinline__ uint2 ops_ld_codes(const uint8_t* p, long long c, long long n, bool v8) {
+  if (v8 && c + 8 <= n) return __ldg(reinterpret_cast<const uint2*>(p + c));
+  uint2 q = make_uint2(0, 0);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t b = c + i < n ? __ldg(p + c + i) : 0;
+    if (i < 4) q.x |= b << (8 * i);
+    else q.y |= b << (8 * (i - 4));
+  }
+  return q;
+}
+
+// Infinite and NaN elements become NaN (which fmaxf leaves out of the block's
+// maximum and the conversion turns into the e4m3 NaN).
+__device__ __forceinline__ float ops_finite(float x) {
+  return fabsf(x) <= 3.402823466e38f ? x : __int_as_float(0x7fffffff);
+}
+// Least e >= -126 with amax <= 448 * 2^e = 1.75 * 2^(e + 8); 0 for amax = 0.
+// With amax = 1.f * 2^x that is x - 8, one more where 1.f > 1.75.
+__device__ __forceinline__ int ops_exponent(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  if (b == 0) return 0;
+  const int e = (int)(b >> 23) - 135 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return e < -126 ? -126 : e;
+}
+__device__ __forceinline__ float ops_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// four e4m3 codes of v * s (round to nearest even; |v * s| <= 448 or NaN)
+__device__ __forceinline__ uint32_t ops_codes4(const float* v, float s) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[1] * s), "f"(v[0] * s));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[3] * s), "f"(v[2] * s));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+__device__ __forceinline__ uint2 ops_codes8(const float* v, float s) {
+  return make_uint2(ops_codes4(v, s), ops_codes4(v + 4, s));
+}
+// values of eight codes, times s
+__device__ __forceinline__ void ops_values8(uint2 q, float s, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint16_t h = (uint16_t)((i < 2 ? q.x : q.y) >> (16 * (i & 1)));
+    uint32_t f;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(h));
+    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&f));
+    v[2 * i] = t.x * s;
+    v[2 * i + 1] = t.y * s;
+  }
+}
+__device__ __forceinline__ float ops_max8(const float* v) {
+  float a = fmaxf(0.f, fabsf(v[0]));       // 0 also where all eight are NaN
+#pragma unroll
+  for (int i = 1; i < 8; ++i) a = fmaxf(a, fabsf(v[i]));
+  return a;
+}
+// maximum over the 16 lanes that hold one block of 128
+__device__ __forceinline__ float ops_max16(float a) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  return a;
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+static inline bool ops_aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+static inline int ops_size(int dtype) { return dtype == MT_DT_FP32 ? 4 : 2; }
+static inline bool ops_dtype_ok(int dtype) { return dtype == MT_DT_FP32 || dtype == MT_DT_BF16; }
+// a matrix of the caller: non-null, aligned to its element, rows at least as long as they are used
+static inline bool ops_mat_ok(const void* p, int dtype, int64_t ld, int64_t cols) {
+  return p && ops_aligned(p, ops_size(dtype)) && ld >= cols && ld <= (1LL << 40);
+}
+// 16-byte accesses to every row
+static inline bool ops_vec(const void* p, int dtype, int64_t ld) {
+  return ops_aligned(p, 16) && (ld * ops_size(dtype)) % 16 == 0;
+}
+static inline int64_t ops_blocks(const mt_mat8* m) {
+  return m->halves ? 2 * ((m->cols / 2 + 127) / 128) : (m->cols + 127) / 128;
+}
+static inline bool ops_mat8_ok(const mt_mat8* m) {
+  if (!m || !m->codes || !m->scales || m->reserved0) return false;
+  if (m->rows < 0 || m->cols < 1 || m->batch < 1 || m->cols > OPS_MAX_ROWS) return false;
+  if (m->rows > OPS_MAX_ROWS || m->rows * m->batch > OPS_MAX_ROWS) return false;
+  if (m->block_rows != 1 && m->block_rows != 128) return false;
+  if (m->halves != 0 && (m->halves != 1 || m->block_rows != 1 || m->cols % 2)) return false;
+  if (!ops_aligned(m->codes, 16) || m->ld % 16 || m->ld < m->cols || m->ld > (1LL << 40)) return false;
+  return m->lds >= ops_blocks(m) && m->lds <= (1LL << 40);
+}
+static inline int ops_launched() { return cudaGetLastError() == cudaSuccess ? MT_OK : MT_ERR_LAUNCH; }

@@ -1,0 +1,484 @@
+// quant8.cu - matrices into 8 bits and back (mt_quant8, mt_quant8_t,
+// mt_dequant8) and the SwiGLU that keeps its inputs there (mt_swiglu8,
+// mt_swiglu8_bwd).
+#include "ops8.cuh"
+
+namespace {
+
+struct Mat8 {
+  uint8_t* q;
+  uint8_t* s;
+  long long rows, cols, ld, lds;
+};
+Mat8 mat8(const mt_mat8* m) { return {(uint8_t*)m->codes, (uint8_t*)m->scales, m->rows, m->cols, m->ld, m->lds}; }
+
+// ---------------------------------------------------------------------------
+// 1 x 128 blocks along the rows
+// ---------------------------------------------------------------------------
+// A half warp holds one block in registers (8 elements per lane): its maximum
+// is four shuffles, x is read once and the codes are written once.  A warp
+// takes R rows of the same 256 columns and issues all their loads first.
+// Columns come in `parts` of `pcols` with blocks of their own.
+template <class T, bool VEC, int R>
+__global__ void __launch_bounds__(256) quant_rows_k(const T* x, long long ldx, const int* n_rows, Mat8 o, int parts,
+                                                    long long pcols) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long lim = ops_row_limit(n_rows, o.rows);
+  const long long r0 = ((long long)blockIdx.x * 8 + warp) * R;
+  if (r0 >= lim) return;
+  const long long chunks = (pcols + 255) / 256, pblocks = (pcols + 127) / 128;
+  const bool v8 = (pcols & 7) == 0;
+  for (long long ch = blockIdx.y; ch < parts * chunks; ch += gridDim.y) {
+    const long long part = ch / chunks, c = (ch % chunks) * 256 + lane * 8, base = part * pcols;
+    float v[R][8];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (r0 + i < lim) ops_ld8<VEC>(x + (r0 + i) * ldx + base, c, pcols, v[i]);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (r0 + i >= lim) break;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = ops_finite(v[i][j]);
+      const int e = ops_exponent(ops_max16(ops_max8(v[i])));
+      ops_st_codes(o.q + (r0 + i) * o.ld + base, c, pcols, ops_codes8(v[i], ops_pow2(-e)), v8 || parts == 1);
+      if ((lane & 15) == 0 && c < pcols) o.s[(r0 + i) * o.lds + part * pblocks + (c >> 7)] = (uint8_t)(e + 127);
+    }
+  }
+}
+
+template <class T, bool VEC>
+__global__ void __launch_bounds__(256) dequant_k(Mat8 a, const int* n_rows, int parts, long long pcols, T* out,
+                                                 long long ldo) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long lim = ops_row_limit(n_rows, a.rows);
+  const long long r0 = ((long long)blockIdx.x * 8 + warp) * 4;
+  if (r0 >= lim) return;
+  const long long chunks = (pcols + 255) / 256, pblocks = (pcols + 127) / 128;
+  const bool v8 = (pcols & 7) == 0 || parts == 1;
+  for (long long ch = blockIdx.y; ch < parts * chunks; ch += gridDim.y) {
+    const long long part = ch / chunks, c = (ch % chunks) * 256 + lane * 8, base = part * pcols;
+    if (c >= pcols) continue;
+    uint2 q[4];
+    int s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (r0 + i < lim) {
+        q[i] = ops_ld_codes(a.q + (r0 + i) * a.ld + base, c, pcols, v8);
+        s[i] = __ldg(a.s + (r0 + i) * a.lds + part * pblocks + (c >> 7));
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (r0 + i < lim) {
+        float v[8];
+        ops_values8(q[i], ops_pow2(s[i] - 127), v);
+        ops_st8<VEC>(out + (r0 + i) * ldo + base, c, pcols, v);
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// 128 x 128 tiles: blocks of 128 x 128, straight or transposed, and
+// transposed 1 x 128 blocks (128 rows of one column)
+// ---------------------------------------------------------------------------
+enum { T_BLOCK = 0, T_BLOCK_T = 1, T_COLS_T = 2 };
+
+// Eight consecutive elements of source row r: a plain matrix, or the values of
+// an 8-bit one.
+struct Src8 {
+  const uint8_t* q;
+  const uint8_t* s;
+  long long ld, lds;
+};
+template <bool VEC>
+__device__ __forceinline__ void src_ld8(const float* x, long long ldx, const Src8&, long long r, long long c,
+                                        long long n, float* v) {
+  ops_ld8<VEC>(x + r * ldx, c, n, v);
+}
+template <bool VEC>
+__device__ __forceinline__ void src_ld8(const __nv_bfloat16* x, long long ldx, const Src8&, long long r, long long c,
+                                        long long n, float* v) {
+  ops_ld8<VEC>(x + r * ldx, c, n, v);
+}
+template <bool VEC>
+__device__ __forceinline__ void src_ld8(const uint8_t*, long long, const Src8& a, long long r, long long c,
+                                        long long n, float* v) {
+  if (c >= n) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    return;
+  }
+  ops_values8(ops_ld_codes(a.q + r * a.ld, c, n, true), ops_pow2((int)__ldg(a.s + r * a.lds + (c >> 7)) - 127), v);
+}
+
+// One CTA per tile; a thread holds 8 rows x 8 columns.  A column's maximum
+// goes over 8 rows in registers, two lanes by shuffle and 8 warps through
+// shared memory; transposed codes go through a 16 KB tile whose 8-byte chunks
+// are swizzled by the source column group, which keeps both sides free of bank
+// conflicts.  Memory-bound: each byte is read and written once.
+template <class T, bool VEC, int MODE>
+__global__ void __launch_bounds__(256) quant_tile_k(const T* x, long long ldx, Src8 src, const int* n_rows, Mat8 o,
+                                                    long long rows, long long cols) {
+  __shared__ float part[8][128];
+  __shared__ int ex[128];
+  __shared__ __align__(16) uint2 tile[MODE == T_BLOCK ? 1 : 128 * 16];
+  const int tid = threadIdx.x, warp = tid >> 5, tc = tid & 15, tr = tid >> 4;
+  const long long b = blockIdx.z;
+  const long long lim = ops_row_limit(n_rows, rows);
+  for (long long rt = blockIdx.x; rt * 128 < lim; rt += gridDim.x) {
+    for (long long ct = blockIdx.y; ct * 128 < cols; ct += gridDim.y) {
+      const long long r0 = rt * 128 + tr * 8, c0 = ct * 128 + tc * 8;
+      float v[8][8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (r0 + i < lim) {
+          src_ld8<VEC>(x + b * rows * ldx, ldx, src, r0 + i, c0, cols, v[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+        }
+      }
+      float m[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        m[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i][j] = ops_finite(v[i][j]);
+          m[j] = fmaxf(m[j], fabsf(v[i][j]));
+        }
+        m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+      }
+      if ((tid & 16) == 0) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 4)
+          *reinterpret_cast<float4*>(&part[warp][tc * 8 + j]) = make_float4(m[j], m[j + 1], m[j + 2], m[j + 3]);
+      }
+      __syncthreads();
+      if (tid < 128) {
+        float a = part[0][tid];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) a = fmaxf(a, part[w][tid]);
+        if (MODE != T_COLS_T) {
+#pragma unroll
+          for (int s = 16; s > 0; s >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
+          if ((tid & 31) == 0) part[0][tid] = a;      // read by this thread's own warp alone so far
+        } else {
+          const int e = ops_exponent(a);
+          ex[tid] = e;
+          if (ct * 128 + tid < cols) o.s[(b * cols + ct * 128 + tid) * o.lds + rt] = (uint8_t)(e + 127);
+        }
+      }
+      __syncthreads();
+      int e0 = 0;
+      if (MODE != T_COLS_T) {
+        e0 = ops_exponent(fmaxf(fmaxf(part[0][0], part[0][32]), fmaxf(part[0][64], part[0][96])));
+        if (tid == 0) {
+          if (MODE == T_BLOCK) o.s[(b * ((rows + 127) / 128) + rt) * o.lds + ct] = (uint8_t)(e0 + 127);
+          else o.s[(b * ((cols + 127) / 128) + ct) * o.lds + rt] = (uint8_t)(e0 + 127);
+        }
+      }
+      if (MODE == T_BLOCK) {
+        const float s = ops_pow2(-e0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (r0 + i < rows) ops_st_codes(o.q + (b * rows + r0 + i) * o.ld, c0, cols, ops_codes8(v[i], s), true);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float s = ops_pow2(-(MODE == T_COLS_T ? ex[tc * 8 + j] : e0));
+          float t[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) t[i] = v[i][j];
+          tile[(tc * 8 + j) * 16 + (tr ^ tc)] = ops_codes8(t, s);
+        }
+        __syncthreads();
+        const long long left = lim - rt * 128;     // codes of an output row in this tile
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = (tid >> 3) + 32 * i, k = (tid & 7) * 2;
+          if (ct * 128 + c < cols) {
+            const uint2 a = tile[c * 16 + (k ^ (c >> 3))], d = tile[c * 16 + ((k + 1) ^ (c >> 3))];
+            uint8_t* p = o.q + (b * cols + ct * 128 + c) * o.ld + rt * 128;
+            if (k * 8 + 16 <= left) {
+              *reinterpret_cast<uint4*>(p + k * 8) = make_uint4(a.x, a.y, d.x, d.y);
+            } else {
+              ops_st_codes(p, k * 8, left, a, false);
+              ops_st_codes(p, k * 8 + 8, left, d, false);
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// SwiGLU
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float sigmoid_f(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+
+// Half a warp holds one block of g and the same block of u: act and, where
+// asked for, g and u leave as codes in the same pass.  R rows per warp, loads first.
+template <class T, bool VEC, bool SAVE, int R>
+__global__ void __launch_bounds__(256) swiglu_k(const T* gu, long long ldgu, const int* n_rows, Mat8 act, Mat8 sv) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long F = act.cols, lim = ops_row_limit(n_rows, act.rows), nb = (F + 127) / 128;
+  const long long r0 = ((long long)blockIdx.x * 8 + warp) * R;
+  if (r0 >= lim) return;
+  const bool v8 = (F & 7) == 0;
+  for (long long c = lane * 8 + 256LL * blockIdx.y; c - lane * 8 < F; c += 256LL * gridDim.y) {
+    float g[R][8], u[R][8];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (r0 + i < lim) {
+        ops_ld8<VEC>(gu + (r0 + i) * ldgu, c, F, g[i]);
+        ops_ld8<VEC>(gu + (r0 + i) * ldgu + F, c, F, u[i]);
+      }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const long long r = r0 + i;
+      if (r >= lim) break;
+      float a[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] = ops_finite(g[i][j] * sigmoid_f(g[i][j]) * u[i][j]);
+      const int e = ops_exponent(ops_max16(ops_max8(a)));
+      ops_st_codes(act.q + r * act.ld, c, F, ops_codes8(a, ops_pow2(-e)), true);
+      const bool first = (lane & 15) == 0 && c < F;
+      if (first) act.s[r * act.lds + (c >> 7)] = (uint8_t)(e + 127);
+      if (SAVE) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          g[i][j] = ops_finite(g[i][j]);
+          u[i][j] = ops_finite(u[i][j]);
+        }
+        const int eg = ops_exponent(ops_max16(ops_max8(g[i]))), eu = ops_exponent(ops_max16(ops_max8(u[i])));
+        ops_st_codes(sv.q + r * sv.ld, c, F, ops_codes8(g[i], ops_pow2(-eg)), true);
+        ops_st_codes(sv.q + r * sv.ld + F, c, F, ops_codes8(u[i], ops_pow2(-eu)), v8);
+        if (first) {
+          sv.s[r * sv.lds + (c >> 7)] = (uint8_t)(eg + 127);
+          sv.s[r * sv.lds + nb + (c >> 7)] = (uint8_t)(eu + 127);
+        }
+      }
+    }
+  }
+}
+
+template <class T, bool VEC, int R>
+__global__ void __launch_bounds__(256) swiglu_bwd_k(const T* da, long long ldda, Mat8 sv, const int* n_rows, T* dgu,
+                                                    long long lddgu, T* act, long long ldact) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long F = sv.cols / 2, lim = ops_row_limit(n_rows, sv.rows), nb = (F + 127) / 128;
+  const long long r0 = ((long long)blockIdx.x * 8 + warp) * R;
+  if (r0 >= lim) return;
+  const bool v8 = (F & 7) == 0;
+  for (long long c = lane * 8 + 256LL * blockIdx.y; c < F; c += 256LL * gridDim.y) {
+    float d[R][8];
+    uint2 qg[R], qu[R];
+    int eg[R], eu[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const long long r = r0 + i;
+      if (r < lim) {
+        ops_ld8<VEC>(da + r * ldda, c, F, d[i]);
+        qg[i] = ops_ld_codes(sv.q + r * sv.ld, c, F, true);
+        qu[i] = ops_ld_codes(sv.q + r * sv.ld + F, c, F, v8);
+        eg[i] = __ldg(sv.s + r * sv.lds + (c >> 7));
+        eu[i] = __ldg(sv.s + r * sv.lds + nb + (c >> 7));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const long long r = r0 + i;
+      if (r >= lim) break;
+      float g[8], u[8], a[8];
+      ops_values8(qg[i], ops_pow2(eg[i] - 127), g);
+      ops_values8(qu[i], ops_pow2(eu[i] - 127), u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float s = sigmoid_f(g[j]), gs = g[j] * s, x = d[i][j];
+        a[j] = gs * u[j];
+        d[i][j] = x * u[j] * (s + gs * (1.f - s));
+        u[j] = x * gs;
+      }
+      ops_st8<VEC>(dgu + r * lddgu, c, F, d[i]);
+      ops_st8<VEC>(dgu + r * lddgu + F, c, F, u);
+      if (act) ops_st8<VEC>(act + r * ldact, c, F, a);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+// Rows per warp: one where that still leaves every SM fewer than 16 warps, so
+// that small matrices spread; four otherwise, for loads in flight.
+int rows_per_warp(int64_t rows, int64_t cols) { return rows * ((cols + 255) / 256) <= 152 * 16 ? 1 : 4; }
+unsigned row_ctas(int64_t rows, int r) { return (unsigned)((rows + 8 * r - 1) / (8 * r)); }
+unsigned col_ctas(int64_t cols, int per) {
+  const int64_t n = (cols + per - 1) / per;
+  return (unsigned)(n < 1024 ? n : 1024);
+}
+
+template <class T, bool VEC>
+void quant_rows_t(const void* x, int64_t ldx, const int* n_rows, const mt_mat8* o, cudaStream_t st) {
+  const int parts = o->halves ? 2 : 1;
+  const int64_t pc = o->cols / parts, chunks = (pc + 255) / 256 * parts;
+  const int r = rows_per_warp(o->rows, chunks * 256);
+  const dim3 grid(row_ctas(o->rows, r), col_ctas(chunks, 1));
+  if (r == 1) quant_rows_k<T, VEC, 1><<<grid, 256, 0, st>>>((const T*)x, ldx, n_rows, mat8(o), parts, pc);
+  else quant_rows_k<T, VEC, 4><<<grid, 256, 0, st>>>((const T*)x, ldx, n_rows, mat8(o), parts, pc);
+}
+template <class T, bool VEC, int MODE>
+void quant_tile_t(const void* x, int64_t ldx, const Src8& src, const int* n_rows, const mt_mat8* o, int64_t rows,
+                  int64_t cols, cudaStream_t st) {
+  const int64_t rt = (rows + 127) / 128, ct = (cols + 127) / 128;
+  const dim3 grid((unsigned)rt, (unsigned)(ct < 32768 ? ct : 32768), (unsigned)o->batch);
+  quant_tile_k<T, VEC, MODE><<<grid, 256, 0, st>>>((const T*)x, ldx, src, n_rows, mat8(o), rows, cols);
+}
+template <class T, bool VEC>
+void dequant_t(const mt_mat8* a, const int* n_rows, void* out, int64_t ldo, cudaStream_t st) {
+  const int parts = a->halves ? 2 : 1;
+  const int64_t pc = a->cols / parts, chunks = (pc + 255) / 256 * parts;
+  const dim3 grid(row_ctas(a->rows, 4), col_ctas(chunks, 1));
+  dequant_k<T, VEC><<<grid, 256, 0, st>>>(mat8(a), n_rows, parts, pc, (T*)out, ldo);
+}
+template <class T, bool VEC>
+void swiglu_t(const void* gu, int64_t ldgu, const int* n_rows, const mt_mat8* act, const mt_mat8* sv,
+              cudaStream_t st) {
+  const int r = rows_per_warp(act->rows, act->cols) == 1 ? 1 : 2;
+  const dim3 grid(row_ctas(act->rows, r), col_ctas(act->cols, 256));
+  const Mat8 a = mat8(act), s = sv ? mat8(sv) : Mat8{};
+  auto k = sv ? (r == 1 ? swiglu_k<T, VEC, true, 1> : swiglu_k<T, VEC, true, 2>)
+              : (r == 1 ? swiglu_k<T, VEC, false, 1> : swiglu_k<T, VEC, false, 2>);
+  k<<<grid, 256, 0, st>>>((const T*)gu, ldgu, n_rows, a, s);
+}
+template <class T, bool VEC>
+void swiglu_bwd_t(const void* da, int64_t ldda, const mt_mat8* sv, const int* n_rows, void* dgu, int64_t lddgu,
+                  void* act, int64_t ldact, cudaStream_t st) {
+  const int64_t F = sv->cols / 2;
+  const int r = rows_per_warp(sv->rows, F) == 1 ? 1 : 2;
+  const dim3 grid(row_ctas(sv->rows, r), col_ctas(F, 256));
+  auto k = r == 1 ? swiglu_bwd_k<T, VEC, 1> : swiglu_bwd_k<T, VEC, 2>;
+  k<<<grid, 256, 0, st>>>((const T*)da, ldda, mat8(sv), n_rows, (T*)dgu, lddgu, (T*)act, ldact);
+}
+
+bool limit_ok(const int32_t* n_rows) { return !n_rows || ops_aligned(n_rows, 4); }
+
+}  // namespace
+
+extern "C" {
+
+int32_t mt_quant8(const void* x, int32_t dtype, int64_t ldx, const int32_t* n_rows, const mt_mat8* out, void* stream) {
+  if (!ops_mat8_ok(out) || !ops_dtype_ok(dtype) || !limit_ok(n_rows)) return MT_ERR_ARG;
+  if (n_rows && (out->batch != 1 || out->block_rows != 1)) return MT_ERR_ARG;
+  if (out->rows == 0) return MT_OK;
+  if (!ops_mat_ok(x, dtype, ldx, out->cols)) return MT_ERR_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool vec = ops_vec(x, dtype, ldx);
+  if (out->block_rows == 1) {
+    mt_mat8 o = *out;            // stacked matrices are one tall one
+    o.rows *= o.batch;
+    const bool v = vec && (!o.halves || (o.cols / 2) * ops_size(dtype) % 16 == 0);
+    if (dtype == MT_DT_FP32) v ? quant_rows_t<float, true>(x, ldx, n_rows, &o, st) : quant_rows_t<float, false>(x, ldx, n_rows, &o, st);
+    else v ? quant_rows_t<__nv_bfloat16, true>(x, ldx, n_rows, &o, st) : quant_rows_t<__nv_bfloat16, false>(x, ldx, n_rows, &o, st);
+  } else {
+    if (out->batch > 65535) return MT_ERR_UNSUPPORTED;
+    const Src8 none{};
+    if (dtype == MT_DT_FP32)
+      vec ? quant_tile_t<float, true, T_BLOCK>(x, ldx, none, nullptr, out, out->rows, out->cols, st)
+          : quant_tile_t<float, false, T_BLOCK>(x, ldx, none, nullptr, out, out->rows, out->cols, st);
+    else
+      vec ? quant_tile_t<__nv_bfloat16, true, T_BLOCK>(x, ldx, none, nullptr, out, out->rows, out->cols, st)
+          : quant_tile_t<__nv_bfloat16, false, T_BLOCK>(x, ldx, none, nullptr, out, out->rows, out->cols, st);
+  }
+  return ops_launched();
+}
+
+int32_t mt_quant8_t(const void* x, int32_t dtype, int64_t ldx, const mt_mat8* x8, const int32_t* n_rows,
+                    const mt_mat8* out, void* stream) {
+  if (!ops_mat8_ok(out) || out->halves || !limit_ok(n_rows)) return MT_ERR_ARG;
+  if (n_rows && out->batch != 1) return MT_ERR_ARG;
+  if ((x != nullptr) == (x8 != nullptr) && out->rows) return MT_ERR_ARG;
+  if (out->rows == 0) return MT_OK;
+  if (out->batch > 65535) return MT_ERR_UNSUPPORTED;
+  cudaStream_t st = (cudaStream_t)stream;
+  const int64_t rows = out->cols, cols = out->rows;
+  if (x8) {
+    if (!ops_mat8_ok(x8) || x8->block_rows != 1 || x8->batch != 1 || x8->halves || out->batch != 1 || x8->rows != rows ||
+        x8->cols != cols)
+      return MT_ERR_ARG;
+    const Src8 src{(const uint8_t*)x8->codes, (const uint8_t*)x8->scales, x8->ld, x8->lds};
+    if (out->block_rows == 1) quant_tile_t<uint8_t, true, T_COLS_T>(nullptr, 0, src, n_rows, out, rows, cols, st);
+    else quant_tile_t<uint8_t, true, T_BLOCK_T>(nullptr, 0, src, n_rows, out, rows, cols, st);
+    return ops_launched();
+  }
+  if (!ops_dtype_ok(dtype) || !ops_mat_ok(x, dtype, ldx, cols)) return MT_ERR_ARG;
+  const bool vec = ops_vec(x, dtype, ldx);
+  const Src8 none{};
+  if (dtype == MT_DT_FP32) {
+    if (out->block_rows == 1)
+      vec ? quant_tile_t<float, true, T_COLS_T>(x, ldx, none, n_rows, out, rows, cols, st)
+          : quant_tile_t<float, false, T_COLS_T>(x, ldx, none, n_rows, out, rows, cols, st);
+    else
+      vec ? quant_tile_t<float, true, T_BLOCK_T>(x, ldx, none, n_rows, out, rows, cols, st)
+          : quant_tile_t<float, false, T_BLOCK_T>(x, ldx, none, n_rows, out, rows, cols, st);
+  } else {
+    if (out->block_rows == 1)
+      vec ? quant_tile_t<__nv_bfloat16, true, T_COLS_T>(x, ldx, none, n_rows, out, rows, cols, st)
+          : quant_tile_t<__nv_bfloat16, false, T_COLS_T>(x, ldx, none, n_rows, out, rows, cols, st);
+    else
+      vec ? quant_tile_t<__nv_bfloat16, true, T_BLOCK_T>(x, ldx, none, n_rows, out, rows, cols, st)
+          : quant_tile_t<__nv_bfloat16, false, T_BLOCK_T>(x, ldx, none, n_rows, out, rows, cols, st);
+  }
+  return ops_launched();
+}
+
+int32_t mt_dequant8(const mt_mat8* a, const int32_t* n_rows, void* out, int32_t dtype, int64_t ldo, void* stream) {
+  if (!ops_mat8_ok(a) || a->block_rows != 1 || a->batch != 1 || !ops_dtype_ok(dtype) || !limit_ok(n_rows))
+    return MT_ERR_ARG;
+  if (a->rows == 0) return MT_OK;
+  if (!ops_mat_ok(out, dtype, ldo, a->cols)) return MT_ERR_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool vec = ops_vec(out, dtype, ldo) && (!a->halves || (a->cols / 2) * ops_size(dtype) % 16 == 0);
+  if (dtype == MT_DT_FP32) vec ? dequant_t<float, true>(a, n_rows, out, ldo, st) : dequant_t<float, false>(a, n_rows, out, ldo, st);
+  else vec ? dequant_t<__nv_bfloat16, true>(a, n_rows, out, ldo, st) : dequant_t<__nv_bfloat16, false>(a, n_rows, out, ldo, st);
+  return ops_launched();
+}
+
+int32_t mt_swiglu8(const void* gu, int32_t dtype, int64_t ldgu, const int32_t* n_rows, const mt_mat8* act,
+                   const mt_mat8* saved, void* stream) {
+  if (!ops_mat8_ok(act) || act->block_rows != 1 || act->batch != 1 || act->halves || !ops_dtype_ok(dtype) ||
+      !limit_ok(n_rows))
+    return MT_ERR_ARG;
+  if (saved && (!ops_mat8_ok(saved) || saved->block_rows != 1 || saved->batch != 1 || !saved->halves ||
+                saved->rows != act->rows || saved->cols != 2 * act->cols))
+    return MT_ERR_ARG;
+  if (act->rows == 0) return MT_OK;
+  if (!ops_mat_ok(gu, dtype, ldgu, 2 * act->cols)) return MT_ERR_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool vec = ops_vec(gu, dtype, ldgu) && act->cols * ops_size(dtype) % 16 == 0;
+  if (dtype == MT_DT_FP32) vec ? swiglu_t<float, true>(gu, ldgu, n_rows, act, saved, st) : swiglu_t<float, false>(gu, ldgu, n_rows, act, saved, st);
+  else vec ? swiglu_t<__nv_bfloat16, true>(gu, ldgu, n_rows, act, saved, st) : swiglu_t<__nv_bfloat16, false>(gu, ldgu, n_rows, act, saved, st);
+  return ops_launched();
+}
+
+int32_t mt_swiglu8_bwd(const void* dact, int32_t dtype, int64_t ldda, const mt_mat8* saved, const int32_t* n_rows,
+                       void* dgu, int64_t lddgu, void* act, int64_t ldact, void* stream) {
+  if (!ops_mat8_ok(saved) || saved->block_rows != 1 || saved->batch != 1 || !saved->halves || !ops_dtype_ok(dtype) ||
+      !limit_ok(n_rows))
+    return MT_ERR_ARG;
+  if (saved->rows == 0) return MT_OK;
+  const int64_t F = saved->cols / 2;
+  if (!ops_mat_ok(dact, dtype, ldda, F) || !ops_mat_ok(dgu, dtype, lddgu, 2 * F) ||
+      (act && !ops_mat_ok(act, dtype, ldact, F)))
+    return MT_ERR_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool vec = ops_vec(dact, dtype, ldda) && ops_vec(dgu, dtype, lddgu) && (!act || ops_vec(act, dtype, ldact)) &&
+                   F * ops_size(dtype) % 16 == 0;
+  if (dtype == MT_DT_FP32) vec ? swiglu_bwd_t<float, true>(dact, ldda, saved, n_rows, dgu, lddgu, act, ldact, st) : swiglu_bwd_t<float, false>(dact, ldda, saved, n_rows, dgu, lddgu, act, ldact, st);
+  else vec ? swiglu_bwd_t<__nv_bfloat16, true>(dact, ldda, saved, n_rows, dgu, lddgu, act, ldact, st) : swiglu_bwd_t<__nv_bfloat16, false>(dact, ldda, saved, n_rows, dgu, lddgu, act, ldact, st);
+  return ops_launched();
+}
+
+}  // extern "C"

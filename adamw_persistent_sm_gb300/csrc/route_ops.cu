@@ -1,0 +1,507 @@
+// route_ops.cu - tokens sorted by expert and back (mt_route_order,
+// mt_dispatch, mt_dispatch8, mt_combine, mt_combine_bwd).
+#include "ops8.cuh"
+
+namespace {
+
+constexpr int RO_E = MT_MAX_EXPERTS;
+constexpr int RO_SMALL = 8192;        // assignments that one CTA sorts alone
+constexpr int RO_CHUNK = 2048;        // assignments per CTA otherwise
+
+// Expert of an assignment, -1 for none; counts indices out of range.
+__device__ __forceinline__ int ro_expert(const int* idx, long long a, long long n, int E, int* status) {
+  if (a >= n) return -1;
+  const int e = __ldg(idx + a);
+  if (e >= 0 && e < E) return e;
+  if (e != -1 && atomicCAS(status, 0, (int)MT_ERR_DEVICE_BOUNDS) == 0) status[1] = 3;
+  return -1;
+}
+
+// offs[0..E] of the padded segments, from the counts in cnt (first warp).
+__device__ __forceinline__ void ro_offsets(const int* cnt, int E, int* offs) {
+  const int l = threadIdx.x;
+  if (l < 32) {
+    const int c0 = 2 * l < E ? (cnt[2 * l] + 127) & ~127 : 0, c1 = 2 * l + 1 < E ? (cnt[2 * l + 1] + 127) & ~127 : 0;
+    int s = c0 + c1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, s, o);
+      if (l >= o) s += t;
+    }
+    if (l == 0) offs[0] = 0;
+    if (2 * l < E) offs[2 * l + 1] = s - c1;
+    if (2 * l + 1 < E) offs[2 * l + 2] = s;
+  }
+}
+
+// Lanes of the warp whose assignment names the same expert.
+__device__ __forceinline__ unsigned ro_peers(int e) { return __match_any_sync(0xffffffffu, e); }
+
+// Counting sort of assignments [a0, a1) by a CTA of NW warps, each warp taking
+// `span` consecutive ones (a multiple of 32): wh[warp][e] counts, then holds the
+// next row of expert e for the warp, so rows ascend with the assignment.  Two
+// reads of idx (the second from cache) instead of keeping choices in registers.
+template <int NW>
+struct RoSmem {
+  int wh[NW][RO_E];
+  int cnt[RO_E], before[RO_E], offs[RO_E + 1];
+};
+
+template <int NW>
+__device__ __forceinline__ void ro_count(RoSmem<NW>& s, const int* idx, long long w0, long long w1, long long n, int E,
+                                         int* status) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int e = lane; e < RO_E; e += 32) s.wh[warp][e] = 0;
+  __syncwarp();
+  for (long long a = w0; a < w1; a += 32) {
+    const int e = ro_expert(idx, a + lane, n, E, status);
+    const unsigned peers = ro_peers(e);
+    if (e >= 0 && lane == __ffs(peers) - 1) s.wh[warp][e] += __popc(peers);
+    __syncwarp();
+  }
+}
+template <int NW>
+__device__ __forceinline__ void ro_place(RoSmem<NW>& s, const int* idx, long long w0, long long w1, long long n, int E,
+                                         int* status, int* perm, int* row) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (long long a = w0; a < w1; a += 32) {
+    const int e = ro_expert(idx, a + lane, n, E, status);
+    const unsigned peers = ro_peers(e);
+    int r = -1;
+    if (e >= 0) {
+      r = s.wh[warp][e] + __popc(peers & ((1u << lane) - 1u));
+      perm[r] = (int)(a + lane);
+    }
+    if (a + lane < n) row[a + lane] = r;
+    __syncwarp();
+    if (e >= 0 && lane == __ffs(peers) - 1) s.wh[warp][e] += __popc(peers);
+    __syncwarp();
+  }
+}
+// -1 at the rows no assignment takes, spread over `nt` threads
+__device__ __forceinline__ void ro_pads(const int* cnt, const int* offs, int E, long long rows, int* perm, long long t,
+                                        long long nt) {
+  for (long long i = t; i < (long long)E * 128; i += nt) {
+    const int e = (int)(i >> 7);
+    const int r = offs[e] + cnt[e] + (int)(i & 127);
+    if (r < offs[e + 1]) perm[r] = -1;
+  }
+  for (long long r = offs[E] + t; r < rows; r += nt) perm[r] = -1;
+}
+
+// Few assignments: one CTA, one launch (latency of two global round trips).
+__global__ void __launch_bounds__(1024) ro_small(const int* idx, int n, int E, long long rows, int* offs, int* perm,
+                                                 int* row, int* status) {
+  __shared__ RoSmem<32> s;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int span = ((n + 31) / 32 + 31) & ~31;
+  const int w0 = warp * span < n ? warp * span : n, w1 = w0 + span < n ? w0 + span : n;
+  ro_count(s, idx, w0, w1, n, E, status);
+  __syncthreads();
+  if (tid < E) {
+    int c = 0;
+    for (int w = 0; w < 32; ++w) {
+      const int t = s.wh[w][tid];
+      s.wh[w][tid] = c;
+      c += t;
+    }
+    s.cnt[tid] = c;
+  }
+  __syncthreads();
+  ro_offsets(s.cnt, E, s.offs);
+  __syncthreads();
+  if (tid <= E) offs[tid] = s.offs[tid];
+  for (int i = tid; i < 32 * RO_E; i += 1024)
+    if ((i & (RO_E - 1)) < E) s.wh[i / RO_E][i & (RO_E - 1)] += s.offs[i & (RO_E - 1)];
+  __syncthreads();
+  ro_place(s, idx, w0, w1, n, E, status, perm, row);
+  ro_pads(s.cnt, s.offs, E, rows, perm, tid, 1024);
+}
+
+// Many: every CTA counts its chunk, then every CTA sums the counts before its
+// own and places it.
+__global__ void __launch_bounds__(256) ro_hist(const int* idx, long long n, int E, int* hist, int* status) {
+  __shared__ RoSmem<8> s;
+  const long long a0 = (long long)blockIdx.x * RO_CHUNK + (threadIdx.x >> 5) * (RO_CHUNK / 8);
+  const long long a1 = a0 + RO_CHUNK / 8 < n ? a0 + RO_CHUNK / 8 : n;
+  ro_count(s, idx, a0, a1, n, E, status);
+  __syncthreads();
+  if (threadIdx.x < RO_E) {
+    int c = 0;
+    for (int w = 0; w < 8; ++w) c += s.wh[w][threadIdx.x];
+    hist[(long long)blockIdx.x * RO_E + threadIdx.x] = c;
+  }
+}
+__global__ void __launch_bounds__(256) ro_scatter(const int* idx, long long n, int E, long long rows, const int* hist,
+                                                  int* offs, int* perm, int* row, int* status) {
+  __shared__ RoSmem<8> s;
+  __shared__ int part[2][4][RO_E];
+  const int tid = threadIdx.x, e = tid & (RO_E - 1), p = tid / RO_E;
+  const long long a0 = (long long)blockIdx.x * RO_CHUNK + (tid >> 5) * (RO_CHUNK / 8);
+  const long long a1 = a0 + RO_CHUNK / 8 < n ? a0 + RO_CHUNK / 8 : n;
+  int all = 0, mine = 0;
+#pragma unroll 8
+  for (int c = p; c < (int)gridDim.x; c += 4) {
+    const int h = __ldg(hist + (long long)c * RO_E + e);
+    all += h;
+    if (c < (int)blockIdx.x) mine += h;
+  }
+  part[0][p][e] = all;
+  part[1][p][e] = mine;
+  ro_count(s, idx, a0, a1, n, E, status);
+  __syncthreads();
+  if (tid < RO_E) {
+    s.cnt[tid] = part[0][0][tid] + part[0][1][tid] + part[0][2][tid] + part[0][3][tid];
+    s.before[tid] = part[1][0][tid] + part[1][1][tid] + part[1][2][tid] + part[1][3][tid];
+  }
+  __syncthreads();
+  ro_offsets(s.cnt, E, s.offs);
+  __syncthreads();
+  if (tid < E) {
+    int c = s.offs[tid] + s.before[tid];
+    for (int w = 0; w < 8; ++w) {
+      const int t = s.wh[w][tid];
+      s.wh[w][tid] = c;
+      c += t;
+    }
+  }
+  if (blockIdx.x == 0 && tid <= E) offs[tid] = s.offs[tid];
+  __syncthreads();
+  ro_place(s, idx, a0, a1, n, E, status, perm, row);
+  ro_pads(s.cnt, s.offs, E, rows, perm, blockIdx.x * 256LL + tid, gridDim.x * 256LL);
+}
+
+// ---------------------------------------------------------------------------
+// rows there and back
+// ---------------------------------------------------------------------------
+// Padding row i of E * 128 candidates (the last 128 rows of each segment), or
+// -1: the rows that no token writes.
+__device__ __forceinline__ long long pad_row(long long i, int E, const int* offs, const int* perm, long long rows) {
+  const int e = (int)(i >> 7);
+  if (e >= E) return -1;
+  const long long r = (long long)__ldg(offs + e + 1) - 128 + (i & 127);
+  if (r < 0 || r < __ldg(offs + e) || r >= rows) return -1;
+  return __ldg(perm + r) < 0 ? r : -1;
+}
+
+// A warp holds one token's chunk of 256 columns (8 per lane) and writes it to
+// the token's rows: x is read once however many experts take it, which leaves
+// the write of the copies as the bound.  The CTAs behind the tokens' write the
+// padding rows.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(256) dispatch_k(const T* x, long long ldx, long long tokens, long long width, int K,
+                                                  int E, const int* offs, const int* perm, const int* row,
+                                                  long long rows, T* out, long long ldo, long long tok_ctas) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float zero[8] = {};
+  if (blockIdx.x >= tok_ctas) {
+    const long long r = pad_row((blockIdx.x - tok_ctas) * 8 + warp, E, offs, perm, rows);
+    if (r < 0) return;
+    for (long long c = lane * 8 + 256LL * blockIdx.y; c < width; c += 256LL * gridDim.y)
+      ops_st8<VEC>(out + r * ldo, c, width, zero);
+    return;
+  }
+  const long long t = (long long)blockIdx.x * 8 + warp;
+  if (t >= tokens) return;
+  const int mine = lane < K ? __ldg(row + t * K + lane) : -1;
+  for (long long c = lane * 8 + 256LL * blockIdx.y; c - lane * 8 < width; c += 256LL * gridDim.y) {
+    float v[8];
+    ops_ld8<VEC>(x + t * ldx, c, width, v);
+    for (int k = 0; k < K; ++k) {
+      const long long r = __shfl_sync(0xffffffffu, mine, k);
+      if (r >= 0 && r < rows) ops_st8<VEC>(out + r * ldo, c, width, v);
+    }
+  }
+}
+
+// The same with the row's blocks quantised in registers (a block of 128 lies
+// in 16 lanes), once per token.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(256) dispatch8_k(const T* x, long long ldx, long long tokens, long long width, int K,
+                                                   int E, const int* offs, const int* perm, const int* row,
+                                                   long long rows, uint8_t* q, long long ldq, uint8_t* sc,
+                                                   long long lds, long long tok_ctas) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x >= tok_ctas) {
+    const long long r = pad_row((blockIdx.x - tok_ctas) * 8 + warp, E, offs, perm, rows);
+    if (r < 0) return;
+    for (long long c = lane * 8 + 256LL * blockIdx.y; c < width; c += 256LL * gridDim.y) {
+      ops_st_codes(q + r * ldq, c, width, make_uint2(0, 0), true);
+      if ((lane & 15) == 0) sc[r * lds + (c >> 7)] = 127;
+    }
+    return;
+  }
+  const long long t = (long long)blockIdx.x * 8 + warp;
+  if (t >= tokens) return;
+  const int mine = lane < K ? __ldg(row + t * K + lane) : -1;
+  for (long long c = lane * 8 + 256LL * blockIdx.y; c - lane * 8 < width; c += 256LL * gridDim.y) {
+    float v[8];
+    ops_ld8<VEC>(x + t * ldx, c, width, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = ops_finite(v[i]);
+    const int e = ops_exponent(ops_max16(ops_max8(v)));
+    const uint2 codes = ops_codes8(v, ops_pow2(-e));
+    for (int k = 0; k < K; ++k) {
+      const long long r = __shfl_sync(0xffffffffu, mine, k);
+      if (r < 0 || r >= rows) continue;
+      ops_st_codes(q + r * ldq, c, width, codes, true);
+      if ((lane & 15) == 0 && c < width) sc[r * lds + (c >> 7)] = (uint8_t)(e + 127);
+    }
+  }
+}
+
+// A warp sums one token's chunk of 256 columns over its slots in order, in
+// fp32.  KM bounds K so that every slot's load is in flight before the first sum.
+template <class T, bool VEC, int KM>
+__global__ void __launch_bounds__(256) combine_k(const T* y, long long ldy, long long rows, const int* row,
+                                                 const float* w, long long tokens, int K, long long width, T* out,
+                                                 long long ldo) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long t = (long long)blockIdx.x * 8 + warp;
+  if (t >= tokens) return;
+  int mine = lane < K ? __ldg(row + t * K + lane) : -1;
+  if (mine >= rows) mine = -1;
+  const float wm = lane < K ? (w ? __ldg(w + t * K + lane) : 1.f) : 0.f;
+  for (long long c = lane * 8 + 256LL * blockIdx.y; c - lane * 8 < width; c += 256LL * gridDim.y) {
+    float v[KM][8], s[8] = {};
+    bool on[KM];
+#pragma unroll
+    for (int k = 0; k < KM; ++k) {
+      const long long r = __shfl_sync(0xffffffffu, mine, k);
+      on[k] = r >= 0;
+      if (on[k]) ops_ld8<VEC>(y + r * ldy, c, width, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < KM; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, wm, k);
+      if (on[k]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = fmaf(wk, v[k][i], s[i]);
+      }
+    }
+    ops_st8<VEC>(out + t * ldo, c, width, s);
+  }
+}
+
+// A warp takes one token's whole row: dout is read once for its slots, each
+// slot's y row is read for the dot product and its dy row written.
+template <class T, bool VEC, int KM>
+__global__ void __launch_bounds__(256) combine_bwd_k(const T* dout, long long lddo, const T* y, long long ldy,
+                                                     const int* offs, const int* perm, const int* row, long long rows,
+                                                     const float* w, long long tokens, int K, int E, long long width,
+                                                     T* dy, long long lddy, float* dw, long long tok_ctas) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float zero[8] = {};
+  if (blockIdx.x >= tok_ctas) {
+    const long long r = pad_row((blockIdx.x - tok_ctas) * 8 + warp, E, offs, perm, rows);
+    if (r < 0) return;
+    for (long long c = lane * 8; c < width; c += 256) ops_st8<VEC>(dy + r * lddy, c, width, zero);
+    return;
+  }
+  const long long t = (long long)blockIdx.x * 8 + warp;
+  if (t >= tokens) return;
+  int mine = lane < K ? __ldg(row + t * K + lane) : -1;
+  if (mine >= rows) mine = -1;
+  const float wm = lane < K ? __ldg(w + t * K + lane) : 0.f;
+  float dot[KM] = {};
+  for (long long c = lane * 8; c - lane * 8 < width; c += 256) {
+    float d[8], v[KM][8];
+    ops_ld8<VEC>(dout + t * lddo, c, width, d);
+#pragma unroll
+    for (int k = 0; k < KM; ++k) {
+      const long long r = __shfl_sync(0xffffffffu, mine, k);
+      if (r >= 0) ops_ld8<VEC>(y + r * ldy, c, width, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < KM; ++k) {
+      const long long r = __shfl_sync(0xffffffffu, mine, k);
+      const float wk = __shfl_sync(0xffffffffu, wm, k);
+      if (r < 0) continue;
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o[i] = wk * d[i];
+        dot[k] = fmaf(d[i], v[k][i], dot[k]);
+      }
+      ops_st8<VEC>(dy + r * lddy, c, width, o);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < KM; ++k) {
+    float s = dot[k];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == k && k < K) dw[t * K + k] = s;
+  }
+}
+
+int route_ok(int64_t tokens, int32_t K, int32_t E) {
+  if (tokens < 0 || K < 1 || E < 1) return MT_ERR_ARG;
+  if (E > MT_MAX_EXPERTS || K > 8 || K > E || tokens > OPS_MAX_ROWS) return MT_ERR_UNSUPPORTED;
+  if (tokens * K + (int64_t)E * 128 > OPS_MAX_ROWS) return MT_ERR_UNSUPPORTED;
+  return MT_OK;
+}
+int64_t route_rows(int64_t tokens, int32_t K, int32_t E) {
+  return (tokens * K + (int64_t)E * 127 + 127) / 128 * 128;
+}
+// chunks of 256 columns as a second grid dimension (a CTA walks on from there)
+unsigned col_chunks(int64_t width) {
+  const int64_t n = (width + 255) / 256;
+  return (unsigned)(n < 1024 ? n : 1024);
+}
+
+template <class T>
+int dispatch_t(const void* x, int64_t ldx, int64_t tokens, int64_t width, int K, int E, const int* offs,
+               const int* perm, const int* row, int64_t rows, void* out, int64_t ldo, bool vec, cudaStream_t st) {
+  const long long tc = (tokens + 7) / 8;
+  const dim3 grid((unsigned)(tc + E * 16), col_chunks(width));
+  if (vec)
+    dispatch_k<T, true><<<grid, 256, 0, st>>>((const T*)x, ldx, tokens, width, K, E, offs, perm, row, rows, (T*)out,
+                                              ldo, tc);
+  else
+    dispatch_k<T, false><<<grid, 256, 0, st>>>((const T*)x, ldx, tokens, width, K, E, offs, perm, row, rows, (T*)out,
+                                               ldo, tc);
+  return ops_launched();
+}
+template <class T>
+int dispatch8_t(const void* x, int64_t ldx, int64_t tokens, int K, int E, const int* offs, const int* perm,
+                const int* row, const mt_mat8* o, bool vec, cudaStream_t st) {
+  const long long tc = (tokens + 7) / 8;
+  const dim3 grid((unsigned)(tc + E * 16), col_chunks(o->cols));
+  if (vec)
+    dispatch8_k<T, true><<<grid, 256, 0, st>>>((const T*)x, ldx, tokens, o->cols, K, E, offs, perm, row, o->rows,
+                                               (uint8_t*)o->codes, o->ld, (uint8_t*)o->scales, o->lds, tc);
+  else
+    dispatch8_k<T, false><<<grid, 256, 0, st>>>((const T*)x, ldx, tokens, o->cols, K, E, offs, perm, row, o->rows,
+                                                (uint8_t*)o->codes, o->ld, (uint8_t*)o->scales, o->lds, tc);
+  return ops_launched();
+}
+template <class T, bool VEC>
+int combine_t(const void* y, int64_t ldy, int64_t rows, const int* row, const float* w, int64_t tokens, int K,
+              int64_t width, void* out, int64_t ldo, cudaStream_t st) {
+  const dim3 grid((unsigned)((tokens + 7) / 8), col_chunks(width));
+  auto k = K <= 2 ? combine_k<T, VEC, 2> : K <= 4 ? combine_k<T, VEC, 4> : combine_k<T, VEC, 8>;
+  k<<<grid, 256, 0, st>>>((const T*)y, ldy, rows, row, w, tokens, K, width, (T*)out, ldo);
+  return ops_launched();
+}
+template <class T, bool VEC>
+int combine_bwd_t(const void* dout, int64_t lddo, const void* y, int64_t ldy, const int* offs, const int* perm,
+                  const int* row, int64_t rows, const float* w, int64_t tokens, int K, int E, int64_t width, void* dy,
+                  int64_t lddy, float* dw, cudaStream_t st) {
+  const long long tc = (tokens + 7) / 8;
+  auto k = K <= 2 ? combine_bwd_k<T, VEC, 2> : K <= 4 ? combine_bwd_k<T, VEC, 4> : combine_bwd_k<T, VEC, 8>;
+  k<<<(unsigned)(tc + E * 16), 256, 0, st>>>((const T*)dout, lddo, (const T*)y, ldy, offs, perm, row, rows, w, tokens,
+                                             K, E, width, (T*)dy, lddy, dw, tc);
+  return ops_launched();
+}
+
+// checks of the routing triple as the moves read it
+int moves_ok(int64_t tokens, int32_t K, int32_t E, int64_t rows, int64_t width, const void* offs, const void* perm,
+             const void* row) {
+  const int st = route_ok(tokens, K, E);
+  if (st) return st;
+  if (rows < 0 || width < 1) return MT_ERR_ARG;
+  if (rows > OPS_MAX_ROWS || width > OPS_MAX_ROWS) return MT_ERR_UNSUPPORTED;
+  if (!offs || !perm || !row || !ops_aligned(offs, 4) || !ops_aligned(perm, 4) || !ops_aligned(row, 4))
+    return MT_ERR_ARG;
+  // perm and offs were made for this many rows
+  return rows == route_rows(tokens, K, E) ? MT_OK : MT_ERR_ARG;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t mt_route_rows(int64_t n_tokens, int32_t top_k, int32_t n_experts) {
+  const int st = route_ok(n_tokens, top_k, n_experts);
+  return st ? -st : route_rows(n_tokens, top_k, n_experts);
+}
+
+int64_t mt_route_ws_bytes(int64_t n_tokens, int32_t top_k, int32_t n_experts) {
+  const int st = route_ok(n_tokens, top_k, n_experts);
+  if (st) return -st;
+  const int64_t n = n_tokens * top_k;
+  return n <= RO_SMALL ? 16 : (n + RO_CHUNK - 1) / RO_CHUNK * RO_E * 4;
+}
+
+int32_t mt_route_order(const int32_t* idx, int64_t n_tokens, int32_t top_k, int32_t n_experts, int32_t* offs,
+                       int32_t* perm, int32_t* row, void* ws, int64_t ws_bytes, int32_t* status, void* stream) {
+  const int st = route_ok(n_tokens, top_k, n_experts);
+  if (st) return st;
+  if (!offs || !perm || !status || (n_tokens && (!idx || !row))) return MT_ERR_ARG;
+  if (!ops_aligned(idx, 4) || !ops_aligned(offs, 4) || !ops_aligned(perm, 4) || !ops_aligned(row, 4) ||
+      !ops_aligned(status, 4))
+    return MT_ERR_ARG;
+  const int64_t n = n_tokens * top_k, rows = route_rows(n_tokens, top_k, n_experts);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (n <= RO_SMALL) {
+    ro_small<<<1, 1024, 0, s>>>(idx, (int)n, n_experts, rows, offs, perm, row, status);
+    return ops_launched();
+  }
+  if (!ws || !ops_aligned(ws, 16)) return MT_ERR_ARG;
+  if (ws_bytes < mt_route_ws_bytes(n_tokens, top_k, n_experts)) return MT_ERR_ARENA_SMALL;
+  const unsigned chunks = (unsigned)((n + RO_CHUNK - 1) / RO_CHUNK);
+  ro_hist<<<chunks, 256, 0, s>>>(idx, n, n_experts, (int*)ws, status);
+  ro_scatter<<<chunks, 256, 0, s>>>(idx, n, n_experts, rows, (const int*)ws, offs, perm, row, status);
+  return ops_launched();
+}
+
+int32_t mt_dispatch(const void* x, int32_t dtype, int64_t ldx, int64_t n_tokens, int64_t width, int32_t top_k,
+                    int32_t n_experts, const int32_t* offs, const int32_t* perm, const int32_t* row, int64_t rows,
+                    void* out, int64_t ldo, void* stream) {
+  const int st = moves_ok(n_tokens, top_k, n_experts, rows, width, offs, perm, row);
+  if (st) return st;
+  if (!ops_dtype_ok(dtype) || !ops_mat_ok(out, dtype, ldo, width)) return MT_ERR_ARG;
+  if (n_tokens == 0) return MT_OK;
+  if (!ops_mat_ok(x, dtype, ldx, width)) return MT_ERR_ARG;
+  const bool vec = ops_vec(x, dtype, ldx) && ops_vec(out, dtype, ldo);
+  auto f = dtype == MT_DT_FP32 ? dispatch_t<float> : dispatch_t<__nv_bfloat16>;
+  return f(x, ldx, n_tokens, width, top_k, n_experts, offs, perm, row, rows, out, ldo, vec, (cudaStream_t)stream);
+}
+
+int32_t mt_dispatch8(const void* x, int32_t dtype, int64_t ldx, int64_t n_tokens, int32_t top_k, int32_t n_experts,
+                     const int32_t* offs, const int32_t* perm, const int32_t* row, const mt_mat8* out, void* stream) {
+  if (!ops_mat8_ok(out) || out->block_rows != 1 || out->batch != 1 || out->halves) return MT_ERR_ARG;
+  const int st = moves_ok(n_tokens, top_k, n_experts, out->rows, out->cols, offs, perm, row);
+  if (st) return st;
+  if (!ops_dtype_ok(dtype)) return MT_ERR_ARG;
+  if (n_tokens == 0) return MT_OK;
+  if (!ops_mat_ok(x, dtype, ldx, out->cols)) return MT_ERR_ARG;
+  auto f = dtype == MT_DT_FP32 ? dispatch8_t<float> : dispatch8_t<__nv_bfloat16>;
+  return f(x, ldx, n_tokens, top_k, n_experts, offs, perm, row, out, ops_vec(x, dtype, ldx), (cudaStream_t)stream);
+}
+
+int32_t mt_combine(const void* y, int32_t dtype, int64_t ldy, int64_t rows, const int32_t* row, const float* w,
+                   int64_t n_tokens, int32_t top_k, int64_t width, void* out, int64_t ldo, void* stream) {
+  const int st = route_ok(n_tokens, top_k, MT_MAX_EXPERTS);
+  if (st) return st;
+  if (rows < 0 || width < 1 || !ops_dtype_ok(dtype)) return MT_ERR_ARG;
+  if (rows > OPS_MAX_ROWS || width > OPS_MAX_ROWS) return MT_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return MT_OK;
+  if (!row || !ops_aligned(row, 4) || !ops_aligned(w, 4)) return MT_ERR_ARG;
+  if (!ops_mat_ok(y, dtype, ldy, width) || !ops_mat_ok(out, dtype, ldo, width)) return MT_ERR_ARG;
+  const bool vec = ops_vec(y, dtype, ldy) && ops_vec(out, dtype, ldo);
+  auto f = dtype == MT_DT_FP32 ? (vec ? combine_t<float, true> : combine_t<float, false>)
+                               : (vec ? combine_t<__nv_bfloat16, true> : combine_t<__nv_bfloat16, false>);
+  return f(y, ldy, rows, row, w, n_tokens, top_k, width, out, ldo, (cudaStream_t)stream);
+}
+
+int32_t mt_combine_bwd(const void* dout, int32_t dtype, int64_t lddo, const void* y, int64_t ldy, const int32_t* offs,
+                       const int32_t* perm, const int32_t* row, int64_t rows, const float* w, int64_t n_tokens,
+                       int32_t top_k, int32_t n_experts, int64_t width, void* dy, int64_t lddy, float* dw,
+                       void* stream) {
+  const int st = moves_ok(n_tokens, top_k, n_experts, rows, width, offs, perm, row);
+  if (st) return st;
+  if (!ops_dtype_ok(dtype)) return MT_ERR_ARG;
+  if (n_tokens == 0) return MT_OK;
+  if (!w || !dw || !ops_aligned(w, 4) || !ops_aligned(dw, 4)) return MT_ERR_ARG;
+  if (!ops_mat_ok(dout, dtype, lddo, width) || !ops_mat_ok(y, dtype, ldy, width) || !ops_mat_ok(dy, dtype, lddy, width))
+    return MT_ERR_ARG;
+  const bool vec = ops_vec(dout, dtype, lddo) && ops_vec(y, dtype, ldy) && ops_vec(dy, dtype, lddy);
+  auto f = dtype == MT_DT_FP32 ? (vec ? combine_bwd_t<float, true> : combine_bwd_t<float, false>)
+                               : (vec ? combine_bwd_t<__nv_bfloat16, true> : combine_bwd_t<__nv_bfloat16, false>);
+  return f(dout, lddo, y, ldy, offs, perm, row, rows, w, n_tokens, top_k, n_experts, width, dy, lddy, dw,
+           (cudaStream_t)stream);
+}
+
+}  // extern "C"

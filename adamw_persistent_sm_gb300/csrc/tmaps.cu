@@ -121,3 +121,21 @@ int mt_build_debug_maps(KArgs* a, const void* A, long long a_rows, long long a_c
   if (C) ok &= encode_epi(&a->maps[c_f32 ? MAP_E_Y : MAP_E_QKV], C, c_rows, c_cols, c_f32);
   return ok ? MT_OK : MT_ERR_ARG;
 }
+
+int mt_encode_map(CUtensorMap* m, int type, const void* base, long long cols, long long rows, long long mats,
+                  long long row_bytes, long long mat_bytes, unsigned bc, unsigned br) {
+  std::call_once(g_once, resolve);
+  if (!g_encode) return MT_ERR_CUDA;
+  const int rank = type == MT_MAP_U8 ? 2 : 3;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)mats};
+  cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)mat_bytes};
+  cuuint32_t box[3] = {bc, br, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType dt = type == MT_MAP_U8     ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                 : type == MT_MAP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  const CUresult r = g_encode(m, dt, rank, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MT_OK : MT_ERR_ARG;
+}

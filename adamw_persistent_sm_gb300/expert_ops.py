@@ -1,0 +1,467 @@
+"""The expert layer's stand-alone operators on torch tensors.
+
+The functions check types, shapes and devices, pass pointers to the C ABI
+(``include/moe_train.h`` has each operator's definition) on the tensors'
+device and its current stream, and return the outputs.  Outputs may be given
+(``out=`` and the like); otherwise they are allocated through torch.  Nothing
+here synchronises: a device-side failure is reported by :func:`check`.
+
+* :class:`Route` - tokens sorted by expert and back, and the gradients;
+* :class:`Tensor8`, :func:`quant8`, :func:`quant8_t`, :func:`dequant8`,
+  :func:`gemm8`, :func:`gemm8_reduce` - products of e4m3 matrices with a
+  power-of-two scale per block of 128;
+* :func:`swiglu8`, :func:`swiglu8_bwd` - SwiGLU that saves its inputs in 8 bits.
+
+Matrices may be views whose rows are contiguous (any row stride).
+"""
+from __future__ import annotations
+
+import ctypes as C
+
+import torch
+
+from . import binding as B
+
+_DTYPES = {torch.float32: B.MT_DT_FP32, torch.bfloat16: B.MT_DT_BF16}
+_status: dict = {}          # device index -> int32 [2] status words
+
+
+def _error(what: str, st: int) -> Exception:
+    from .trainer import StatusError
+    return StatusError(f"{what}: {B.status_string(st)} ({st})")
+
+
+class _On:
+    """The device of a call's tensors made current, where it is not already;
+    gives the current stream there."""
+
+    __slots__ = ("dev", "prev")
+
+    def __init__(self, dev: torch.device):
+        self.dev = dev.index
+
+    def __enter__(self) -> int:
+        cur = torch.cuda.current_device()
+        self.prev = cur if cur != self.dev else None
+        if self.prev is not None:
+            torch.cuda.set_device(self.dev)
+        return torch._C._cuda_getCurrentRawStream(self.dev)
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            torch.cuda.set_device(self.prev)
+
+
+def _status_word(dev: torch.device) -> torch.Tensor:
+    t = _status.get(dev.index)
+    if t is None:
+        t = _status[dev.index] = torch.zeros(2, dtype=torch.int32, device=dev)
+        torch.cuda.synchronize(dev)         # once per device: zeroed before any other stream uses it
+    return t
+
+
+def check(device: str | torch.device = "cuda") -> None:
+    """Wait for the device and raise if an operator reported a failure there
+    since the last call (an index out of range, a wait that ran out)."""
+    dev = _device(device)
+    t = _status_word(dev)
+    torch.cuda.synchronize(dev)
+    st, site = t.tolist()
+    if st != B.MT_OK:
+        t.zero_()
+        raise _error(f"device-side check (site {site})", st)
+
+
+def _device(device) -> torch.device:
+    dev = torch.device(device)
+    if dev.type != "cuda":
+        raise ValueError(f"expected a CUDA device, got {dev}")
+    return dev if dev.index is not None else torch.device("cuda", torch.cuda.current_device())
+
+
+def _mat(t: torch.Tensor, what: str, dev, rows: int | None = None, cols: int | None = None, dtype=None) -> int:
+    """Checks a [rows, cols] matrix with contiguous rows; its row stride."""
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{what}: {t.dtype} where {dtype or 'float32 or bfloat16'} is needed")
+    if t.dim() != 2 or t.device != dev:
+        raise ValueError(f"{what}: expected a matrix on {dev}, got {tuple(t.shape)} on {t.device}")
+    r, c = t.shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{what}: expected [{rows}, {cols}], got [{r}, {c}]")
+    s0, s1 = t.stride()
+    if (c > 1 and s1 != 1) or (r > 1 and s0 < c):
+        raise ValueError(f"{what}: rows must be contiguous and may not overlap (strides {s0}, {s1})")
+    return s0 if r > 1 else max(s0, c)
+
+
+def _ints(t: torch.Tensor, what: str, dev, shape) -> int:
+    if t.dtype != torch.int32 or t.device != dev or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what}: expected contiguous int32 {tuple(shape)} on {dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _limit(n_rows, dev) -> int:
+    if n_rows is None:
+        return 0
+    return _ints(n_rows, "n_rows", dev, (1,))
+
+
+# ---------------------------------------------------------------------------
+# matrices in 8 bits
+# ---------------------------------------------------------------------------
+class Tensor8:
+    """A matrix, or a stack of them, held as e4m3 codes and scale bytes.
+
+    ``codes`` uint8 [rows, ld] or [batch, rows, ld], ld a multiple of 16 and at
+    least ``cols``; ``scales`` uint8 [rows, blocks] (block_rows 1) or
+    [ceil(rows / 128), blocks] (block_rows 128), with the same batch dimension.
+    ``halves``: the columns are two parts with blocks of their own.
+    """
+
+    __slots__ = ("codes", "scales", "cols", "block_rows", "halves", "device", "_mat", "_ref")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int, block_rows: int = 1,
+                 halves: bool = False):
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+            raise TypeError("codes and scales are uint8")
+        if codes.dim() not in (2, 3) or scales.dim() != codes.dim() or codes.device != scales.device \
+                or codes.device.type != "cuda":
+            raise ValueError("codes and scales are matrices, or stacks of them, on one CUDA device")
+        if block_rows not in (1, 128) or cols < 1 or (halves and (cols % 2 or block_rows != 1)):
+            raise ValueError(f"block_rows {block_rows}, cols {cols}, halves {halves}")
+        batch = codes.shape[0] if codes.dim() == 3 else 1
+        rows, ld = codes.shape[-2:]
+        blocks = 2 * -(-(cols // 2) // 128) if halves else -(-cols // 128)
+        need = (-(-rows // 128) if block_rows == 128 else rows, blocks)
+        if tuple(scales.shape[-2:]) != need or (codes.dim() == 3 and scales.shape[0] != batch):
+            raise ValueError(f"scales: expected {need} for each matrix, got {tuple(scales.shape)}")
+        if ld < cols or ld % 16 or not codes.is_contiguous() or not scales.is_contiguous() \
+                or codes.data_ptr() % 16:
+            raise ValueError(f"codes: rows of {ld} bytes hold {cols} columns, start on 16-byte boundaries "
+                             "and are contiguous, as are the scales")
+        self.codes, self.scales, self.cols, self.block_rows, self.halves = codes, scales, cols, block_rows, halves
+        self.device = codes.device
+        # an empty tensor has no storage: any address stands in for it
+        self._mat = B.mt_mat8(codes.data_ptr() or 16, scales.data_ptr() or 16, rows, cols, ld, blocks, block_rows,
+                              max(batch, 1), int(halves), 0)
+        self._ref = C.byref(self._mat)
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[-2]
+
+    @property
+    def batch(self) -> int:
+        return self.codes.shape[0] if self.codes.dim() == 3 else 1
+
+    @property
+    def shape(self) -> tuple:
+        return (*self.codes.shape[:-1], self.cols)
+
+    def __getitem__(self, i: int) -> "Tensor8":
+        """Matrix i of a stack (a view)."""
+        if self.codes.dim() != 3:
+            raise IndexError("not a stack of matrices")
+        return Tensor8(self.codes[i], self.scales[i], self.cols, self.block_rows, self.halves)
+
+
+def empty8(rows: int, cols: int, device="cuda", block_rows: int = 1, batch: int | None = None,
+           halves: bool = False) -> Tensor8:
+    """Buffers for an 8-bit matrix, or a stack of ``batch``."""
+    dev = _device(device)
+    lead = () if batch is None else (batch,)
+    blocks = 2 * -(-(cols // 2) // 128) if halves else -(-cols // 128)
+    codes = torch.empty((*lead, rows, -(-cols // 16) * 16), dtype=torch.uint8, device=dev)
+    scales = torch.empty((*lead, -(-rows // 128) if block_rows == 128 else rows, blocks), dtype=torch.uint8,
+                         device=dev)
+    return Tensor8(codes, scales, cols, block_rows, halves)
+
+
+def _as_matrix(x: torch.Tensor, what: str, dev) -> tuple[int, int]:
+    """A matrix or a stack whose matrices follow one another: (batch, row stride)."""
+    if x.dim() == 2:
+        return 1, _mat(x, what, dev)
+    if x.dim() != 3:
+        raise ValueError(f"{what}: expected a matrix or a stack of matrices, got {tuple(x.shape)}")
+    if x.shape[0] > 1 and x.shape[1] > 0 and x.stride(0) != x.shape[1] * x.stride(1):
+        raise ValueError(f"{what}: the matrices of a stack must follow one another")
+    if x.shape[1] == 1:
+        return x.shape[0], _mat(x[:, 0], what, dev)
+    return x.shape[0], _mat(x[0], what, dev) if x.shape[0] else x.shape[2]
+
+
+def quant8(x: torch.Tensor, block_rows: int = 1, out: Tensor8 | None = None, n_rows: torch.Tensor | None = None,
+           halves: bool = False) -> Tensor8:
+    """x [rows, cols] or [batch, rows, cols] in 8 bits.  ``n_rows`` (device
+    int32 [1]): only rows below it are written."""
+    dev = x.device
+    batch, ldx = _as_matrix(x, "x", dev)
+    if out is None:
+        out = empty8(x.shape[-2], x.shape[-1], dev, block_rows, batch if x.dim() == 3 else None, halves)
+    if out.shape != tuple(x.shape) or out.device != dev:
+        raise ValueError(f"out: expected {tuple(x.shape)} on {dev}, got {out.shape} on {out.device}")
+    if batch == 0:
+        return out
+    with _On(dev) as s:
+        st = B.load().mt_quant8(x.data_ptr(), _DTYPES[x.dtype], ldx, _limit(n_rows, dev), out._ref, s)
+    if st:
+        raise _error("mt_quant8", st)
+    return out
+
+
+def quant8_t(x, block_rows: int = 1, out: Tensor8 | None = None, n_rows: torch.Tensor | None = None) -> Tensor8:
+    """The transpose of x [rows, cols] in 8 bits, [cols, rows]: with block_rows
+    1 each scale covers 128 rows of a column of x.  x is a matrix, a stack, or
+    a :class:`Tensor8` saved earlier (block_rows 1)."""
+    dev = x.device
+    rows, cols = x.shape[-2:]
+    lead = tuple(x.shape[:-2])
+    src, ptr, dt, ldx = None, 0, 0, 0
+    if isinstance(x, Tensor8):
+        src = x._ref
+    else:
+        _, ldx = _as_matrix(x, "x", dev)
+        ptr, dt = x.data_ptr(), _DTYPES[x.dtype]
+    if out is None:
+        out = empty8(cols, rows, dev, block_rows, lead[0] if lead else None)
+    if out.shape != (*lead, cols, rows) or out.device != dev:
+        raise ValueError(f"out: expected {(*lead, cols, rows)} on {dev}, got {out.shape} on {out.device}")
+    if lead and lead[0] == 0:
+        return out
+    with _On(dev) as s:
+        st = B.load().mt_quant8_t(ptr, dt, ldx, src, _limit(n_rows, dev), out._ref, s)
+    if st:
+        raise _error("mt_quant8_t", st)
+    return out
+
+
+def dequant8(a: Tensor8, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+             n_rows: torch.Tensor | None = None) -> torch.Tensor:
+    """The values of an 8-bit matrix (block_rows 1)."""
+    dev = a.device
+    if out is None:
+        out = torch.empty(a.shape, dtype=dtype, device=dev)
+    ldo = _mat(out, "out", dev, a.rows, a.cols)
+    with _On(dev) as s:
+        st = B.load().mt_dequant8(a._ref, _limit(n_rows, dev), out.data_ptr(), _DTYPES[out.dtype], ldo, s)
+    if st:
+        raise _error("mt_dequant8", st)
+    return out
+
+
+def gemm8(a: Tensor8, b: Tensor8, out: torch.Tensor | None = None, offs: torch.Tensor | None = None,
+          dtype: torch.dtype = torch.bfloat16, accumulate: bool = False) -> torch.Tensor:
+    """a b^T: a [M, K]; b [N, K], or with ``offs`` (int32 [E+1] row starts) [E, N, K]."""
+    dev = a.device
+    if b.device != dev:
+        raise ValueError(f"b is on {b.device}, a on {dev}")
+    seg = b.batch if offs is not None else 0
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((a.rows, b.rows), dtype=dtype, device=dev)
+    ldc = _mat(out, "out", dev, a.rows, b.rows)
+    po = 0 if offs is None else _ints(offs, "offs", dev, (seg + 1,))
+    with _On(dev) as s:
+        st = B.load().mt_gemm8(a._ref, b._ref, po, seg, out.data_ptr(), _DTYPES[out.dtype], ldc, int(accumulate),
+                               _status_word(dev).data_ptr(), s)
+    if st:
+        raise _error("mt_gemm8", st)
+    return out
+
+
+def gemm8_reduce(a: Tensor8, b: Tensor8, offs: torch.Tensor, out: torch.Tensor | None = None,
+                 accumulate: bool = False) -> torch.Tensor:
+    """out[e] = a[:, offs[e]:offs[e+1]] b[:, same]^T in fp32: a [M, P], b [N, P]."""
+    dev = a.device
+    seg = offs.numel() - 1
+    if b.device != dev:
+        raise ValueError(f"b is on {b.device}, a on {dev}")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((max(seg, 0), a.rows, b.rows), dtype=torch.float32, device=dev)
+    if out.dim() != 3 or out.dtype != torch.float32 or tuple(out.shape) != (seg, a.rows, b.rows):
+        raise ValueError(f"out: expected float32 {(seg, a.rows, b.rows)}, got {out.dtype} {tuple(out.shape)}")
+    _, ldc = _as_matrix(out, "out", dev)
+    with _On(dev) as s:
+        st = B.load().mt_gemm8_reduce(a._ref, b._ref, _ints(offs, "offs", dev, (seg + 1,)), seg, out.data_ptr(), ldc,
+                                      int(accumulate), _status_word(dev).data_ptr(), s)
+    if st:
+        raise _error("mt_gemm8_reduce", st)
+    return out
+
+
+def swiglu8(gu: torch.Tensor, act: Tensor8 | None = None, saved: Tensor8 | None = None,
+            n_rows: torch.Tensor | None = None) -> Tensor8:
+    """silu(g) * u of gu = [g | u], in 8 bits; ``saved`` (empty8 with halves)
+    receives g and u for :func:`swiglu8_bwd`."""
+    dev = gu.device
+    ld = _mat(gu, "gu", dev)
+    rows, cols = gu.shape
+    if cols % 2 or cols < 2:
+        raise ValueError(f"gu: an even number of columns, got {cols}")
+    if act is None:
+        act = empty8(rows, cols // 2, dev)
+    if act.shape != (rows, cols // 2) or act.device != dev or (saved is not None and saved.device != dev):
+        raise ValueError(f"act: expected {(rows, cols // 2)} on {dev}, got {act.shape} on {act.device}")
+    with _On(dev) as s:
+        st = B.load().mt_swiglu8(gu.data_ptr(), _DTYPES[gu.dtype], ld, _limit(n_rows, dev), act._ref,
+                                 saved._ref if saved is not None else None, s)
+    if st:
+        raise _error("mt_swiglu8", st)
+    return act
+
+
+def swiglu8_bwd(dact: torch.Tensor, saved: Tensor8, dgu: torch.Tensor | None = None,
+                act: torch.Tensor | None = None, n_rows: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of :func:`swiglu8` at the saved g and u; ``act``, where given,
+    receives silu(g) * u of the saved values."""
+    dev = dact.device
+    ldd = _mat(dact, "dact", dev, saved.rows, saved.cols // 2)
+    if saved.device != dev:
+        raise ValueError(f"saved is on {saved.device}, dact on {dev}")
+    if dgu is None:
+        dgu = torch.empty(saved.shape, dtype=dact.dtype, device=dev)
+    ldg = _mat(dgu, "dgu", dev, saved.rows, saved.cols, dact.dtype)
+    lda = 0 if act is None else _mat(act, "act", dev, *dact.shape, dact.dtype)
+    with _On(dev) as s:
+        st = B.load().mt_swiglu8_bwd(dact.data_ptr(), _DTYPES[dact.dtype], ldd, saved._ref, _limit(n_rows, dev),
+                                     dgu.data_ptr(), ldg, 0 if act is None else act.data_ptr(), lda, s)
+    if st:
+        raise _error("mt_swiglu8_bwd", st)
+    return dgu
+
+
+# ---------------------------------------------------------------------------
+# tokens sorted by expert and back
+# ---------------------------------------------------------------------------
+class Route:
+    """Buffers of a routing of ``n_tokens`` x ``top_k`` assignments over
+    ``n_experts``, refilled by :meth:`order`: ``offs`` [E+1] segment starts,
+    ``perm`` [rows] the assignment at each row, ``row`` [n_tokens, top_k] the
+    row of each assignment (all int32, -1 for none)."""
+
+    def __init__(self, n_tokens: int, top_k: int, n_experts: int, device="cuda"):
+        dev = _device(device)
+        rows = B.load().mt_route_rows(n_tokens, top_k, n_experts)
+        if rows < 0:
+            raise _error("mt_route_rows", -rows)
+        self._set(torch.empty(n_experts + 1, dtype=torch.int32, device=dev),
+                  torch.empty(rows, dtype=torch.int32, device=dev),
+                  torch.empty((n_tokens, top_k), dtype=torch.int32, device=dev))
+        self.ws = torch.empty(B.load().mt_route_ws_bytes(n_tokens, top_k, n_experts), dtype=torch.uint8, device=dev)
+
+    @classmethod
+    def of(cls, offs: torch.Tensor, perm: torch.Tensor, row: torch.Tensor) -> "Route":
+        """A routing ordered before, from its three tensors."""
+        r = cls.__new__(cls)
+        r._set(offs, perm, row)
+        r.ws = None
+        return r
+
+    def _set(self, offs, perm, row):
+        self.device = offs.device
+        if row.dim() != 2 or offs.dim() != 1 or perm.dim() != 1 or self.device.type != "cuda":
+            raise ValueError("offs [E+1], perm [rows] and row [tokens, top_k] on a CUDA device")
+        self.n_tokens, self.top_k = row.shape
+        self.n_experts, self.rows = offs.numel() - 1, perm.numel()
+        rows = B.load().mt_route_rows(self.n_tokens, self.top_k, self.n_experts)
+        if rows < 0:
+            raise _error("mt_route_rows", -rows)
+        if rows != self.rows:
+            raise ValueError(f"perm: expected {rows} rows, got {self.rows}")
+        self.offs, self.perm, self.row = offs, perm, row
+        self._ptrs = (_ints(offs, "offs", self.device, offs.shape), _ints(perm, "perm", self.device, perm.shape),
+                      _ints(row, "row", self.device, row.shape))
+
+    def order(self, idx: torch.Tensor) -> "Route":
+        """Sort idx int32 [n_tokens, top_k] (-1: no expert)."""
+        dev = self.device
+        if self.ws is None:
+            self.ws = torch.empty(B.load().mt_route_ws_bytes(self.n_tokens, self.top_k, self.n_experts),
+                                  dtype=torch.uint8, device=dev)
+        p = _ints(idx, "idx", dev, self.row.shape)
+        with _On(dev) as s:
+            st = B.load().mt_route_order(p, self.n_tokens, self.top_k, self.n_experts, *self._ptrs,
+                                         self.ws.data_ptr(), self.ws.numel(), _status_word(dev).data_ptr(), s)
+        if st:
+            raise _error("mt_route_order", st)
+        return self
+
+    def dispatch(self, x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+        """x [n_tokens, width] to the rows of its experts, [rows, width]; zeros
+        in padding rows; rows behind the last segment are left as they were."""
+        dev = self.device
+        ldx = _mat(x, "x", dev, self.n_tokens)
+        if out is None:
+            out = torch.empty((self.rows, x.shape[1]), dtype=x.dtype, device=dev)
+        ldo = _mat(out, "out", dev, self.rows, x.shape[1], x.dtype)
+        with _On(dev) as s:
+            st = B.load().mt_dispatch(x.data_ptr(), _DTYPES[x.dtype], ldx, self.n_tokens, x.shape[1], self.top_k,
+                                      self.n_experts, *self._ptrs, self.rows, out.data_ptr(), ldo, s)
+        if st:
+            raise _error("mt_dispatch", st)
+        return out
+
+    def dispatch8(self, x: torch.Tensor, out: Tensor8 | None = None) -> Tensor8:
+        """:meth:`dispatch` with the rows quantised on their way."""
+        dev = self.device
+        ldx = _mat(x, "x", dev, self.n_tokens)
+        if out is None:
+            out = empty8(self.rows, x.shape[1], dev)
+        if out.shape != (self.rows, x.shape[1]) or out.device != dev:
+            raise ValueError(f"out: expected {(self.rows, x.shape[1])} on {dev}, got {out.shape} on {out.device}")
+        with _On(dev) as s:
+            st = B.load().mt_dispatch8(x.data_ptr(), _DTYPES[x.dtype], ldx, self.n_tokens, self.top_k, self.n_experts,
+                                       *self._ptrs, out._ref, s)
+        if st:
+            raise _error("mt_dispatch8", st)
+        return out
+
+    def _weights(self, w: torch.Tensor, what: str) -> int:
+        if w.dtype != torch.float32 or w.device != self.device or w.shape != self.row.shape or not w.is_contiguous():
+            raise ValueError(f"{what}: expected contiguous float32 {tuple(self.row.shape)} on {self.device}")
+        return w.data_ptr()
+
+    def combine(self, y: torch.Tensor, w: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+        """Rows y [rows, width] back to tokens, weighted by w float32
+        [n_tokens, top_k] (None: plain sums)."""
+        dev = self.device
+        ldy = _mat(y, "y", dev, self.rows)
+        if out is None:
+            out = torch.empty((self.n_tokens, y.shape[1]), dtype=y.dtype, device=dev)
+        ldo = _mat(out, "out", dev, self.n_tokens, y.shape[1], y.dtype)
+        pw = 0 if w is None else self._weights(w, "w")
+        with _On(dev) as s:
+            st = B.load().mt_combine(y.data_ptr(), _DTYPES[y.dtype], ldy, self.rows, self._ptrs[2], pw, self.n_tokens,
+                                     self.top_k, y.shape[1], out.data_ptr(), ldo, s)
+        if st:
+            raise _error("mt_combine", st)
+        return out
+
+    def dispatch_bwd(self, dxs: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+        """Gradient of :meth:`dispatch`: the sum of each token's rows."""
+        return self.combine(dxs, None, out)
+
+    def combine_bwd(self, dout: torch.Tensor, y: torch.Tensor, w: torch.Tensor, dy: torch.Tensor | None = None,
+                    dw: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+        """Gradients of :meth:`combine` for y (zeros in padding rows, rows
+        behind the last segment left as they were) and for w."""
+        dev = self.device
+        width = dout.shape[-1]
+        ldd = _mat(dout, "dout", dev, self.n_tokens)
+        ldy = _mat(y, "y", dev, self.rows, width, dout.dtype)
+        if dy is None:
+            dy = torch.empty((self.rows, width), dtype=dout.dtype, device=dev)
+        if dw is None:
+            dw = torch.empty(self.row.shape, dtype=torch.float32, device=dev)
+        ldg = _mat(dy, "dy", dev, self.rows, width, dout.dtype)
+        with _On(dev) as s:
+            st = B.load().mt_combine_bwd(dout.data_ptr(), _DTYPES[dout.dtype], ldd, y.data_ptr(), ldy, *self._ptrs,
+                                         self.rows, self._weights(w, "w"), self.n_tokens, self.top_k, self.n_experts,
+                                         width, dy.data_ptr(), ldg, self._weights(dw, "dw"), s)
+        if st:
+            raise _error("mt_combine_bwd", st)
+        return dy, dw

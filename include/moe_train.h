@@ -386,6 +386,159 @@ int32_t mt_debug_gemm(const void* A, int32_t a_mn, const void* B, int32_t b_mn, 
                       int32_t K, int32_t rag, const int32_t* offs, int32_t nseg, int32_t precision, int32_t use_tc,
                       void* arena, int64_t arena_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Stand-alone operators of the expert layer.
+ *
+ * The update above runs routing, gather, expert products and combine fused
+ * in one kernel and in bf16.  These entry points offer the same steps on the
+ * caller's own tensors, and the expert products with 8-bit operands:
+ *   route   - mt_route_order, mt_dispatch, mt_dispatch8, mt_combine,
+ *             mt_combine_bwd: tokens sorted by expert and back, with weights
+ *             applied, and the gradients;
+ *   product - mt_quant8, mt_quant8_t, mt_dequant8, mt_gemm8, mt_gemm8_reduce:
+ *             products of e4m3 matrices with one scale per block of 128;
+ *   SwiGLU  - mt_swiglu8, mt_swiglu8_bwd: the expert nonlinearity with its
+ *             inputs saved in 8 bits, and the backward pass that reads them.
+ *
+ * Conventions beyond those at the top of this file:
+ *  - Matrices are row-major with a row stride in ELEMENTS (ld >= columns).
+ *    Pointers need the alignment of their element type; 16-byte alignment of
+ *    a buffer and of its row stride selects vector accesses (same results).
+ *    mt_mat8.codes is 16-byte aligned and mt_mat8.ld a multiple of 16.
+ *  - Work is enqueued on `stream`, which belongs to the current device, where
+ *    all the buffers must be.  No call allocates, synchronises or keeps
+ *    anything; every launch can be captured into a CUDA graph.
+ *  - Outputs may not overlap inputs or one another.  Calls that share an
+ *    output, a workspace or a status word must be ordered by the caller.
+ *  - `status` (device int32[2], zeroed by the caller once) receives an
+ *    mt_status and an error site when a device-side check fails; the first
+ *    failure stays.  It may be shared by any number of calls.
+ *  - A count of zero (tokens, rows) is valid and enqueues nothing unless
+ *    stated.
+ * Results are bitwise reproducible: no order of additions depends on timing.
+ */
+enum { MT_DT_FP32 = 0, MT_DT_BF16 = 1 };   /* element types, numbered as MT_PREC_* */
+
+/*
+ * A matrix held in 8 bits: e4m3 codes and one power-of-two scale per block of
+ * 128 elements (host struct, copied at call time; the buffers are the
+ * caller's device memory).  Element (b, r, c) is
+ *   e4m3(codes[(b*rows + r)*ld + c]) * 2^(scale byte - 127),
+ * its scale byte lying at
+ *   scales[(b*rows + r)*lds + c/128]                    block_rows == 1
+ *   scales[(b*ceil(rows/128) + r/128)*lds + c/128]      block_rows == 128.
+ * halves == 1 (block_rows 1, cols even): the columns are two parts of cols/2,
+ * each with its own blocks, the second part's scale bytes following the first's
+ * (byte c/128, or ceil(cols/2/128) + (c - cols/2)/128).
+ * Quantisation: e is the least integer >= -126 with amax <= 448 * 2^e over the
+ * block's finite elements (0 if they are all zero); code = x * 2^-e rounded to
+ * nearest even; NaN and infinite elements become the e4m3 NaN.  A power of
+ * two loses nothing against a free scale: the codes are floating-point, and
+ * scaling, restoring and transposing are then exact.
+ * Limits: rows * batch and cols <= 2^30.
+ */
+typedef struct mt_mat8 {
+  void* codes;
+  void* scales;
+  int64_t rows, cols;      /* of one matrix */
+  int64_t ld;              /* bytes from row to row of codes */
+  int64_t lds;             /* bytes from row to row of scales */
+  int32_t block_rows;      /* 1 or 128 */
+  int32_t batch;           /* matrices, stacked (>= 1) */
+  int32_t halves;          /* 0 or 1 */
+  int32_t reserved0;       /* must be 0 */
+} mt_mat8;
+
+/* Rows that every routing of n_tokens * top_k assignments fits in, when each
+ * expert's segment is padded to a multiple of 128 rows:
+ * round_up(n_tokens * top_k + n_experts * 127, 128); or a negative mt_status.
+ * Limits as the update's: top_k <= min(8, n_experts), n_experts <= 64, at most
+ * 2^30 rows. */
+int64_t mt_route_rows(int64_t n_tokens, int32_t top_k, int32_t n_experts);
+/* Bytes of device workspace (16-byte aligned) for mt_route_order. */
+int64_t mt_route_ws_bytes(int64_t n_tokens, int32_t top_k, int32_t n_experts);
+
+/* Sort assignments by expert.  idx int32 [n_tokens, top_k]: expert of
+ * assignment a = t*top_k + k, or -1 for none (a masked or padding token); an
+ * index outside [-1, n_experts) counts as -1 and reports
+ * MT_ERR_DEVICE_BOUNDS.  A token may name an expert twice.  Outputs:
+ *   offs int32 [n_experts+1]  segment starts, multiples of 128, offs[0] = 0;
+ *   perm int32 [rows]         assignment at each row, ascending within a
+ *                             segment, -1 in padding and past offs[n_experts]
+ *                             (rows = mt_route_rows(...));
+ *   row  int32 [n_tokens, top_k]  row of each assignment, -1 for none.
+ * All outputs are written whole also for n_tokens == 0. */
+int32_t mt_route_order(const int32_t* idx, int64_t n_tokens, int32_t top_k, int32_t n_experts, int32_t* offs,
+                       int32_t* perm, int32_t* row, void* ws, int64_t ws_bytes, int32_t* status, void* stream);
+
+/* Rows to their experts: out[row[t,k]] = x[t] (row strides ldx, ldo; types as
+ * dtype), zeros in the padding rows of each segment; rows from
+ * offs[n_experts] on are left as they were.  offs, perm, row and rows as
+ * mt_route_order left them; entries of row outside [0, rows) count as -1. */
+int32_t mt_dispatch(const void* x, int32_t dtype, int64_t ldx, int64_t n_tokens, int64_t width, int32_t top_k,
+                    int32_t n_experts, const int32_t* offs, const int32_t* perm, const int32_t* row, int64_t rows,
+                    void* out, int64_t ldo, void* stream);
+/* The same with each row quantised on its way (out->rows = rows, out->cols =
+ * width, block_rows 1, batch 1, halves 0). */
+int32_t mt_dispatch8(const void* x, int32_t dtype, int64_t ldx, int64_t n_tokens, int32_t top_k, int32_t n_experts,
+                     const int32_t* offs, const int32_t* perm, const int32_t* row, const mt_mat8* out, void* stream);
+
+/* And back: out[t] = sum over k, in slot order, of w[t,k] * y[row[t,k]]
+ * (fp32 sums, rounded once); slots without a row add nothing, a token without
+ * any gets zeros.  w fp32 [n_tokens, top_k], or NULL for plain sums - the
+ * gradient of mt_dispatch. */
+int32_t mt_combine(const void* y, int32_t dtype, int64_t ldy, int64_t rows, const int32_t* row, const float* w,
+                   int64_t n_tokens, int32_t top_k, int64_t width, void* out, int64_t ldo, void* stream);
+/* Gradient of mt_combine: dy[row[t,k]] = w[t,k] * dout[t], zeros in padding
+ * rows, rows from offs[n_experts] on left as they were; dw[t,k] =
+ * <dout[t], y[row[t,k]]> (fp32 [n_tokens, top_k]), 0 for slots without a row. */
+int32_t mt_combine_bwd(const void* dout, int32_t dtype, int64_t lddo, const void* y, int64_t ldy, const int32_t* offs,
+                       const int32_t* perm, const int32_t* row, int64_t rows, const float* w, int64_t n_tokens,
+                       int32_t top_k, int32_t n_experts, int64_t width, void* dy, int64_t lddy, float* dw,
+                       void* stream);
+
+/* Quantise x [batch][rows][cols] (row stride ldx, matrices rows*ldx apart) into
+ * out.  n_rows: device int32 or NULL; only rows below it (clamped to out->rows)
+ * are written; batch 1 and block_rows 1 where it is given. */
+int32_t mt_quant8(const void* x, int32_t dtype, int64_t ldx, const int32_t* n_rows, const mt_mat8* out, void* stream);
+/* Quantise the transpose: out [batch][cols][rows] of x [batch][rows][cols],
+ * i.e. with block_rows 1 each scale covers 128 consecutive rows of one column
+ * of x.  The source is either x (x8 NULL) or an 8-bit matrix x8 with batch 1,
+ * block_rows 1, halves 0 (x NULL, dtype ignored).  With n_rows (a multiple of
+ * 128; batch 1) only the blocks below it are written. */
+int32_t mt_quant8_t(const void* x, int32_t dtype, int64_t ldx, const mt_mat8* x8, const int32_t* n_rows,
+                    const mt_mat8* out, void* stream);
+/* Values of an 8-bit matrix (block_rows 1, batch 1): out [rows, cols]. */
+int32_t mt_dequant8(const mt_mat8* a, const int32_t* n_rows, void* out, int32_t dtype, int64_t ldo, void* stream);
+
+/* C = A B^T on the tensor cores with fp32 sums: A [M, K] (batch 1, block_rows
+ * 1, halves 0), B [N, K] or, by expert, [n_seg][N][K] (block_rows 1 or 128), C
+ * [M, N] of dtype.  offs NULL: dense (n_seg 0, B batch 1).  Otherwise offs is
+ * device int32 [n_seg+1] of multiples of 128 as mt_route_order makes them, and
+ * rows offs[e]..offs[e+1]-1 of C are A's times B[e]; rows from offs[n_seg] on
+ * are left as they were.  accumulate 1: C += (fp32 C only).  A product of two
+ * scales below 2^-126 counts as 0, above 2^127 as 2^127. */
+int32_t mt_gemm8(const mt_mat8* a, const mt_mat8* b, const int32_t* offs, int32_t n_seg, void* c, int32_t dtype,
+                 int64_t ldc, int32_t accumulate, int32_t* status, void* stream);
+/* C[e] = A[:, offs[e]..offs[e+1]) B[:, same)^T: the reduction split into
+ * segments, as the experts' weight gradients are (A [M, P], B [N, P], both
+ * block_rows 1; C fp32 [n_seg][M][N], matrices M*ldc apart).  An empty segment
+ * gives zeros (with accumulate: changes nothing). */
+int32_t mt_gemm8_reduce(const mt_mat8* a, const mt_mat8* b, const int32_t* offs, int32_t n_seg, float* c, int64_t ldc,
+                        int32_t accumulate, int32_t* status, void* stream);
+
+/* act = quantised silu(g) * u of gu [rows, 2*width] = [g | u]; act->cols =
+ * width.  saved: NULL, or an 8-bit matrix [rows, 2*width] with halves 1 that
+ * keeps g and u for the backward pass.  n_rows as in mt_quant8. */
+int32_t mt_swiglu8(const void* gu, int32_t dtype, int64_t ldgu, const int32_t* n_rows, const mt_mat8* act,
+                   const mt_mat8* saved, void* stream);
+/* Backward from the saved 8-bit g and u: with s = sigmoid(g),
+ * dgu = [dact * u * s * (1 + g * (1 - s)) | dact * g * s], and, where act is
+ * not NULL, act = g * s * u (the down product's input for its weight
+ * gradient).  All of dtype; rows from *n_rows on are left as they were. */
+int32_t mt_swiglu8_bwd(const void* dact, int32_t dtype, int64_t ldda, const mt_mat8* saved, const int32_t* n_rows,
+                       void* dgu, int64_t lddgu, void* act, int64_t ldact, void* stream);
+
 /* Stable text for a status code. */
 const char* mt_status_string(int32_t status);
 

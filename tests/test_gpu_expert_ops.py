@@ -1,0 +1,597 @@
+"""The stand-alone expert operators on the GPU against their definitions in
+float64 on the host (tests/expert_ref.py), with bounds derived from the
+roundings each operator makes: U32 = 2^-24 per fp32 operation, half a step for
+the rounding to the output type."""
+import numpy as np
+import pytest
+import torch
+
+import expert_ref as R
+
+pytestmark = pytest.mark.gpu
+
+U32 = 2.0 ** -24
+DT = {"fp32": torch.float32, "bf16": torch.bfloat16}
+HALF_STEP = {torch.float32: 0.0, torch.bfloat16: 2.0 ** -8}     # of the output's rounding (fp32: counted in U32)
+
+
+@pytest.fixture(scope="module")
+def ops():
+    from adamw_persistent_sm_gb300 import expert_ops
+    yield expert_ops
+    expert_ops.check()
+
+
+def rnd(seed, *shape, std=1.0, dtype=torch.float32):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * std).to(dtype).cuda()
+
+
+def strided(t, pad, shift=0):
+    """t as a view of a wider buffer: rows `pad` elements further apart, starting `shift` in."""
+    buf = torch.full((t.shape[0], t.shape[1] + pad + shift), float("nan"), dtype=t.dtype, device=t.device)
+    v = buf[:, shift:shift + t.shape[1]]
+    v.copy_(t)
+    return v
+
+
+def close(got, want, bound, what=""):
+    got = R.as64(got) if isinstance(got, torch.Tensor) else got
+    assert np.array_equal(np.isfinite(want), np.isfinite(got)), what
+    f = np.isfinite(want)
+    bad = np.abs(got - want)[f] > np.broadcast_to(bound, want.shape)[f]
+    assert not bad.any(), (what, int(bad.sum()), float(np.abs(got - want)[f][bad].max()))
+
+
+# ---------------------------------------------------------------------------
+# route
+# ---------------------------------------------------------------------------
+def choices(seed, t, k, e, how):
+    g = np.random.default_rng(seed)
+    idx = np.stack([g.permutation(e)[:k] for _ in range(t)]).astype(np.int32) if t else np.zeros((0, k), np.int32)
+    if how == "dropped":
+        idx[g.random(t) < 0.4] = -1
+        idx[g.random((t, k)) < 0.1] = -1
+    elif how == "none":
+        idx[:] = -1
+    elif how == "one":
+        idx[:] = e - 1                   # every slot of every token names the same expert
+    elif how == "skewed":
+        idx = (g.random((t, k)) ** 4 * e).astype(np.int32)
+    return idx
+
+
+ROUTES = [(0, 2, 4, "even"), (1, 1, 1, "even"), (1, 2, 16, "even"), (1, 2, 16, "none"), (5, 8, 8, "even"),
+          (127, 1, 3, "one"), (128, 2, 2, "even"), (129, 4, 5, "dropped"), (1000, 3, 7, "skewed"),
+          (1024, 8, 64, "even"), (1025, 8, 64, "dropped"), (8193, 1, 33, "one"), (4097, 2, 16, "dropped"),
+          (5000, 2, 16, "none"), (20000, 8, 64, "skewed"), (32768, 2, 16, "even")]
+
+
+@pytest.mark.parametrize("t,k,e,how", ROUTES)
+def test_route_order(ops, t, k, e, how):
+    idx = choices(t + k, t, k, e, how)
+    r = ops.Route(t, k, e)
+    for b in (r.offs, r.perm, r.row):
+        b.fill_(12345)
+    r.order(torch.from_numpy(idx).cuda())
+    offs, perm, row = R.order(idx, e)
+    assert np.array_equal(r.offs.cpu().numpy(), offs)
+    assert np.array_equal(r.perm.cpu().numpy(), perm)
+    assert np.array_equal(r.row.cpu().numpy(), row)
+    ops.check()
+
+
+@pytest.mark.parametrize("t", [10, 9000])
+def test_route_order_reports_bad_indices(ops, t):
+    idx = choices(1, t, 2, 8, "even")
+    bad = idx.copy()
+    bad[3, 0], bad[t - 1, 1], bad[5, 0] = 8, -2, 2 ** 31 - 1
+    r = ops.Route(t, 2, 8).order(torch.from_numpy(bad).cuda())
+    from adamw_persistent_sm_gb300.trainer import StatusError
+    with pytest.raises(StatusError, match="out of range"):
+        ops.check()
+    ops.check()                                        # reported once
+    bad[3, 0] = bad[t - 1, 1] = bad[5, 0] = -1
+    for got, want in zip((r.offs, r.perm, r.row), R.order(bad, 8)):
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
+MOVES = [(1, 2, 16, "even", 768), (7, 3, 5, "dropped", 1), (40, 8, 8, "even", 100), (300, 2, 4, "one", 7),
+         (257, 4, 9, "skewed", 264), (64, 1, 64, "even", 1000), (33, 2, 3, "none", 128), (90, 5, 6, "dropped", 2050)]
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("layout", ["plain", "wide", "shifted"])
+@pytest.mark.parametrize("t,k,e,how,width", MOVES)
+def test_moves(ops, t, k, e, how, width, layout, dt):
+    """dispatch, dispatch8, combine and their gradients; rows behind the last
+    segment and rows that no slot names are NaN and must reach nothing."""
+    dtype = DT[dt]
+    pad, shift = {"plain": (0, 0), "wide": (8, 0), "shifted": (3, 1)}[layout]
+    idx = choices(t, t, k, e, how)
+    r = ops.Route(t, k, e).order(torch.from_numpy(idx).cuda())
+    offs, perm, row = R.order(idx, e)
+    n = perm.size
+    x, dout = (strided(rnd(i, t, width, dtype=dtype), pad, shift) for i in (1, 2))
+    w = rnd(3, t, k)
+    y = rnd(4, n, width, dtype=dtype)
+    y[torch.from_numpy(perm < 0).cuda()] = float("nan")
+    y = strided(y, pad, shift)
+    ww = R.as64(w).copy()
+    live = perm >= 0
+
+    out = strided(torch.full((n, width), 7.0, dtype=dtype, device="cuda"), pad, shift)
+    xs = R.as64(r.dispatch(x, out=out))
+    want = np.zeros((n, width))
+    want[live] = R.as64(x)[perm[live] // k]
+    want[offs[-1]:] = 7.0
+    assert np.array_equal(xs, want)
+
+    t8 = ops.empty8(n, width)
+    t8.codes.fill_(0x55)
+    t8.scales.fill_(0x33)
+    r.dispatch8(x, out=t8)
+    codes, scales = R.quant(want[:offs[-1]])
+    assert np.array_equal(t8.codes.cpu().numpy()[:offs[-1], :width], codes)
+    assert np.array_equal(t8.scales.cpu().numpy()[:offs[-1]], scales)
+    assert (t8.codes[offs[-1]:] == 0x55).all() and (t8.scales[offs[-1]:] == 0x33).all()
+
+    yy = np.where(live[:, None], R.as64(y), 0.0)
+    for weights in (w, None):
+        got = r.combine(y, weights)
+        wk = ww if weights is not None else np.ones_like(ww)
+        term = np.where((row >= 0)[:, :, None], yy[np.maximum(row, 0)] * wk[:, :, None], 0.0)
+        ref = term.sum(1)
+        close(got, ref, (k + 1) * U32 * np.abs(term).sum(1) + HALF_STEP[dtype] * np.abs(ref) * (1 + 1e-3), "combine")
+
+    dy = strided(torch.full((n, width), 7.0, dtype=dtype, device="cuda"), pad, shift)
+    dy, dw = r.combine_bwd(dout, y, w, dy=dy)
+    dd = R.as64(dout)
+    ref = np.zeros((n, width))
+    ref[live] = dd[perm[live] // k] * ww.reshape(-1)[perm[live]][:, None]
+    ref[offs[-1]:] = 7.0
+    close(dy, ref, (U32 + HALF_STEP[dtype] * (1 + 1e-3)) * np.abs(ref), "dy")
+    prod = np.where((row >= 0)[:, :, None], dd[:, None, :] * yy[np.maximum(row, 0)], 0.0)
+    close(dw, prod.sum(-1), (width + 1) * U32 * np.abs(prod).sum(-1), "dw")
+    ops.check()
+
+
+def test_move_gradients_by_differences(ops):
+    """d<combine(dispatch-like y, w), g>/dy and /dw against central differences
+    of the operator itself (fp32; the map is linear in y and in w, so the
+    difference quotient has rounding error alone: 2 eps terms / step)."""
+    t, k, e, width = 9, 2, 4, 12
+    r = ops.Route(t, k, e).order(torch.from_numpy(choices(5, t, k, e, "dropped")).cuda())
+    y, w, g = rnd(1, r.rows, width), rnd(2, t, k), rnd(3, t, width)
+    dy, dw = r.combine_bwd(g, y, w, dy=torch.zeros(r.rows, width, device="cuda"))
+    f = lambda yy, ww: float((r.combine(yy, ww).double() * g.double()).sum())  # noqa: E731
+    h = 0.5
+    scale = float((g.abs().sum() * (y.abs().max() + h) * (w.abs().max() + h)))
+    tol = 2 * 4 * U32 * scale / (2 * h)
+    for i in (int(r.row[r.row >= 0][0]), int(r.row.max())):
+        d = torch.zeros_like(y)
+        d[i, 5] = h
+        assert abs((f(y + d, w) - f(y - d, w)) / (2 * h) - float(dy[i, 5])) <= tol
+    for i in range(t):
+        d = torch.zeros_like(w)
+        d[i, 1] = h
+        assert abs((f(y, w + d) - f(y, w - d)) / (2 * h) - float(dw[i, 1])) <= tol
+    x, gs = rnd(4, t, width), rnd(5, r.rows, width)
+    dx = r.dispatch_bwd(gs)
+    d = torch.zeros_like(x)
+    d[4] = h
+    q = ((r.dispatch(x + d, out=torch.zeros_like(gs)) - r.dispatch(x - d, out=torch.zeros_like(gs))).double()
+         * gs.double()).sum() / (2 * h)
+    assert abs(float(q) - float(dx[4].double().sum())) <= tol
+
+
+# ---------------------------------------------------------------------------
+# 8 bits and back
+# ---------------------------------------------------------------------------
+def specials(rows, cols, seed=0):
+    """Values across the range of fp32, with borders, subnormals, zeros, infinities and NaN."""
+    g = np.random.default_rng(seed)
+    x = (g.normal(size=(rows, cols)) * 2.0 ** g.integers(-40, 40, (rows, 1))).astype(np.float32)
+    x[0] = 0
+    if rows > 6:
+        x[1, ::2] = 448.0
+        x[2] = np.float32(448.0) * (1 + 2.0 ** -23)
+        x[3] = 2.0 ** -140                       # subnormal: the exponent stops at -126
+        x[4, 0], x[4, -1] = np.inf, np.nan
+        x[5] = -np.inf
+        x[6] = 3.0e38 * np.sign(x[6])
+    return x
+
+
+QUANT = [(1, 1), (1, 768), (7, 100), (128, 128), (130, 264), (300, 1000), (33, 2050)]
+
+
+def codes_equal(t, want, what):
+    codes, scales = want
+    assert np.array_equal(t.scales.cpu().numpy(), scales), what
+    assert np.array_equal(t.codes.cpu().numpy()[:, :t.cols], codes), what
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,cols", QUANT)
+def test_quant_codes(ops, rows, cols, dt):
+    """Every code and scale byte, straight and transposed, over plain and
+    strided rows; and the values read back."""
+    x = torch.from_numpy(specials(rows, cols)).to(DT[dt]).cuda()
+    x64 = R.as64(x)
+    for v in (x, strided(x, 8), strided(x, 3, 1)):
+        codes_equal(ops.quant8(v), R.quant(x64), "rows")
+        codes_equal(ops.quant8(v, block_rows=128), R.quant(x64, 128), "blocks")
+        codes_equal(ops.quant8_t(v), R.quant(x64.T), "columns")
+        codes_equal(ops.quant8_t(v, block_rows=128), R.quant(x64.T, 128), "blocks transposed")
+    t = ops.quant8(x)
+    val = R.value8(t)
+    assert np.array_equal(R.as64(ops.dequant8(t, torch.float32)), val, equal_nan=True)
+    out = strided(torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda"), 3, 1)
+    assert np.array_equal(R.as64(ops.dequant8(t, out=out)), R.rounded(val, torch.bfloat16), equal_nan=True)
+    # a saved matrix transposed: quantised again from its values
+    codes_equal(ops.quant8_t(t), R.quant(np.where(np.isnan(val), np.nan, val).T), "from 8 bits")
+    codes_equal(ops.quant8_t(t, block_rows=128), R.quant(val.T, 128), "from 8 bits, blocks")
+
+
+@pytest.mark.parametrize("cols", [2, 200, 256, 514, 1024])
+def test_quant_halves(ops, cols):
+    x = torch.from_numpy(specials(20, cols, 1)).cuda()
+    t = ops.quant8(x, halves=True)
+    codes_equal(t, R.quant(R.as64(x), halves=True), cols)
+    assert np.array_equal(R.as64(ops.dequant8(t, torch.float32)), R.value8(t), equal_nan=True)
+
+
+@pytest.mark.parametrize("shape", [(3, 100, 200), (2, 128, 128), (1, 1, 5), (4, 257, 96)])
+def test_quant_stacks(ops, shape):
+    x = rnd(1, *shape)
+    x64 = R.as64(x)
+    for t, tr in ((ops.quant8(x), False), (ops.quant8(x, 128), False), (ops.quant8_t(x), True), (ops.quant8_t(x, 128), True)):
+        for i in range(shape[0]):
+            codes_equal(t[i], R.quant(x64[i].T if tr else x64[i], t.block_rows), (i, tr))
+
+
+@pytest.mark.parametrize("limit", [-5, 0, 128, 384, 1000])
+def test_row_limits(ops, limit):
+    """Only rows below the device's count are written, in every operator that takes one."""
+    rows, cols = 500, 272
+    n = torch.tensor([limit], dtype=torch.int32, device="cuda")
+    m = min(max(limit, 0), rows)
+    x = rnd(2, rows, cols)
+    a = ops.empty8(rows, cols)
+    b = ops.empty8(cols, rows)
+    c = ops.empty8(rows, cols // 2)
+    s = ops.empty8(rows, cols, halves=True)
+    for t in (a, b, c, s):
+        t.codes.fill_(0x55)
+        t.scales.fill_(0x33)
+    ops.quant8(x, out=a, n_rows=n)
+    ops.quant8_t(x, out=b, n_rows=n)
+    ops.swiglu8(x, act=c, saved=s, n_rows=n)
+    want, wt = R.quant(R.as64(x)), R.quant(R.as64(x).T)
+    assert np.array_equal(a.codes.cpu().numpy()[:m, :cols], want[0][:m]) and (a.codes[m:] == 0x55).all()
+    assert np.array_equal(a.scales.cpu().numpy()[:m], want[1][:m]) and (a.scales[m:] == 0x33).all()
+    assert np.array_equal(b.codes.cpu().numpy()[:, :m], wt[0][:, :m]) and (b.codes[:, m:] == 0x55).all()
+    mb = -(-m // 128)
+    assert np.array_equal(b.scales.cpu().numpy()[:, :mb], wt[1][:, :mb]) and (b.scales[:, mb:] == 0x33).all()
+    for t in (c, s):
+        assert (t.codes[m:] == 0x55).all() and (t.scales[m:] == 0x33).all()
+    codes, scales = R.quant(R.as64(x), halves=True)
+    assert np.array_equal(s.codes.cpu().numpy()[:m, :cols], codes[:m])
+    full = ops.quant8(x, halves=True)
+    d = torch.full((rows, cols), 7.0, device="cuda")
+    ops.dequant8(full, out=d, n_rows=n)
+    assert (d[m:] == 7).all() and np.array_equal(R.as64(d[:m]), R.value8(full)[:m])
+    d.fill_(7.0)
+    ops.swiglu8_bwd(x[:, :cols // 2], full, dgu=d, n_rows=n)
+    assert (d[m:] == 7).all() and not (d[:m] == 7).any()
+
+
+# ---------------------------------------------------------------------------
+# products
+# ---------------------------------------------------------------------------
+def product_close(got, a, b, dtype, k, extra=0.0):
+    """Sums of k exact products: at most k roundings (of up to a whole step, 2 U32) of partial sums no
+    larger than the sum of magnitudes."""
+    ref, mag = a @ b.T + extra, np.abs(a) @ np.abs(b).T + np.abs(extra)
+    close(got, ref, (k + 2) * 2 * U32 * mag + HALF_STEP[dtype] * np.abs(ref) * (1 + 1e-3))
+
+
+PRODUCTS = [(1, 1, 1), (1, 2304, 768), (2, 8, 16), (100, 72, 130), (128, 256, 128), (129, 257, 129), (300, 1000, 777),
+            (700, 640, 512), (1000, 2000, 200), (513, 64, 2300)]
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("m,n,k", PRODUCTS)
+def test_gemm_dense(ops, m, n, k, block_rows, dt):
+    a = ops.quant8(rnd(1, m, k))
+    b = ops.quant8(rnd(2, n, k, std=0.02), block_rows=block_rows)
+    av, bv = R.value8(a), R.value8(b)
+    product_close(ops.gemm8(a, b, dtype=DT[dt]), av, bv, DT[dt], k)
+    for pad, shift in ((8, 0), (3, 1)):
+        buf = torch.full((m, n + pad + shift), 7.0, dtype=DT[dt], device="cuda")
+        product_close(ops.gemm8(a, b, out=buf[:, shift:shift + n]), av, bv, DT[dt], k)
+        assert (buf[:, :shift] == 7).all() and (buf[:, shift + n:] == 7).all()
+        if dt == "fp32":
+            buf[:, shift:shift + n] = rnd(5, m, n)
+            before = R.as64(buf[:, shift:shift + n])
+            product_close(ops.gemm8(a, b, out=buf[:, shift:shift + n], accumulate=True), av, bv, DT[dt], k, before)
+            assert (buf[:, :shift] == 7).all() and (buf[:, shift + n:] == 7).all()
+    ops.check()
+
+
+SEGMENTS = [[0, 128], [0, 0, 0], [0, 128, 128, 384], [0, 0, 256, 256, 640, 640], [0, 1280]]
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("offs", SEGMENTS)
+@pytest.mark.parametrize("n,k", [(72, 130), (264, 256), (1024, 100)])
+def test_gemm_by_expert(ops, offs, n, k, block_rows, dt):
+    rows, e = 1280, len(offs) - 1
+    a = ops.quant8(rnd(1, rows, k))
+    a.codes[offs[-1]:] = 0x7F                          # behind the last segment: NaN
+    b = ops.quant8(rnd(2, e, n, k, std=0.02), block_rows=block_rows)
+    out = torch.full((rows, n), 7.0, dtype=DT[dt], device="cuda")
+    ops.gemm8(a, b, out=out, offs=torch.tensor(offs, dtype=torch.int32, device="cuda"))
+    av, bv = R.value8(a), R.value8(b)
+    for i in range(e):
+        product_close(out[offs[i]:offs[i + 1]], av[offs[i]:offs[i + 1]], bv[i], DT[dt], k)
+    assert (out[offs[-1]:] == 7).all()
+    ops.check()
+
+
+@pytest.mark.parametrize("offs", SEGMENTS + [[0, 1152, 1280]])
+@pytest.mark.parametrize("m,n", [(16, 40), (130, 257), (256, 768), (33, 1000)])
+def test_gemm_reduce(ops, offs, m, n):
+    p, e = 1280, len(offs) - 1
+    a, b = ops.quant8_t(rnd(1, p, m)), ops.quant8_t(rnd(2, p, n))
+    a.codes[:, offs[-1]:] = 0x7F
+    o = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    av, bv = R.value8(a), R.value8(b)
+    for pad, shift in ((0, 0), (3, 1)):
+        buf = torch.full((e, m, n + pad + shift), 7.0, device="cuda")
+        out = buf[:, :, shift:shift + n]
+        for acc in (False, True):
+            before = R.as64(out) if acc else np.zeros((e, m, n))
+            ops.gemm8_reduce(a, b, o, out=out, accumulate=acc)
+            for i in range(e):
+                s = slice(offs[i], offs[i + 1])
+                product_close(out[i], av[:, s], bv[:, s], torch.float32, offs[i + 1] - offs[i], before[i])
+        assert (buf[:, :, :shift] == 7).all() and (buf[:, :, shift + n:] == 7).all()
+    ops.check()
+
+
+def test_gemm_keeps_nan_and_large_scales_in_their_rows(ops):
+    x = rnd(1, 200, 300)
+    x[17, 5] = float("nan")
+    x[60] *= 2.0 ** 100
+    x[61] *= 2.0 ** -60
+    w = rnd(2, 90, 300, std=2.0 ** -30)
+    a, b = ops.quant8(x), ops.quant8(w, block_rows=128)
+    c = ops.gemm8(a, b, dtype=torch.float32)
+    assert torch.isnan(c[17]).all() and torch.isfinite(torch.cat([c[:17], c[18:]])).all()
+    keep = np.arange(200) != 17
+    product_close(c[torch.from_numpy(keep).cuda()], R.value8(a)[keep], R.value8(b), torch.float32, 300)
+
+
+def test_bad_segment_starts_stay_in_bounds(ops):
+    """Starts that no routing makes are cut to block boundaries inside the
+    operands: no access leaves a buffer, whatever they hold."""
+    a, b = ops.quant8(rnd(1, 256, 128)), ops.quant8(rnd(2, 3, 64, 128))
+    at, bt = ops.quant8_t(rnd(1, 256, 128)), ops.quant8_t(rnd(2, 256, 64))
+    for o in ([0, 100, 5000, 2 ** 31 - 1], [-128, 300, 200, 100], [2 ** 31 - 1, 0, -2 ** 31, 77]):
+        o = torch.tensor(o, dtype=torch.int32, device="cuda")
+        ops.gemm8(a, b, offs=o)
+        ops.gemm8_reduce(at, bt, o)
+    ops.check()
+
+
+# ---------------------------------------------------------------------------
+# SwiGLU
+# ---------------------------------------------------------------------------
+def gu_values(rows, width, dtype):
+    x = rnd(7, rows, 2 * width)
+    x[0] = 0
+    if rows > 4:
+        x[1, :width] = 100.0
+        x[2, :width] = -100.0
+        x[3] *= 2.0 ** -60
+        x[4, :width] = -20.0
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,width", [(1, 512), (2, 1), (5, 7), (130, 128), (200, 264), (19, 1040)])
+def test_swiglu(ops, rows, width, dt):
+    """The 8-bit results lie within half a step of the exact ones plus the
+    fp32 error of silu(g) u: (|g| + 8) 2^-22 relative (the exponential's
+    2 + 1.2 |g| ulp, the quotient's 2 and three roundings)."""
+    for pad, shift in ((0, 0), (3, 1)):
+        gu = strided(gu_values(rows, width, DT[dt]), pad, shift)
+        saved = ops.empty8(rows, 2 * width, halves=True)
+        act = ops.swiglu8(gu, saved=saved)
+        g, u = np.split(R.as64(gu), 2, axis=1)
+        codes_equal(saved, R.quant(R.as64(gu), halves=True), "saved")
+        exact = g * R.sigmoid(g) * u
+        err = (np.abs(g) + 8) * 2.0 ** -22 * np.abs(exact) + 1e-37 * (1 + np.abs(u))
+        val = R.value8(act)
+        s = 2.0 ** (np.repeat(act.scales.cpu().numpy(), 128, 1)[:, :width].astype(float) - 127)
+        step = np.maximum(2.0 ** -4 * np.abs(exact), 2.0 ** -10 * s)
+        close(val, exact, step * (1 + 2.0 ** -4) + err, "act")
+        # scales: the least that holds the block, up to that error at a border
+        for c in range(0, width, 128):
+            top, slack = np.abs(exact[:, c:c + 128]).max(1), err[:, c:c + 128].max(1)
+            sc = s[:, c]
+            assert (top - slack <= 448 * sc).all()
+            assert ((top + slack > 224 * sc) | (sc == 1) | (sc == 2.0 ** -126)).all()
+        only = ops.swiglu8(gu)
+        assert torch.equal(only.codes[:, :width], act.codes[:, :width]) and torch.equal(only.scales, act.scales)
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,width", [(1, 512), (2, 1), (5, 7), (130, 128), (200, 264), (19, 1040)])
+def test_swiglu_backward(ops, rows, width, dt):
+    dtype = DT[dt]
+    saved = ops.quant8(gu_values(rows, width, torch.float32), halves=True)
+    g, u = np.split(R.value8(saved), 2, axis=1)
+    for pad, shift in ((0, 0), (3, 1)):
+        da = strided(rnd(8, rows, width, dtype=dtype), pad, shift)
+        act = strided(torch.zeros(rows, width, dtype=dtype, device="cuda"), pad, shift)
+        dgu = strided(torch.zeros(rows, 2 * width, dtype=dtype, device="cuda"), pad, shift)
+        ops.swiglu8_bwd(da, saved, dgu=dgu, act=act)
+        d, s = R.as64(da), R.sigmoid(g)
+        rel = (np.abs(g) + 8) * 2.0 ** -22
+        tiny = 1e-37 * (1 + np.abs(d)) * (1 + np.abs(u))
+        for got, ref, mag in ((dgu[:, :width], d * u * s * (1 + g * (1 - s)), np.abs(d * u) * (s + np.abs(g) * s)),
+                              (dgu[:, width:], d * g * s, np.abs(d * g * s)), (act, g * s * u, np.abs(g * s * u))):
+            close(got, ref, rel * mag + tiny + HALF_STEP[dtype] * np.abs(ref) * (1 + 1e-2))
+
+
+def test_swiglu_backward_by_differences(ops):
+    """dgu against central differences of silu(g) u in float64 at the saved
+    values: error h^2/6 of a third derivative below 1, plus the fp32 bound."""
+    saved = ops.quant8(rnd(3, 40, 64), halves=True)
+    g, u = np.split(R.value8(saved), 2, axis=1)
+    da = rnd(4, 40, 32)
+    dgu, d, h = R.as64(ops.swiglu8_bwd(da, saved)), R.as64(da), 1e-4
+    f = lambda g, u: g * R.sigmoid(g) * u  # noqa: E731
+    num = np.concatenate([(f(g + h, u) - f(g - h, u)) / (2 * h), (f(g, u + h) - f(g, u - h)) / (2 * h)], 1)
+    dd = np.concatenate([d, d], 1)
+    size = np.abs(dd) * (1 + np.abs(np.concatenate([u, g], 1))) * (1 + np.abs(np.concatenate([g, g], 1)))
+    close(dgu, dd * num, size * (h * h + 1e-11 / h + 20 * 2.0 ** -22))
+
+
+# ---------------------------------------------------------------------------
+# streams, graphs, repetition
+# ---------------------------------------------------------------------------
+def chain(ops, r, idx, x, w8, wd8, w, bufs):
+    """Order, gather in 8 bits, product, SwiGLU, product, combine."""
+    xs8, gu, act8, saved, y, out = bufs
+    r.order(idx)
+    r.dispatch8(x, out=xs8)
+    ops.gemm8(xs8, w8, out=gu, offs=r.offs)
+    ops.swiglu8(gu, act=act8, saved=saved, n_rows=r.offs[-1:])
+    ops.gemm8(act8, wd8, out=y, offs=r.offs)
+    return r.combine(y, w, out=out)
+
+
+def chain_inputs(ops, seed, t=300, k=2, e=6, d=256, f=136):
+    r = ops.Route(t, k, e)
+    idx = torch.from_numpy(choices(seed, t, k, e, "dropped")).cuda()
+    x = rnd(seed, t, d, dtype=torch.bfloat16)
+    w8 = ops.quant8(rnd(seed + 1, e, 2 * f, d, std=0.05), 128)
+    wd8 = ops.quant8(rnd(seed + 2, e, d, f, std=0.05), 128)
+    w = torch.softmax(rnd(seed + 3, t, k), 1)
+    n = r.rows
+    bufs = (ops.empty8(n, d), torch.zeros(n, 2 * f, dtype=torch.bfloat16, device="cuda"), ops.empty8(n, f),
+            ops.empty8(n, 2 * f, halves=True), torch.zeros(n, d, dtype=torch.bfloat16, device="cuda"),
+            torch.zeros(t, d, dtype=torch.bfloat16, device="cuda"))
+    return r, idx, x, w8, wd8, w, bufs
+
+
+def test_chain_matches_definition(ops):
+    """The forward chain against float64 steps, each taking the device's own
+    8-bit operands, so that every bound stays one step's."""
+    r, idx, x, w8, wd8, w, bufs = chain_inputs(ops, 1)
+    out = chain(ops, r, idx, x, w8, wd8, w, bufs)
+    xs8, gu, act8, saved, y, _ = bufs
+    offs, perm, row = R.order(idx.cpu().numpy(), 6)
+    live = perm >= 0
+    end = offs[-1]
+    xs = np.zeros((perm.size, 256))
+    xs[live] = R.as64(x)[perm[live] // 2]
+    assert np.array_equal(xs8.codes.cpu().numpy()[:end], R.quant(xs[:end])[0])
+    xv, av, wv, wdv = R.value8(xs8), R.value8(act8), R.value8(w8), R.value8(wd8)
+    for e in range(6):
+        s = slice(offs[e], offs[e + 1])
+        product_close(gu[s], xv[s], wv[e], torch.bfloat16, 256)
+        product_close(y[s], av[s], wdv[e], torch.bfloat16, 136)
+    g, u = np.split(R.as64(gu)[:end], 2, axis=1)
+    ref = g * R.sigmoid(g) * u
+    sc = 2.0 ** (np.repeat(act8.scales.cpu().numpy()[:end], 128, 1)[:, :136].astype(float) - 127)
+    close(av[:end], ref, np.maximum(2.0 ** -4 * np.abs(ref), 2.0 ** -10 * sc) * (1 + 2.0 ** -4) + 1e-5 * np.abs(ref))
+    yy, ww = np.where(live[:, None], R.as64(y), 0.0), R.as64(w)
+    term = np.where((row >= 0)[:, :, None], yy[np.maximum(row, 0)] * ww[:, :, None], 0.0)
+    close(out, term.sum(1), 3 * U32 * np.abs(term).sum(1) + 2.0 ** -8 * 1.001 * np.abs(term.sum(1)))
+
+
+def test_chain_captured_and_replayed(ops):
+    """A captured chain gives the eager result bit for bit, also on inputs
+    written after the capture, and on a stream of its own."""
+    a = chain_inputs(ops, 1)
+    want = chain(ops, *a).clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    b = chain_inputs(ops, 1)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        chain(ops, *b)
+    for t in b[6][1:2] + b[6][4:]:
+        t.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(b[6][5], want)
+    c = chain_inputs(ops, 9)
+    want = chain(ops, *c).clone()
+    b[1].copy_(c[1])
+    b[2].copy_(c[2])
+    b[5].copy_(c[5])
+    for dst, src in ((b[3], c[3]), (b[4], c[4])):
+        dst.codes.copy_(src.codes)
+        dst.scales.copy_(src.scales)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(b[6][5], want)
+    ops.check()
+
+
+def test_two_streams_at_once(ops):
+    one, two = chain_inputs(ops, 1, t=2000), chain_inputs(ops, 2, t=1500, e=11)
+    w1, w2 = chain(ops, *one).clone(), chain(ops, *two).clone()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(s1):
+            chain(ops, *one)
+        with torch.cuda.stream(s2):
+            chain(ops, *two)
+    torch.cuda.synchronize()
+    assert torch.equal(one[6][5], w1) and torch.equal(two[6][5], w2)
+    ops.check()
+
+
+def test_wrapper_refusals(ops):
+    x = rnd(1, 10, 64)
+    r = ops.Route(10, 2, 4)
+    with pytest.raises(ValueError):
+        r.dispatch(x[:9])
+    with pytest.raises(ValueError):
+        r.dispatch(x.t().contiguous().t())
+    with pytest.raises(TypeError):
+        r.dispatch(x.half())
+    with pytest.raises(TypeError):
+        r.dispatch(x, out=torch.empty(r.rows, 64, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        r.order(torch.zeros(10, 2, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):
+        r.combine(torch.zeros(r.rows, 64, device="cuda"), torch.zeros(10, 2, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        ops.quant8(x.expand(3, 10, 64))
+    with pytest.raises(ValueError):
+        ops.quant8(x, out=ops.empty8(10, 65))
+    with pytest.raises(ValueError):
+        ops.swiglu8(x[:, :63])
+    a, b = ops.quant8(x), ops.quant8(x[:, :63].contiguous())
+    from adamw_persistent_sm_gb300.trainer import StatusError
+    with pytest.raises(StatusError):
+        ops.gemm8(a, b)
+    with pytest.raises(StatusError):
+        ops.gemm8(a, ops.quant8(x), dtype=torch.bfloat16, out=torch.zeros(10, 10, dtype=torch.bfloat16, device="cuda"),
+                  accumulate=True)
+    with pytest.raises(StatusError):
+        ops.dequant8(ops.quant8(x, block_rows=128))
+    with pytest.raises(ValueError):
+        ops.Tensor8(a.codes[:, :48], a.scales, 48)

@@ -116,6 +116,8 @@ class Tensor8:
     ``codes`` uint8 [rows, ld] or [batch, rows, ld], ld a multiple of 16 and at
     least ``cols``; ``scales`` uint8 [rows, blocks] (block_rows 1) or
     [ceil(rows / 128), blocks] (block_rows 128), with the same batch dimension.
+    Scale rows may lie further apart; a multiple of four bytes, as
+    :func:`empty8` makes them, lets products read them by words.
     ``halves``: the columns are two parts with blocks of their own.
     """
 
@@ -136,14 +138,17 @@ class Tensor8:
         need = (-(-rows // 128) if block_rows == 128 else rows, blocks)
         if tuple(scales.shape[-2:]) != need or (codes.dim() == 3 and scales.shape[0] != batch):
             raise ValueError(f"scales: expected {need} for each matrix, got {tuple(scales.shape)}")
-        if ld < cols or ld % 16 or not codes.is_contiguous() or not scales.is_contiguous() \
-                or codes.data_ptr() % 16:
+        if ld < cols or ld % 16 or not codes.is_contiguous() or codes.data_ptr() % 16:
             raise ValueError(f"codes: rows of {ld} bytes hold {cols} columns, start on 16-byte boundaries "
-                             "and are contiguous, as are the scales")
+                             "and are contiguous")
+        lds = scales.stride(-2) if need[0] > 1 else max(scales.stride(-2), blocks)
+        if lds < blocks or (blocks > 1 and scales.stride(-1) != 1) or \
+                (batch > 1 and need[0] and scales.stride(0) != need[0] * lds):
+            raise ValueError(f"scales: rows are contiguous and matrices follow one another (strides {scales.stride()})")
         self.codes, self.scales, self.cols, self.block_rows, self.halves = codes, scales, cols, block_rows, halves
         self.device = codes.device
         # an empty tensor has no storage: any address stands in for it
-        self._mat = B.mt_mat8(codes.data_ptr() or 16, scales.data_ptr() or 16, rows, cols, ld, blocks, block_rows,
+        self._mat = B.mt_mat8(codes.data_ptr() or 16, scales.data_ptr() or 16, rows, cols, ld, lds, block_rows,
                               max(batch, 1), int(halves), 0)
         self._ref = C.byref(self._mat)
 
@@ -173,9 +178,9 @@ def empty8(rows: int, cols: int, device="cuda", block_rows: int = 1, batch: int 
     lead = () if batch is None else (batch,)
     blocks = 2 * -(-(cols // 2) // 128) if halves else -(-cols // 128)
     codes = torch.empty((*lead, rows, -(-cols // 16) * 16), dtype=torch.uint8, device=dev)
-    scales = torch.empty((*lead, -(-rows // 128) if block_rows == 128 else rows, blocks), dtype=torch.uint8,
-                         device=dev)
-    return Tensor8(codes, scales, cols, block_rows, halves)
+    scales = torch.empty((*lead, -(-rows // 128) if block_rows == 128 else rows, -(-blocks // 4) * 4),
+                         dtype=torch.uint8, device=dev)
+    return Tensor8(codes, scales[..., :blocks], cols, block_rows, halves)
 
 
 def _as_matrix(x: torch.Tensor, what: str, dev) -> tuple[int, int]:

@@ -516,8 +516,8 @@ int32_t mt_dequant8(const mt_mat8* a, const int32_t* n_rows, void* out, int32_t 
  * [M, N] of dtype.  offs NULL: dense (n_seg 0, B batch 1).  Otherwise offs is
  * device int32 [n_seg+1] of multiples of 128 as mt_route_order makes them, and
  * rows offs[e]..offs[e+1]-1 of C are A's times B[e]; rows from offs[n_seg] on
- * are left as they were.  accumulate 1: C += (fp32 C only).  A product of two
- * scales below 2^-126 counts as 0, above 2^127 as 2^127. */
+ * are left as they were.  accumulate 1: C += (fp32 C only).  A scale byte of
+ * 255 is NaN (the quantisers write none). */
 int32_t mt_gemm8(const mt_mat8* a, const mt_mat8* b, const int32_t* offs, int32_t n_seg, void* c, int32_t dtype,
                  int64_t ldc, int32_t accumulate, int32_t* status, void* stream);
 /* C[e] = A[:, offs[e]..offs[e+1]) B[:, same)^T: the reduction split into

@@ -93,8 +93,8 @@ __device__ __forceinline__ uint2 ops_ld_codes(const uint8_t* p, long long c, lon
   return q;
 }
 
-// Infinite and NaN elements become NaN (which fmaxf leaves out of the block's
-// maximum and the conversion turns into the e4m3 NaN).
+// Infinite and NaN elements become NaN (which the conversion turns into the
+// e4m3 NaN).
 __device__ __forceinline__ float ops_finite(float x) {
   return fabsf(x) <= 3.402823466e38f ? x : __int_as_float(0x7fffffff);
 }
@@ -129,17 +129,111 @@ __device__ __forceinline__ void ops_values8(uint2 q, float s, float* v) {
     v[2 * i + 1] = t.y * s;
   }
 }
-__device__ __forceinline__ float ops_max8(const float* v) {
-  float a = fmaxf(0.f, fabsf(v[0]));       // 0 also where all eight are NaN
+// ---------------------------------------------------------------------------
+// Eight elements of a row as they lie in memory.  Magnitudes are compared as
+// integers - the bits of |x|, whose order is the values' and which put
+// infinities and NaN on top - so that a block's maximum also tells whether
+// every element is finite: the rare block with others is looked at again, and
+// the usual one pays nothing per element for the question.
+// ---------------------------------------------------------------------------
+#define OPS_INF 0x7f800000u
+__device__ __forceinline__ uint32_t ops_max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <class T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 u;
+  template <bool VEC>
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, long long c, long long n) {
+    if (VEC && c + 8 <= n) {
+      u = __ldg(reinterpret_cast<const uint4*>(p + c));
+      return;
+    }
+    uint32_t h[8];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) a = fmaxf(a, fabsf(v[i]));
-  return a;
+    for (int i = 0; i < 8; ++i) h[i] = c + i < n ? __ldg(reinterpret_cast<const uint16_t*>(p) + c + i) : 0;
+    u = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+  }
+  template <bool VEC>
+  __device__ __forceinline__ void store(__nv_bfloat16* p, long long c, long long n) const {
+    if (VEC && c + 8 <= n) {
+      *reinterpret_cast<uint4*>(p + c) = u;
+      return;
+    }
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < n) reinterpret_cast<uint16_t*>(p)[c + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+  }
+  // bits (fp32) of the largest magnitude
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = 0x7fff7fffu;
+    const uint32_t a = ops_max_u16x2(ops_max_u16x2(u.x & m, u.y & m), ops_max_u16x2(u.z & m, u.w & m));
+    return max(a << 16, a & 0xffff0000u);
+  }
+  __device__ __forceinline__ void values(float* v) const {
+    v[0] = ops_lo(u.x); v[1] = ops_hi(u.x); v[2] = ops_lo(u.y); v[3] = ops_hi(u.y);
+    v[4] = ops_lo(u.z); v[5] = ops_hi(u.z); v[6] = ops_lo(u.w); v[7] = ops_hi(u.w);
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  template <bool VEC>
+  __device__ __forceinline__ void load(const float* p, long long c, long long n) {
+    float v[8];
+    ops_ld8<VEC>(p, c, n, v);
+    a = make_float4(v[0], v[1], v[2], v[3]);
+    b = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  template <bool VEC>
+  __device__ __forceinline__ void store(float* p, long long c, long long n) const {
+    float v[8];
+    values(v);
+    ops_st8<VEC>(p, c, n, v);
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    float v[8];
+    values(v);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    return m;
+  }
+  __device__ __forceinline__ void values(float* v) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+__device__ __forceinline__ uint32_t ops_top8(const float* v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+  return m;
 }
 // maximum over the 16 lanes that hold one block of 128
-__device__ __forceinline__ float ops_max16(float a) {
+__device__ __forceinline__ uint32_t ops_max16(uint32_t a) {
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
   return a;
+}
+// Codes of eight elements v of a block whose largest magnitude (over 16 lanes)
+// has the bits `top`, and the block's exponent.  The whole warp calls it.
+__device__ __forceinline__ uint2 ops_quantise(float* v, uint32_t top, int* e) {
+  if (__any_sync(0xffffffffu, top >= OPS_INF)) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = ops_finite(v[i]);
+      if (v[i] == v[i]) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    }
+    top = ops_max16(m);
+  }
+  *e = ops_exponent(__uint_as_float(top));
+  return ops_codes8(v, ops_pow2(-*e));
 }
 
 // ---------------------------------------------------------------------------

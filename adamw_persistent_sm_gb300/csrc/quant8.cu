@@ -1,6 +1,8 @@
 // quant8.cu - matrices into 8 bits and back (mt_quant8, mt_quant8_t,
 // mt_dequant8) and the SwiGLU that keeps its inputs there (mt_swiglu8,
 // mt_swiglu8_bwd).
+#include <string.h>
+
 #include "ops8.cuh"
 
 namespace {
@@ -30,17 +32,25 @@ __global__ void __launch_bounds__(256) quant_rows_k(const T* x, long long ldx, c
   const bool v8 = (pcols & 7) == 0;
   for (long long ch = blockIdx.y; ch < parts * chunks; ch += gridDim.y) {
     const long long part = ch / chunks, c = (ch % chunks) * 256 + lane * 8, base = part * pcols;
-    float v[R][8];
+    Raw8<T> x8[R];
+    uint32_t top[R];
 #pragma unroll
     for (int i = 0; i < R; ++i)
-      if (r0 + i < lim) ops_ld8<VEC>(x + (r0 + i) * ldx + base, c, pcols, v[i]);
+      if (r0 + i < lim) x8[i].template load<VEC>(x + (r0 + i) * ldx + base, c, pcols);
+#pragma unroll
+    for (int i = 0; i < R; ++i) top[i] = r0 + i < lim ? x8[i].top() : 0;
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1)
+#pragma unroll
+      for (int i = 0; i < R; ++i) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], d));
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (r0 + i >= lim) break;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = ops_finite(v[i][j]);
-      const int e = ops_exponent(ops_max16(ops_max8(v[i])));
-      ops_st_codes(o.q + (r0 + i) * o.ld + base, c, pcols, ops_codes8(v[i], ops_pow2(-e)), v8 || parts == 1);
+      float v[8];
+      int e;
+      x8[i].values(v);
+      const uint2 q = ops_quantise(v, top[i], &e);
+      ops_st_codes(o.q + (r0 + i) * o.ld + base, c, pcols, q, v8 || parts == 1);
       if ((lane & 15) == 0 && c < pcols) o.s[(r0 + i) * o.lds + part * pblocks + (c >> 7)] = (uint8_t)(e + 127);
     }
   }
@@ -82,43 +92,83 @@ __global__ void __launch_bounds__(256) dequant_k(Mat8 a, const int* n_rows, int 
 // ---------------------------------------------------------------------------
 enum { T_BLOCK = 0, T_BLOCK_T = 1, T_COLS_T = 2 };
 
-// Eight consecutive elements of source row r: a plain matrix, or the values of
-// an 8-bit one.
+// Eight elements of a row of an 8-bit matrix, kept as codes and scale.
 struct Src8 {
   const uint8_t* q;
   const uint8_t* s;
   long long ld, lds;
 };
-template <bool VEC>
-__device__ __forceinline__ void src_ld8(const float* x, long long ldx, const Src8&, long long r, long long c,
-                                        long long n, float* v) {
-  ops_ld8<VEC>(x + r * ldx, c, n, v);
-}
-template <bool VEC>
-__device__ __forceinline__ void src_ld8(const __nv_bfloat16* x, long long ldx, const Src8&, long long r, long long c,
-                                        long long n, float* v) {
-  ops_ld8<VEC>(x + r * ldx, c, n, v);
-}
-template <bool VEC>
-__device__ __forceinline__ void src_ld8(const uint8_t*, long long, const Src8& a, long long r, long long c,
-                                        long long n, float* v) {
-  if (c >= n) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    return;
+struct RawCodes {
+  uint2 q;
+  float s;
+  __device__ __forceinline__ void values(float* v) const { ops_values8(q, s, v); }
+};
+template <class T>
+struct Tile8 {
+  typedef Raw8<T> Raw;
+  template <bool VEC>
+  static __device__ __forceinline__ void load(Raw& w, const T* x, long long ldx, const Src8&, long long r, long long c,
+                                              long long n) {
+    w.template load<VEC>(x + r * ldx, c, n);
   }
-  ops_values8(ops_ld_codes(a.q + r * a.ld, c, n, true), ops_pow2((int)__ldg(a.s + r * a.lds + (c >> 7)) - 127), v);
+  static __device__ __forceinline__ void zero(Raw& w) { memset(&w, 0, sizeof(w)); }
+};
+template <>
+struct Tile8<uint8_t> {
+  typedef RawCodes Raw;
+  template <bool VEC>
+  static __device__ __forceinline__ void load(Raw& w, const uint8_t*, long long, const Src8& a, long long r,
+                                              long long c, long long n) {
+    w.q = make_uint2(0, 0);
+    w.s = 1.f;
+    if (c >= n) return;
+    w.q = ops_ld_codes(a.q + r * a.ld, c, n, true);
+    w.s = ops_pow2((int)__ldg(a.s + r * a.lds + (c >> 7)) - 127);
+  }
+  static __device__ __forceinline__ void zero(Raw& w) {
+    w.q = make_uint2(0, 0);
+    w.s = 1.f;
+  }
+};
+// bits of the largest magnitude in each of the eight columns over eight rows
+__device__ __forceinline__ void tile_top(const Raw8<__nv_bfloat16>* w, uint32_t* m) {
+  uint32_t a[4] = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t u[4] = {w[i].u.x, w[i].u.y, w[i].u.z, w[i].u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[j] = ops_max_u16x2(a[j], u[j] & 0x7fff7fffu);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    m[2 * j] = a[j] << 16;
+    m[2 * j + 1] = a[j] & 0xffff0000u;
+  }
+}
+template <class RAW>
+__device__ __forceinline__ void tile_top(const RAW* w, uint32_t* m) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m[j] = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float v[8];
+    w[i].values(v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m[j] = max(m[j], __float_as_uint(v[j]) & 0x7fffffffu);
+  }
 }
 
-// One CTA per tile; a thread holds 8 rows x 8 columns.  A column's maximum
-// goes over 8 rows in registers, two lanes by shuffle and 8 warps through
-// shared memory; transposed codes go through a 16 KB tile whose 8-byte chunks
-// are swizzled by the source column group, which keeps both sides free of bank
-// conflicts.  Memory-bound: each byte is read and written once.
+// One CTA per tile; a thread holds 8 rows x 8 columns as they came from memory.
+// A column's maximum goes over 8 rows in registers, two lanes by shuffle and 8
+// warps through shared memory; transposed codes go through a 16 KB tile whose
+// 8-byte chunks are swizzled by the source column group, which keeps both sides
+// free of bank conflicts.  Memory-bound: each byte is read and written once, and
+// three CTAs per SM (85 registers) keep loads in flight while others convert.
 template <class T, bool VEC, int MODE>
-__global__ void __launch_bounds__(256) quant_tile_k(const T* x, long long ldx, Src8 src, const int* n_rows, Mat8 o,
-                                                    long long rows, long long cols) {
-  __shared__ float part[8][128];
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) quant_tile_k(const T* x, long long ldx, Src8 src,
+                                                                            const int* n_rows, Mat8 o, long long rows,
+                                                                            long long cols) {
+  __shared__ uint32_t part[8][128];
   __shared__ int ex[128];
   __shared__ __align__(16) uint2 tile[MODE == T_BLOCK ? 1 : 128 * 16];
   const int tid = threadIdx.x, warp = tid >> 5, tc = tid & 15, tr = tid >> 4;
@@ -127,43 +177,50 @@ __global__ void __launch_bounds__(256) quant_tile_k(const T* x, long long ldx, S
   for (long long rt = blockIdx.x; rt * 128 < lim; rt += gridDim.x) {
     for (long long ct = blockIdx.y; ct * 128 < cols; ct += gridDim.y) {
       const long long r0 = rt * 128 + tr * 8, c0 = ct * 128 + tc * 8;
-      float v[8][8];
+      typename Tile8<T>::Raw w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (r0 + i < lim) {
-          src_ld8<VEC>(x + b * rows * ldx, ldx, src, r0 + i, c0, cols, v[i]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-        }
+        if (r0 + i < lim) Tile8<T>::template load<VEC>(w[i], x + b * rows * ldx, ldx, src, r0 + i, c0, cols);
+        else Tile8<T>::zero(w[i]);
       }
-      float m[8];
+      uint32_t m[8];
+      tile_top(w, m);
+      bool odd = false;             // an infinity or NaN somewhere in the tile
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        m[j] = 0.f;
+      for (int j = 0; j < 8; ++j) odd |= m[j] >= OPS_INF;
+      odd = __syncthreads_or(odd);
+      if (odd) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m[j] = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          v[i][j] = ops_finite(v[i][j]);
-          m[j] = fmaxf(m[j], fabsf(v[i][j]));
+          float v[8];
+          w[i].values(v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t a = __float_as_uint(v[j]) & 0x7fffffffu;
+            if (a < OPS_INF) m[j] = max(m[j], a);
+          }
         }
-        m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m[j] = max(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
       if ((tid & 16) == 0) {
 #pragma unroll
         for (int j = 0; j < 8; j += 4)
-          *reinterpret_cast<float4*>(&part[warp][tc * 8 + j]) = make_float4(m[j], m[j + 1], m[j + 2], m[j + 3]);
+          *reinterpret_cast<uint4*>(&part[warp][tc * 8 + j]) = make_uint4(m[j], m[j + 1], m[j + 2], m[j + 3]);
       }
       __syncthreads();
       if (tid < 128) {
-        float a = part[0][tid];
+        uint32_t a = part[0][tid];
 #pragma unroll
-        for (int w = 1; w < 8; ++w) a = fmaxf(a, part[w][tid]);
+        for (int k = 1; k < 8; ++k) a = max(a, part[k][tid]);
         if (MODE != T_COLS_T) {
 #pragma unroll
-          for (int s = 16; s > 0; s >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
+          for (int s = 16; s > 0; s >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, s));
           if ((tid & 31) == 0) part[0][tid] = a;      // read by this thread's own warp alone so far
         } else {
-          const int e = ops_exponent(a);
+          const int e = ops_exponent(__uint_as_float(a));
           ex[tid] = e;
           if (ct * 128 + tid < cols) o.s[(b * cols + ct * 128 + tid) * o.lds + rt] = (uint8_t)(e + 127);
         }
@@ -171,7 +228,7 @@ __global__ void __launch_bounds__(256) quant_tile_k(const T* x, long long ldx, S
       __syncthreads();
       int e0 = 0;
       if (MODE != T_COLS_T) {
-        e0 = ops_exponent(fmaxf(fmaxf(part[0][0], part[0][32]), fmaxf(part[0][64], part[0][96])));
+        e0 = ops_exponent(__uint_as_float(max(max(part[0][0], part[0][32]), max(part[0][64], part[0][96]))));
         if (tid == 0) {
           if (MODE == T_BLOCK) o.s[(b * ((rows + 127) / 128) + rt) * o.lds + ct] = (uint8_t)(e0 + 127);
           else o.s[(b * ((cols + 127) / 128) + ct) * o.lds + rt] = (uint8_t)(e0 + 127);
@@ -180,17 +237,38 @@ __global__ void __launch_bounds__(256) quant_tile_k(const T* x, long long ldx, S
       if (MODE == T_BLOCK) {
         const float s = ops_pow2(-e0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (r0 + i < rows) ops_st_codes(o.q + (b * rows + r0 + i) * o.ld, c0, cols, ops_codes8(v[i], s), true);
-      } else {
+        for (int i = 0; i < 8; ++i) {
+          float v[8];
+          w[i].values(v);
+          if (odd) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float s = ops_pow2(-(MODE == T_COLS_T ? ex[tc * 8 + j] : e0));
-          float t[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) t[i] = v[i][j];
-          tile[(tc * 8 + j) * 16 + (tr ^ tc)] = ops_codes8(t, s);
+            for (int j = 0; j < 8; ++j) v[j] = ops_finite(v[j]);
+          }
+          if (r0 + i < rows) ops_st_codes(o.q + (b * rows + r0 + i) * o.ld, c0, cols, ops_codes8(v, s), true);
         }
+      } else {
+        uint2 out[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          float v[4][8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            w[i + k].values(v[k]);
+            if (odd) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[k][j] = ops_finite(v[k][j]);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float t[4] = {v[0][j], v[1][j], v[2][j], v[3][j]};
+            const uint32_t q = ops_codes4(t, ops_pow2(-(MODE == T_COLS_T ? ex[tc * 8 + j] : e0)));
+            if (i == 0) out[j].x = q;
+            else out[j].y = q;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) tile[(tc * 8 + j) * 16 + (tr ^ tc)] = out[j];
         __syncthreads();
         const long long left = lim - rt * 128;     // codes of an output row in this tile
 #pragma unroll
@@ -216,7 +294,14 @@ __global__ void __launch_bounds__(256) quant_tile_k(const T* x, long long ldx, S
 // ---------------------------------------------------------------------------
 // SwiGLU
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float sigmoid_f(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+// 1 / (1 + 2^(-g log2 e)) on the two approximate instructions (2 and 1 ulp): the
+// product's rounding adds |g| 2^-24, far inside the 8-bit results' steps.
+__device__ __forceinline__ float sigmoid_f(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
 
 // Half a warp holds one block of g and the same block of u: act and, where
 // asked for, g and u leave as codes in the same pass.  R rows per warp, loads first.
@@ -228,33 +313,32 @@ __global__ void __launch_bounds__(256) swiglu_k(const T* gu, long long ldgu, con
   if (r0 >= lim) return;
   const bool v8 = (F & 7) == 0;
   for (long long c = lane * 8 + 256LL * blockIdx.y; c - lane * 8 < F; c += 256LL * gridDim.y) {
-    float g[R][8], u[R][8];
+    Raw8<T> g8[R], u8[R];
 #pragma unroll
     for (int i = 0; i < R; ++i)
       if (r0 + i < lim) {
-        ops_ld8<VEC>(gu + (r0 + i) * ldgu, c, F, g[i]);
-        ops_ld8<VEC>(gu + (r0 + i) * ldgu + F, c, F, u[i]);
+        g8[i].template load<VEC>(gu + (r0 + i) * ldgu, c, F);
+        u8[i].template load<VEC>(gu + (r0 + i) * ldgu + F, c, F);
       }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const long long r = r0 + i;
       if (r >= lim) break;
-      float a[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) a[j] = ops_finite(g[i][j] * sigmoid_f(g[i][j]) * u[i][j]);
-      const int e = ops_exponent(ops_max16(ops_max8(a)));
-      ops_st_codes(act.q + r * act.ld, c, F, ops_codes8(a, ops_pow2(-e)), true);
       const bool first = (lane & 15) == 0 && c < F;
+      float g[8], u[8], a[8];
+      g8[i].values(g);
+      u8[i].values(u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] = g[j] * sigmoid_f(g[j]) * u[j];
+      int e;
+      const uint2 q = ops_quantise(a, ops_max16(ops_top8(a)), &e);
+      ops_st_codes(act.q + r * act.ld, c, F, q, true);
       if (first) act.s[r * act.lds + (c >> 7)] = (uint8_t)(e + 127);
       if (SAVE) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          g[i][j] = ops_finite(g[i][j]);
-          u[i][j] = ops_finite(u[i][j]);
-        }
-        const int eg = ops_exponent(ops_max16(ops_max8(g[i]))), eu = ops_exponent(ops_max16(ops_max8(u[i])));
-        ops_st_codes(sv.q + r * sv.ld, c, F, ops_codes8(g[i], ops_pow2(-eg)), true);
-        ops_st_codes(sv.q + r * sv.ld + F, c, F, ops_codes8(u[i], ops_pow2(-eu)), v8);
+        int eg, eu;
+        const uint2 qg = ops_quantise(g, ops_max16(g8[i].top()), &eg), qu = ops_quantise(u, ops_max16(u8[i].top()), &eu);
+        ops_st_codes(sv.q + r * sv.ld, c, F, qg, true);
+        ops_st_codes(sv.q + r * sv.ld + F, c, F, qu, v8);
         if (first) {
           sv.s[r * sv.lds + (c >> 7)] = (uint8_t)(eg + 127);
           sv.s[r * sv.lds + nb + (c >> 7)] = (uint8_t)(eu + 127);

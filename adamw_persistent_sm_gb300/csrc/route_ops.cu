@@ -205,11 +205,11 @@ __global__ void __launch_bounds__(256) dispatch_k(const T* x, long long ldx, lon
   if (t >= tokens) return;
   const int mine = lane < K ? __ldg(row + t * K + lane) : -1;
   for (long long c = lane * 8 + 256LL * blockIdx.y; c - lane * 8 < width; c += 256LL * gridDim.y) {
-    float v[8];
-    ops_ld8<VEC>(x + t * ldx, c, width, v);
+    Raw8<T> v;
+    v.template load<VEC>(x + t * ldx, c, width);
     for (int k = 0; k < K; ++k) {
       const long long r = __shfl_sync(0xffffffffu, mine, k);
-      if (r >= 0 && r < rows) ops_st8<VEC>(out + r * ldo, c, width, v);
+      if (r >= 0 && r < rows) v.template store<VEC>(out + r * ldo, c, width);
     }
   }
 }
@@ -235,12 +235,12 @@ __global__ void __launch_bounds__(256) dispatch8_k(const T* x, long long ldx, lo
   if (t >= tokens) return;
   const int mine = lane < K ? __ldg(row + t * K + lane) : -1;
   for (long long c = lane * 8 + 256LL * blockIdx.y; c - lane * 8 < width; c += 256LL * gridDim.y) {
+    Raw8<T> x8;
     float v[8];
-    ops_ld8<VEC>(x + t * ldx, c, width, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = ops_finite(v[i]);
-    const int e = ops_exponent(ops_max16(ops_max8(v)));
-    const uint2 codes = ops_codes8(v, ops_pow2(-e));
+    int e;
+    x8.template load<VEC>(x + t * ldx, c, width);
+    x8.values(v);
+    const uint2 codes = ops_quantise(v, ops_max16(x8.top()), &e);
     for (int k = 0; k < K; ++k) {
       const long long r = __shfl_sync(0xffffffffu, mine, k);
       if (r < 0 || r >= rows) continue;
@@ -250,9 +250,11 @@ __global__ void __launch_bounds__(256) dispatch8_k(const T* x, long long ldx, lo
   }
 }
 
-// A warp sums one token's chunk of 256 columns over its slots in order, in
-// fp32.  KM bounds K so that every slot's load is in flight before the first sum.
-template <class T, bool VEC, int KM>
+// A warp sums one token's row over its slots in order, in fp32.  KM bounds K, CH
+// chunks of 256 columns are taken at once: every load of all slots and chunks is
+// in flight before the first sum (8 of 16 bytes per lane and more), so that the
+// trip for the row numbers is paid once for a whole row.
+template <class T, bool VEC, int KM, int CH>
 __global__ void __launch_bounds__(256) combine_k(const T* y, long long ldy, long long rows, const int* row,
                                                  const float* w, long long tokens, int K, long long width, T* out,
                                                  long long ldo) {
@@ -262,30 +264,38 @@ __global__ void __launch_bounds__(256) combine_k(const T* y, long long ldy, long
   int mine = lane < K ? __ldg(row + t * K + lane) : -1;
   if (mine >= rows) mine = -1;
   const float wm = lane < K ? (w ? __ldg(w + t * K + lane) : 1.f) : 0.f;
-  for (long long c = lane * 8 + 256LL * blockIdx.y; c - lane * 8 < width; c += 256LL * gridDim.y) {
-    float v[KM][8], s[8] = {};
-    bool on[KM];
+  for (long long c0 = 256LL * CH * blockIdx.y; c0 < width; c0 += 256LL * CH * gridDim.y) {
+    Raw8<T> v[KM][CH];
 #pragma unroll
     for (int k = 0; k < KM; ++k) {
       const long long r = __shfl_sync(0xffffffffu, mine, k);
-      on[k] = r >= 0;
-      if (on[k]) ops_ld8<VEC>(y + r * ldy, c, width, v[k]);
+#pragma unroll
+      for (int h = 0; h < CH; ++h)
+        if (r >= 0 && c0 + 256 * h < width) v[k][h].template load<VEC>(y + r * ldy, c0 + 256 * h + lane * 8, width);
     }
 #pragma unroll
-    for (int k = 0; k < KM; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, wm, k);
-      if (on[k]) {
+    for (int h = 0; h < CH; ++h) {
+      if (c0 + 256 * h >= width) break;
+      float s[8] = {};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = fmaf(wk, v[k][i], s[i]);
+      for (int k = 0; k < KM; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, wm, k);
+        if (__shfl_sync(0xffffffffu, mine, k) >= 0) {
+          float x[8];
+          v[k][h].values(x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[i] = fmaf(wk, x[i], s[i]);
+        }
       }
+      ops_st8<VEC>(out + t * ldo, c0 + 256 * h + lane * 8, width, s);
     }
-    ops_st8<VEC>(out + t * ldo, c, width, s);
   }
 }
 
 // A warp takes one token's whole row: dout is read once for its slots, each
-// slot's y row is read for the dot product and its dy row written.
-template <class T, bool VEC, int KM>
+// slot's y row is read for the dot product and its dy row written; CH chunks at
+// once as above.
+template <class T, bool VEC, int KM, int CH>
 __global__ void __launch_bounds__(256) combine_bwd_k(const T* dout, long long lddo, const T* y, long long ldy,
                                                      const int* offs, const int* perm, const int* row, long long rows,
                                                      const float* w, long long tokens, int K, int E, long long width,
@@ -304,26 +314,37 @@ __global__ void __launch_bounds__(256) combine_bwd_k(const T* dout, long long ld
   if (mine >= rows) mine = -1;
   const float wm = lane < K ? __ldg(w + t * K + lane) : 0.f;
   float dot[KM] = {};
-  for (long long c = lane * 8; c - lane * 8 < width; c += 256) {
-    float d[8], v[KM][8];
-    ops_ld8<VEC>(dout + t * lddo, c, width, d);
+  for (long long c0 = 0; c0 < width; c0 += 256 * CH) {
+    Raw8<T> d8[CH], v8[KM][CH];
+#pragma unroll
+    for (int h = 0; h < CH; ++h)
+      if (c0 + 256 * h < width) d8[h].template load<VEC>(dout + t * lddo, c0 + 256 * h + lane * 8, width);
 #pragma unroll
     for (int k = 0; k < KM; ++k) {
       const long long r = __shfl_sync(0xffffffffu, mine, k);
-      if (r >= 0) ops_ld8<VEC>(y + r * ldy, c, width, v[k]);
+#pragma unroll
+      for (int h = 0; h < CH; ++h)
+        if (r >= 0 && c0 + 256 * h < width) v8[k][h].template load<VEC>(y + r * ldy, c0 + 256 * h + lane * 8, width);
     }
 #pragma unroll
-    for (int k = 0; k < KM; ++k) {
-      const long long r = __shfl_sync(0xffffffffu, mine, k);
-      const float wk = __shfl_sync(0xffffffffu, wm, k);
-      if (r < 0) continue;
-      float o[8];
+    for (int h = 0; h < CH; ++h) {
+      if (c0 + 256 * h >= width) break;
+      float d[8];
+      d8[h].values(d);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        o[i] = wk * d[i];
-        dot[k] = fmaf(d[i], v[k][i], dot[k]);
+      for (int k = 0; k < KM; ++k) {
+        const long long r = __shfl_sync(0xffffffffu, mine, k);
+        const float wk = __shfl_sync(0xffffffffu, wm, k);
+        if (r < 0) continue;
+        float o[8], v[8];
+        v8[k][h].values(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          o[i] = wk * d[i];
+          dot[k] = fmaf(d[i], v[i], dot[k]);
+        }
+        ops_st8<VEC>(dy + r * lddy, c0 + 256 * h + lane * 8, width, o);
       }
-      ops_st8<VEC>(dy + r * lddy, c, width, o);
     }
   }
 #pragma unroll
@@ -379,8 +400,11 @@ int dispatch8_t(const void* x, int64_t ldx, int64_t tokens, int K, int E, const 
 template <class T, bool VEC>
 int combine_t(const void* y, int64_t ldy, int64_t rows, const int* row, const float* w, int64_t tokens, int K,
               int64_t width, void* out, int64_t ldo, cudaStream_t st) {
-  const dim3 grid((unsigned)((tokens + 7) / 8), col_chunks(width));
-  auto k = K <= 2 ? combine_k<T, VEC, 2> : K <= 4 ? combine_k<T, VEC, 4> : combine_k<T, VEC, 8>;
+  // few tokens spread their columns over the grid, many take a row per warp
+  const int64_t per = K <= 2 ? (sizeof(T) == 4 ? 2 : 4) : K <= 4 ? (sizeof(T) == 4 ? 1 : 2) : 1;
+  const dim3 grid((unsigned)((tokens + 7) / 8), col_chunks((width + per - 1) / per));
+  constexpr bool F = sizeof(T) == 4;
+  auto k = K <= 2 ? combine_k<T, VEC, 2, F ? 2 : 4> : K <= 4 ? combine_k<T, VEC, 4, F ? 1 : 2> : combine_k<T, VEC, 8, 1>;
   k<<<grid, 256, 0, st>>>((const T*)y, ldy, rows, row, w, tokens, K, width, (T*)out, ldo);
   return ops_launched();
 }
@@ -389,7 +413,10 @@ int combine_bwd_t(const void* dout, int64_t lddo, const void* y, int64_t ldy, co
                   const int* row, int64_t rows, const float* w, int64_t tokens, int K, int E, int64_t width, void* dy,
                   int64_t lddy, float* dw, cudaStream_t st) {
   const long long tc = (tokens + 7) / 8;
-  auto k = K <= 2 ? combine_bwd_k<T, VEC, 2> : K <= 4 ? combine_bwd_k<T, VEC, 4> : combine_bwd_k<T, VEC, 8>;
+  constexpr bool F = sizeof(T) == 4;
+  auto k = K <= 2   ? combine_bwd_k<T, VEC, 2, F ? 2 : 3>
+           : K <= 4 ? combine_bwd_k<T, VEC, 4, F ? 1 : 2>
+                    : combine_bwd_k<T, VEC, 8, 1>;
   k<<<(unsigned)(tc + E * 16), 256, 0, st>>>((const T*)dout, lddo, (const T*)y, ldy, offs, perm, row, rows, w, tokens,
                                              K, E, width, (T*)dy, lddy, dw, tc);
   return ops_launched();

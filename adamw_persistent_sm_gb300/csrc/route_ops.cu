@@ -5,13 +5,13 @@
 namespace {
 
 constexpr int RO_E = MT_MAX_EXPERTS;
-constexpr int RO_SMALL = 8192;        // assignments that one CTA sorts alone
-constexpr int RO_CHUNK = 2048;        // assignments per CTA otherwise
+constexpr int RO_SMALL = 4096;        // assignments that one CTA sorts alone,
+constexpr int RO_CLUSTER = 1 << 18;   // that a cluster of eight sorts,
+constexpr int RO_CTAS = 8;
+constexpr int RO_CHUNK = 2048;        // and per CTA of a grid otherwise
 
 // Expert of an assignment, -1 for none; counts indices out of range.
-__device__ __forceinline__ int ro_expert(const int* idx, long long a, long long n, int E, int* status) {
-  if (a >= n) return -1;
-  const int e = __ldg(idx + a);
+__device__ __forceinline__ int ro_expert(int e, int E, int* status) {
   if (e >= 0 && e < E) return e;
   if (e != -1 && atomicCAS(status, 0, (int)MT_ERR_DEVICE_BOUNDS) == 0) status[1] = 3;
   return -1;
@@ -34,6 +34,12 @@ __device__ __forceinline__ void ro_offsets(const int* cnt, int E, int* offs) {
   }
 }
 
+// Assignments a, a + 32, a + 64, a + 96; -1 from w1 on.
+__device__ __forceinline__ void ro_load(const int* idx, long long a, long long w1, int* v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = a + 32 * j < w1 ? __ldg(idx + a + 32 * j) : -1;
+}
+
 // Lanes of the warp whose assignment names the same expert.
 __device__ __forceinline__ unsigned ro_peers(int e) { return __match_any_sync(0xffffffffu, e); }
 
@@ -48,34 +54,44 @@ struct RoSmem {
 };
 
 template <int NW>
-__device__ __forceinline__ void ro_count(RoSmem<NW>& s, const int* idx, long long w0, long long w1, long long n, int E,
-                                         int* status) {
+__device__ __forceinline__ void ro_count(RoSmem<NW>& s, const int* idx, long long w0, long long w1, int E, int* status) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e = lane; e < RO_E; e += 32) s.wh[warp][e] = 0;
   __syncwarp();
-  for (long long a = w0; a < w1; a += 32) {
-    const int e = ro_expert(idx, a + lane, n, E, status);
-    const unsigned peers = ro_peers(e);
-    if (e >= 0 && lane == __ffs(peers) - 1) s.wh[warp][e] += __popc(peers);
-    __syncwarp();
+  for (long long a0 = w0; a0 < w1; a0 += 128) {
+    int v[4];                            // four loads in flight
+    ro_load(idx, a0 + lane, w1, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = ro_expert(v[j], E, status);
+      const unsigned peers = ro_peers(e);
+      if (e >= 0 && lane == __ffs(peers) - 1) s.wh[warp][e] += __popc(peers);
+      __syncwarp();
+    }
   }
 }
 template <int NW>
-__device__ __forceinline__ void ro_place(RoSmem<NW>& s, const int* idx, long long w0, long long w1, long long n, int E,
-                                         int* status, int* perm, int* row) {
+__device__ __forceinline__ void ro_place(RoSmem<NW>& s, const int* idx, long long w0, long long w1, int E, int* status,
+                                         int* perm, int* row) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (long long a = w0; a < w1; a += 32) {
-    const int e = ro_expert(idx, a + lane, n, E, status);
-    const unsigned peers = ro_peers(e);
-    int r = -1;
-    if (e >= 0) {
-      r = s.wh[warp][e] + __popc(peers & ((1u << lane) - 1u));
-      perm[r] = (int)(a + lane);
+  for (long long a0 = w0; a0 < w1; a0 += 128) {
+    int v[4];
+    ro_load(idx, a0 + lane, w1, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const long long a = a0 + 32 * j + lane;
+      const int e = ro_expert(v[j], E, status);
+      const unsigned peers = ro_peers(e);
+      int r = -1;
+      if (e >= 0) {
+        r = s.wh[warp][e] + __popc(peers & ((1u << lane) - 1u));
+        perm[r] = (int)a;
+      }
+      if (a < w1) row[a] = r;
+      __syncwarp();
+      if (e >= 0 && lane == __ffs(peers) - 1) s.wh[warp][e] += __popc(peers);
+      __syncwarp();
     }
-    if (a + lane < n) row[a + lane] = r;
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(peers) - 1) s.wh[warp][e] += __popc(peers);
-    __syncwarp();
   }
 }
 // -1 at the rows no assignment takes, spread over `nt` threads
@@ -89,33 +105,69 @@ __device__ __forceinline__ void ro_pads(const int* cnt, const int* offs, int E, 
   for (long long r = offs[E] + t; r < rows; r += nt) perm[r] = -1;
 }
 
-// Few assignments: one CTA, one launch (latency of two global round trips).
-__global__ void __launch_bounds__(1024) ro_small(const int* idx, int n, int E, long long rows, int* offs, int* perm,
-                                                 int* row, int* status) {
+__device__ __forceinline__ void ro_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int ro_remote(const int* p, int cta) {
+  uint32_t a;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(cta));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Up to RO_SMALL assignments one CTA, up to RO_CLUSTER a cluster of eight whose
+// CTAs read one another's counts in shared memory: one launch, bound by the two
+// trips to idx (a counting and a placing launch over the whole grid took 20 us
+// for 65536 assignments).
+template <int NC>
+__global__ void __launch_bounds__(1024) ro_sort(const int* idx, int n, int E, long long rows, int* offs, int* perm,
+                                                int* row, int* status) {
   __shared__ RoSmem<32> s;
-  const int tid = threadIdx.x, warp = tid >> 5;
-  const int span = ((n + 31) / 32 + 31) & ~31;
-  const int w0 = warp * span < n ? warp * span : n, w1 = w0 + span < n ? w0 + span : n;
-  ro_count(s, idx, w0, w1, n, E, status);
+  const int tid = threadIdx.x, warp = tid >> 5, cta = blockIdx.x;
+  const int span = ((n + 32 * NC - 1) / (32 * NC) + 31) & ~31;
+  const int w0 = min((cta * 32 + warp) * span, n), w1 = min(w0 + span, n);
+  ro_count(s, idx, w0, w1, E, status);
   __syncthreads();
-  if (tid < E) {
+  if (tid < RO_E) {
     int c = 0;
+#pragma unroll 8
     for (int w = 0; w < 32; ++w) {
       const int t = s.wh[w][tid];
       s.wh[w][tid] = c;
       c += t;
     }
-    s.cnt[tid] = c;
+    s.before[tid] = c;                   // of this CTA, for the cluster
+  }
+  int base = 0;
+  if (NC > 1) {
+    ro_cluster_sync();
+    if (tid < RO_E) {
+      int all = 0;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int t = ro_remote(&s.before[tid], c);
+        if (c < cta) base += t;
+        all += t;
+      }
+      s.cnt[tid] = all;
+    }
+  } else if (tid < RO_E) {
+    s.cnt[tid] = s.before[tid];
   }
   __syncthreads();
   ro_offsets(s.cnt, E, s.offs);
   __syncthreads();
-  if (tid <= E) offs[tid] = s.offs[tid];
-  for (int i = tid; i < 32 * RO_E; i += 1024)
-    if ((i & (RO_E - 1)) < E) s.wh[i / RO_E][i & (RO_E - 1)] += s.offs[i & (RO_E - 1)];
+  if (cta == 0 && tid <= E) offs[tid] = s.offs[tid];
+  if (NC > 1) ro_cluster_sync();         // the counts have been read
+  if (tid < E) s.before[tid] = s.offs[tid] + base;
   __syncthreads();
-  ro_place(s, idx, w0, w1, n, E, status, perm, row);
-  ro_pads(s.cnt, s.offs, E, rows, perm, tid, 1024);
+  for (int i = tid; i < 32 * RO_E; i += 1024)
+    if ((i & (RO_E - 1)) < E) s.wh[i / RO_E][i & (RO_E - 1)] += s.before[i & (RO_E - 1)];
+  __syncthreads();
+  ro_place(s, idx, w0, w1, E, status, perm, row);
+  ro_pads(s.cnt, s.offs, E, rows, perm, cta * 1024 + tid, NC * 1024);
 }
 
 // Many: every CTA counts its chunk, then every CTA sums the counts before its
@@ -124,7 +176,7 @@ __global__ void __launch_bounds__(256) ro_hist(const int* idx, long long n, int 
   __shared__ RoSmem<8> s;
   const long long a0 = (long long)blockIdx.x * RO_CHUNK + (threadIdx.x >> 5) * (RO_CHUNK / 8);
   const long long a1 = a0 + RO_CHUNK / 8 < n ? a0 + RO_CHUNK / 8 : n;
-  ro_count(s, idx, a0, a1, n, E, status);
+  ro_count(s, idx, a0, a1, E, status);
   __syncthreads();
   if (threadIdx.x < RO_E) {
     int c = 0;
@@ -148,7 +200,7 @@ __global__ void __launch_bounds__(256) ro_scatter(const int* idx, long long n, i
   }
   part[0][p][e] = all;
   part[1][p][e] = mine;
-  ro_count(s, idx, a0, a1, n, E, status);
+  ro_count(s, idx, a0, a1, E, status);
   __syncthreads();
   if (tid < RO_E) {
     s.cnt[tid] = part[0][0][tid] + part[0][1][tid] + part[0][2][tid] + part[0][3][tid];
@@ -167,7 +219,7 @@ __global__ void __launch_bounds__(256) ro_scatter(const int* idx, long long n, i
   }
   if (blockIdx.x == 0 && tid <= E) offs[tid] = s.offs[tid];
   __syncthreads();
-  ro_place(s, idx, a0, a1, n, E, status, perm, row);
+  ro_place(s, idx, a0, a1, E, status, perm, row);
   ro_pads(s.cnt, s.offs, E, rows, perm, blockIdx.x * 256LL + tid, gridDim.x * 256LL);
 }
 
@@ -448,7 +500,7 @@ int64_t mt_route_ws_bytes(int64_t n_tokens, int32_t top_k, int32_t n_experts) {
   const int st = route_ok(n_tokens, top_k, n_experts);
   if (st) return -st;
   const int64_t n = n_tokens * top_k;
-  return n <= RO_SMALL ? 16 : (n + RO_CHUNK - 1) / RO_CHUNK * RO_E * 4;
+  return n <= RO_CLUSTER ? 16 : (n + RO_CHUNK - 1) / RO_CHUNK * RO_E * 4;
 }
 
 int32_t mt_route_order(const int32_t* idx, int64_t n_tokens, int32_t top_k, int32_t n_experts, int32_t* offs,
@@ -462,8 +514,26 @@ int32_t mt_route_order(const int32_t* idx, int64_t n_tokens, int32_t top_k, int3
   const int64_t n = n_tokens * top_k, rows = route_rows(n_tokens, top_k, n_experts);
   cudaStream_t s = (cudaStream_t)stream;
   if (n <= RO_SMALL) {
-    ro_small<<<1, 1024, 0, s>>>(idx, (int)n, n_experts, rows, offs, perm, row, status);
+    ro_sort<1><<<1, 1024, 0, s>>>(idx, (int)n, n_experts, rows, offs, perm, row, status);
     return ops_launched();
+  }
+  if (n <= RO_CLUSTER) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(RO_CTAS);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = RO_CTAS;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, ro_sort<RO_CTAS>, (const int*)idx, (int)n, (int)n_experts, (long long)rows, (int*)offs,
+                           (int*)perm, (int*)row, (int*)status) != cudaSuccess) {
+      cudaGetLastError();
+      return MT_ERR_LAUNCH;
+    }
+    return MT_OK;
   }
   if (!ws || !ops_aligned(ws, 16)) return MT_ERR_ARG;
   if (ws_bytes < mt_route_ws_bytes(n_tokens, top_k, n_experts)) return MT_ERR_ARENA_SMALL;

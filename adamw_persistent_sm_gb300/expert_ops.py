@@ -23,7 +23,7 @@ import torch
 from . import binding as B
 
 _DTYPES = {torch.float32: B.MT_DT_FP32, torch.bfloat16: B.MT_DT_BF16}
-_status: dict = {}          # device index -> int32 [2] status words
+_status: dict = {}          # device index -> (int32 [2] status words, their address)
 
 
 def _error(what: str, st: int) -> Exception:
@@ -31,40 +31,37 @@ def _error(what: str, st: int) -> Exception:
     return StatusError(f"{what}: {B.status_string(st)} ({st})")
 
 
-class _On:
-    """The device of a call's tensors made current, where it is not already;
-    gives the current stream there."""
-
-    __slots__ = ("dev", "prev")
-
-    def __init__(self, dev: torch.device):
-        self.dev = dev.index
-
-    def __enter__(self) -> int:
-        cur = torch.cuda.current_device()
-        self.prev = cur if cur != self.dev else None
-        if self.prev is not None:
-            torch.cuda.set_device(self.dev)
-        return torch._C._cuda_getCurrentRawStream(self.dev)
-
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            torch.cuda.set_device(self.prev)
+_current = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _status_word(dev: torch.device) -> torch.Tensor:
-    t = _status.get(dev.index)
+def _call(what: str, fn, dev: int, *args) -> None:
+    """One call of the C ABI with the device's current stream, on that device."""
+    if _current() == dev:
+        st = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _raw_stream(dev))
+    if st:
+        raise _error(what, st)
+
+
+def _status_word(dev: int) -> int:
+    """Address of the device's status words."""
+    t = _status.get(dev)
     if t is None:
-        t = _status[dev.index] = torch.zeros(2, dtype=torch.int32, device=dev)
+        t = torch.zeros(2, dtype=torch.int32, device=f"cuda:{dev}")
         torch.cuda.synchronize(dev)         # once per device: zeroed before any other stream uses it
-    return t
+        t = _status[dev] = (t, t.data_ptr())
+    return t[1]
 
 
 def check(device: str | torch.device = "cuda") -> None:
     """Wait for the device and raise if an operator reported a failure there
     since the last call (an index out of range, a wait that ran out)."""
-    dev = _device(device)
-    t = _status_word(dev)
+    dev = _device(device).index
+    _status_word(dev)
+    t = _status[dev][0]
     torch.cuda.synchronize(dev)
     st, site = t.tolist()
     if st != B.MT_OK:
@@ -79,29 +76,31 @@ def _device(device) -> torch.device:
     return dev if dev.index is not None else torch.device("cuda", torch.cuda.current_device())
 
 
-def _mat(t: torch.Tensor, what: str, dev, rows: int | None = None, cols: int | None = None, dtype=None) -> int:
-    """Checks a [rows, cols] matrix with contiguous rows; its row stride."""
-    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+def _mat(t: torch.Tensor, what: str, dev: int, rows: int | None = None, cols: int | None = None,
+         dtype=None) -> int:
+    """Checks a [rows, cols] matrix with contiguous rows on a device; its row stride."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or t.get_device() != dev or dev < 0:
+        raise ValueError(f"{what}: expected a matrix on cuda:{dev}, got {tuple(shape)} on {t.device}")
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype is not dtype):
         raise TypeError(f"{what}: {t.dtype} where {dtype or 'float32 or bfloat16'} is needed")
-    if t.dim() != 2 or t.device != dev:
-        raise ValueError(f"{what}: expected a matrix on {dev}, got {tuple(t.shape)} on {t.device}")
-    r, c = t.shape
+    r, c = shape
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError(f"{what}: expected [{rows}, {cols}], got [{r}, {c}]")
-    s0, s1 = t.stride()
-    if (c > 1 and s1 != 1) or (r > 1 and s0 < c):
+    s0, s1 = strides
+    if (s1 != 1 and c > 1) or (s0 < c and r > 1):
         raise ValueError(f"{what}: rows must be contiguous and may not overlap (strides {s0}, {s1})")
-    return s0 if r > 1 else max(s0, c)
+    return s0 if s0 >= c else c
 
 
-def _ints(t: torch.Tensor, what: str, dev, shape) -> int:
-    if t.dtype != torch.int32 or t.device != dev or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{what}: expected contiguous int32 {tuple(shape)} on {dev}, got {t.dtype} "
+def _ints(t: torch.Tensor, what: str, dev: int, shape) -> int:
+    if t.dtype is not torch.int32 or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: expected contiguous int32 {tuple(shape)} on cuda:{dev}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _limit(n_rows, dev) -> int:
+def _limit(n_rows, dev: int) -> int:
     if n_rows is None:
         return 0
     return _ints(n_rows, "n_rows", dev, (1,))
@@ -121,7 +120,8 @@ class Tensor8:
     ``halves``: the columns are two parts with blocks of their own.
     """
 
-    __slots__ = ("codes", "scales", "cols", "block_rows", "halves", "device", "_mat", "_ref")
+    __slots__ = ("codes", "scales", "rows", "cols", "batch", "shape", "block_rows", "halves", "device", "_dev",
+                 "_mat", "_ref")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int, block_rows: int = 1,
                  halves: bool = False):
@@ -146,23 +146,12 @@ class Tensor8:
                 (batch > 1 and need[0] and scales.stride(0) != need[0] * lds):
             raise ValueError(f"scales: rows are contiguous and matrices follow one another (strides {scales.stride()})")
         self.codes, self.scales, self.cols, self.block_rows, self.halves = codes, scales, cols, block_rows, halves
-        self.device = codes.device
+        self.device, self._dev = codes.device, codes.get_device()
+        self.rows, self.batch, self.shape = rows, batch, (*codes.shape[:-1], cols)
         # an empty tensor has no storage: any address stands in for it
         self._mat = B.mt_mat8(codes.data_ptr() or 16, scales.data_ptr() or 16, rows, cols, ld, lds, block_rows,
                               max(batch, 1), int(halves), 0)
         self._ref = C.byref(self._mat)
-
-    @property
-    def rows(self) -> int:
-        return self.codes.shape[-2]
-
-    @property
-    def batch(self) -> int:
-        return self.codes.shape[0] if self.codes.dim() == 3 else 1
-
-    @property
-    def shape(self) -> tuple:
-        return (*self.codes.shape[:-1], self.cols)
 
     def __getitem__(self, i: int) -> "Tensor8":
         """Matrix i of a stack (a view)."""
@@ -200,18 +189,15 @@ def quant8(x: torch.Tensor, block_rows: int = 1, out: Tensor8 | None = None, n_r
            halves: bool = False) -> Tensor8:
     """x [rows, cols] or [batch, rows, cols] in 8 bits.  ``n_rows`` (device
     int32 [1]): only rows below it are written."""
-    dev = x.device
+    dev = x.get_device()
     batch, ldx = _as_matrix(x, "x", dev)
     if out is None:
         out = empty8(x.shape[-2], x.shape[-1], dev, block_rows, batch if x.dim() == 3 else None, halves)
-    if out.shape != tuple(x.shape) or out.device != dev:
-        raise ValueError(f"out: expected {tuple(x.shape)} on {dev}, got {out.shape} on {out.device}")
+    if out.shape != tuple(x.shape) or out._dev != dev:
+        raise ValueError(f"out: expected {tuple(x.shape)} on cuda:{dev}, got {out.shape} on {out.device}")
     if batch == 0:
         return out
-    with _On(dev) as s:
-        st = B.load().mt_quant8(x.data_ptr(), _DTYPES[x.dtype], ldx, _limit(n_rows, dev), out._ref, s)
-    if st:
-        raise _error("mt_quant8", st)
+    _call("mt_quant8", B.load().mt_quant8, dev, x.data_ptr(), _DTYPES[x.dtype], ldx, _limit(n_rows, dev), out._ref)
     return out
 
 
@@ -219,7 +205,7 @@ def quant8_t(x, block_rows: int = 1, out: Tensor8 | None = None, n_rows: torch.T
     """The transpose of x [rows, cols] in 8 bits, [cols, rows]: with block_rows
     1 each scale covers 128 rows of a column of x.  x is a matrix, a stack, or
     a :class:`Tensor8` saved earlier (block_rows 1)."""
-    dev = x.device
+    dev = x._dev if isinstance(x, Tensor8) else x.get_device()
     rows, cols = x.shape[-2:]
     lead = tuple(x.shape[:-2])
     src, ptr, dt, ldx = None, 0, 0, 0
@@ -230,37 +216,32 @@ def quant8_t(x, block_rows: int = 1, out: Tensor8 | None = None, n_rows: torch.T
         ptr, dt = x.data_ptr(), _DTYPES[x.dtype]
     if out is None:
         out = empty8(cols, rows, dev, block_rows, lead[0] if lead else None)
-    if out.shape != (*lead, cols, rows) or out.device != dev:
-        raise ValueError(f"out: expected {(*lead, cols, rows)} on {dev}, got {out.shape} on {out.device}")
+    if out.shape != (*lead, cols, rows) or out._dev != dev:
+        raise ValueError(f"out: expected {(*lead, cols, rows)} on cuda:{dev}, got {out.shape} on {out.device}")
     if lead and lead[0] == 0:
         return out
-    with _On(dev) as s:
-        st = B.load().mt_quant8_t(ptr, dt, ldx, src, _limit(n_rows, dev), out._ref, s)
-    if st:
-        raise _error("mt_quant8_t", st)
+    _call("mt_quant8_t", B.load().mt_quant8_t, dev, ptr, dt, ldx, src, _limit(n_rows, dev), out._ref)
     return out
 
 
 def dequant8(a: Tensor8, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
              n_rows: torch.Tensor | None = None) -> torch.Tensor:
     """The values of an 8-bit matrix (block_rows 1)."""
-    dev = a.device
+    dev = a._dev
     if out is None:
         out = torch.empty(a.shape, dtype=dtype, device=dev)
     ldo = _mat(out, "out", dev, a.rows, a.cols)
-    with _On(dev) as s:
-        st = B.load().mt_dequant8(a._ref, _limit(n_rows, dev), out.data_ptr(), _DTYPES[out.dtype], ldo, s)
-    if st:
-        raise _error("mt_dequant8", st)
+    _call("mt_dequant8", B.load().mt_dequant8, dev, a._ref, _limit(n_rows, dev), out.data_ptr(), _DTYPES[out.dtype],
+          ldo)
     return out
 
 
 def gemm8(a: Tensor8, b: Tensor8, out: torch.Tensor | None = None, offs: torch.Tensor | None = None,
           dtype: torch.dtype = torch.bfloat16, accumulate: bool = False) -> torch.Tensor:
     """a b^T: a [M, K]; b [N, K], or with ``offs`` (int32 [E+1] row starts) [E, N, K]."""
-    dev = a.device
-    if b.device != dev:
-        raise ValueError(f"b is on {b.device}, a on {dev}")
+    dev = a._dev
+    if b._dev != dev:
+        raise ValueError(f"b is on {b.device}, a on cuda:{dev}")
     seg = b.batch if offs is not None else 0
     if out is None:
         if accumulate:
@@ -268,21 +249,18 @@ def gemm8(a: Tensor8, b: Tensor8, out: torch.Tensor | None = None, offs: torch.T
         out = torch.empty((a.rows, b.rows), dtype=dtype, device=dev)
     ldc = _mat(out, "out", dev, a.rows, b.rows)
     po = 0 if offs is None else _ints(offs, "offs", dev, (seg + 1,))
-    with _On(dev) as s:
-        st = B.load().mt_gemm8(a._ref, b._ref, po, seg, out.data_ptr(), _DTYPES[out.dtype], ldc, int(accumulate),
-                               _status_word(dev).data_ptr(), s)
-    if st:
-        raise _error("mt_gemm8", st)
+    _call("mt_gemm8", B.load().mt_gemm8, dev, a._ref, b._ref, po, seg, out.data_ptr(), _DTYPES[out.dtype], ldc,
+          int(accumulate), _status_word(dev))
     return out
 
 
 def gemm8_reduce(a: Tensor8, b: Tensor8, offs: torch.Tensor, out: torch.Tensor | None = None,
                  accumulate: bool = False) -> torch.Tensor:
     """out[e] = a[:, offs[e]:offs[e+1]] b[:, same]^T in fp32: a [M, P], b [N, P]."""
-    dev = a.device
+    dev = a._dev
     seg = offs.numel() - 1
-    if b.device != dev:
-        raise ValueError(f"b is on {b.device}, a on {dev}")
+    if b._dev != dev:
+        raise ValueError(f"b is on {b.device}, a on cuda:{dev}")
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
@@ -290,11 +268,8 @@ def gemm8_reduce(a: Tensor8, b: Tensor8, offs: torch.Tensor, out: torch.Tensor |
     if out.dim() != 3 or out.dtype != torch.float32 or tuple(out.shape) != (seg, a.rows, b.rows):
         raise ValueError(f"out: expected float32 {(seg, a.rows, b.rows)}, got {out.dtype} {tuple(out.shape)}")
     _, ldc = _as_matrix(out, "out", dev)
-    with _On(dev) as s:
-        st = B.load().mt_gemm8_reduce(a._ref, b._ref, _ints(offs, "offs", dev, (seg + 1,)), seg, out.data_ptr(), ldc,
-                                      int(accumulate), _status_word(dev).data_ptr(), s)
-    if st:
-        raise _error("mt_gemm8_reduce", st)
+    _call("mt_gemm8_reduce", B.load().mt_gemm8_reduce, dev, a._ref, b._ref, _ints(offs, "offs", dev, (seg + 1,)),
+          seg, out.data_ptr(), ldc, int(accumulate), _status_word(dev))
     return out
 
 
@@ -302,20 +277,17 @@ def swiglu8(gu: torch.Tensor, act: Tensor8 | None = None, saved: Tensor8 | None 
             n_rows: torch.Tensor | None = None) -> Tensor8:
     """silu(g) * u of gu = [g | u], in 8 bits; ``saved`` (empty8 with halves)
     receives g and u for :func:`swiglu8_bwd`."""
-    dev = gu.device
+    dev = gu.get_device()
     ld = _mat(gu, "gu", dev)
     rows, cols = gu.shape
     if cols % 2 or cols < 2:
         raise ValueError(f"gu: an even number of columns, got {cols}")
     if act is None:
         act = empty8(rows, cols // 2, dev)
-    if act.shape != (rows, cols // 2) or act.device != dev or (saved is not None and saved.device != dev):
-        raise ValueError(f"act: expected {(rows, cols // 2)} on {dev}, got {act.shape} on {act.device}")
-    with _On(dev) as s:
-        st = B.load().mt_swiglu8(gu.data_ptr(), _DTYPES[gu.dtype], ld, _limit(n_rows, dev), act._ref,
-                                 saved._ref if saved is not None else None, s)
-    if st:
-        raise _error("mt_swiglu8", st)
+    if act.shape != (rows, cols // 2) or act._dev != dev or (saved is not None and saved._dev != dev):
+        raise ValueError(f"act: expected {(rows, cols // 2)} on cuda:{dev}, got {act.shape} on {act.device}")
+    _call("mt_swiglu8", B.load().mt_swiglu8, dev, gu.data_ptr(), _DTYPES[gu.dtype], ld, _limit(n_rows, dev),
+          act._ref, saved._ref if saved is not None else None)
     return act
 
 
@@ -323,19 +295,16 @@ def swiglu8_bwd(dact: torch.Tensor, saved: Tensor8, dgu: torch.Tensor | None = N
                 act: torch.Tensor | None = None, n_rows: torch.Tensor | None = None) -> torch.Tensor:
     """Gradient of :func:`swiglu8` at the saved g and u; ``act``, where given,
     receives silu(g) * u of the saved values."""
-    dev = dact.device
+    dev = dact.get_device()
     ldd = _mat(dact, "dact", dev, saved.rows, saved.cols // 2)
-    if saved.device != dev:
-        raise ValueError(f"saved is on {saved.device}, dact on {dev}")
+    if saved._dev != dev:
+        raise ValueError(f"saved is on {saved.device}, dact on cuda:{dev}")
     if dgu is None:
         dgu = torch.empty(saved.shape, dtype=dact.dtype, device=dev)
     ldg = _mat(dgu, "dgu", dev, saved.rows, saved.cols, dact.dtype)
     lda = 0 if act is None else _mat(act, "act", dev, *dact.shape, dact.dtype)
-    with _On(dev) as s:
-        st = B.load().mt_swiglu8_bwd(dact.data_ptr(), _DTYPES[dact.dtype], ldd, saved._ref, _limit(n_rows, dev),
-                                     dgu.data_ptr(), ldg, 0 if act is None else act.data_ptr(), lda, s)
-    if st:
-        raise _error("mt_swiglu8_bwd", st)
+    _call("mt_swiglu8_bwd", B.load().mt_swiglu8_bwd, dev, dact.data_ptr(), _DTYPES[dact.dtype], ldd, saved._ref,
+          _limit(n_rows, dev), dgu.data_ptr(), ldg, 0 if act is None else act.data_ptr(), lda)
     return dgu
 
 
@@ -367,7 +336,7 @@ class Route:
         return r
 
     def _set(self, offs, perm, row):
-        self.device = offs.device
+        self.device, self._dev = offs.device, offs.get_device()
         if row.dim() != 2 or offs.dim() != 1 or perm.dim() != 1 or self.device.type != "cuda":
             raise ValueError("offs [E+1], perm [rows] and row [tokens, top_k] on a CUDA device")
         self.n_tokens, self.top_k = row.shape
@@ -378,72 +347,62 @@ class Route:
         if rows != self.rows:
             raise ValueError(f"perm: expected {rows} rows, got {self.rows}")
         self.offs, self.perm, self.row = offs, perm, row
-        self._ptrs = (_ints(offs, "offs", self.device, offs.shape), _ints(perm, "perm", self.device, perm.shape),
-                      _ints(row, "row", self.device, row.shape))
+        dev = self._dev
+        self._ptrs = (_ints(offs, "offs", dev, offs.shape), _ints(perm, "perm", dev, perm.shape),
+                      _ints(row, "row", dev, row.shape))
 
     def order(self, idx: torch.Tensor) -> "Route":
         """Sort idx int32 [n_tokens, top_k] (-1: no expert)."""
-        dev = self.device
+        dev = self._dev
         if self.ws is None:
             self.ws = torch.empty(B.load().mt_route_ws_bytes(self.n_tokens, self.top_k, self.n_experts),
                                   dtype=torch.uint8, device=dev)
         p = _ints(idx, "idx", dev, self.row.shape)
-        with _On(dev) as s:
-            st = B.load().mt_route_order(p, self.n_tokens, self.top_k, self.n_experts, *self._ptrs,
-                                         self.ws.data_ptr(), self.ws.numel(), _status_word(dev).data_ptr(), s)
-        if st:
-            raise _error("mt_route_order", st)
+        _call("mt_route_order", B.load().mt_route_order, dev, p, self.n_tokens, self.top_k, self.n_experts,
+              *self._ptrs, self.ws.data_ptr(), self.ws.numel(), _status_word(dev))
         return self
 
     def dispatch(self, x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
         """x [n_tokens, width] to the rows of its experts, [rows, width]; zeros
         in padding rows; rows behind the last segment are left as they were."""
-        dev = self.device
+        dev = self._dev
         ldx = _mat(x, "x", dev, self.n_tokens)
         if out is None:
             out = torch.empty((self.rows, x.shape[1]), dtype=x.dtype, device=dev)
         ldo = _mat(out, "out", dev, self.rows, x.shape[1], x.dtype)
-        with _On(dev) as s:
-            st = B.load().mt_dispatch(x.data_ptr(), _DTYPES[x.dtype], ldx, self.n_tokens, x.shape[1], self.top_k,
-                                      self.n_experts, *self._ptrs, self.rows, out.data_ptr(), ldo, s)
-        if st:
-            raise _error("mt_dispatch", st)
+        _call("mt_dispatch", B.load().mt_dispatch, dev, x.data_ptr(), _DTYPES[x.dtype], ldx, self.n_tokens,
+              x.shape[1], self.top_k, self.n_experts, *self._ptrs, self.rows, out.data_ptr(), ldo)
         return out
 
     def dispatch8(self, x: torch.Tensor, out: Tensor8 | None = None) -> Tensor8:
         """:meth:`dispatch` with the rows quantised on their way."""
-        dev = self.device
+        dev = self._dev
         ldx = _mat(x, "x", dev, self.n_tokens)
         if out is None:
             out = empty8(self.rows, x.shape[1], dev)
-        if out.shape != (self.rows, x.shape[1]) or out.device != dev:
-            raise ValueError(f"out: expected {(self.rows, x.shape[1])} on {dev}, got {out.shape} on {out.device}")
-        with _On(dev) as s:
-            st = B.load().mt_dispatch8(x.data_ptr(), _DTYPES[x.dtype], ldx, self.n_tokens, self.top_k, self.n_experts,
-                                       *self._ptrs, out._ref, s)
-        if st:
-            raise _error("mt_dispatch8", st)
+        if out.shape != (self.rows, x.shape[1]) or out._dev != dev:
+            raise ValueError(f"out: expected {(self.rows, x.shape[1])} on cuda:{dev}, got {out.shape} on {out.device}")
+        _call("mt_dispatch8", B.load().mt_dispatch8, dev, x.data_ptr(), _DTYPES[x.dtype], ldx, self.n_tokens,
+              self.top_k, self.n_experts, *self._ptrs, out._ref)
         return out
 
     def _weights(self, w: torch.Tensor, what: str) -> int:
-        if w.dtype != torch.float32 or w.device != self.device or w.shape != self.row.shape or not w.is_contiguous():
+        if w.dtype is not torch.float32 or w.get_device() != self._dev or w.shape != self.row.shape \
+                or not w.is_contiguous():
             raise ValueError(f"{what}: expected contiguous float32 {tuple(self.row.shape)} on {self.device}")
         return w.data_ptr()
 
     def combine(self, y: torch.Tensor, w: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
         """Rows y [rows, width] back to tokens, weighted by w float32
         [n_tokens, top_k] (None: plain sums)."""
-        dev = self.device
+        dev = self._dev
         ldy = _mat(y, "y", dev, self.rows)
         if out is None:
             out = torch.empty((self.n_tokens, y.shape[1]), dtype=y.dtype, device=dev)
         ldo = _mat(out, "out", dev, self.n_tokens, y.shape[1], y.dtype)
         pw = 0 if w is None else self._weights(w, "w")
-        with _On(dev) as s:
-            st = B.load().mt_combine(y.data_ptr(), _DTYPES[y.dtype], ldy, self.rows, self._ptrs[2], pw, self.n_tokens,
-                                     self.top_k, y.shape[1], out.data_ptr(), ldo, s)
-        if st:
-            raise _error("mt_combine", st)
+        _call("mt_combine", B.load().mt_combine, dev, y.data_ptr(), _DTYPES[y.dtype], ldy, self.rows, self._ptrs[2],
+              pw, self.n_tokens, self.top_k, y.shape[1], out.data_ptr(), ldo)
         return out
 
     def dispatch_bwd(self, dxs: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
@@ -454,7 +413,7 @@ class Route:
                     dw: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
         """Gradients of :meth:`combine` for y (zeros in padding rows, rows
         behind the last segment left as they were) and for w."""
-        dev = self.device
+        dev = self._dev
         width = dout.shape[-1]
         ldd = _mat(dout, "dout", dev, self.n_tokens)
         ldy = _mat(y, "y", dev, self.rows, width, dout.dtype)
@@ -463,10 +422,7 @@ class Route:
         if dw is None:
             dw = torch.empty(self.row.shape, dtype=torch.float32, device=dev)
         ldg = _mat(dy, "dy", dev, self.rows, width, dout.dtype)
-        with _On(dev) as s:
-            st = B.load().mt_combine_bwd(dout.data_ptr(), _DTYPES[dout.dtype], ldd, y.data_ptr(), ldy, *self._ptrs,
-                                         self.rows, self._weights(w, "w"), self.n_tokens, self.top_k, self.n_experts,
-                                         width, dy.data_ptr(), ldg, self._weights(dw, "dw"), s)
-        if st:
-            raise _error("mt_combine_bwd", st)
+        _call("mt_combine_bwd", B.load().mt_combine_bwd, dev, dout.data_ptr(), _DTYPES[dout.dtype], ldd,
+              y.data_ptr(), ldy, *self._ptrs, self.rows, self._weights(w, "w"), self.n_tokens, self.top_k,
+              self.n_experts, width, dy.data_ptr(), ldg, self._weights(dw, "dw"))
         return dy, dw

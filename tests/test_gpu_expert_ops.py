@@ -64,7 +64,7 @@ def choices(seed, t, k, e, how):
 ROUTES = [(0, 2, 4, "even"), (1, 1, 1, "even"), (1, 2, 16, "even"), (1, 2, 16, "none"), (5, 8, 8, "even"),
           (127, 1, 3, "one"), (128, 2, 2, "even"), (129, 4, 5, "dropped"), (1000, 3, 7, "skewed"),
           (1024, 8, 64, "even"), (1025, 8, 64, "dropped"), (8193, 1, 33, "one"), (4097, 2, 16, "dropped"),
-          (5000, 2, 16, "none"), (20000, 8, 64, "skewed"), (32768, 2, 16, "even")]
+          (5000, 2, 16, "none"), (20000, 8, 64, "skewed"), (32768, 2, 16, "even"), (40001, 8, 64, "dropped")]
 
 
 @pytest.mark.parametrize("t,k,e,how", ROUTES)
@@ -81,7 +81,7 @@ def test_route_order(ops, t, k, e, how):
     ops.check()
 
 
-@pytest.mark.parametrize("t", [10, 9000])
+@pytest.mark.parametrize("t", [10, 9000, 140000])
 def test_route_order_reports_bad_indices(ops, t):
     idx = choices(1, t, 2, 8, "even")
     bad = idx.copy()

@@ -14,17 +14,19 @@
 // device
 // ---------------------------------------------------------------------------
 // n_rows of the C ABI: rows below *p (clamped), or all of them
-__device__ __forceinline__ long long ops_row_limit(const int* p, long long rows) {
+__device__ __forceinline__ int ops_row_limit(const int* p, int rows) {
   if (!p) return rows;
-  const long long v = *p;
+  const int v = *p;
   return v < 0 ? 0 : v < rows ? v : rows;
 }
 
-// Elements c..c+7 of a row, zeros from column n on.  VEC: row start and c are
-// 16-byte aligned.
-template <bool VEC>
-__device__ __forceinline__ void ops_ld8(const float* p, long long c, long long n, float* v) {
-  if (VEC && c + 8 <= n) {
+// Elements c..c+7 of a row, zeros from column n on.  VEC 0: any alignment; 1: row
+// start and c are 16-byte aligned; 2: and every lane's eight lie inside the row,
+// which the launch knows from the sizes (no test per access, and the loads of a
+// loop stay together).
+template <int VEC>
+__device__ __forceinline__ void ops_ld8(const float* p, int c, int n, float* v) {
+  if (VEC == 2 || (VEC && c + 8 <= n)) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(p + c)), b = __ldg(reinterpret_cast<const float4*>(p + c + 4));
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     return;
@@ -34,9 +36,9 @@ __device__ __forceinline__ void ops_ld8(const float* p, long long c, long long n
 }
 __device__ __forceinline__ float ops_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float ops_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
-template <bool VEC>
-__device__ __forceinline__ void ops_ld8(const __nv_bfloat16* p, long long c, long long n, float* v) {
-  if (VEC && c + 8 <= n) {
+template <int VEC>
+__device__ __forceinline__ void ops_ld8(const __nv_bfloat16* p, int c, int n, float* v) {
+  if (VEC == 2 || (VEC && c + 8 <= n)) {
     const uint4 u = __ldg(reinterpret_cast<const uint4*>(p + c));
     v[0] = ops_lo(u.x); v[1] = ops_hi(u.x); v[2] = ops_lo(u.y); v[3] = ops_hi(u.y);
     v[4] = ops_lo(u.z); v[5] = ops_hi(u.z); v[6] = ops_lo(u.w); v[7] = ops_hi(u.w);
@@ -49,9 +51,9 @@ __device__ __forceinline__ uint32_t ops_bf2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-template <bool VEC>
-__device__ __forceinline__ void ops_st8(float* p, long long c, long long n, const float* v) {
-  if (VEC && c + 8 <= n) {
+template <int VEC>
+__device__ __forceinline__ void ops_st8(float* p, int c, int n, const float* v) {
+  if (VEC == 2 || (VEC && c + 8 <= n)) {
     *reinterpret_cast<float4*>(p + c) = make_float4(v[0], v[1], v[2], v[3]);
     *reinterpret_cast<float4*>(p + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
     return;
@@ -60,9 +62,9 @@ __device__ __forceinline__ void ops_st8(float* p, long long c, long long n, cons
   for (int i = 0; i < 8; ++i)
     if (c + i < n) p[c + i] = v[i];
 }
-template <bool VEC>
-__device__ __forceinline__ void ops_st8(__nv_bfloat16* p, long long c, long long n, const float* v) {
-  if (VEC && c + 8 <= n) {
+template <int VEC>
+__device__ __forceinline__ void ops_st8(__nv_bfloat16* p, int c, int n, const float* v) {
+  if (VEC == 2 || (VEC && c + 8 <= n)) {
     *reinterpret_cast<uint4*>(p + c) =
         make_uint4(ops_bf2(v[0], v[1]), ops_bf2(v[2], v[3]), ops_bf2(v[4], v[5]), ops_bf2(v[6], v[7]));
     return;
@@ -72,8 +74,9 @@ __device__ __forceinline__ void ops_st8(__nv_bfloat16* p, long long c, long long
     if (c + i < n) p[c + i] = __float2bfloat16_rn(v[i]);
 }
 // Eight codes; `v8`: the address is 8-byte aligned.
-__device__ __forceinline__ void ops_st_codes(uint8_t* p, long long c, long long n, uint2 q, bool v8) {
-  if (v8 && c + 8 <= n) {
+template <int VEC>
+__device__ __forceinline__ void ops_st_codes(uint8_t* p, int c, int n, uint2 q, bool v8) {
+  if (VEC == 2 || (v8 && c + 8 <= n)) {
     *reinterpret_cast<uint2*>(p + c) = q;
     return;
   }
@@ -81,8 +84,9 @@ __device__ __forceinline__ void ops_st_codes(uint8_t* p, long long c, long long 
   for (int i = 0; i < 8; ++i)
     if (c + i < n) p[c + i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
 }
-__device__ __forceinline__ uint2 ops_ld_codes(const uint8_t* p, long long c, long long n, bool v8) {
-  if (v8 && c + 8 <= n) return __ldg(reinterpret_cast<const uint2*>(p + c));
+template <int VEC>
+__device__ __forceinline__ uint2 ops_ld_codes(const uint8_t* p, int c, int n, bool v8) {
+  if (VEC == 2 || (v8 && c + 8 <= n)) return __ldg(reinterpret_cast<const uint2*>(p + c));
   uint2 q = make_uint2(0, 0);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -107,13 +111,26 @@ __device__ __forceinline__ int ops_exponent(float amax) {
   return e < -126 ? -126 : e;
 }
 __device__ __forceinline__ float ops_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-// four e4m3 codes of v * s (round to nearest even; |v * s| <= 448 or NaN)
-__device__ __forceinline__ uint32_t ops_codes4(const float* v, float s) {
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[1] * s), "f"(v[0] * s));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[3] * s), "f"(v[2] * s));
-  return (uint32_t)lo | ((uint32_t)hi << 16);
+// four e4m3 codes of v * s (round to nearest even; |v * s| <= 448 or NaN); the
+// products two at a time (one issue slot for both)
+__device__ __forceinline__ uint32_t ops_codes4(float v0, float v1, float v2, float v3, float s) {
+  uint32_t q;
+  asm("{\n\t.reg .b64 a, b, s;\n\t.reg .f32 x, y, z, w;\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b64 s, {%5, %5};\n\t"
+      "mov.b64 a, {%1, %2};\n\t"
+      "mov.b64 b, {%3, %4};\n\t"
+      "mul.rn.f32x2 a, a, s;\n\t"
+      "mul.rn.f32x2 b, b, s;\n\t"
+      "mov.b64 {x, y}, a;\n\t"
+      "mov.b64 {z, w}, b;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, y, x;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, w, z;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(q)
+      : "f"(v0), "f"(v1), "f"(v2), "f"(v3), "f"(s));
+  return q;
 }
+__device__ __forceinline__ uint32_t ops_codes4(const float* v, float s) { return ops_codes4(v[0], v[1], v[2], v[3], s); }
 __device__ __forceinline__ uint2 ops_codes8(const float* v, float s) {
   return make_uint2(ops_codes4(v, s), ops_codes4(v + 4, s));
 }
@@ -142,14 +159,20 @@ __device__ __forceinline__ uint32_t ops_max_u16x2(uint32_t a, uint32_t b) {
   asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+// largest magnitude of three, NaN if any is
+__device__ __forceinline__ float ops_max3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 template <class T>
 struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
   uint4 u;
-  template <bool VEC>
-  __device__ __forceinline__ void load(const __nv_bfloat16* p, long long c, long long n) {
-    if (VEC && c + 8 <= n) {
+  template <int VEC>
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int c, int n) {
+    if (VEC == 2 || (VEC && c + 8 <= n)) {
       u = __ldg(reinterpret_cast<const uint4*>(p + c));
       return;
     }
@@ -158,9 +181,9 @@ struct Raw8<__nv_bfloat16> {
     for (int i = 0; i < 8; ++i) h[i] = c + i < n ? __ldg(reinterpret_cast<const uint16_t*>(p) + c + i) : 0;
     u = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
   }
-  template <bool VEC>
-  __device__ __forceinline__ void store(__nv_bfloat16* p, long long c, long long n) const {
-    if (VEC && c + 8 <= n) {
+  template <int VEC>
+  __device__ __forceinline__ void store(__nv_bfloat16* p, int c, int n) const {
+    if (VEC == 2 || (VEC && c + 8 <= n)) {
       *reinterpret_cast<uint4*>(p + c) = u;
       return;
     }
@@ -183,36 +206,31 @@ struct Raw8<__nv_bfloat16> {
 template <>
 struct Raw8<float> {
   float4 a, b;
-  template <bool VEC>
-  __device__ __forceinline__ void load(const float* p, long long c, long long n) {
+  template <int VEC>
+  __device__ __forceinline__ void load(const float* p, int c, int n) {
     float v[8];
     ops_ld8<VEC>(p, c, n, v);
     a = make_float4(v[0], v[1], v[2], v[3]);
     b = make_float4(v[4], v[5], v[6], v[7]);
   }
-  template <bool VEC>
-  __device__ __forceinline__ void store(float* p, long long c, long long n) const {
+  template <int VEC>
+  __device__ __forceinline__ void store(float* p, int c, int n) const {
     float v[8];
     values(v);
     ops_st8<VEC>(p, c, n, v);
   }
   __device__ __forceinline__ uint32_t top() const {
-    float v[8];
-    values(v);
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-    return m;
+    const float m = ops_max3(ops_max3(a.x, a.y, a.z), ops_max3(a.w, b.x, b.y), b.z);
+    return __float_as_uint(ops_max3(m, b.w, b.w));
   }
   __device__ __forceinline__ void values(float* v) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
 };
+// the same of values in registers
 __device__ __forceinline__ uint32_t ops_top8(const float* v) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-  return m;
+  const float m = ops_max3(ops_max3(v[0], v[1], v[2]), ops_max3(v[3], v[4], v[5]), v[6]);
+  return __float_as_uint(ops_max3(m, v[7], v[7]));
 }
 // maximum over the 16 lanes that hold one block of 128
 __device__ __forceinline__ uint32_t ops_max16(uint32_t a) {

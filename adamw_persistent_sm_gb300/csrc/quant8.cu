@@ -10,9 +10,12 @@ namespace {
 struct Mat8 {
   uint8_t* q;
   uint8_t* s;
-  long long rows, cols, ld, lds;
+  long long ld, lds;
+  int rows, cols;
 };
-Mat8 mat8(const mt_mat8* m) { return {(uint8_t*)m->codes, (uint8_t*)m->scales, m->rows, m->cols, m->ld, m->lds}; }
+Mat8 mat8(const mt_mat8* m) {
+  return {(uint8_t*)m->codes, (uint8_t*)m->scales, m->ld, m->lds, (int)m->rows, (int)m->cols};
+}
 
 // ---------------------------------------------------------------------------
 // 1 x 128 blocks along the rows
@@ -21,24 +24,24 @@ Mat8 mat8(const mt_mat8* m) { return {(uint8_t*)m->codes, (uint8_t*)m->scales, m
 // is four shuffles, x is read once and the codes are written once.  A warp
 // takes R rows of the same 256 columns and issues all their loads first.
 // Columns come in `parts` of `pcols` with blocks of their own.
-template <class T, bool VEC, int R>
+template <class T, int VEC, int R>
 __global__ void __launch_bounds__(256) quant_rows_k(const T* x, long long ldx, const int* n_rows, Mat8 o, int parts,
-                                                    long long pcols) {
+                                                    int pcols) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long lim = ops_row_limit(n_rows, o.rows);
-  const long long r0 = ((long long)blockIdx.x * 8 + warp) * R;
+  const int lim = ops_row_limit(n_rows, o.rows);
+  const int r0 = ((int)blockIdx.x * 8 + warp) * R;
   if (r0 >= lim) return;
-  const long long chunks = (pcols + 255) / 256, pblocks = (pcols + 127) / 128;
+  const int chunks = (pcols + 255) / 256, pblocks = (pcols + 127) / 128;
   const bool v8 = (pcols & 7) == 0;
-  for (long long ch = blockIdx.y; ch < parts * chunks; ch += gridDim.y) {
-    const long long part = ch / chunks, c = (ch % chunks) * 256 + lane * 8, base = part * pcols;
+  for (int ch = blockIdx.y; ch < parts * chunks; ch += gridDim.y) {
+    const int part = ch / chunks, c = (ch - part * chunks) * 256 + lane * 8, base = part * pcols;
     Raw8<T> x8[R];
     uint32_t top[R];
+    // rows past the limit repeat the last one, and are not stored
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (r0 + i < lim) x8[i].template load<VEC>(x + (r0 + i) * ldx + base, c, pcols);
+    for (int i = 0; i < R; ++i) x8[i].template load<VEC>(x + (long long)min(r0 + i, lim - 1) * ldx + base, c, pcols);
 #pragma unroll
-    for (int i = 0; i < R; ++i) top[i] = r0 + i < lim ? x8[i].top() : 0;
+    for (int i = 0; i < R; ++i) top[i] = x8[i].top();
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1)
 #pragma unroll
@@ -50,38 +53,38 @@ __global__ void __launch_bounds__(256) quant_rows_k(const T* x, long long ldx, c
       int e;
       x8[i].values(v);
       const uint2 q = ops_quantise(v, top[i], &e);
-      ops_st_codes(o.q + (r0 + i) * o.ld + base, c, pcols, q, v8 || parts == 1);
-      if ((lane & 15) == 0 && c < pcols) o.s[(r0 + i) * o.lds + part * pblocks + (c >> 7)] = (uint8_t)(e + 127);
+      ops_st_codes<VEC>(o.q + (long long)(r0 + i) * o.ld + base, c, pcols, q, v8 || parts == 1);
+      if ((lane & 15) == 0 && c < pcols) o.s[(long long)(r0 + i) * o.lds + part * pblocks + (c >> 7)] = (uint8_t)(e + 127);
     }
   }
 }
 
-template <class T, bool VEC>
-__global__ void __launch_bounds__(256) dequant_k(Mat8 a, const int* n_rows, int parts, long long pcols, T* out,
+template <class T, int VEC>
+__global__ void __launch_bounds__(256) dequant_k(Mat8 a, const int* n_rows, int parts, int pcols, T* out,
                                                  long long ldo) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long lim = ops_row_limit(n_rows, a.rows);
-  const long long r0 = ((long long)blockIdx.x * 8 + warp) * 4;
+  const int lim = ops_row_limit(n_rows, a.rows);
+  const int r0 = ((int)blockIdx.x * 8 + warp) * 4;
   if (r0 >= lim) return;
-  const long long chunks = (pcols + 255) / 256, pblocks = (pcols + 127) / 128;
+  const int chunks = (pcols + 255) / 256, pblocks = (pcols + 127) / 128;
   const bool v8 = (pcols & 7) == 0 || parts == 1;
-  for (long long ch = blockIdx.y; ch < parts * chunks; ch += gridDim.y) {
-    const long long part = ch / chunks, c = (ch % chunks) * 256 + lane * 8, base = part * pcols;
+  for (int ch = blockIdx.y; ch < parts * chunks; ch += gridDim.y) {
+    const int part = ch / chunks, c = (ch - part * chunks) * 256 + lane * 8, base = part * pcols;
     if (c >= pcols) continue;
     uint2 q[4];
     int s[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (r0 + i < lim) {
-        q[i] = ops_ld_codes(a.q + (r0 + i) * a.ld + base, c, pcols, v8);
-        s[i] = __ldg(a.s + (r0 + i) * a.lds + part * pblocks + (c >> 7));
-      }
+    for (int i = 0; i < 4; ++i) {
+      const long long r = min(r0 + i, lim - 1);
+      q[i] = ops_ld_codes<VEC>(a.q + r * a.ld + base, c, pcols, v8);
+      s[i] = __ldg(a.s + r * a.lds + part * pblocks + (c >> 7));
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (r0 + i < lim) {
         float v[8];
         ops_values8(q[i], ops_pow2(s[i] - 127), v);
-        ops_st8<VEC>(out + (r0 + i) * ldo + base, c, pcols, v);
+        ops_st8<VEC>(out + (long long)(r0 + i) * ldo + base, c, pcols, v);
       }
   }
 }
@@ -106,9 +109,9 @@ struct RawCodes {
 template <class T>
 struct Tile8 {
   typedef Raw8<T> Raw;
-  template <bool VEC>
-  static __device__ __forceinline__ void load(Raw& w, const T* x, long long ldx, const Src8&, long long r, long long c,
-                                              long long n) {
+  template <int VEC>
+  static __device__ __forceinline__ void load(Raw& w, const T* x, long long ldx, const Src8&, long long r, int c,
+                                              int n) {
     w.template load<VEC>(x + r * ldx, c, n);
   }
   static __device__ __forceinline__ void zero(Raw& w) { memset(&w, 0, sizeof(w)); }
@@ -116,13 +119,13 @@ struct Tile8 {
 template <>
 struct Tile8<uint8_t> {
   typedef RawCodes Raw;
-  template <bool VEC>
+  template <int VEC>
   static __device__ __forceinline__ void load(Raw& w, const uint8_t*, long long, const Src8& a, long long r,
-                                              long long c, long long n) {
+                                              int c, int n) {
     w.q = make_uint2(0, 0);
     w.s = 1.f;
-    if (c >= n) return;
-    w.q = ops_ld_codes(a.q + r * a.ld, c, n, true);
+    if (VEC != 2 && c >= n) return;
+    w.q = ops_ld_codes<VEC>(a.q + r * a.ld, c, n, true);
     w.s = ops_pow2((int)__ldg(a.s + r * a.lds + (c >> 7)) - 127);
   }
   static __device__ __forceinline__ void zero(Raw& w) {
@@ -164,24 +167,29 @@ __device__ __forceinline__ void tile_top(const RAW* w, uint32_t* m) {
 // 8-byte chunks are swizzled by the source column group, which keeps both sides
 // free of bank conflicts.  Memory-bound: each byte is read and written once, and
 // three CTAs per SM (85 registers) keep loads in flight while others convert.
-template <class T, bool VEC, int MODE>
+template <class T, int VEC, int MODE>
 __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) quant_tile_k(const T* x, long long ldx, Src8 src,
-                                                                            const int* n_rows, Mat8 o, long long rows,
-                                                                            long long cols) {
+                                                                            const int* n_rows, Mat8 o, int rows, int cols) {
   __shared__ uint32_t part[8][128];
   __shared__ int ex[128];
   __shared__ __align__(16) uint2 tile[MODE == T_BLOCK ? 1 : 128 * 16];
   const int tid = threadIdx.x, warp = tid >> 5, tc = tid & 15, tr = tid >> 4;
-  const long long b = blockIdx.z;
-  const long long lim = ops_row_limit(n_rows, rows);
-  for (long long rt = blockIdx.x; rt * 128 < lim; rt += gridDim.x) {
-    for (long long ct = blockIdx.y; ct * 128 < cols; ct += gridDim.y) {
-      const long long r0 = rt * 128 + tr * 8, c0 = ct * 128 + tc * 8;
+  const int b = blockIdx.z;
+  const int lim = ops_row_limit(n_rows, rows);
+  for (int rt = blockIdx.x; rt * 128 < lim; rt += gridDim.x) {
+    for (int ct = blockIdx.y; ct * 128 < cols; ct += gridDim.y) {
+      const int r0 = rt * 128 + tr * 8, c0 = ct * 128 + tc * 8;
       typename Tile8<T>::Raw w[8];
+      const T* xb = x + (long long)b * rows * ldx;
+      if (rt * 128 + 128 <= lim) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (r0 + i < lim) Tile8<T>::template load<VEC>(w[i], x + b * rows * ldx, ldx, src, r0 + i, c0, cols);
-        else Tile8<T>::zero(w[i]);
+        for (int i = 0; i < 8; ++i) Tile8<T>::template load<VEC>(w[i], xb, ldx, src, r0 + i, c0, cols);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (r0 + i < lim) Tile8<T>::template load<VEC>(w[i], xb, ldx, src, r0 + i, c0, cols);
+          else Tile8<T>::zero(w[i]);
+        }
       }
       uint32_t m[8];
       tile_top(w, m);
@@ -222,7 +230,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) quant_tile_k(cons
         } else {
           const int e = ops_exponent(__uint_as_float(a));
           ex[tid] = e;
-          if (ct * 128 + tid < cols) o.s[(b * cols + ct * 128 + tid) * o.lds + rt] = (uint8_t)(e + 127);
+          if (ct * 128 + tid < cols) o.s[(long long)(b * cols + ct * 128 + tid) * o.lds + rt] = (uint8_t)(e + 127);
         }
       }
       __syncthreads();
@@ -230,8 +238,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) quant_tile_k(cons
       if (MODE != T_COLS_T) {
         e0 = ops_exponent(__uint_as_float(max(max(part[0][0], part[0][32]), max(part[0][64], part[0][96]))));
         if (tid == 0) {
-          if (MODE == T_BLOCK) o.s[(b * ((rows + 127) / 128) + rt) * o.lds + ct] = (uint8_t)(e0 + 127);
-          else o.s[(b * ((cols + 127) / 128) + ct) * o.lds + rt] = (uint8_t)(e0 + 127);
+          if (MODE == T_BLOCK) o.s[(long long)(b * ((rows + 127) / 128) + rt) * o.lds + ct] = (uint8_t)(e0 + 127);
+          else o.s[(long long)(b * ((cols + 127) / 128) + ct) * o.lds + rt] = (uint8_t)(e0 + 127);
         }
       }
       if (MODE == T_BLOCK) {
@@ -244,10 +252,12 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) quant_tile_k(cons
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = ops_finite(v[j]);
           }
-          if (r0 + i < rows) ops_st_codes(o.q + (b * rows + r0 + i) * o.ld, c0, cols, ops_codes8(v, s), true);
+          if (r0 + i < rows) ops_st_codes<VEC>(o.q + (long long)(b * rows + r0 + i) * o.ld, c0, cols, ops_codes8(v, s), true);
         }
       } else {
-        uint2 out[8];
+        float sc[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sc[j] = ops_pow2(-(MODE == T_COLS_T ? ex[tc * 8 + j] : e0));
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
           float v[4][8];
@@ -260,28 +270,23 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) quant_tile_k(cons
             }
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float t[4] = {v[0][j], v[1][j], v[2][j], v[3][j]};
-            const uint32_t q = ops_codes4(t, ops_pow2(-(MODE == T_COLS_T ? ex[tc * 8 + j] : e0)));
-            if (i == 0) out[j].x = q;
-            else out[j].y = q;
-          }
+          for (int j = 0; j < 8; ++j)
+            reinterpret_cast<uint32_t*>(tile)[((tc * 8 + j) * 16 + (tr ^ tc)) * 2 + i / 4] =
+                ops_codes4(v[0][j], v[1][j], v[2][j], v[3][j], sc[j]);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) tile[(tc * 8 + j) * 16 + (tr ^ tc)] = out[j];
         __syncthreads();
-        const long long left = lim - rt * 128;     // codes of an output row in this tile
+        const int left = lim - rt * 128;     // codes of an output row in this tile
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int c = (tid >> 3) + 32 * i, k = (tid & 7) * 2;
           if (ct * 128 + c < cols) {
             const uint2 a = tile[c * 16 + (k ^ (c >> 3))], d = tile[c * 16 + ((k + 1) ^ (c >> 3))];
-            uint8_t* p = o.q + (b * cols + ct * 128 + c) * o.ld + rt * 128;
+            uint8_t* p = o.q + (long long)(b * cols + ct * 128 + c) * o.ld + rt * 128;
             if (k * 8 + 16 <= left) {
               *reinterpret_cast<uint4*>(p + k * 8) = make_uint4(a.x, a.y, d.x, d.y);
             } else {
-              ops_st_codes(p, k * 8, left, a, false);
-              ops_st_codes(p, k * 8 + 8, left, d, false);
+              ops_st_codes<0>(p, k * 8, left, a, false);
+              ops_st_codes<0>(p, k * 8 + 8, left, d, false);
             }
           }
         }
@@ -305,21 +310,21 @@ __device__ __forceinline__ float sigmoid_f(float g) {
 
 // Half a warp holds one block of g and the same block of u: act and, where
 // asked for, g and u leave as codes in the same pass.  R rows per warp, loads first.
-template <class T, bool VEC, bool SAVE, int R>
+template <class T, int VEC, bool SAVE, int R>
 __global__ void __launch_bounds__(256) swiglu_k(const T* gu, long long ldgu, const int* n_rows, Mat8 act, Mat8 sv) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long F = act.cols, lim = ops_row_limit(n_rows, act.rows), nb = (F + 127) / 128;
-  const long long r0 = ((long long)blockIdx.x * 8 + warp) * R;
+  const int F = act.cols, lim = ops_row_limit(n_rows, act.rows), nb = (F + 127) / 128;
+  const int r0 = ((int)blockIdx.x * 8 + warp) * R;
   if (r0 >= lim) return;
   const bool v8 = (F & 7) == 0;
-  for (long long c = lane * 8 + 256LL * blockIdx.y; c - lane * 8 < F; c += 256LL * gridDim.y) {
+  for (int c = lane * 8 + 256 * (int)blockIdx.y; c - lane * 8 < F; c += 256 * (int)gridDim.y) {
     Raw8<T> g8[R], u8[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (r0 + i < lim) {
-        g8[i].template load<VEC>(gu + (r0 + i) * ldgu, c, F);
-        u8[i].template load<VEC>(gu + (r0 + i) * ldgu + F, c, F);
-      }
+    for (int i = 0; i < R; ++i) {
+      const T* p = gu + (long long)min(r0 + i, lim - 1) * ldgu;
+      g8[i].template load<VEC>(p, c, F);
+      u8[i].template load<VEC>(p + F, c, F);
+    }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const long long r = r0 + i;
@@ -332,13 +337,24 @@ __global__ void __launch_bounds__(256) swiglu_k(const T* gu, long long ldgu, con
       for (int j = 0; j < 8; ++j) a[j] = g[j] * sigmoid_f(g[j]) * u[j];
       int e;
       const uint2 q = ops_quantise(a, ops_max16(ops_top8(a)), &e);
-      ops_st_codes(act.q + r * act.ld, c, F, q, true);
+      ops_st_codes<VEC>(act.q + r * act.ld, c, F, q, true);
       if (first) act.s[r * act.lds + (c >> 7)] = (uint8_t)(e + 127);
       if (SAVE) {
         int eg, eu;
-        const uint2 qg = ops_quantise(g, ops_max16(g8[i].top()), &eg), qu = ops_quantise(u, ops_max16(u8[i].top()), &eu);
-        ops_st_codes(sv.q + r * sv.ld, c, F, qg, true);
-        ops_st_codes(sv.q + r * sv.ld + F, c, F, qu, v8);
+        uint32_t tg = g8[i].top(), tu = u8[i].top();
+        if (sizeof(T) == 2) {            // 16 bits each: one word goes round
+          uint32_t t = (tg >> 16) | tu;
+#pragma unroll
+          for (int d = 8; d > 0; d >>= 1) t = ops_max_u16x2(t, __shfl_xor_sync(0xffffffffu, t, d));
+          tg = t << 16;
+          tu = t & 0xffff0000u;
+        } else {
+          tg = ops_max16(tg);
+          tu = ops_max16(tu);
+        }
+        const uint2 qg = ops_quantise(g, tg, &eg), qu = ops_quantise(u, tu, &eu);
+        ops_st_codes<VEC>(sv.q + r * sv.ld, c, F, qg, true);
+        ops_st_codes<VEC>(sv.q + r * sv.ld + F, c, F, qu, v8);
         if (first) {
           sv.s[r * sv.lds + (c >> 7)] = (uint8_t)(eg + 127);
           sv.s[r * sv.lds + nb + (c >> 7)] = (uint8_t)(eu + 127);
@@ -348,28 +364,26 @@ __global__ void __launch_bounds__(256) swiglu_k(const T* gu, long long ldgu, con
   }
 }
 
-template <class T, bool VEC, int R>
+template <class T, int VEC, int R>
 __global__ void __launch_bounds__(256) swiglu_bwd_k(const T* da, long long ldda, Mat8 sv, const int* n_rows, T* dgu,
                                                     long long lddgu, T* act, long long ldact) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long F = sv.cols / 2, lim = ops_row_limit(n_rows, sv.rows), nb = (F + 127) / 128;
-  const long long r0 = ((long long)blockIdx.x * 8 + warp) * R;
+  const int F = sv.cols / 2, lim = ops_row_limit(n_rows, sv.rows), nb = (F + 127) / 128;
+  const int r0 = ((int)blockIdx.x * 8 + warp) * R;
   if (r0 >= lim) return;
   const bool v8 = (F & 7) == 0;
-  for (long long c = lane * 8 + 256LL * blockIdx.y; c < F; c += 256LL * gridDim.y) {
+  for (int c = lane * 8 + 256 * (int)blockIdx.y; c < F; c += 256 * (int)gridDim.y) {
     float d[R][8];
     uint2 qg[R], qu[R];
     int eg[R], eu[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const long long r = r0 + i;
-      if (r < lim) {
-        ops_ld8<VEC>(da + r * ldda, c, F, d[i]);
-        qg[i] = ops_ld_codes(sv.q + r * sv.ld, c, F, true);
-        qu[i] = ops_ld_codes(sv.q + r * sv.ld + F, c, F, v8);
-        eg[i] = __ldg(sv.s + r * sv.lds + (c >> 7));
-        eu[i] = __ldg(sv.s + r * sv.lds + nb + (c >> 7));
-      }
+      const long long r = min(r0 + i, lim - 1);
+      ops_ld8<VEC>(da + r * ldda, c, F, d[i]);
+      qg[i] = ops_ld_codes<VEC>(sv.q + r * sv.ld, c, F, true);
+      qu[i] = ops_ld_codes<VEC>(sv.q + r * sv.ld + F, c, F, v8);
+      eg[i] = __ldg(sv.s + r * sv.lds + (c >> 7));
+      eu[i] = __ldg(sv.s + r * sv.lds + nb + (c >> 7));
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -404,30 +418,30 @@ unsigned col_ctas(int64_t cols, int per) {
   return (unsigned)(n < 1024 ? n : 1024);
 }
 
-template <class T, bool VEC>
+template <class T, int VEC>
 void quant_rows_t(const void* x, int64_t ldx, const int* n_rows, const mt_mat8* o, cudaStream_t st) {
   const int parts = o->halves ? 2 : 1;
   const int64_t pc = o->cols / parts, chunks = (pc + 255) / 256 * parts;
   const int r = rows_per_warp(o->rows, chunks * 256);
   const dim3 grid(row_ctas(o->rows, r), col_ctas(chunks, 1));
-  if (r == 1) quant_rows_k<T, VEC, 1><<<grid, 256, 0, st>>>((const T*)x, ldx, n_rows, mat8(o), parts, pc);
-  else quant_rows_k<T, VEC, 4><<<grid, 256, 0, st>>>((const T*)x, ldx, n_rows, mat8(o), parts, pc);
+  if (r == 1) quant_rows_k<T, VEC, 1><<<grid, 256, 0, st>>>((const T*)x, ldx, n_rows, mat8(o), parts, (int)pc);
+  else quant_rows_k<T, VEC, 4><<<grid, 256, 0, st>>>((const T*)x, ldx, n_rows, mat8(o), parts, (int)pc);
 }
-template <class T, bool VEC, int MODE>
+template <class T, int VEC, int MODE>
 void quant_tile_t(const void* x, int64_t ldx, const Src8& src, const int* n_rows, const mt_mat8* o, int64_t rows,
                   int64_t cols, cudaStream_t st) {
   const int64_t rt = (rows + 127) / 128, ct = (cols + 127) / 128;
   const dim3 grid((unsigned)rt, (unsigned)(ct < 32768 ? ct : 32768), (unsigned)o->batch);
-  quant_tile_k<T, VEC, MODE><<<grid, 256, 0, st>>>((const T*)x, ldx, src, n_rows, mat8(o), rows, cols);
+  quant_tile_k<T, VEC, MODE><<<grid, 256, 0, st>>>((const T*)x, ldx, src, n_rows, mat8(o), (int)rows, (int)cols);
 }
-template <class T, bool VEC>
+template <class T, int VEC>
 void dequant_t(const mt_mat8* a, const int* n_rows, void* out, int64_t ldo, cudaStream_t st) {
   const int parts = a->halves ? 2 : 1;
   const int64_t pc = a->cols / parts, chunks = (pc + 255) / 256 * parts;
   const dim3 grid(row_ctas(a->rows, 4), col_ctas(chunks, 1));
-  dequant_k<T, VEC><<<grid, 256, 0, st>>>(mat8(a), n_rows, parts, pc, (T*)out, ldo);
+  dequant_k<T, VEC><<<grid, 256, 0, st>>>(mat8(a), n_rows, parts, (int)pc, (T*)out, ldo);
 }
-template <class T, bool VEC>
+template <class T, int VEC>
 void swiglu_t(const void* gu, int64_t ldgu, const int* n_rows, const mt_mat8* act, const mt_mat8* sv,
               cudaStream_t st) {
   const int r = rows_per_warp(act->rows, act->cols) == 1 ? 1 : 2;
@@ -437,7 +451,7 @@ void swiglu_t(const void* gu, int64_t ldgu, const int* n_rows, const mt_mat8* ac
               : (r == 1 ? swiglu_k<T, VEC, false, 1> : swiglu_k<T, VEC, false, 2>);
   k<<<grid, 256, 0, st>>>((const T*)gu, ldgu, n_rows, a, s);
 }
-template <class T, bool VEC>
+template <class T, int VEC>
 void swiglu_bwd_t(const void* da, int64_t ldda, const mt_mat8* sv, const int* n_rows, void* dgu, int64_t lddgu,
                   void* act, int64_t ldact, cudaStream_t st) {
   const int64_t F = sv->cols / 2;
@@ -446,6 +460,16 @@ void swiglu_bwd_t(const void* da, int64_t ldda, const mt_mat8* sv, const int* n_
   auto k = r == 1 ? swiglu_bwd_k<T, VEC, 1> : swiglu_bwd_k<T, VEC, 2>;
   k<<<grid, 256, 0, st>>>((const T*)da, ldda, mat8(sv), n_rows, (T*)dgu, lddgu, (T*)act, ldact);
 }
+
+// Instantiations by element type and access mode (see ops_ld8): 2 where every
+// chunk of `width` columns is whole.
+int vec_mode(bool vec, int64_t width, int chunk) { return !vec ? 0 : width % chunk ? 1 : 2; }
+#define OPS_PICK(f, dtype, vec, ...)                                                                     \
+  ((dtype) == MT_DT_FP32 ? ((vec) == 2 ? f<float, 2 __VA_ARGS__> : (vec) ? f<float, 1 __VA_ARGS__> : f<float, 0 __VA_ARGS__>) \
+                         : ((vec) == 2 ? f<__nv_bfloat16, 2 __VA_ARGS__>                                 \
+                            : (vec)    ? f<__nv_bfloat16, 1 __VA_ARGS__>                                 \
+                                       : f<__nv_bfloat16, 0 __VA_ARGS__>))
+#define OPS_COMMA ,
 
 bool limit_ok(const int32_t* n_rows) { return !n_rows || ops_aligned(n_rows, 4); }
 
@@ -463,18 +487,14 @@ int32_t mt_quant8(const void* x, int32_t dtype, int64_t ldx, const int32_t* n_ro
   if (out->block_rows == 1) {
     mt_mat8 o = *out;            // stacked matrices are one tall one
     o.rows *= o.batch;
-    const bool v = vec && (!o.halves || (o.cols / 2) * ops_size(dtype) % 16 == 0);
-    if (dtype == MT_DT_FP32) v ? quant_rows_t<float, true>(x, ldx, n_rows, &o, st) : quant_rows_t<float, false>(x, ldx, n_rows, &o, st);
-    else v ? quant_rows_t<__nv_bfloat16, true>(x, ldx, n_rows, &o, st) : quant_rows_t<__nv_bfloat16, false>(x, ldx, n_rows, &o, st);
+    const int64_t part = o.halves ? o.cols / 2 : o.cols;
+    const int v = vec_mode(vec && (!o.halves || part * ops_size(dtype) % 16 == 0), part, 256);
+    OPS_PICK(quant_rows_t, dtype, v)(x, ldx, n_rows, &o, st);
   } else {
     if (out->batch > 65535) return MT_ERR_UNSUPPORTED;
     const Src8 none{};
-    if (dtype == MT_DT_FP32)
-      vec ? quant_tile_t<float, true, T_BLOCK>(x, ldx, none, nullptr, out, out->rows, out->cols, st)
-          : quant_tile_t<float, false, T_BLOCK>(x, ldx, none, nullptr, out, out->rows, out->cols, st);
-    else
-      vec ? quant_tile_t<__nv_bfloat16, true, T_BLOCK>(x, ldx, none, nullptr, out, out->rows, out->cols, st)
-          : quant_tile_t<__nv_bfloat16, false, T_BLOCK>(x, ldx, none, nullptr, out, out->rows, out->cols, st);
+    const int v = vec_mode(vec, out->cols, 128);
+    OPS_PICK(quant_tile_t, dtype, v, OPS_COMMA T_BLOCK)(x, ldx, none, nullptr, out, out->rows, out->cols, st);
   }
   return ops_launched();
 }
@@ -493,28 +513,17 @@ int32_t mt_quant8_t(const void* x, int32_t dtype, int64_t ldx, const mt_mat8* x8
         x8->cols != cols)
       return MT_ERR_ARG;
     const Src8 src{(const uint8_t*)x8->codes, (const uint8_t*)x8->scales, x8->ld, x8->lds};
-    if (out->block_rows == 1) quant_tile_t<uint8_t, true, T_COLS_T>(nullptr, 0, src, n_rows, out, rows, cols, st);
-    else quant_tile_t<uint8_t, true, T_BLOCK_T>(nullptr, 0, src, n_rows, out, rows, cols, st);
+    auto f = out->block_rows == 1 ? (cols % 128 ? quant_tile_t<uint8_t, 1, T_COLS_T> : quant_tile_t<uint8_t, 2, T_COLS_T>)
+                                  : (cols % 128 ? quant_tile_t<uint8_t, 1, T_BLOCK_T> : quant_tile_t<uint8_t, 2, T_BLOCK_T>);
+    f(nullptr, 0, src, n_rows, out, rows, cols, st);
     return ops_launched();
   }
   if (!ops_dtype_ok(dtype) || !ops_mat_ok(x, dtype, ldx, cols)) return MT_ERR_ARG;
-  const bool vec = ops_vec(x, dtype, ldx);
+  const int v = vec_mode(ops_vec(x, dtype, ldx), cols, 128);
   const Src8 none{};
-  if (dtype == MT_DT_FP32) {
-    if (out->block_rows == 1)
-      vec ? quant_tile_t<float, true, T_COLS_T>(x, ldx, none, n_rows, out, rows, cols, st)
-          : quant_tile_t<float, false, T_COLS_T>(x, ldx, none, n_rows, out, rows, cols, st);
-    else
-      vec ? quant_tile_t<float, true, T_BLOCK_T>(x, ldx, none, n_rows, out, rows, cols, st)
-          : quant_tile_t<float, false, T_BLOCK_T>(x, ldx, none, n_rows, out, rows, cols, st);
-  } else {
-    if (out->block_rows == 1)
-      vec ? quant_tile_t<__nv_bfloat16, true, T_COLS_T>(x, ldx, none, n_rows, out, rows, cols, st)
-          : quant_tile_t<__nv_bfloat16, false, T_COLS_T>(x, ldx, none, n_rows, out, rows, cols, st);
-    else
-      vec ? quant_tile_t<__nv_bfloat16, true, T_BLOCK_T>(x, ldx, none, n_rows, out, rows, cols, st)
-          : quant_tile_t<__nv_bfloat16, false, T_BLOCK_T>(x, ldx, none, n_rows, out, rows, cols, st);
-  }
+  auto f = out->block_rows == 1 ? OPS_PICK(quant_tile_t, dtype, v, OPS_COMMA T_COLS_T)
+                                : OPS_PICK(quant_tile_t, dtype, v, OPS_COMMA T_BLOCK_T);
+  f(x, ldx, none, n_rows, out, rows, cols, st);
   return ops_launched();
 }
 
@@ -524,9 +533,9 @@ int32_t mt_dequant8(const mt_mat8* a, const int32_t* n_rows, void* out, int32_t 
   if (a->rows == 0) return MT_OK;
   if (!ops_mat_ok(out, dtype, ldo, a->cols)) return MT_ERR_ARG;
   cudaStream_t st = (cudaStream_t)stream;
-  const bool vec = ops_vec(out, dtype, ldo) && (!a->halves || (a->cols / 2) * ops_size(dtype) % 16 == 0);
-  if (dtype == MT_DT_FP32) vec ? dequant_t<float, true>(a, n_rows, out, ldo, st) : dequant_t<float, false>(a, n_rows, out, ldo, st);
-  else vec ? dequant_t<__nv_bfloat16, true>(a, n_rows, out, ldo, st) : dequant_t<__nv_bfloat16, false>(a, n_rows, out, ldo, st);
+  const int64_t part = a->halves ? a->cols / 2 : a->cols;
+  const int v = vec_mode(ops_vec(out, dtype, ldo) && (!a->halves || part * ops_size(dtype) % 16 == 0), part, 256);
+  OPS_PICK(dequant_t, dtype, v)(a, n_rows, out, ldo, st);
   return ops_launched();
 }
 
@@ -541,9 +550,8 @@ int32_t mt_swiglu8(const void* gu, int32_t dtype, int64_t ldgu, const int32_t* n
   if (act->rows == 0) return MT_OK;
   if (!ops_mat_ok(gu, dtype, ldgu, 2 * act->cols)) return MT_ERR_ARG;
   cudaStream_t st = (cudaStream_t)stream;
-  const bool vec = ops_vec(gu, dtype, ldgu) && act->cols * ops_size(dtype) % 16 == 0;
-  if (dtype == MT_DT_FP32) vec ? swiglu_t<float, true>(gu, ldgu, n_rows, act, saved, st) : swiglu_t<float, false>(gu, ldgu, n_rows, act, saved, st);
-  else vec ? swiglu_t<__nv_bfloat16, true>(gu, ldgu, n_rows, act, saved, st) : swiglu_t<__nv_bfloat16, false>(gu, ldgu, n_rows, act, saved, st);
+  const int v = vec_mode(ops_vec(gu, dtype, ldgu) && act->cols * ops_size(dtype) % 16 == 0, act->cols, 256);
+  OPS_PICK(swiglu_t, dtype, v)(gu, ldgu, n_rows, act, saved, st);
   return ops_launched();
 }
 
@@ -558,10 +566,9 @@ int32_t mt_swiglu8_bwd(const void* dact, int32_t dtype, int64_t ldda, const mt_m
       (act && !ops_mat_ok(act, dtype, ldact, F)))
     return MT_ERR_ARG;
   cudaStream_t st = (cudaStream_t)stream;
-  const bool vec = ops_vec(dact, dtype, ldda) && ops_vec(dgu, dtype, lddgu) && (!act || ops_vec(act, dtype, ldact)) &&
-                   F * ops_size(dtype) % 16 == 0;
-  if (dtype == MT_DT_FP32) vec ? swiglu_bwd_t<float, true>(dact, ldda, saved, n_rows, dgu, lddgu, act, ldact, st) : swiglu_bwd_t<float, false>(dact, ldda, saved, n_rows, dgu, lddgu, act, ldact, st);
-  else vec ? swiglu_bwd_t<__nv_bfloat16, true>(dact, ldda, saved, n_rows, dgu, lddgu, act, ldact, st) : swiglu_bwd_t<__nv_bfloat16, false>(dact, ldda, saved, n_rows, dgu, lddgu, act, ldact, st);
+  const int v = vec_mode(ops_vec(dact, dtype, ldda) && ops_vec(dgu, dtype, lddgu) && (!act || ops_vec(act, dtype, ldact)) &&
+                             F * ops_size(dtype) % 16 == 0, F, 256);
+  OPS_PICK(swiglu_bwd_t, dtype, v)(dact, ldda, saved, n_rows, dgu, lddgu, act, ldact, st);
   return ops_launched();
 }
 

@@ -240,8 +240,8 @@ __device__ __forceinline__ long long pad_row(long long i, int E, const int* offs
 // the token's rows: x is read once however many experts take it, which leaves
 // the write of the copies as the bound.  The CTAs behind the tokens' write the
 // padding rows.
-template <class T, bool VEC>
-__global__ void __launch_bounds__(256) dispatch_k(const T* x, long long ldx, long long tokens, long long width, int K,
+template <class T, int VEC>
+__global__ void __launch_bounds__(256) dispatch_k(const T* x, long long ldx, long long tokens, int width, int K,
                                                   int E, const int* offs, const int* perm, const int* row,
                                                   long long rows, T* out, long long ldo, long long tok_ctas) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -249,14 +249,14 @@ __global__ void __launch_bounds__(256) dispatch_k(const T* x, long long ldx, lon
   if (blockIdx.x >= tok_ctas) {
     const long long r = pad_row((blockIdx.x - tok_ctas) * 8 + warp, E, offs, perm, rows);
     if (r < 0) return;
-    for (long long c = lane * 8 + 256LL * blockIdx.y; c < width; c += 256LL * gridDim.y)
+    for (int c = lane * 8 + 256 * (int)blockIdx.y; c < width; c += 256 * (int)gridDim.y)
       ops_st8<VEC>(out + r * ldo, c, width, zero);
     return;
   }
   const long long t = (long long)blockIdx.x * 8 + warp;
   if (t >= tokens) return;
   const int mine = lane < K ? __ldg(row + t * K + lane) : -1;
-  for (long long c = lane * 8 + 256LL * blockIdx.y; c - lane * 8 < width; c += 256LL * gridDim.y) {
+  for (int c = lane * 8 + 256 * (int)blockIdx.y; c - lane * 8 < width; c += 256 * (int)gridDim.y) {
     Raw8<T> v;
     v.template load<VEC>(x + t * ldx, c, width);
     for (int k = 0; k < K; ++k) {
@@ -268,8 +268,8 @@ __global__ void __launch_bounds__(256) dispatch_k(const T* x, long long ldx, lon
 
 // The same with the row's blocks quantised in registers (a block of 128 lies
 // in 16 lanes), once per token.
-template <class T, bool VEC>
-__global__ void __launch_bounds__(256) dispatch8_k(const T* x, long long ldx, long long tokens, long long width, int K,
+template <class T, int VEC, int CH>
+__global__ void __launch_bounds__(256) dispatch8_k(const T* x, long long ldx, long long tokens, int width, int K,
                                                    int E, const int* offs, const int* perm, const int* row,
                                                    long long rows, uint8_t* q, long long ldq, uint8_t* sc,
                                                    long long lds, long long tok_ctas) {
@@ -277,27 +277,36 @@ __global__ void __launch_bounds__(256) dispatch8_k(const T* x, long long ldx, lo
   if (blockIdx.x >= tok_ctas) {
     const long long r = pad_row((blockIdx.x - tok_ctas) * 8 + warp, E, offs, perm, rows);
     if (r < 0) return;
-    for (long long c = lane * 8 + 256LL * blockIdx.y; c < width; c += 256LL * gridDim.y) {
-      ops_st_codes(q + r * ldq, c, width, make_uint2(0, 0), true);
+    for (int c = lane * 8 + 256 * (int)blockIdx.y; c < width; c += 256 * (int)gridDim.y) {
+      ops_st_codes<VEC>(q + r * ldq, c, width, make_uint2(0, 0), true);
       if ((lane & 15) == 0) sc[r * lds + (c >> 7)] = 127;
     }
     return;
   }
   const long long t = (long long)blockIdx.x * 8 + warp;
   if (t >= tokens) return;
-  const int mine = lane < K ? __ldg(row + t * K + lane) : -1;
-  for (long long c = lane * 8 + 256LL * blockIdx.y; c - lane * 8 < width; c += 256LL * gridDim.y) {
-    Raw8<T> x8;
-    float v[8];
-    int e;
-    x8.template load<VEC>(x + t * ldx, c, width);
-    x8.values(v);
-    const uint2 codes = ops_quantise(v, ops_max16(x8.top()), &e);
-    for (int k = 0; k < K; ++k) {
-      const long long r = __shfl_sync(0xffffffffu, mine, k);
-      if (r < 0 || r >= rows) continue;
-      ops_st_codes(q + r * ldq, c, width, codes, true);
-      if ((lane & 15) == 0 && c < width) sc[r * lds + (c >> 7)] = (uint8_t)(e + 127);
+  int mine = lane < K ? __ldg(row + t * K + lane) : -1;
+  if (mine >= rows) mine = -1;
+  for (int c0 = 256 * CH * (int)blockIdx.y; c0 < width; c0 += 256 * CH * (int)gridDim.y) {
+    Raw8<T> x8[CH];
+#pragma unroll
+    for (int h = 0; h < CH; ++h)
+      if (c0 + 256 * h < width) x8[h].template load<VEC>(x + t * ldx, c0 + 256 * h + lane * 8, width);
+#pragma unroll
+    for (int h = 0; h < CH; ++h) {
+      const int c = c0 + 256 * h + lane * 8;
+      if (c0 + 256 * h >= width) break;
+      float v[8];
+      int e;
+      x8[h].values(v);
+      const uint2 codes = ops_quantise(v, ops_max16(x8[h].top()), &e);
+      const bool first = (lane & 15) == 0 && c < width;
+      for (int k = 0; k < K; ++k) {
+        const int r = __shfl_sync(0xffffffffu, mine, k);
+        if (r < 0) continue;
+        ops_st_codes<VEC>(q + (long long)r * ldq, c, width, codes, true);
+        if (first) sc[(long long)r * lds + (c >> 7)] = (uint8_t)(e + 127);
+      }
     }
   }
 }
@@ -306,9 +315,9 @@ __global__ void __launch_bounds__(256) dispatch8_k(const T* x, long long ldx, lo
 // chunks of 256 columns are taken at once: every load of all slots and chunks is
 // in flight before the first sum (8 of 16 bytes per lane and more), so that the
 // trip for the row numbers is paid once for a whole row.
-template <class T, bool VEC, int KM, int CH>
+template <class T, int VEC, int KM, int CH>
 __global__ void __launch_bounds__(256) combine_k(const T* y, long long ldy, long long rows, const int* row,
-                                                 const float* w, long long tokens, int K, long long width, T* out,
+                                                 const float* w, long long tokens, int K, int width, T* out,
                                                  long long ldo) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long t = (long long)blockIdx.x * 8 + warp;
@@ -316,7 +325,7 @@ __global__ void __launch_bounds__(256) combine_k(const T* y, long long ldy, long
   int mine = lane < K ? __ldg(row + t * K + lane) : -1;
   if (mine >= rows) mine = -1;
   const float wm = lane < K ? (w ? __ldg(w + t * K + lane) : 1.f) : 0.f;
-  for (long long c0 = 256LL * CH * blockIdx.y; c0 < width; c0 += 256LL * CH * gridDim.y) {
+  for (int c0 = 256 * CH * (int)blockIdx.y; c0 < width; c0 += 256 * CH * (int)gridDim.y) {
     Raw8<T> v[KM][CH];
 #pragma unroll
     for (int k = 0; k < KM; ++k) {
@@ -347,17 +356,17 @@ __global__ void __launch_bounds__(256) combine_k(const T* y, long long ldy, long
 // A warp takes one token's whole row: dout is read once for its slots, each
 // slot's y row is read for the dot product and its dy row written; CH chunks at
 // once as above.
-template <class T, bool VEC, int KM, int CH>
+template <class T, int VEC, int KM, int CH>
 __global__ void __launch_bounds__(256) combine_bwd_k(const T* dout, long long lddo, const T* y, long long ldy,
                                                      const int* offs, const int* perm, const int* row, long long rows,
-                                                     const float* w, long long tokens, int K, int E, long long width,
+                                                     const float* w, long long tokens, int K, int E, int width,
                                                      T* dy, long long lddy, float* dw, long long tok_ctas) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float zero[8] = {};
   if (blockIdx.x >= tok_ctas) {
     const long long r = pad_row((blockIdx.x - tok_ctas) * 8 + warp, E, offs, perm, rows);
     if (r < 0) return;
-    for (long long c = lane * 8; c < width; c += 256) ops_st8<VEC>(dy + r * lddy, c, width, zero);
+    for (int c = lane * 8; c < width; c += 256) ops_st8<VEC>(dy + r * lddy, c, width, zero);
     return;
   }
   const long long t = (long long)blockIdx.x * 8 + warp;
@@ -366,7 +375,7 @@ __global__ void __launch_bounds__(256) combine_bwd_k(const T* dout, long long ld
   if (mine >= rows) mine = -1;
   const float wm = lane < K ? __ldg(w + t * K + lane) : 0.f;
   float dot[KM] = {};
-  for (long long c0 = 0; c0 < width; c0 += 256 * CH) {
+  for (int c0 = 0; c0 < width; c0 += 256 * CH) {
     Raw8<T> d8[CH], v8[KM][CH];
 #pragma unroll
     for (int h = 0; h < CH; ++h)
@@ -423,44 +432,43 @@ unsigned col_chunks(int64_t width) {
   return (unsigned)(n < 1024 ? n : 1024);
 }
 
+// How the lanes access rows of `width` (see ops_ld8).
+int vec_mode(bool vec, int64_t width) { return !vec ? 0 : width % 256 ? 1 : 2; }
+
 template <class T>
 int dispatch_t(const void* x, int64_t ldx, int64_t tokens, int64_t width, int K, int E, const int* offs,
-               const int* perm, const int* row, int64_t rows, void* out, int64_t ldo, bool vec, cudaStream_t st) {
+               const int* perm, const int* row, int64_t rows, void* out, int64_t ldo, int vec, cudaStream_t st) {
   const long long tc = (tokens + 7) / 8;
   const dim3 grid((unsigned)(tc + E * 16), col_chunks(width));
-  if (vec)
-    dispatch_k<T, true><<<grid, 256, 0, st>>>((const T*)x, ldx, tokens, width, K, E, offs, perm, row, rows, (T*)out,
-                                              ldo, tc);
-  else
-    dispatch_k<T, false><<<grid, 256, 0, st>>>((const T*)x, ldx, tokens, width, K, E, offs, perm, row, rows, (T*)out,
-                                               ldo, tc);
+  auto k = vec == 2 ? dispatch_k<T, 2> : vec ? dispatch_k<T, 1> : dispatch_k<T, 0>;
+  k<<<grid, 256, 0, st>>>((const T*)x, ldx, tokens, (int)width, K, E, offs, perm, row, rows, (T*)out, ldo, tc);
   return ops_launched();
 }
-template <class T>
+template <class T, int VEC>
 int dispatch8_t(const void* x, int64_t ldx, int64_t tokens, int K, int E, const int* offs, const int* perm,
-                const int* row, const mt_mat8* o, bool vec, cudaStream_t st) {
+                const int* row, const mt_mat8* o, cudaStream_t st) {
   const long long tc = (tokens + 7) / 8;
-  const dim3 grid((unsigned)(tc + E * 16), col_chunks(o->cols));
-  if (vec)
-    dispatch8_k<T, true><<<grid, 256, 0, st>>>((const T*)x, ldx, tokens, o->cols, K, E, offs, perm, row, o->rows,
-                                               (uint8_t*)o->codes, o->ld, (uint8_t*)o->scales, o->lds, tc);
-  else
-    dispatch8_k<T, false><<<grid, 256, 0, st>>>((const T*)x, ldx, tokens, o->cols, K, E, offs, perm, row, o->rows,
-                                                (uint8_t*)o->codes, o->ld, (uint8_t*)o->scales, o->lds, tc);
+  // few tokens spread their columns over the grid, many take a row per warp
+  constexpr int CH = sizeof(T) == 4 ? 2 : 4;
+  const bool wide = tokens * ((o->cols + 255) / 256) > 152 * 16;
+  const dim3 grid((unsigned)(tc + E * 16), col_chunks(wide ? (o->cols + CH - 1) / CH : o->cols));
+  auto k = wide ? dispatch8_k<T, VEC, CH> : dispatch8_k<T, VEC, 1>;
+  k<<<grid, 256, 0, st>>>((const T*)x, ldx, tokens, (int)o->cols, K, E, offs, perm, row, o->rows, (uint8_t*)o->codes,
+                          o->ld, (uint8_t*)o->scales, o->lds, tc);
   return ops_launched();
 }
-template <class T, bool VEC>
+template <class T, int VEC>
 int combine_t(const void* y, int64_t ldy, int64_t rows, const int* row, const float* w, int64_t tokens, int K,
               int64_t width, void* out, int64_t ldo, cudaStream_t st) {
   // few tokens spread their columns over the grid, many take a row per warp
-  const int64_t per = K <= 2 ? (sizeof(T) == 4 ? 2 : 4) : K <= 4 ? (sizeof(T) == 4 ? 1 : 2) : 1;
-  const dim3 grid((unsigned)((tokens + 7) / 8), col_chunks((width + per - 1) / per));
   constexpr bool F = sizeof(T) == 4;
+  const int64_t per = K <= 2 ? (F ? 2 : 4) : K <= 4 ? (F ? 1 : 2) : 1;
+  const dim3 grid((unsigned)((tokens + 7) / 8), col_chunks((width + per - 1) / per));
   auto k = K <= 2 ? combine_k<T, VEC, 2, F ? 2 : 4> : K <= 4 ? combine_k<T, VEC, 4, F ? 1 : 2> : combine_k<T, VEC, 8, 1>;
-  k<<<grid, 256, 0, st>>>((const T*)y, ldy, rows, row, w, tokens, K, width, (T*)out, ldo);
+  k<<<grid, 256, 0, st>>>((const T*)y, ldy, rows, row, w, tokens, K, (int)width, (T*)out, ldo);
   return ops_launched();
 }
-template <class T, bool VEC>
+template <class T, int VEC>
 int combine_bwd_t(const void* dout, int64_t lddo, const void* y, int64_t ldy, const int* offs, const int* perm,
                   const int* row, int64_t rows, const float* w, int64_t tokens, int K, int E, int64_t width, void* dy,
                   int64_t lddy, float* dw, cudaStream_t st) {
@@ -470,7 +478,7 @@ int combine_bwd_t(const void* dout, int64_t lddo, const void* y, int64_t ldy, co
            : K <= 4 ? combine_bwd_k<T, VEC, 4, F ? 1 : 2>
                     : combine_bwd_k<T, VEC, 8, 1>;
   k<<<(unsigned)(tc + E * 16), 256, 0, st>>>((const T*)dout, lddo, (const T*)y, ldy, offs, perm, row, rows, w, tokens,
-                                             K, E, width, (T*)dy, lddy, dw, tc);
+                                             K, E, (int)width, (T*)dy, lddy, dw, tc);
   return ops_launched();
 }
 
@@ -551,7 +559,7 @@ int32_t mt_dispatch(const void* x, int32_t dtype, int64_t ldx, int64_t n_tokens,
   if (!ops_dtype_ok(dtype) || !ops_mat_ok(out, dtype, ldo, width)) return MT_ERR_ARG;
   if (n_tokens == 0) return MT_OK;
   if (!ops_mat_ok(x, dtype, ldx, width)) return MT_ERR_ARG;
-  const bool vec = ops_vec(x, dtype, ldx) && ops_vec(out, dtype, ldo);
+  const int vec = vec_mode(ops_vec(x, dtype, ldx) && ops_vec(out, dtype, ldo), width);
   auto f = dtype == MT_DT_FP32 ? dispatch_t<float> : dispatch_t<__nv_bfloat16>;
   return f(x, ldx, n_tokens, width, top_k, n_experts, offs, perm, row, rows, out, ldo, vec, (cudaStream_t)stream);
 }
@@ -564,8 +572,11 @@ int32_t mt_dispatch8(const void* x, int32_t dtype, int64_t ldx, int64_t n_tokens
   if (!ops_dtype_ok(dtype)) return MT_ERR_ARG;
   if (n_tokens == 0) return MT_OK;
   if (!ops_mat_ok(x, dtype, ldx, out->cols)) return MT_ERR_ARG;
-  auto f = dtype == MT_DT_FP32 ? dispatch8_t<float> : dispatch8_t<__nv_bfloat16>;
-  return f(x, ldx, n_tokens, top_k, n_experts, offs, perm, row, out, ops_vec(x, dtype, ldx), (cudaStream_t)stream);
+  const int vec = vec_mode(ops_vec(x, dtype, ldx), out->cols);
+  auto f = dtype == MT_DT_FP32
+               ? (vec == 2 ? dispatch8_t<float, 2> : vec ? dispatch8_t<float, 1> : dispatch8_t<float, 0>)
+               : (vec == 2 ? dispatch8_t<__nv_bfloat16, 2> : vec ? dispatch8_t<__nv_bfloat16, 1> : dispatch8_t<__nv_bfloat16, 0>);
+  return f(x, ldx, n_tokens, top_k, n_experts, offs, perm, row, out, (cudaStream_t)stream);
 }
 
 int32_t mt_combine(const void* y, int32_t dtype, int64_t ldy, int64_t rows, const int32_t* row, const float* w,
@@ -577,9 +588,10 @@ int32_t mt_combine(const void* y, int32_t dtype, int64_t ldy, int64_t rows, cons
   if (n_tokens == 0) return MT_OK;
   if (!row || !ops_aligned(row, 4) || !ops_aligned(w, 4)) return MT_ERR_ARG;
   if (!ops_mat_ok(y, dtype, ldy, width) || !ops_mat_ok(out, dtype, ldo, width)) return MT_ERR_ARG;
-  const bool vec = ops_vec(y, dtype, ldy) && ops_vec(out, dtype, ldo);
-  auto f = dtype == MT_DT_FP32 ? (vec ? combine_t<float, true> : combine_t<float, false>)
-                               : (vec ? combine_t<__nv_bfloat16, true> : combine_t<__nv_bfloat16, false>);
+  const int vec = vec_mode(ops_vec(y, dtype, ldy) && ops_vec(out, dtype, ldo), width);
+  auto f = dtype == MT_DT_FP32
+               ? (vec == 2 ? combine_t<float, 2> : vec ? combine_t<float, 1> : combine_t<float, 0>)
+               : (vec == 2 ? combine_t<__nv_bfloat16, 2> : vec ? combine_t<__nv_bfloat16, 1> : combine_t<__nv_bfloat16, 0>);
   return f(y, ldy, rows, row, w, n_tokens, top_k, width, out, ldo, (cudaStream_t)stream);
 }
 
@@ -594,9 +606,12 @@ int32_t mt_combine_bwd(const void* dout, int32_t dtype, int64_t lddo, const void
   if (!w || !dw || !ops_aligned(w, 4) || !ops_aligned(dw, 4)) return MT_ERR_ARG;
   if (!ops_mat_ok(dout, dtype, lddo, width) || !ops_mat_ok(y, dtype, ldy, width) || !ops_mat_ok(dy, dtype, lddy, width))
     return MT_ERR_ARG;
-  const bool vec = ops_vec(dout, dtype, lddo) && ops_vec(y, dtype, ldy) && ops_vec(dy, dtype, lddy);
-  auto f = dtype == MT_DT_FP32 ? (vec ? combine_bwd_t<float, true> : combine_bwd_t<float, false>)
-                               : (vec ? combine_bwd_t<__nv_bfloat16, true> : combine_bwd_t<__nv_bfloat16, false>);
+  const int vec = vec_mode(ops_vec(dout, dtype, lddo) && ops_vec(y, dtype, ldy) && ops_vec(dy, dtype, lddy), width);
+  auto f = dtype == MT_DT_FP32
+               ? (vec == 2 ? combine_bwd_t<float, 2> : vec ? combine_bwd_t<float, 1> : combine_bwd_t<float, 0>)
+               : (vec == 2 ? combine_bwd_t<__nv_bfloat16, 2>
+                  : vec    ? combine_bwd_t<__nv_bfloat16, 1>
+                           : combine_bwd_t<__nv_bfloat16, 0>);
   return f(dout, lddo, y, ldy, offs, perm, row, rows, w, n_tokens, top_k, n_experts, width, dy, lddy, dw,
            (cudaStream_t)stream);
 }

@@ -461,9 +461,12 @@ void swiglu_bwd_t(const void* da, int64_t ldda, const mt_mat8* sv, const int* n_
   k<<<grid, 256, 0, st>>>((const T*)da, ldda, mat8(sv), n_rows, (T*)dgu, lddgu, (T*)act, ldact);
 }
 
-// Instantiations by element type and access mode (see ops_ld8): 2 where every
-// chunk of `width` columns is whole.
-int vec_mode(bool vec, int64_t width, int chunk) { return !vec ? 0 : width % chunk ? 1 : 2; }
+// Instantiations by element type and access mode (see ops_ld8); a second part of
+// the columns has to start as well aligned as the row.
+int part_vec(int vec, int dtype, int64_t part) {
+  const int64_t b = part * ops_size(dtype);
+  return ops_least(vec, b % (8 * ops_size(dtype)) == 0 ? 2 : b % 16 == 0 ? 1 : 0);
+}
 #define OPS_PICK(f, dtype, vec, ...)                                                                     \
   ((dtype) == MT_DT_FP32 ? ((vec) == 2 ? f<float, 2 __VA_ARGS__> : (vec) ? f<float, 1 __VA_ARGS__> : f<float, 0 __VA_ARGS__>) \
                          : ((vec) == 2 ? f<__nv_bfloat16, 2 __VA_ARGS__>                                 \
@@ -483,17 +486,17 @@ int32_t mt_quant8(const void* x, int32_t dtype, int64_t ldx, const int32_t* n_ro
   if (out->rows == 0) return MT_OK;
   if (!ops_mat_ok(x, dtype, ldx, out->cols)) return MT_ERR_ARG;
   cudaStream_t st = (cudaStream_t)stream;
-  const bool vec = ops_vec(x, dtype, ldx);
+  const int vec = ops_vec(x, dtype, ldx);
   if (out->block_rows == 1) {
     mt_mat8 o = *out;            // stacked matrices are one tall one
     o.rows *= o.batch;
     const int64_t part = o.halves ? o.cols / 2 : o.cols;
-    const int v = vec_mode(vec && (!o.halves || part * ops_size(dtype) % 16 == 0), part, 256);
+    const int v = ops_mode(o.halves ? part_vec(vec, dtype, part) : vec, part, 256);
     OPS_PICK(quant_rows_t, dtype, v)(x, ldx, n_rows, &o, st);
   } else {
     if (out->batch > 65535) return MT_ERR_UNSUPPORTED;
     const Src8 none{};
-    const int v = vec_mode(vec, out->cols, 128);
+    const int v = ops_mode(vec, out->cols, 128);
     OPS_PICK(quant_tile_t, dtype, v, OPS_COMMA T_BLOCK)(x, ldx, none, nullptr, out, out->rows, out->cols, st);
   }
   return ops_launched();
@@ -519,7 +522,7 @@ int32_t mt_quant8_t(const void* x, int32_t dtype, int64_t ldx, const mt_mat8* x8
     return ops_launched();
   }
   if (!ops_dtype_ok(dtype) || !ops_mat_ok(x, dtype, ldx, cols)) return MT_ERR_ARG;
-  const int v = vec_mode(ops_vec(x, dtype, ldx), cols, 128);
+  const int v = ops_mode(ops_vec(x, dtype, ldx), cols, 128);
   const Src8 none{};
   auto f = out->block_rows == 1 ? OPS_PICK(quant_tile_t, dtype, v, OPS_COMMA T_COLS_T)
                                 : OPS_PICK(quant_tile_t, dtype, v, OPS_COMMA T_BLOCK_T);
@@ -534,7 +537,7 @@ int32_t mt_dequant8(const mt_mat8* a, const int32_t* n_rows, void* out, int32_t 
   if (!ops_mat_ok(out, dtype, ldo, a->cols)) return MT_ERR_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   const int64_t part = a->halves ? a->cols / 2 : a->cols;
-  const int v = vec_mode(ops_vec(out, dtype, ldo) && (!a->halves || part * ops_size(dtype) % 16 == 0), part, 256);
+  const int vec = ops_vec(out, dtype, ldo), v = ops_mode(a->halves ? part_vec(vec, dtype, part) : vec, part, 256);
   OPS_PICK(dequant_t, dtype, v)(a, n_rows, out, ldo, st);
   return ops_launched();
 }
@@ -550,7 +553,7 @@ int32_t mt_swiglu8(const void* gu, int32_t dtype, int64_t ldgu, const int32_t* n
   if (act->rows == 0) return MT_OK;
   if (!ops_mat_ok(gu, dtype, ldgu, 2 * act->cols)) return MT_ERR_ARG;
   cudaStream_t st = (cudaStream_t)stream;
-  const int v = vec_mode(ops_vec(gu, dtype, ldgu) && act->cols * ops_size(dtype) % 16 == 0, act->cols, 256);
+  const int v = ops_mode(part_vec(ops_vec(gu, dtype, ldgu), dtype, act->cols), act->cols, 256);
   OPS_PICK(swiglu_t, dtype, v)(gu, ldgu, n_rows, act, saved, st);
   return ops_launched();
 }
@@ -566,8 +569,8 @@ int32_t mt_swiglu8_bwd(const void* dact, int32_t dtype, int64_t ldda, const mt_m
       (act && !ops_mat_ok(act, dtype, ldact, F)))
     return MT_ERR_ARG;
   cudaStream_t st = (cudaStream_t)stream;
-  const int v = vec_mode(ops_vec(dact, dtype, ldda) && ops_vec(dgu, dtype, lddgu) && (!act || ops_vec(act, dtype, ldact)) &&
-                             F * ops_size(dtype) % 16 == 0, F, 256);
+  const int vec = ops_least(ops_vec(dact, dtype, ldda), ops_least(ops_vec(dgu, dtype, lddgu), act ? ops_vec(act, dtype, ldact) : 2));
+  const int v = ops_mode(part_vec(vec, dtype, F), F, 256);
   OPS_PICK(swiglu_bwd_t, dtype, v)(dact, ldda, saved, n_rows, dgu, lddgu, act, ldact, st);
   return ops_launched();
 }

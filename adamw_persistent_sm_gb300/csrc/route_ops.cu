@@ -432,9 +432,6 @@ unsigned col_chunks(int64_t width) {
   return (unsigned)(n < 1024 ? n : 1024);
 }
 
-// How the lanes access rows of `width` (see ops_ld8).
-int vec_mode(bool vec, int64_t width) { return !vec ? 0 : width % 256 ? 1 : 2; }
-
 template <class T>
 int dispatch_t(const void* x, int64_t ldx, int64_t tokens, int64_t width, int K, int E, const int* offs,
                const int* perm, const int* row, int64_t rows, void* out, int64_t ldo, int vec, cudaStream_t st) {
@@ -559,7 +556,7 @@ int32_t mt_dispatch(const void* x, int32_t dtype, int64_t ldx, int64_t n_tokens,
   if (!ops_dtype_ok(dtype) || !ops_mat_ok(out, dtype, ldo, width)) return MT_ERR_ARG;
   if (n_tokens == 0) return MT_OK;
   if (!ops_mat_ok(x, dtype, ldx, width)) return MT_ERR_ARG;
-  const int vec = vec_mode(ops_vec(x, dtype, ldx) && ops_vec(out, dtype, ldo), width);
+  const int vec = ops_mode(ops_least(ops_vec(x, dtype, ldx), ops_vec(out, dtype, ldo)), width, 256);
   auto f = dtype == MT_DT_FP32 ? dispatch_t<float> : dispatch_t<__nv_bfloat16>;
   return f(x, ldx, n_tokens, width, top_k, n_experts, offs, perm, row, rows, out, ldo, vec, (cudaStream_t)stream);
 }
@@ -572,7 +569,7 @@ int32_t mt_dispatch8(const void* x, int32_t dtype, int64_t ldx, int64_t n_tokens
   if (!ops_dtype_ok(dtype)) return MT_ERR_ARG;
   if (n_tokens == 0) return MT_OK;
   if (!ops_mat_ok(x, dtype, ldx, out->cols)) return MT_ERR_ARG;
-  const int vec = vec_mode(ops_vec(x, dtype, ldx), out->cols);
+  const int vec = ops_mode(ops_vec(x, dtype, ldx), out->cols, 256);
   auto f = dtype == MT_DT_FP32
                ? (vec == 2 ? dispatch8_t<float, 2> : vec ? dispatch8_t<float, 1> : dispatch8_t<float, 0>)
                : (vec == 2 ? dispatch8_t<__nv_bfloat16, 2> : vec ? dispatch8_t<__nv_bfloat16, 1> : dispatch8_t<__nv_bfloat16, 0>);
@@ -588,7 +585,7 @@ int32_t mt_combine(const void* y, int32_t dtype, int64_t ldy, int64_t rows, cons
   if (n_tokens == 0) return MT_OK;
   if (!row || !ops_aligned(row, 4) || !ops_aligned(w, 4)) return MT_ERR_ARG;
   if (!ops_mat_ok(y, dtype, ldy, width) || !ops_mat_ok(out, dtype, ldo, width)) return MT_ERR_ARG;
-  const int vec = vec_mode(ops_vec(y, dtype, ldy) && ops_vec(out, dtype, ldo), width);
+  const int vec = ops_mode(ops_least(ops_vec(y, dtype, ldy), ops_vec(out, dtype, ldo)), width, 256);
   auto f = dtype == MT_DT_FP32
                ? (vec == 2 ? combine_t<float, 2> : vec ? combine_t<float, 1> : combine_t<float, 0>)
                : (vec == 2 ? combine_t<__nv_bfloat16, 2> : vec ? combine_t<__nv_bfloat16, 1> : combine_t<__nv_bfloat16, 0>);
@@ -606,7 +603,7 @@ int32_t mt_combine_bwd(const void* dout, int32_t dtype, int64_t lddo, const void
   if (!w || !dw || !ops_aligned(w, 4) || !ops_aligned(dw, 4)) return MT_ERR_ARG;
   if (!ops_mat_ok(dout, dtype, lddo, width) || !ops_mat_ok(y, dtype, ldy, width) || !ops_mat_ok(dy, dtype, lddy, width))
     return MT_ERR_ARG;
-  const int vec = vec_mode(ops_vec(dout, dtype, lddo) && ops_vec(y, dtype, ldy) && ops_vec(dy, dtype, lddy), width);
+  const int vec = ops_mode(ops_least(ops_vec(dout, dtype, lddo), ops_least(ops_vec(y, dtype, ldy), ops_vec(dy, dtype, lddy))), width, 256);
   auto f = dtype == MT_DT_FP32
                ? (vec == 2 ? combine_bwd_t<float, 2> : vec ? combine_bwd_t<float, 1> : combine_bwd_t<float, 0>)
                : (vec == 2 ? combine_bwd_t<__nv_bfloat16, 2>

@@ -161,35 +161,53 @@ __device__ __forceinline__ void tile_top(const RAW* w, uint32_t* m) {
   }
 }
 
-// One CTA per tile; a thread holds 8 rows x 8 columns as they came from memory.
-// A column's maximum goes over 8 rows in registers, two lanes by shuffle and 8
-// warps through shared memory; transposed codes go through a 16 KB tile whose
-// 8-byte chunks are swizzled by the source column group, which keeps both sides
-// free of bank conflicts.  Memory-bound: each byte is read and written once, and
-// three CTAs per SM (85 registers) keep loads in flight while others convert.
+// A thread holds 8 rows x 8 columns of a tile as they came from memory.  A column's
+// maximum goes over 8 rows in registers, two lanes by shuffle and 8 warps through
+// shared memory; transposed codes go through a 16 KB tile whose 8-byte chunks are
+// swizzled by the source column group, which keeps both sides free of bank
+// conflicts.  Memory-bound: each byte is read and written once.  A CTA walks over
+// tiles, columns fastest, and (PRE) reads the next while it converts one.
 template <class T, int VEC, int MODE>
-__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) quant_tile_k(const T* x, long long ldx, Src8 src,
-                                                                            const int* n_rows, Mat8 o, int rows, int cols) {
+__global__ void __launch_bounds__(256, sizeof(T) == 1 ? 3 : 2) quant_tile_k(const T* x, long long ldx, Src8 src, const int* n_rows, Mat8 o,
+                                                       int rows, int cols) {
+  // fp32: two tiles would not fit the registers; codes: bound by their conversions,
+  // three CTAs without reading ahead take 30 us where two that do take 35
+  constexpr bool PRE = sizeof(T) == 2;
   __shared__ uint32_t part[8][128];
   __shared__ int ex[128];
   __shared__ __align__(16) uint2 tile[MODE == T_BLOCK ? 1 : 128 * 16];
+  typedef typename Tile8<T>::Raw Raw;
   const int tid = threadIdx.x, warp = tid >> 5, tc = tid & 15, tr = tid >> 4;
-  const int b = blockIdx.z;
+  const int b = blockIdx.z, nct = (cols + 127) / 128;
   const int lim = ops_row_limit(n_rows, rows);
-  for (int rt = blockIdx.x; rt * 128 < lim; rt += gridDim.x) {
-    for (int ct = blockIdx.y; ct * 128 < cols; ct += gridDim.y) {
+  const long long tiles = (long long)((lim + 127) / 128) * nct;
+  const T* xb = x + (long long)b * rows * ldx;
+  auto load = [&](Raw* w, long long t) {
+    const int rt = (int)(t / nct), r0 = rt * 128 + tr * 8, c0 = (int)(t - (long long)rt * nct) * 128 + tc * 8;
+    if (rt * 128 + 128 <= lim) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) Tile8<T>::template load<VEC>(w[i], xb, ldx, src, r0 + i, c0, cols);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (r0 + i < lim) Tile8<T>::template load<VEC>(w[i], xb, ldx, src, r0 + i, c0, cols);
+        else Tile8<T>::zero(w[i]);
+      }
+    }
+  };
+  Raw next[8];
+  if (PRE && blockIdx.x < tiles) load(next, blockIdx.x);
+  for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
+    {
+      const int rt = (int)(t / nct), ct = (int)(t - (long long)rt * nct);
       const int r0 = rt * 128 + tr * 8, c0 = ct * 128 + tc * 8;
-      typename Tile8<T>::Raw w[8];
-      const T* xb = x + (long long)b * rows * ldx;
-      if (rt * 128 + 128 <= lim) {
+      Raw w[8];
+      if (PRE) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) Tile8<T>::template load<VEC>(w[i], xb, ldx, src, r0 + i, c0, cols);
+        for (int i = 0; i < 8; ++i) w[i] = next[i];
+        if (t + gridDim.x < tiles) load(next, t + gridDim.x);
       } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (r0 + i < lim) Tile8<T>::template load<VEC>(w[i], xb, ldx, src, r0 + i, c0, cols);
-          else Tile8<T>::zero(w[i]);
-        }
+        load(w, t);
       }
       uint32_t m[8];
       tile_top(w, m);
@@ -430,8 +448,9 @@ void quant_rows_t(const void* x, int64_t ldx, const int* n_rows, const mt_mat8* 
 template <class T, int VEC, int MODE>
 void quant_tile_t(const void* x, int64_t ldx, const Src8& src, const int* n_rows, const mt_mat8* o, int64_t rows,
                   int64_t cols, cudaStream_t st) {
-  const int64_t rt = (rows + 127) / 128, ct = (cols + 127) / 128;
-  const dim3 grid((unsigned)rt, (unsigned)(ct < 32768 ? ct : 32768), (unsigned)o->batch);
+  const int64_t tiles = ((rows + 127) / 128) * ((cols + 127) / 128);
+  const int64_t most = (152 * (sizeof(T) == 1 ? 3 : 2) + o->batch - 1) / o->batch;         // the CTAs that fit at one time
+  const dim3 grid((unsigned)(tiles < most ? tiles : most), 1, (unsigned)o->batch);
   quant_tile_k<T, VEC, MODE><<<grid, 256, 0, st>>>((const T*)x, ldx, src, n_rows, mat8(o), (int)rows, (int)cols);
 }
 template <class T, int VEC>

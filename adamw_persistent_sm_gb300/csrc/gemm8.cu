@@ -280,18 +280,19 @@ __global__ void __launch_bounds__(G8_THREADS, 1) gemm8_k(const __grid_constant__
     mbar_init(done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  // segment starts, kept inside the operands and on block boundaries whatever
-  // they hold (a TMA coordinate has to be a multiple of 16)
-  if (g.mode != G8_DENSE && tid <= g.nseg) {
-    const int lim = g.mode == G8_ROWS ? (g.M + 127) & ~127 : g.K;
-    int v = __ldg(g.offs + tid) & ~127;
-    v = v < 0 ? 0 : v > lim ? lim : v;
-    offs[tid] = v & ~127;
-  }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + G8_TMEM), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  ops_begin();
+  // segment starts, kept inside the operands and on block boundaries whatever
+  // they hold (a TMA coordinate has to be a multiple of 16)
+  if (g.mode != G8_DENSE && tid <= g.nseg) {
+    const int lim = g.mode == G8_ROWS ? (g.M + 127) & ~127 : g.K;
+    int v = g.offs[tid] & ~127;
+    v = v < 0 ? 0 : v > lim ? lim : v;
+    offs[tid] = v & ~127;
   }
   tc_fence_before();
   __syncthreads();
@@ -434,12 +435,12 @@ __global__ void __launch_bounds__(G8_THREADS, 1) gemm8_k(const __grid_constant__
           if (words) {
             // the aligned words that hold the bytes lie in the same row
             const uint32_t* q = reinterpret_cast<const uint32_t*>(p[j] + kb - sh);
-            lo[j] = __ldg(q);
-            hi[j] = sh + n > 4 ? __ldg(q + 1) : 0;
+            lo[j] = q[0];
+            hi[j] = sh + n > 4 ? q[1] : 0;
           } else {
             lo[j] = hi[j] = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) lo[j] |= (uint32_t)__ldg(p[j] + kb + (i < n ? i : n - 1)) << (8 * i);
+            for (int i = 0; i < 4; ++i) lo[j] |= (uint32_t)p[j][kb + (i < n ? i : n - 1)] << (8 * i);
           }
         }
       };
@@ -642,8 +643,7 @@ int launch(G8Args& g, const mt_mat8* a, const mt_mat8* b, int64_t segs, bool f32
       g_dev[dev].prepared[which] = true;
     }
   }
-  k<<<(unsigned)(tiles < sms ? tiles : sms), G8_THREADS, smem, st>>>(g);
-  return ops_launched();
+  return ops_launch(k, (unsigned)(tiles < sms ? tiles : sms), G8_THREADS, smem, st, 1, g);
 }
 
 bool operand_ok(const mt_mat8* m) { return ops_mat8_ok(m) && !m->halves; }

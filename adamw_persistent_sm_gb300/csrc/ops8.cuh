@@ -13,6 +13,16 @@
 // ---------------------------------------------------------------------------
 // device
 // ---------------------------------------------------------------------------
+// First thing in every kernel: let the next one of the stream be launched while
+// this one runs, and wait for the one before to be done with its memory (both
+// without effect where the launch does not ask for it, see ops_launch).  What a
+// kernel reads may thus be written while it is already resident: plain loads, no
+// read-only ones.
+__device__ __forceinline__ void ops_begin() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // n_rows of the C ABI: rows below *p (clamped), or all of them
 __device__ __forceinline__ int ops_row_limit(const int* p, int rows) {
   if (!p) return rows;
@@ -29,25 +39,25 @@ __device__ __forceinline__ int ops_row_limit(const int* p, int rows) {
 template <int VEC>
 __device__ __forceinline__ void ops_ld8(const float* p, int c, int n, float* v) {
   if constexpr (VEC == 2) {
-    asm volatile("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                  : "l"(p + c));
     return;
   }
   if (VEC == 2 || (VEC && c + 8 <= n)) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p + c)), b = __ldg(reinterpret_cast<const float4*>(p + c + 4));
+    const float4 a = *reinterpret_cast<const float4*>(p + c), b = *reinterpret_cast<const float4*>(p + c + 4);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = c + i < n ? __ldg(p + c + i) : 0.f;
+  for (int i = 0; i < 8; ++i) v[i] = c + i < n ? p[c + i] : 0.f;
 }
 __device__ __forceinline__ float ops_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float ops_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 template <int VEC>
 __device__ __forceinline__ void ops_ld8(const __nv_bfloat16* p, int c, int n, float* v) {
   if (VEC == 2 || (VEC && c + 8 <= n)) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p + c));
+    const uint4 u = *reinterpret_cast<const uint4*>(p + c);
     v[0] = ops_lo(u.x); v[1] = ops_hi(u.x); v[2] = ops_lo(u.y); v[3] = ops_hi(u.y);
     v[4] = ops_lo(u.z); v[5] = ops_hi(u.z); v[6] = ops_lo(u.w); v[7] = ops_hi(u.w);
     return;
@@ -100,11 +110,11 @@ __device__ __forceinline__ void ops_st_codes(uint8_t* p, int c, int n, uint2 q, 
 }
 template <int VEC>
 __device__ __forceinline__ uint2 ops_ld_codes(const uint8_t* p, int c, int n, bool v8) {
-  if (VEC == 2 || (v8 && c + 8 <= n)) return __ldg(reinterpret_cast<const uint2*>(p + c));
+  if (VEC == 2 || (v8 && c + 8 <= n)) return *reinterpret_cast<const uint2*>(p + c);
   uint2 q = make_uint2(0, 0);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t b = c + i < n ? __ldg(p + c + i) : 0;
+    const uint32_t b = c + i < n ? p[c + i] : 0;
     if (i < 4) q.x |= b << (8 * i);
     else q.y |= b << (8 * (i - 4));
   }
@@ -187,12 +197,12 @@ struct Raw8<__nv_bfloat16> {
   template <int VEC>
   __device__ __forceinline__ void load(const __nv_bfloat16* p, int c, int n) {
     if (VEC == 2 || (VEC && c + 8 <= n)) {
-      u = __ldg(reinterpret_cast<const uint4*>(p + c));
+      u = *reinterpret_cast<const uint4*>(p + c);
       return;
     }
     uint32_t h[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = c + i < n ? __ldg(reinterpret_cast<const uint16_t*>(p) + c + i) : 0;
+    for (int i = 0; i < 8; ++i) h[i] = c + i < n ? reinterpret_cast<const uint16_t*>(p)[c + i] : 0;
     u = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
   }
   template <int VEC>
@@ -300,4 +310,28 @@ static inline bool ops_mat8_ok(const mt_mat8* m) {
   if (!ops_aligned(m->codes, 16) || m->ld % 16 || m->ld < m->cols || m->ld > (1LL << 40)) return false;
   return m->lds >= ops_blocks(m) && m->lds <= (1LL << 40);
 }
-static inline int ops_launched() { return cudaGetLastError() == cudaSuccess ? MT_OK : MT_ERR_LAUNCH; }
+// A launch that may become resident while the kernel before it in the stream
+// drains (a chain of moves loses 3 to 5 us per boundary otherwise); `cluster` CTAs
+// per cluster.
+template <class... P, class... A>
+static int ops_launch(void (*k)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t st, unsigned cluster,
+                      A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, k, (P)args...) != cudaSuccess) {
+    cudaGetLastError();
+    return MT_ERR_LAUNCH;
+  }
+  return MT_OK;
+}

@@ -27,6 +27,7 @@ Mat8 mat8(const mt_mat8* m) {
 template <class T, int VEC, int R>
 __global__ void __launch_bounds__(256) quant_rows_k(const T* x, long long ldx, const int* n_rows, Mat8 o, int parts,
                                                     int pcols) {
+  ops_begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lim = ops_row_limit(n_rows, o.rows);
   const int r0 = ((int)blockIdx.x * 8 + warp) * R;
@@ -62,6 +63,7 @@ __global__ void __launch_bounds__(256) quant_rows_k(const T* x, long long ldx, c
 template <class T, int VEC>
 __global__ void __launch_bounds__(256) dequant_k(Mat8 a, const int* n_rows, int parts, int pcols, T* out,
                                                  long long ldo) {
+  ops_begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lim = ops_row_limit(n_rows, a.rows);
   const int r0 = ((int)blockIdx.x * 8 + warp) * 4;
@@ -77,7 +79,7 @@ __global__ void __launch_bounds__(256) dequant_k(Mat8 a, const int* n_rows, int 
     for (int i = 0; i < 4; ++i) {
       const long long r = min(r0 + i, lim - 1);
       q[i] = ops_ld_codes<VEC>(a.q + r * a.ld + base, c, pcols, v8);
-      s[i] = __ldg(a.s + r * a.lds + part * pblocks + (c >> 7));
+      s[i] = a.s[r * a.lds + part * pblocks + (c >> 7)];
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -126,7 +128,7 @@ struct Tile8<uint8_t> {
     w.s = 1.f;
     if (VEC != 2 && c >= n) return;
     w.q = ops_ld_codes<VEC>(a.q + r * a.ld, c, n, true);
-    w.s = ops_pow2((int)__ldg(a.s + r * a.lds + (c >> 7)) - 127);
+    w.s = ops_pow2((int)a.s[r * a.lds + (c >> 7)] - 127);
   }
   static __device__ __forceinline__ void zero(Raw& w) {
     w.q = make_uint2(0, 0);
@@ -176,6 +178,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 1 ? 3 : 2) quant_tile_k(cons
   __shared__ uint32_t part[8][128];
   __shared__ int ex[128];
   __shared__ __align__(16) uint2 tile[MODE == T_BLOCK ? 1 : 128 * 16];
+  ops_begin();
   typedef typename Tile8<T>::Raw Raw;
   const int tid = threadIdx.x, warp = tid >> 5, tc = tid & 15, tr = tid >> 4;
   const int b = blockIdx.z, nct = (cols + 127) / 128;
@@ -329,7 +332,8 @@ __device__ __forceinline__ float sigmoid_f(float g) {
 // Half a warp holds one block of g and the same block of u: act and, where
 // asked for, g and u leave as codes in the same pass.  R rows per warp, loads first.
 template <class T, int VEC, bool SAVE, int R>
-__global__ void __launch_bounds__(256) swiglu_k(const T* gu, long long ldgu, const int* n_rows, Mat8 act, Mat8 sv) {
+__global__ void __launch_bounds__(256, SAVE ? 4 : 1) swiglu_k(const T* gu, long long ldgu, const int* n_rows, Mat8 act, Mat8 sv) {
+  ops_begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int F = act.cols, lim = ops_row_limit(n_rows, act.rows), nb = (F + 127) / 128;
   const int r0 = ((int)blockIdx.x * 8 + warp) * R;
@@ -382,45 +386,33 @@ __global__ void __launch_bounds__(256) swiglu_k(const T* gu, long long ldgu, con
   }
 }
 
-template <class T, int VEC, int R>
+template <class T, int VEC>
 __global__ void __launch_bounds__(256) swiglu_bwd_k(const T* da, long long ldda, Mat8 sv, const int* n_rows, T* dgu,
                                                     long long lddgu, T* act, long long ldact) {
+  ops_begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int F = sv.cols / 2, lim = ops_row_limit(n_rows, sv.rows), nb = (F + 127) / 128;
-  const int r0 = ((int)blockIdx.x * 8 + warp) * R;
-  if (r0 >= lim) return;
+  const long long r = (long long)blockIdx.x * 8 + warp;
+  if (r >= lim) return;
   const bool v8 = (F & 7) == 0;
   for (int c = lane * 8 + 256 * (int)blockIdx.y; c < F; c += 256 * (int)gridDim.y) {
-    float d[R][8];
-    uint2 qg[R], qu[R];
-    int eg[R], eu[R];
+    float d[8], g[8], u[8], a[8];
+    ops_ld8<VEC>(da + r * ldda, c, F, d);
+    const uint2 qg = ops_ld_codes<VEC>(sv.q + r * sv.ld, c, F, true);
+    const uint2 qu = ops_ld_codes<VEC>(sv.q + r * sv.ld + F, c, F, v8);
+    const int eg = sv.s[r * sv.lds + (c >> 7)], eu = sv.s[r * sv.lds + nb + (c >> 7)];
+    ops_values8(qg, ops_pow2(eg - 127), g);
+    ops_values8(qu, ops_pow2(eu - 127), u);
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const long long r = min(r0 + i, lim - 1);
-      ops_ld8<VEC>(da + r * ldda, c, F, d[i]);
-      qg[i] = ops_ld_codes<VEC>(sv.q + r * sv.ld, c, F, true);
-      qu[i] = ops_ld_codes<VEC>(sv.q + r * sv.ld + F, c, F, v8);
-      eg[i] = __ldg(sv.s + r * sv.lds + (c >> 7));
-      eu[i] = __ldg(sv.s + r * sv.lds + nb + (c >> 7));
+    for (int j = 0; j < 8; ++j) {
+      const float s = sigmoid_f(g[j]), gs = g[j] * s, x = d[j];
+      a[j] = gs * u[j];
+      d[j] = x * u[j] * (s + gs * (1.f - s));
+      u[j] = x * gs;
     }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const long long r = r0 + i;
-      if (r >= lim) break;
-      float g[8], u[8], a[8];
-      ops_values8(qg[i], ops_pow2(eg[i] - 127), g);
-      ops_values8(qu[i], ops_pow2(eu[i] - 127), u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float s = sigmoid_f(g[j]), gs = g[j] * s, x = d[i][j];
-        a[j] = gs * u[j];
-        d[i][j] = x * u[j] * (s + gs * (1.f - s));
-        u[j] = x * gs;
-      }
-      ops_st8<VEC>(dgu + r * lddgu, c, F, d[i]);
-      ops_st8<VEC>(dgu + r * lddgu + F, c, F, u);
-      if (act) ops_st8<VEC>(act + r * ldact, c, F, a);
-    }
+    ops_st8<VEC>(dgu + r * lddgu, c, F, d);
+    ops_st8<VEC>(dgu + r * lddgu + F, c, F, u);
+    if (act) ops_st8<VEC>(act + r * ldact, c, F, a);
   }
 }
 
@@ -437,47 +429,45 @@ unsigned col_ctas(int64_t cols, int per) {
 }
 
 template <class T, int VEC>
-void quant_rows_t(const void* x, int64_t ldx, const int* n_rows, const mt_mat8* o, cudaStream_t st) {
+int quant_rows_t(const void* x, int64_t ldx, const int* n_rows, const mt_mat8* o, cudaStream_t st) {
   const int parts = o->halves ? 2 : 1;
   const int64_t pc = o->cols / parts, chunks = (pc + 255) / 256 * parts;
   const int r = rows_per_warp(o->rows, chunks * 256);
-  const dim3 grid(row_ctas(o->rows, r), col_ctas(chunks, 1));
-  if (r == 1) quant_rows_k<T, VEC, 1><<<grid, 256, 0, st>>>((const T*)x, ldx, n_rows, mat8(o), parts, (int)pc);
-  else quant_rows_k<T, VEC, 4><<<grid, 256, 0, st>>>((const T*)x, ldx, n_rows, mat8(o), parts, (int)pc);
+  return ops_launch(r == 1 ? quant_rows_k<T, VEC, 1> : quant_rows_k<T, VEC, 4>,
+                    dim3(row_ctas(o->rows, r), col_ctas(chunks, 1)), 256, 0, st, 1, (const T*)x, ldx, n_rows, mat8(o),
+                    parts, pc);
 }
 template <class T, int VEC, int MODE>
-void quant_tile_t(const void* x, int64_t ldx, const Src8& src, const int* n_rows, const mt_mat8* o, int64_t rows,
-                  int64_t cols, cudaStream_t st) {
+int quant_tile_t(const void* x, int64_t ldx, const Src8& src, const int* n_rows, const mt_mat8* o, int64_t rows,
+                 int64_t cols, cudaStream_t st) {
   const int64_t tiles = ((rows + 127) / 128) * ((cols + 127) / 128);
-  const int64_t most = (152 * (sizeof(T) == 1 ? 3 : 2) + o->batch - 1) / o->batch;         // the CTAs that fit at one time
+  const int64_t most = (152 * (sizeof(T) == 1 ? 3 : 2) + o->batch - 1) / o->batch;     // the CTAs that fit at one time
   const dim3 grid((unsigned)(tiles < most ? tiles : most), 1, (unsigned)o->batch);
-  quant_tile_k<T, VEC, MODE><<<grid, 256, 0, st>>>((const T*)x, ldx, src, n_rows, mat8(o), (int)rows, (int)cols);
+  return ops_launch(quant_tile_k<T, VEC, MODE>, grid, 256, 0, st, 1, (const T*)x, ldx, src, n_rows, mat8(o), rows, cols);
 }
 template <class T, int VEC>
-void dequant_t(const mt_mat8* a, const int* n_rows, void* out, int64_t ldo, cudaStream_t st) {
+int dequant_t(const mt_mat8* a, const int* n_rows, void* out, int64_t ldo, cudaStream_t st) {
   const int parts = a->halves ? 2 : 1;
   const int64_t pc = a->cols / parts, chunks = (pc + 255) / 256 * parts;
-  const dim3 grid(row_ctas(a->rows, 4), col_ctas(chunks, 1));
-  dequant_k<T, VEC><<<grid, 256, 0, st>>>(mat8(a), n_rows, parts, (int)pc, (T*)out, ldo);
+  return ops_launch(dequant_k<T, VEC>, dim3(row_ctas(a->rows, 4), col_ctas(chunks, 1)), 256, 0, st, 1, mat8(a), n_rows,
+                    parts, pc, (T*)out, ldo);
+}
+// With checkpoints two rows per warp share the loads' trip (52 -> 46 us at 65536 x
+// 512, 64 registers); without, and backward, more warps do better (33 -> 30 and 64
+// -> 54 us).
+template <class T, int VEC>
+int swiglu_t(const void* gu, int64_t ldgu, const int* n_rows, const mt_mat8* act, const mt_mat8* sv,
+             cudaStream_t st) {
+  const int r = !sv || rows_per_warp(act->rows, act->cols) == 1 ? 1 : 2;
+  auto k = !sv ? swiglu_k<T, VEC, false, 1> : r == 1 ? swiglu_k<T, VEC, true, 1> : swiglu_k<T, VEC, true, 2>;
+  return ops_launch(k, dim3(row_ctas(act->rows, r), col_ctas(act->cols, 256)), 256, 0, st, 1, (const T*)gu, ldgu,
+                    n_rows, mat8(act), sv ? mat8(sv) : Mat8{});
 }
 template <class T, int VEC>
-void swiglu_t(const void* gu, int64_t ldgu, const int* n_rows, const mt_mat8* act, const mt_mat8* sv,
-              cudaStream_t st) {
-  const int r = rows_per_warp(act->rows, act->cols) == 1 ? 1 : 2;
-  const dim3 grid(row_ctas(act->rows, r), col_ctas(act->cols, 256));
-  const Mat8 a = mat8(act), s = sv ? mat8(sv) : Mat8{};
-  auto k = sv ? (r == 1 ? swiglu_k<T, VEC, true, 1> : swiglu_k<T, VEC, true, 2>)
-              : (r == 1 ? swiglu_k<T, VEC, false, 1> : swiglu_k<T, VEC, false, 2>);
-  k<<<grid, 256, 0, st>>>((const T*)gu, ldgu, n_rows, a, s);
-}
-template <class T, int VEC>
-void swiglu_bwd_t(const void* da, int64_t ldda, const mt_mat8* sv, const int* n_rows, void* dgu, int64_t lddgu,
-                  void* act, int64_t ldact, cudaStream_t st) {
-  const int64_t F = sv->cols / 2;
-  const int r = rows_per_warp(sv->rows, F) == 1 ? 1 : 2;
-  const dim3 grid(row_ctas(sv->rows, r), col_ctas(F, 256));
-  auto k = r == 1 ? swiglu_bwd_k<T, VEC, 1> : swiglu_bwd_k<T, VEC, 2>;
-  k<<<grid, 256, 0, st>>>((const T*)da, ldda, mat8(sv), n_rows, (T*)dgu, lddgu, (T*)act, ldact);
+int swiglu_bwd_t(const void* da, int64_t ldda, const mt_mat8* sv, const int* n_rows, void* dgu, int64_t lddgu,
+                 void* act, int64_t ldact, cudaStream_t st) {
+  return ops_launch(swiglu_bwd_k<T, VEC>, dim3(row_ctas(sv->rows, 1), col_ctas(sv->cols / 2, 256)), 256, 0, st, 1,
+                    (const T*)da, ldda, mat8(sv), n_rows, (T*)dgu, lddgu, (T*)act, ldact);
 }
 
 // Instantiations by element type and access mode (see ops_ld8); a second part of
@@ -511,14 +501,13 @@ int32_t mt_quant8(const void* x, int32_t dtype, int64_t ldx, const int32_t* n_ro
     o.rows *= o.batch;
     const int64_t part = o.halves ? o.cols / 2 : o.cols;
     const int v = ops_mode(o.halves ? part_vec(vec, dtype, part) : vec, part, 256);
-    OPS_PICK(quant_rows_t, dtype, v)(x, ldx, n_rows, &o, st);
+    return OPS_PICK(quant_rows_t, dtype, v)(x, ldx, n_rows, &o, st);
   } else {
     if (out->batch > 65535) return MT_ERR_UNSUPPORTED;
     const Src8 none{};
     const int v = ops_mode(vec, out->cols, 128);
-    OPS_PICK(quant_tile_t, dtype, v, OPS_COMMA T_BLOCK)(x, ldx, none, nullptr, out, out->rows, out->cols, st);
+    return OPS_PICK(quant_tile_t, dtype, v, OPS_COMMA T_BLOCK)(x, ldx, none, nullptr, out, out->rows, out->cols, st);
   }
-  return ops_launched();
 }
 
 int32_t mt_quant8_t(const void* x, int32_t dtype, int64_t ldx, const mt_mat8* x8, const int32_t* n_rows,
@@ -537,16 +526,14 @@ int32_t mt_quant8_t(const void* x, int32_t dtype, int64_t ldx, const mt_mat8* x8
     const Src8 src{(const uint8_t*)x8->codes, (const uint8_t*)x8->scales, x8->ld, x8->lds};
     auto f = out->block_rows == 1 ? (cols % 128 ? quant_tile_t<uint8_t, 1, T_COLS_T> : quant_tile_t<uint8_t, 2, T_COLS_T>)
                                   : (cols % 128 ? quant_tile_t<uint8_t, 1, T_BLOCK_T> : quant_tile_t<uint8_t, 2, T_BLOCK_T>);
-    f(nullptr, 0, src, n_rows, out, rows, cols, st);
-    return ops_launched();
+    return f(nullptr, 0, src, n_rows, out, rows, cols, st);
   }
   if (!ops_dtype_ok(dtype) || !ops_mat_ok(x, dtype, ldx, cols)) return MT_ERR_ARG;
   const int v = ops_mode(ops_vec(x, dtype, ldx), cols, 128);
   const Src8 none{};
   auto f = out->block_rows == 1 ? OPS_PICK(quant_tile_t, dtype, v, OPS_COMMA T_COLS_T)
                                 : OPS_PICK(quant_tile_t, dtype, v, OPS_COMMA T_BLOCK_T);
-  f(x, ldx, none, n_rows, out, rows, cols, st);
-  return ops_launched();
+  return f(x, ldx, none, n_rows, out, rows, cols, st);
 }
 
 int32_t mt_dequant8(const mt_mat8* a, const int32_t* n_rows, void* out, int32_t dtype, int64_t ldo, void* stream) {
@@ -557,8 +544,7 @@ int32_t mt_dequant8(const mt_mat8* a, const int32_t* n_rows, void* out, int32_t 
   cudaStream_t st = (cudaStream_t)stream;
   const int64_t part = a->halves ? a->cols / 2 : a->cols;
   const int vec = ops_vec(out, dtype, ldo), v = ops_mode(a->halves ? part_vec(vec, dtype, part) : vec, part, 256);
-  OPS_PICK(dequant_t, dtype, v)(a, n_rows, out, ldo, st);
-  return ops_launched();
+  return OPS_PICK(dequant_t, dtype, v)(a, n_rows, out, ldo, st);
 }
 
 int32_t mt_swiglu8(const void* gu, int32_t dtype, int64_t ldgu, const int32_t* n_rows, const mt_mat8* act,
@@ -573,8 +559,7 @@ int32_t mt_swiglu8(const void* gu, int32_t dtype, int64_t ldgu, const int32_t* n
   if (!ops_mat_ok(gu, dtype, ldgu, 2 * act->cols)) return MT_ERR_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   const int v = ops_mode(part_vec(ops_vec(gu, dtype, ldgu), dtype, act->cols), act->cols, 256);
-  OPS_PICK(swiglu_t, dtype, v)(gu, ldgu, n_rows, act, saved, st);
-  return ops_launched();
+  return OPS_PICK(swiglu_t, dtype, v)(gu, ldgu, n_rows, act, saved, st);
 }
 
 int32_t mt_swiglu8_bwd(const void* dact, int32_t dtype, int64_t ldda, const mt_mat8* saved, const int32_t* n_rows,
@@ -590,8 +575,7 @@ int32_t mt_swiglu8_bwd(const void* dact, int32_t dtype, int64_t ldda, const mt_m
   cudaStream_t st = (cudaStream_t)stream;
   const int vec = ops_least(ops_vec(dact, dtype, ldda), ops_least(ops_vec(dgu, dtype, lddgu), act ? ops_vec(act, dtype, ldact) : 2));
   const int v = ops_mode(part_vec(vec, dtype, F), F, 256);
-  OPS_PICK(swiglu_bwd_t, dtype, v)(dact, ldda, saved, n_rows, dgu, lddgu, act, ldact, st);
-  return ops_launched();
+  return OPS_PICK(swiglu_bwd_t, dtype, v)(dact, ldda, saved, n_rows, dgu, lddgu, act, ldact, st);
 }
 
 }  // extern "C"

@@ -37,7 +37,7 @@ __device__ __forceinline__ void ro_offsets(const int* cnt, int E, int* offs) {
 // Assignments a, a + 32, a + 64, a + 96; -1 from w1 on.
 __device__ __forceinline__ void ro_load(const int* idx, long long a, long long w1, int* v) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = a + 32 * j < w1 ? __ldg(idx + a + 32 * j) : -1;
+  for (int j = 0; j < 4; ++j) v[j] = a + 32 * j < w1 ? idx[a + 32 * j] : -1;
 }
 
 // Lanes of the warp whose assignment names the same expert.
@@ -124,6 +124,7 @@ __device__ __forceinline__ int ro_remote(const int* p, int cta) {
 template <int NC>
 __global__ void __launch_bounds__(1024) ro_sort(const int* idx, int n, int E, long long rows, int* offs, int* perm,
                                                 int* row, int* status) {
+  ops_begin();
   __shared__ RoSmem<32> s;
   const int tid = threadIdx.x, warp = tid >> 5, cta = blockIdx.x;
   const int span = ((n + 32 * NC - 1) / (32 * NC) + 31) & ~31;
@@ -173,6 +174,7 @@ __global__ void __launch_bounds__(1024) ro_sort(const int* idx, int n, int E, lo
 // Many: every CTA counts its chunk, then every CTA sums the counts before its
 // own and places it.
 __global__ void __launch_bounds__(256) ro_hist(const int* idx, long long n, int E, int* hist, int* status) {
+  ops_begin();
   __shared__ RoSmem<8> s;
   const long long a0 = (long long)blockIdx.x * RO_CHUNK + (threadIdx.x >> 5) * (RO_CHUNK / 8);
   const long long a1 = a0 + RO_CHUNK / 8 < n ? a0 + RO_CHUNK / 8 : n;
@@ -186,6 +188,7 @@ __global__ void __launch_bounds__(256) ro_hist(const int* idx, long long n, int 
 }
 __global__ void __launch_bounds__(256) ro_scatter(const int* idx, long long n, int E, long long rows, const int* hist,
                                                   int* offs, int* perm, int* row, int* status) {
+  ops_begin();
   __shared__ RoSmem<8> s;
   __shared__ int part[2][4][RO_E];
   const int tid = threadIdx.x, e = tid & (RO_E - 1), p = tid / RO_E;
@@ -194,7 +197,7 @@ __global__ void __launch_bounds__(256) ro_scatter(const int* idx, long long n, i
   int all = 0, mine = 0;
 #pragma unroll 8
   for (int c = p; c < (int)gridDim.x; c += 4) {
-    const int h = __ldg(hist + (long long)c * RO_E + e);
+    const int h = hist[(long long)c * RO_E + e];
     all += h;
     if (c < (int)blockIdx.x) mine += h;
   }
@@ -231,9 +234,9 @@ __global__ void __launch_bounds__(256) ro_scatter(const int* idx, long long n, i
 __device__ __forceinline__ long long pad_row(long long i, int E, const int* offs, const int* perm, long long rows) {
   const int e = (int)(i >> 7);
   if (e >= E) return -1;
-  const long long r = (long long)__ldg(offs + e + 1) - 128 + (i & 127);
-  if (r < 0 || r < __ldg(offs + e) || r >= rows) return -1;
-  return __ldg(perm + r) < 0 ? r : -1;
+  const long long r = (long long)offs[e + 1] - 128 + (i & 127);
+  if (r < 0 || r < offs[e] || r >= rows) return -1;
+  return perm[r] < 0 ? r : -1;
 }
 
 // A warp holds one token's chunk of 256 columns (8 per lane) and writes it to
@@ -244,6 +247,7 @@ template <class T, int VEC>
 __global__ void __launch_bounds__(256) dispatch_k(const T* x, long long ldx, long long tokens, int width, int K,
                                                   int E, const int* offs, const int* perm, const int* row,
                                                   long long rows, T* out, long long ldo, long long tok_ctas) {
+  ops_begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float zero[8] = {};
   if (blockIdx.x >= tok_ctas) {
@@ -255,7 +259,7 @@ __global__ void __launch_bounds__(256) dispatch_k(const T* x, long long ldx, lon
   }
   const long long t = (long long)blockIdx.x * 8 + warp;
   if (t >= tokens) return;
-  const int mine = lane < K ? __ldg(row + t * K + lane) : -1;
+  const int mine = lane < K ? row[t * K + lane] : -1;
   for (int c = lane * 8 + 256 * (int)blockIdx.y; c - lane * 8 < width; c += 256 * (int)gridDim.y) {
     Raw8<T> v;
     v.template load<VEC>(x + t * ldx, c, width);
@@ -273,6 +277,7 @@ __global__ void __launch_bounds__(256) dispatch8_k(const T* x, long long ldx, lo
                                                    int E, const int* offs, const int* perm, const int* row,
                                                    long long rows, uint8_t* q, long long ldq, uint8_t* sc,
                                                    long long lds, long long tok_ctas) {
+  ops_begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x >= tok_ctas) {
     const long long r = pad_row((blockIdx.x - tok_ctas) * 8 + warp, E, offs, perm, rows);
@@ -285,7 +290,7 @@ __global__ void __launch_bounds__(256) dispatch8_k(const T* x, long long ldx, lo
   }
   const long long t = (long long)blockIdx.x * 8 + warp;
   if (t >= tokens) return;
-  int mine = lane < K ? __ldg(row + t * K + lane) : -1;
+  int mine = lane < K ? row[t * K + lane] : -1;
   if (mine >= rows) mine = -1;
   for (int c0 = 256 * CH * (int)blockIdx.y; c0 < width; c0 += 256 * CH * (int)gridDim.y) {
     Raw8<T> x8[CH];
@@ -319,12 +324,13 @@ template <class T, int VEC, int KM, int CH>
 __global__ void __launch_bounds__(256) combine_k(const T* y, long long ldy, long long rows, const int* row,
                                                  const float* w, long long tokens, int K, int width, T* out,
                                                  long long ldo) {
+  ops_begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long t = (long long)blockIdx.x * 8 + warp;
   if (t >= tokens) return;
-  int mine = lane < K ? __ldg(row + t * K + lane) : -1;
+  int mine = lane < K ? row[t * K + lane] : -1;
   if (mine >= rows) mine = -1;
-  const float wm = lane < K ? (w ? __ldg(w + t * K + lane) : 1.f) : 0.f;
+  const float wm = lane < K ? (w ? w[t * K + lane] : 1.f) : 0.f;
   for (int c0 = 256 * CH * (int)blockIdx.y; c0 < width; c0 += 256 * CH * (int)gridDim.y) {
     Raw8<T> v[KM][CH];
 #pragma unroll
@@ -361,6 +367,7 @@ __global__ void __launch_bounds__(256) combine_bwd_k(const T* dout, long long ld
                                                      const int* offs, const int* perm, const int* row, long long rows,
                                                      const float* w, long long tokens, int K, int E, int width,
                                                      T* dy, long long lddy, float* dw, long long tok_ctas) {
+  ops_begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float zero[8] = {};
   if (blockIdx.x >= tok_ctas) {
@@ -371,9 +378,9 @@ __global__ void __launch_bounds__(256) combine_bwd_k(const T* dout, long long ld
   }
   const long long t = (long long)blockIdx.x * 8 + warp;
   if (t >= tokens) return;
-  int mine = lane < K ? __ldg(row + t * K + lane) : -1;
+  int mine = lane < K ? row[t * K + lane] : -1;
   if (mine >= rows) mine = -1;
-  const float wm = lane < K ? __ldg(w + t * K + lane) : 0.f;
+  const float wm = lane < K ? w[t * K + lane] : 0.f;
   float dot[KM] = {};
   for (int c0 = 0; c0 < width; c0 += 256 * CH) {
     Raw8<T> d8[CH], v8[KM][CH];
@@ -438,8 +445,7 @@ int dispatch_t(const void* x, int64_t ldx, int64_t tokens, int64_t width, int K,
   const long long tc = (tokens + 7) / 8;
   const dim3 grid((unsigned)(tc + E * 16), col_chunks(width));
   auto k = vec == 2 ? dispatch_k<T, 2> : vec ? dispatch_k<T, 1> : dispatch_k<T, 0>;
-  k<<<grid, 256, 0, st>>>((const T*)x, ldx, tokens, (int)width, K, E, offs, perm, row, rows, (T*)out, ldo, tc);
-  return ops_launched();
+  return ops_launch(k, grid, 256, 0, st, 1, (const T*)x, ldx, tokens, (int)width, K, E, offs, perm, row, rows, (T*)out, ldo, tc);
 }
 template <class T, int VEC>
 int dispatch8_t(const void* x, int64_t ldx, int64_t tokens, int K, int E, const int* offs, const int* perm,
@@ -450,9 +456,8 @@ int dispatch8_t(const void* x, int64_t ldx, int64_t tokens, int K, int E, const 
   const bool wide = tokens * ((o->cols + 255) / 256) > 152 * 16;
   const dim3 grid((unsigned)(tc + E * 16), col_chunks(wide ? (o->cols + CH - 1) / CH : o->cols));
   auto k = wide ? dispatch8_k<T, VEC, CH> : dispatch8_k<T, VEC, 1>;
-  k<<<grid, 256, 0, st>>>((const T*)x, ldx, tokens, (int)o->cols, K, E, offs, perm, row, o->rows, (uint8_t*)o->codes,
+  return ops_launch(k, grid, 256, 0, st, 1, (const T*)x, ldx, tokens, (int)o->cols, K, E, offs, perm, row, o->rows, (uint8_t*)o->codes,
                           o->ld, (uint8_t*)o->scales, o->lds, tc);
-  return ops_launched();
 }
 template <class T, int VEC>
 int combine_t(const void* y, int64_t ldy, int64_t rows, const int* row, const float* w, int64_t tokens, int K,
@@ -462,8 +467,7 @@ int combine_t(const void* y, int64_t ldy, int64_t rows, const int* row, const fl
   const int64_t per = K <= 2 ? (F ? 2 : 4) : K <= 4 ? (F ? 1 : 2) : 1;
   const dim3 grid((unsigned)((tokens + 7) / 8), col_chunks((width + per - 1) / per));
   auto k = K <= 2 ? combine_k<T, VEC, 2, F ? 2 : 4> : K <= 4 ? combine_k<T, VEC, 4, F ? 1 : 2> : combine_k<T, VEC, 8, 1>;
-  k<<<grid, 256, 0, st>>>((const T*)y, ldy, rows, row, w, tokens, K, (int)width, (T*)out, ldo);
-  return ops_launched();
+  return ops_launch(k, grid, 256, 0, st, 1, (const T*)y, ldy, rows, row, w, tokens, K, (int)width, (T*)out, ldo);
 }
 template <class T, int VEC>
 int combine_bwd_t(const void* dout, int64_t lddo, const void* y, int64_t ldy, const int* offs, const int* perm,
@@ -474,9 +478,8 @@ int combine_bwd_t(const void* dout, int64_t lddo, const void* y, int64_t ldy, co
   auto k = K <= 2   ? combine_bwd_k<T, VEC, 2, F ? 2 : 3>
            : K <= 4 ? combine_bwd_k<T, VEC, 4, F ? 1 : 2>
                     : combine_bwd_k<T, VEC, 8, 1>;
-  k<<<(unsigned)(tc + E * 16), 256, 0, st>>>((const T*)dout, lddo, (const T*)y, ldy, offs, perm, row, rows, w, tokens,
+  return ops_launch(k, (unsigned)(tc + E * 16), 256, 0, st, 1, (const T*)dout, lddo, (const T*)y, ldy, offs, perm, row, rows, w, tokens,
                                              K, E, (int)width, (T*)dy, lddy, dw, tc);
-  return ops_launched();
 }
 
 // checks of the routing triple as the moves read it
@@ -516,36 +519,20 @@ int32_t mt_route_order(const int32_t* idx, int64_t n_tokens, int32_t top_k, int3
   if (!ops_aligned(idx, 4) || !ops_aligned(offs, 4) || !ops_aligned(perm, 4) || !ops_aligned(row, 4) ||
       !ops_aligned(status, 4))
     return MT_ERR_ARG;
+  if (!ws || !ops_aligned(ws, 16)) return MT_ERR_ARG;
+  if (ws_bytes < mt_route_ws_bytes(n_tokens, top_k, n_experts)) return MT_ERR_ARENA_SMALL;
   const int64_t n = n_tokens * top_k, rows = route_rows(n_tokens, top_k, n_experts);
   cudaStream_t s = (cudaStream_t)stream;
   if (n <= RO_SMALL) {
-    ro_sort<1><<<1, 1024, 0, s>>>(idx, (int)n, n_experts, rows, offs, perm, row, status);
-    return ops_launched();
+    return ops_launch(ro_sort<1>, 1, 1024, 0, s, 1, idx, n, n_experts, rows, offs, perm, row, status);
   }
   if (n <= RO_CLUSTER) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(RO_CTAS);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = s;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = RO_CTAS;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, ro_sort<RO_CTAS>, (const int*)idx, (int)n, (int)n_experts, (long long)rows, (int*)offs,
-                           (int*)perm, (int*)row, (int*)status) != cudaSuccess) {
-      cudaGetLastError();
-      return MT_ERR_LAUNCH;
-    }
-    return MT_OK;
+    return ops_launch(ro_sort<RO_CTAS>, RO_CTAS, 1024, 0, s, RO_CTAS, idx, n, n_experts, rows, offs, perm, row, status);
   }
-  if (!ws || !ops_aligned(ws, 16)) return MT_ERR_ARG;
-  if (ws_bytes < mt_route_ws_bytes(n_tokens, top_k, n_experts)) return MT_ERR_ARENA_SMALL;
   const unsigned chunks = (unsigned)((n + RO_CHUNK - 1) / RO_CHUNK);
-  ro_hist<<<chunks, 256, 0, s>>>(idx, n, n_experts, (int*)ws, status);
-  ro_scatter<<<chunks, 256, 0, s>>>(idx, n, n_experts, rows, (const int*)ws, offs, perm, row, status);
-  return ops_launched();
+  const int rc = ops_launch(ro_hist, chunks, 256, 0, s, 1, idx, n, n_experts, (int*)ws, status);
+  if (rc) return rc;
+  return ops_launch(ro_scatter, chunks, 256, 0, s, 1, idx, n, n_experts, rows, (const int*)ws, offs, perm, row, status);
 }
 
 int32_t mt_dispatch(const void* x, int32_t dtype, int64_t ldx, int64_t n_tokens, int64_t width, int32_t top_k,

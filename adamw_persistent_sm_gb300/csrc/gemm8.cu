@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(G8_THREADS, 1) gemm8_k(const __grid_constant__
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  ops_begin();
+  ops_wait();          // (and no early release: kernels that move in as its CTAs end cost 5 to 15 us)
   // segment starts, kept inside the operands and on block boundaries whatever
   // they hold (a TMA coordinate has to be a multiple of 16)
   if (g.mode != G8_DENSE && tid <= g.nseg) {

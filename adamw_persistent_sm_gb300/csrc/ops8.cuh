@@ -18,9 +18,10 @@
 // without effect where the launch does not ask for it, see ops_launch).  What a
 // kernel reads may thus be written while it is already resident: plain loads, no
 // read-only ones.
+__device__ __forceinline__ void ops_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void ops_begin() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  ops_wait();
 }
 
 // n_rows of the C ABI: rows below *p (clamped), or all of them

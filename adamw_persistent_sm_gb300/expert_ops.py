@@ -159,6 +159,12 @@ class Tensor8:
             raise IndexError("not a stack of matrices")
         return Tensor8(self.codes[i], self.scales[i], self.cols, self.block_rows, self.halves)
 
+    def part(self, lo: int, hi: int) -> "Tensor8":
+        """Rows lo..hi-1 of a matrix with block_rows 1 (a view)."""
+        if self.codes.dim() != 2 or self.block_rows != 1 or not 0 <= lo <= hi <= self.rows:
+            raise IndexError(f"rows {lo}:{hi} of {self.shape}, block_rows {self.block_rows}")
+        return Tensor8(self.codes[lo:hi], self.scales[lo:hi], self.cols, 1, self.halves)
+
 
 def empty8(rows: int, cols: int, device="cuda", block_rows: int = 1, batch: int | None = None,
            halves: bool = False) -> Tensor8:

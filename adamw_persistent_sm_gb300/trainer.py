@@ -116,6 +116,21 @@ class MoETrainer:
                             tok, hp, self.arena.data_ptr(), self.arena_bytes, self.stream)
         _check(st, "mt_debug_run")
 
+    # ---- one layer on the stand-alone operators --------------------------------
+    def expert_layer8(self, slot: int = 0, n_tokens: int | None = None):
+        """Weight slot `slot`'s experts as an :class:`experts8.ExpertLayer8`
+        (8-bit products outside the update kernel), quantised from the current
+        weights; :meth:`expert_grads` gives the matching gradient views."""
+        from .experts8 import ExpertLayer8
+        src = self.shadow if self.shadow is not None else self.params
+        return ExpertLayer8(*(self.view(src, n)[slot] for n in ("w_gate", "w_up", "w_down")),
+                            n_tokens=self.cfg.batch * self.cfg.seq if n_tokens is None else n_tokens,
+                            top_k=self.cfg.top_k, dtype=torch.bfloat16 if self.bf16 else torch.float32)
+
+    def expert_grads(self, slot: int = 0) -> tuple:
+        """The gradient buffer's w_gate, w_up and w_down of a weight slot."""
+        return tuple(self.view(self.grads, n)[slot] for n in ("w_gate", "w_up", "w_down"))
+
     def outputs(self) -> B.mt_outputs:
         return B.mt_read_outputs(self.arena.data_ptr(), self.stream)
 

@@ -543,7 +543,48 @@ def run_trace(args, cfg):
         print(f"    {k_:16s} {by[k_]:9.3f}")
 
 
-OPS = ("attn_fwd", "attn_bwd", "router", "lm_ce", "adamw")
+OPS = ("attn_fwd", "attn_bwd", "router", "lm_ce", "adamw", "experts8")
+
+
+def run_experts8(args, cfg):
+    """--op experts8: one expert layer with 8-bit products (the stand-alone
+    operators), forward and backward on the workload's tokens, timed with CUDA
+    events.  Prints ms and the products' rate for each direction."""
+    import torch
+    from adamw_persistent_sm_gb300 import binding as B, expert_ops
+    from adamw_persistent_sm_gb300.trainer import MoETrainer
+    if args.batch:
+        cfg = cfg.replace(batch=args.batch)
+    cfg = cfg.replace(n_layers=1, n_unique_layers=0)
+    B.load(build_if_missing=True)
+    tr = MoETrainer(cfg, "cuda:0")
+    g = torch.Generator(device="cuda").manual_seed(11)
+    tr.params.normal_(0.0, 0.02, generator=g)
+    tr.sync_shadow()
+    layer, grads = tr.expert_layer8(), tr.expert_grads()
+    T, d, K = cfg.tokens_per_micro, cfg.d_model, cfg.top_k
+    x = torch.randn((T, d), device="cuda", generator=g).to(layer.dtype)
+    dout = (torch.randn((T, d), device="cuda", generator=g) * 1e-3).to(layer.dtype)
+    idx = torch.rand((T, cfg.n_experts), device="cuda", generator=g).topk(K, 1).indices.to(torch.int32).contiguous()
+    w = torch.softmax(torch.randn((T, K), device="cuda", generator=g), 1)
+    flops = 2.0 * T * K * 3 * cfg.d_ff * d
+    res = {"op": "experts8", "config": cfg.name, "batch": cfg.batch, "launches": args.steps,
+           "note": "products of one expert layer, 6 T K F d FLOP forward and twice that backward"}
+    for name, fn, work in (("forward", lambda: layer.forward(x, idx, w), flops),
+                           ("backward", lambda: layer.backward(dout, grads), 2 * flops)):
+        for _ in range(max(1, args.warmup)):
+            fn()
+        torch.cuda.synchronize()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for _ in range(args.steps):
+            fn()
+        e1.record()
+        torch.cuda.synchronize()
+        ms = e0.elapsed_time(e1) / max(1, args.steps)
+        res[name] = {"ms": ms, "tflops": work / ms / 1e9, "frac_of_measured_bf16_peak": work / ms / 1e9 / load_peaks()["bf16"]}
+    expert_ops.check()
+    print(json.dumps(res))
 
 
 def run_op(args, cfg):
@@ -674,7 +715,8 @@ def main():
     ap.add_argument("--cpu-tokens", type=int, default=1024)
     ap.add_argument("--ref-tokens", type=int, default=256)
     ap.add_argument("--trace", action="store_true", help="print the per-job time of one update")
-    ap.add_argument("--op", choices=OPS, help="time one step of the update alone (single-op kernel)")
+    ap.add_argument("--op", choices=OPS, help="time one step of the update alone (single-op kernel); experts8: the expert layer "
+                                                "on the stand-alone 8-bit operators")
     ap.add_argument("--batch", type=int, default=0, help="--op: override the workload's batch")
     ap.add_argument("--layers", type=int, default=0, help="--op: override the workload's layer count")
     ap.add_argument("--no-extra", action="store_true",
@@ -695,6 +737,9 @@ def main():
         return
     if args.trace:
         run_trace(args, cfg)
+        return
+    if args.op == "experts8":
+        run_experts8(args, cfg)
         return
     if args.op:
         run_op(args, cfg)

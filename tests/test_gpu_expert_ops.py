@@ -363,6 +363,100 @@ def test_gemm_reduce(ops, offs, m, n):
     ops.check()
 
 
+def product64(got, a, b, k, dtype, before=None):
+    """product_close on the device, for sizes that the host takes too long for."""
+    av, bv = (torch.from_numpy(R.value8(t)).cuda() for t in (a, b))
+    ref, mag = av @ bv.T, av.abs() @ bv.abs().T
+    if before is not None:
+        ref, mag = ref + before, mag + before.abs()
+    bound = (k + 2) * 2 * U32 * mag + HALF_STEP[dtype] * ref.abs() * (1 + 1e-3)
+    bad = (got.double() - ref).abs() > bound
+    assert not bad.any(), (int(bad.sum()), float((got.double() - ref).abs().max()))
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("m,n,k", [(2500, 4100, 300), (2560, 4096, 640), (5000, 2049, 129)])
+def test_gemm_wide_tiles(ops, m, n, k, block_rows, dt):
+    """Products large enough for 256-column tiles, edges on both sides."""
+    a = ops.quant8(rnd(1, m, k))
+    b = ops.quant8(rnd(2, n, k, std=0.02), block_rows=block_rows)
+    product64(ops.gemm8(a, b, dtype=DT[dt]), a, b, k, DT[dt])
+    buf = torch.full((m, n + 4), 7.0, dtype=DT[dt], device="cuda")
+    product64(ops.gemm8(a, b, out=buf[:, 3:3 + n]), a, b, k, DT[dt])
+    assert (buf[:, :3] == 7).all() and (buf[:, 3 + n:] == 7).all()
+    if dt == "fp32":
+        c = rnd(3, m, n)
+        before = c.double()
+        product64(ops.gemm8(a, b, out=c, accumulate=True), a, b, k, DT[dt], before)
+    ops.check()
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 70, 4097), (130, 300, 9000), (3000, 4200, 4500)])
+def test_gemm_long_sums(ops, m, n, k):
+    """Reductions beyond the 4096 that tensor memory sums: rounded fp32 additions
+    join the parts, so all of them stay within 2^-21 of the sum of magnitudes (the
+    parts' cut-off sums: 128 additions of at most 2^-23 each on a growing sum)."""
+    a, b = ops.quant8(rnd(1, m, k) + 0.5), ops.quant8(rnd(2, n, k) + 0.5, block_rows=1)
+    c = ops.gemm8(a, b, dtype=torch.float32).double()
+    av, bv = (torch.from_numpy(R.value8(t)).cuda() for t in (a, b))
+    assert ((c - av @ bv.T).abs() <= 128 * 2.0 ** -23 / 2 * (av.abs() @ bv.abs().T)).all()
+    ops.check()
+
+
+def test_gemm_reduce_long_segments_and_many(ops):
+    """Segments of zero to 20000 columns and sixty-four of them."""
+    p, m, n, e = 40960, 260, 300, 64
+    g = np.random.default_rng(1)
+    blocks = g.multinomial(320 - 157, [1.0 / e] * e)
+    blocks[5], blocks[9] = 0, blocks[9] + 157
+    offs = np.concatenate([[0], np.cumsum(blocks)]) * 128
+    a, b = ops.quant8_t(rnd(1, p, m)), ops.quant8_t(rnd(2, p, n))
+    out = ops.gemm8_reduce(a, b, torch.from_numpy(offs.astype(np.int32)).cuda())
+    av, bv = (torch.from_numpy(R.value8(t)).cuda() for t in (a, b))
+    for i in range(e):
+        s = slice(int(offs[i]), int(offs[i + 1]))
+        ref, mag = av[:, s] @ bv[:, s].T, av[:, s].abs() @ bv[:, s].abs().T
+        assert ((out[i].double() - ref).abs() <= (s.stop - s.start + 2) * 2 * U32 * mag).all(), i
+    ops.check()
+
+
+def test_gemm_by_expert_wide(ops):
+    """Many rows over sixteen experts, some without any, in wide tiles."""
+    g = np.random.default_rng(2)
+    e, n, k = 16, 1030, 200
+    blocks = g.integers(0, 14, e)
+    blocks[3] = blocks[15] = 0
+    offs = np.concatenate([[0], np.cumsum(blocks)]) * 128
+    rows = int(offs[-1]) + 300
+    a = ops.quant8(rnd(1, rows, k))
+    a.codes[int(offs[-1]):] = 0x7F
+    b = ops.quant8(rnd(2, e, n, k, std=0.02), 128)
+    out = torch.full((rows, n), 7.0, device="cuda")
+    ops.gemm8(a, b, out=out, offs=torch.from_numpy(offs.astype(np.int32)).cuda())
+    for i in range(e):
+        s = slice(int(offs[i]), int(offs[i + 1]))
+        if s.stop > s.start:
+            product64(out[s], a.part(s.start, s.stop), b[i], k, torch.float32)
+    assert (out[int(offs[-1]):] == 7).all()
+    ops.check()
+
+
+def test_gemm_scale_rows_of_any_stride(ops):
+    """Scale bytes whose rows start anywhere (read by bytes) and by words agree."""
+    a, b = ops.quant8(rnd(1, 300, 900)), ops.quant8(rnd(2, 200, 900))
+    want = ops.gemm8(a, b, dtype=torch.float32)
+    for t in (0, 1):
+        m = (a, b)[t]
+        buf = torch.empty(m.rows * 9 + 1, dtype=torch.uint8, device="cuda")
+        odd = buf[1:].view(m.rows, 9)[:, :8]
+        odd.copy_(m.scales)
+        o = ops.Tensor8(m.codes, odd, m.cols)
+        got = ops.gemm8(o if t == 0 else a, o if t else b, dtype=torch.float32)
+        assert torch.equal(got, want)
+    ops.check()
+
+
 def test_gemm_keeps_nan_and_large_scales_in_their_rows(ops):
     x = rnd(1, 200, 300)
     x[17, 5] = float("nan")

@@ -1,0 +1,210 @@
+"""The expert layer on the 8-bit operators: every step of a forward and a
+backward pass against float64 on the device's own operands (so that each
+bound is one step's), the trainer's path to it, and its agreement with the
+update kernel's router."""
+import numpy as np
+import pytest
+import torch
+
+import expert_ref as R
+import moe_inputs as mi
+
+pytestmark = pytest.mark.gpu
+
+U32 = 2.0 ** -24
+STEP = {torch.float32: 0.0, torch.bfloat16: 2.0 ** -8}
+
+
+def rnd(seed, *shape, std=1.0, dtype=torch.float32):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * std).to(dtype).cuda()
+
+
+def near(got, want, bound):
+    got = R.as64(got)
+    assert np.isfinite(got).all()
+    bad = np.abs(got - want) > bound
+    assert not bad.any(), (int(bad.sum()), float(np.abs(got - want).max()))
+
+
+def product(got, a, b, dtype, before=0.0):
+    """Half a step of the output and one step (2 U32) per addition of the sum of magnitudes."""
+    ref = a @ b.T + before
+    near(got, ref, (a.shape[1] + 2) * 2 * U32 * (np.abs(a) @ np.abs(b).T + np.abs(before)) + STEP[dtype] * 1.001 * np.abs(ref))
+
+
+def held(x, **kw):
+    """What x holds after quantisation."""
+    q, s = R.quant(x, **kw)
+    return R.value(q, s, x.shape[1], **{k: v for k, v in kw.items()})
+
+
+def routing(t, k, e, seed):
+    g = np.random.default_rng(seed)
+    idx = np.stack([g.permutation(e)[:k] for _ in range(t)]).astype(np.int32)
+    idx[g.random(t) < 0.2] = -1
+    idx[0, :] = e - 1                       # the same expert in every slot
+    return idx
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("t,k,e,d,f", [(1, 2, 4, 64, 48), (150, 2, 5, 256, 136), (700, 3, 4, 128, 64), (90, 1, 1, 100, 20)])
+def test_layer_step_by_step(t, k, e, d, f, dt):
+    from adamw_persistent_sm_gb300 import expert_ops as ops
+    from adamw_persistent_sm_gb300 import ExpertLayer8
+    dtype = torch.bfloat16 if dt == "bf16" else torch.float32
+    wg, wu, wd = rnd(1, e, f, d, std=0.05), rnd(2, e, f, d, std=0.05), rnd(3, e, d, f, std=0.05)
+    layer = ExpertLayer8(wg, wu, wd, t, k, dtype)
+    idx = routing(t, k, e, 4)
+    x, dout, w = rnd(5, t, d, dtype=dtype), rnd(6, t, d, dtype=dtype), torch.softmax(rnd(7, t, k), 1)
+    out = layer.forward(x, torch.from_numpy(idx).cuda(), w)
+    offs, perm, row = R.order(idx, e)
+    end, live = offs[-1], perm >= 0
+    segs = [slice(offs[i], offs[i + 1]) for i in range(e)]
+    x64, d64, w64 = R.as64(x), R.as64(dout), R.as64(w)
+
+    # the weights' blocks, in both orientations
+    wgu = np.concatenate([R.as64(wg), R.as64(wu)], 1)
+    for i in range(e):
+        v = held(wgu[i], block_rows=128)
+        assert np.array_equal(R.value8(layer.w_gu)[i], v)
+        assert np.array_equal(R.value8(layer.w_gu_t)[i], held(wgu[i].T.copy(), block_rows=128))
+        assert np.array_equal(R.value8(layer.w_down_t)[i], held(R.as64(wd)[i].T.copy(), block_rows=128))
+
+    xs = np.zeros((perm.size, d))
+    xs[live] = x64[perm[live] // k]
+    xv = held(xs[:end]) if end else xs[:0]
+    assert np.array_equal(R.value8(layer.xs8)[:end], xv)
+    gu, av, y = R.as64(layer.gu), R.value8(layer.act8), R.as64(layer.y)
+    for i, s in enumerate(segs):
+        product(layer.gu[s], xv[s], R.value8(layer.w_gu)[i], dtype)
+        product(layer.y[s], av[s], R.value8(layer.w_down)[i], dtype)
+    if end:
+        assert np.array_equal(R.value8(layer.saved)[:end], held(gu[:end], halves=True))
+    term = np.where((row >= 0)[:, :, None], np.where(live[:, None], y, 0.0)[np.maximum(row, 0)] * w64[:, :, None], 0.0)
+    near(out, term.sum(1), (k + 1) * U32 * np.abs(term).sum(1) + STEP[dtype] * 1.001 * np.abs(term.sum(1)))
+
+    grads = tuple(rnd(8 + i, *s, std=0.1) for i, s in enumerate(((e, f, d), (e, f, d), (e, d, f))))
+    before = [R.as64(g).copy() for g in grads]
+    dx, dw, got = layer.backward(dout, grads, accumulate=True)
+    assert all(a is b for a, b in zip(got, grads))
+    b = layer._bwd
+    dy = R.as64(b["dy"])
+    ref = np.zeros((perm.size, d))
+    ref[live] = d64[perm[live] // k] * w64.reshape(-1)[perm[live]][:, None]
+    near(b["dy"][:end], ref[:end], (U32 + STEP[dtype] * 1.001) * np.abs(ref[:end]))
+    prod = np.where((row >= 0)[:, :, None], d64[:, None, :] * np.where(live[:, None], y, 0.0)[np.maximum(row, 0)], 0.0)
+    near(dw, prod.sum(-1), (d + 1) * U32 * np.abs(prod).sum(-1))
+    if end == 0:
+        return
+    dyv, dguv = held(dy[:end]), held(R.as64(b["dgu"])[:end])
+    sv = R.value8(layer.saved)[:end]
+    g, u = sv[:, :f], sv[:, f:]
+    s_, da = R.sigmoid(g), R.as64(b["dact"])[:end]
+    tiny, rel = 1e-37, (np.abs(g) + 8) * 2.0 ** -22
+    half = STEP[dtype] * 1.01
+    for out_, ref, mag in ((b["dgu"][:end, :f], da * u * s_ * (1 + g * (1 - s_)), np.abs(da * u) * (s_ + np.abs(g) * s_)),
+                           (b["dgu"][:end, f:], da * g * s_, np.abs(da * g * s_)), (b["act"][:end], g * s_ * u, np.abs(g * s_ * u))):
+        near(out_, ref, rel * mag + half * np.abs(ref) + tiny)
+    dyt, actt = held(dy[:end].T.copy()), held(R.as64(b["act"])[:end].T.copy())
+    dgut, xst = held(R.as64(b["dgu"])[:end].T.copy()), held(xv.T.copy())
+    for i, s in enumerate(segs):
+        product(b["dact"][s], dyv[s], R.value8(layer.w_down_t)[i], dtype)
+        product(b["dxs"][s], dguv[s], R.value8(layer.w_gu_t)[i], dtype)
+        product(grads[0][i], dgut[:f, s], xst[:, s], torch.float32, before[0][i])
+        product(grads[1][i], dgut[f:, s], xst[:, s], torch.float32, before[1][i])
+        product(grads[2][i], dyt[:, s], actt[:, s], torch.float32, before[2][i])
+    dxs = np.where(live[:, None], R.as64(b["dxs"]), 0.0)
+    term = np.where((row >= 0)[:, :, None], dxs[np.maximum(row, 0)], 0.0)
+    near(dx, term.sum(1), (k + 1) * U32 * np.abs(term).sum(1) + STEP[dtype] * 1.001 * np.abs(term.sum(1)))
+    ops.check()
+
+
+def test_layer_gradients_point_the_right_way():
+    """The whole layer's gradient against float64 autograd of the unquantised
+    layer: 8-bit operands are off by up to 2^-4 each, two at a time over three
+    products in a row; random errors of a third of that stay below a fifth of
+    the gradient's norm (a wrong sign, factor or transposition does not)."""
+    from adamw_persistent_sm_gb300 import ExpertLayer8
+    t, k, e, d, f = 500, 2, 4, 256, 128
+    wg, wu, wd = rnd(1, e, f, d, std=0.05), rnd(2, e, f, d, std=0.05), rnd(3, e, d, f, std=0.05)
+    idx = torch.from_numpy(routing(t, k, e, 4)).cuda()
+    x, dout, w = rnd(5, t, d), rnd(6, t, d), torch.softmax(rnd(7, t, k), 1)
+    layer = ExpertLayer8(wg, wu, wd, t, k, torch.float32)
+    out = layer.forward(x, idx, w)
+    dx, dw, grads = layer.backward(dout)
+    p = [v.double().requires_grad_() for v in (x, w, wg, wu, wd)]
+    ref = torch.zeros(t, d, dtype=torch.float64, device="cuda")
+    for i in range(k):
+        for j in range(e):
+            at = torch.nonzero(idx[:, i] == j)[:, 0]
+            h = p[0][at]
+            act = torch.nn.functional.silu(h @ p[2][j].T) * (h @ p[3][j].T)
+            ref = ref.index_add(0, at, p[1][at, i:i + 1] * (act @ p[4][j].T))
+    ref.backward(dout.double())
+    for got, want in [(out, ref)] + list(zip((dx, dw, *grads), (v.grad for v in p))):
+        rel = float((got.double() - want).norm() / want.norm())
+        assert rel < 0.2, rel
+
+
+def test_trainer_layer_and_router_order():
+    """MoETrainer.expert_layer8 on the update's own routing: the stand-alone
+    order is the update's, its rows are the update's expert inputs in 8 bits,
+    and the gradient views are the trainer's."""
+    from adamw_persistent_sm_gb300 import binding as B
+    from adamw_persistent_sm_gb300 import expert_ops as ops
+    from adamw_persistent_sm_gb300.trainer import MoETrainer
+    cfg = mi.get_config("tiny")
+    tr = MoETrainer(cfg, "cuda:0")
+    tr.load_params(mi.make_params(cfg))
+    toks = torch.as_tensor(mi.make_update_tokens(cfg)[0]).cuda()
+    tr.micro_step(toks, flags=B.MT_FLAG_NO_OPTIMIZER)
+    assert tr.outputs().status == B.MT_OK
+    T, K, E, d = cfg.tokens_per_micro, cfg.top_k, cfg.n_experts, cfg.d_model
+    idx = tr.debug_view(B.MT_VIEW_TOPK_IDX, 1, torch.int32).view(T, K).clone()
+    w = tr.debug_view(B.MT_VIEW_TOPK_W, 1).view(T, K).clone()
+    layer = tr.expert_layer8(1)
+    x = tr.debug_view(B.MT_VIEW_R2, 1).view(T, d).clone()
+    out = layer.forward(x, idx, w)
+    r = layer.route
+    assert torch.equal(r.offs, tr.debug_view(B.MT_VIEW_ROUTE_OFFS, 1, torch.int32))
+    end = int(r.offs[-1])
+    assert torch.equal(r.perm[:end], tr.debug_view(B.MT_VIEW_ROUTE_PERM, 1, torch.int32)[:end])
+    xs = tr.debug_view(B.MT_VIEW_EXPERT_IN, 1).view(-1, d)[:end]
+    assert np.array_equal(R.value8(layer.xs8)[:end], R.value8(ops.quant8(xs.contiguous())))
+    assert out.shape == (T, d) and torch.isfinite(out).all()
+    grads = tr.expert_grads(1)
+    layer.backward(torch.ones(T, d, device="cuda"), grads)
+    assert grads[0].data_ptr() == tr.view(tr.grads, "w_gate")[1].data_ptr() and grads[0].abs().sum() > 0
+    with pytest.raises(RuntimeError):
+        layer.forward(x, idx, w, save=False)
+        layer.backward(torch.ones(T, d, device="cuda"), grads)
+    ops.check()
+
+
+def test_layer_captured_while_an_eager_result_lives():
+    """Forward and backward captured into one graph and replayed give the eager
+    gradients bit for bit, with the eager pass's results still held."""
+    from adamw_persistent_sm_gb300 import ExpertLayer8
+    t, k, e, d, f = 300, 2, 4, 128, 64
+    wg, wu, wd = rnd(1, e, f, d, std=0.05), rnd(2, e, f, d, std=0.05), rnd(3, e, d, f, std=0.05)
+    idx = torch.from_numpy(routing(t, k, e, 4)).cuda()
+    x, dout, w = rnd(5, t, d, dtype=torch.bfloat16), rnd(6, t, d, dtype=torch.bfloat16), torch.softmax(rnd(7, t, k), 1)
+    eager = ExpertLayer8(wg, wu, wd, t, k)
+    out = eager.forward(x, idx, w)
+    dx, dw, grads = eager.backward(dout)
+    layer = ExpertLayer8(wg, wu, wd, t, k)
+    layer.forward(x, idx, w)
+    layer.backward(dout)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o2 = layer.forward(x, idx, w)
+        dx2, dw2, gr2 = layer.backward(dout)
+    for _ in range(3):
+        for v in (o2, dx2, dw2, *gr2):
+            v.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((o2, dx2, dw2, *gr2), (out, dx, dw, *grads)):
+            assert torch.equal(a, b)

@@ -37,7 +37,7 @@ static_assert(G8_REGS_LOAD + 2 * G8_REGS_EPI <= 3 * G8_REGS, "register split exc
 constexpr int G8_A_BYTES = 128 * 128;
 constexpr int G8_WIN = 4096;                 // epilogue window per warp: 32 rows x 128 bytes
 constexpr int G8_STAGES = 4;
-constexpr long long G8_TIMEOUT_NS = 2000000000LL;
+constexpr long long G8_TIMEOUT_NS = 4000000000LL;   // the update's default bound
 enum { G8_DENSE = 0, G8_ROWS = 1, G8_REDUCE = 2 };
 
 constexpr int G8_CHUNK = 32;                 // blocks summed in TMEM
@@ -614,7 +614,7 @@ int launch(G8Args& g, const mt_mat8* a, const mt_mat8* b, int64_t segs, bool f32
   while (bn > 64 && ((int64_t)g.mt * ((g.N + bn - 1) / bn) * batch < sms || g.N <= bn / 2)) bn /= 2;
   g.nt = (g.N + bn - 1) / bn;
   const int64_t tiles = (int64_t)g.mt * g.nt * batch;
-  if (tiles > 0x7fffffff) return MT_ERR_UNSUPPORTED;
+  if (tiles > 0x3fffffff) return MT_ERR_UNSUPPORTED;
   g.ntiles = (int)tiles;
   const bool bcol = b->block_rows == 1;
   rc = mt_encode_map(&g.a, MT_MAP_U8, a->codes, a->cols, a->rows, 1, a->ld, 0, 128, 128);

@@ -8,7 +8,8 @@ constexpr int RO_E = MT_MAX_EXPERTS;
 constexpr int RO_SMALL = 4096;        // assignments that one CTA sorts alone,
 constexpr int RO_CLUSTER = 1 << 18;   // that a cluster of eight sorts,
 constexpr int RO_CTAS = 8;
-constexpr int RO_CHUNK = 2048;        // and per CTA of a grid otherwise
+constexpr int RO_CHUNK = 2048;        // and per CTA of a grid otherwise, or more:
+constexpr int RO_GRID = 1024;         // its CTAs each add up the counts of all
 
 // Expert of an assignment, -1 for none; counts indices out of range.
 __device__ __forceinline__ int ro_expert(int e, int E, int* status) {
@@ -173,11 +174,11 @@ __global__ void __launch_bounds__(1024) ro_sort(const int* idx, int n, int E, lo
 
 // Many: every CTA counts its chunk, then every CTA sums the counts before its
 // own and places it.
-__global__ void __launch_bounds__(256) ro_hist(const int* idx, long long n, int E, int* hist, int* status) {
+__global__ void __launch_bounds__(256) ro_hist(const int* idx, long long n, int chunk, int E, int* hist, int* status) {
   ops_begin();
   __shared__ RoSmem<8> s;
-  const long long a0 = (long long)blockIdx.x * RO_CHUNK + (threadIdx.x >> 5) * (RO_CHUNK / 8);
-  const long long a1 = a0 + RO_CHUNK / 8 < n ? a0 + RO_CHUNK / 8 : n;
+  const long long a0 = (long long)blockIdx.x * chunk + (threadIdx.x >> 5) * (chunk / 8);
+  const long long a1 = a0 + chunk / 8 < n ? a0 + chunk / 8 : n;
   ro_count(s, idx, a0, a1, E, status);
   __syncthreads();
   if (threadIdx.x < RO_E) {
@@ -186,14 +187,14 @@ __global__ void __launch_bounds__(256) ro_hist(const int* idx, long long n, int 
     hist[(long long)blockIdx.x * RO_E + threadIdx.x] = c;
   }
 }
-__global__ void __launch_bounds__(256) ro_scatter(const int* idx, long long n, int E, long long rows, const int* hist,
+__global__ void __launch_bounds__(256) ro_scatter(const int* idx, long long n, int chunk, int E, long long rows, const int* hist,
                                                   int* offs, int* perm, int* row, int* status) {
   ops_begin();
   __shared__ RoSmem<8> s;
   __shared__ int part[2][4][RO_E];
   const int tid = threadIdx.x, e = tid & (RO_E - 1), p = tid / RO_E;
-  const long long a0 = (long long)blockIdx.x * RO_CHUNK + (tid >> 5) * (RO_CHUNK / 8);
-  const long long a1 = a0 + RO_CHUNK / 8 < n ? a0 + RO_CHUNK / 8 : n;
+  const long long a0 = (long long)blockIdx.x * chunk + (tid >> 5) * (chunk / 8);
+  const long long a1 = a0 + chunk / 8 < n ? a0 + chunk / 8 : n;
   int all = 0, mine = 0;
 #pragma unroll 8
   for (int c = p; c < (int)gridDim.x; c += 4) {
@@ -433,6 +434,11 @@ int route_ok(int64_t tokens, int32_t K, int32_t E) {
 int64_t route_rows(int64_t tokens, int32_t K, int32_t E) {
   return (tokens * K + (int64_t)E * 127 + 127) / 128 * 128;
 }
+// assignments per CTA of the grid
+int64_t route_chunk(int64_t n) {
+  const int64_t per = (n + RO_GRID - 1) / RO_GRID;
+  return (per + RO_CHUNK - 1) / RO_CHUNK * RO_CHUNK;
+}
 // chunks of 256 columns as a second grid dimension (a CTA walks on from there)
 unsigned col_chunks(int64_t width) {
   const int64_t n = (width + 255) / 256;
@@ -508,7 +514,7 @@ int64_t mt_route_ws_bytes(int64_t n_tokens, int32_t top_k, int32_t n_experts) {
   const int st = route_ok(n_tokens, top_k, n_experts);
   if (st) return -st;
   const int64_t n = n_tokens * top_k;
-  return n <= RO_CLUSTER ? 16 : (n + RO_CHUNK - 1) / RO_CHUNK * RO_E * 4;
+  return n <= RO_CLUSTER ? 16 : (n + route_chunk(n) - 1) / route_chunk(n) * RO_E * 4;
 }
 
 int32_t mt_route_order(const int32_t* idx, int64_t n_tokens, int32_t top_k, int32_t n_experts, int32_t* offs,
@@ -529,10 +535,12 @@ int32_t mt_route_order(const int32_t* idx, int64_t n_tokens, int32_t top_k, int3
   if (n <= RO_CLUSTER) {
     return ops_launch(ro_sort<RO_CTAS>, RO_CTAS, 1024, 0, s, RO_CTAS, idx, n, n_experts, rows, offs, perm, row, status);
   }
-  const unsigned chunks = (unsigned)((n + RO_CHUNK - 1) / RO_CHUNK);
-  const int rc = ops_launch(ro_hist, chunks, 256, 0, s, 1, idx, n, n_experts, (int*)ws, status);
+  const int64_t chunk = route_chunk(n);
+  const unsigned chunks = (unsigned)((n + chunk - 1) / chunk);
+  const int rc = ops_launch(ro_hist, chunks, 256, 0, s, 1, idx, n, chunk, n_experts, (int*)ws, status);
   if (rc) return rc;
-  return ops_launch(ro_scatter, chunks, 256, 0, s, 1, idx, n, n_experts, rows, (const int*)ws, offs, perm, row, status);
+  return ops_launch(ro_scatter, chunks, 256, 0, s, 1, idx, n, chunk, n_experts, rows, (const int*)ws, offs, perm,
+                    row, status);
 }
 
 int32_t mt_dispatch(const void* x, int32_t dtype, int64_t ldx, int64_t n_tokens, int64_t width, int32_t top_k,

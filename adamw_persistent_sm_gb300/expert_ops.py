@@ -4,7 +4,8 @@ The functions check types, shapes and devices, pass pointers to the C ABI
 (``include/moe_train.h`` has each operator's definition) on the tensors'
 device and its current stream, and return the outputs.  Outputs may be given
 (``out=`` and the like); otherwise they are allocated through torch.  Nothing
-here synchronises: a device-side failure is reported by :func:`check`.
+here synchronises, but for the first call on a device, which has to come before
+a stream capture: a device-side failure is reported by :func:`check`.
 
 * :class:`Route` - tokens sorted by expert and back, and the gradients;
 * :class:`Tensor8`, :func:`quant8`, :func:`quant8_t`, :func:`dequant8`,
@@ -50,6 +51,8 @@ def _status_word(dev: int) -> int:
     """Address of the device's status words."""
     t = _status.get(dev)
     if t is None:
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the first operator, Route or Tensor8 on a device comes before a stream capture")
         t = torch.zeros(2, dtype=torch.int32, device=f"cuda:{dev}")
         torch.cuda.synchronize(dev)         # once per device: zeroed before any other stream uses it
         t = _status[dev] = (t, t.data_ptr())
@@ -147,6 +150,7 @@ class Tensor8:
             raise ValueError(f"scales: rows are contiguous and matrices follow one another (strides {scales.stride()})")
         self.codes, self.scales, self.cols, self.block_rows, self.halves = codes, scales, cols, block_rows, halves
         self.device, self._dev = codes.device, codes.get_device()
+        _status_word(self._dev)
         self.rows, self.batch, self.shape = rows, batch, (*codes.shape[:-1], cols)
         # an empty tensor has no storage: any address stands in for it
         self._mat = B.mt_mat8(codes.data_ptr() or 16, scales.data_ptr() or 16, rows, cols, ld, lds, block_rows,
@@ -343,6 +347,8 @@ class Route:
 
     def _set(self, offs, perm, row):
         self.device, self._dev = offs.device, offs.get_device()
+        if self._dev >= 0:
+            _status_word(self._dev)
         if row.dim() != 2 or offs.dim() != 1 or perm.dim() != 1 or self.device.type != "cuda":
             raise ValueError("offs [E+1], perm [rows] and row [tokens, top_k] on a CUDA device")
         self.n_tokens, self.top_k = row.shape

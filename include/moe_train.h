@@ -435,6 +435,8 @@ enum { MT_DT_FP32 = 0, MT_DT_BF16 = 1 };   /* element types, numbered as MT_PREC
  * nearest even; NaN and infinite elements become the e4m3 NaN.  A power of
  * two loses nothing against a free scale: the codes are floating-point, and
  * scaling, restoring and transposing are then exact.
+ * Products read scale rows by aligned 4-byte words where scales and lds are
+ * multiples of 4, so the buffer is readable to the end of its last word.
  * Limits: rows * batch and cols <= 2^30.
  */
 typedef struct mt_mat8 {

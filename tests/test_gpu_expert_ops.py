@@ -81,6 +81,30 @@ def test_route_order(ops, t, k, e, how):
     ops.check()
 
 
+def test_route_order_of_many_tokens(ops):
+    """Three million assignments (a grid of CTAs with long chunks), against a
+    stable sort on the device."""
+    t, k, e = 400001, 8, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    idx = (torch.rand(t, k, generator=g, device="cuda") ** 2 * e).to(torch.int32)
+    idx[torch.rand(t, generator=g, device="cuda") < 0.1] = -1
+    r = ops.Route(t, k, e).order(idx)
+    a = idx.reshape(-1).long()
+    counts = torch.stack([(a == i).sum() for i in range(e)])
+    offs = torch.cat([torch.zeros(1, dtype=torch.long, device="cuda"), ((counts + 127) // 128 * 128).cumsum(0)])
+    assert torch.equal(r.offs.long(), offs)
+    kept = torch.nonzero(a >= 0)[:, 0]
+    by = kept[torch.sort(a[kept], stable=True).indices]
+    first = torch.cat([torch.zeros(1, dtype=torch.long, device="cuda"), counts.cumsum(0)])[:-1]
+    at = offs[a[by]] + torch.arange(by.numel(), device="cuda") - first[a[by]]
+    perm = torch.full((r.rows,), -1, dtype=torch.long, device="cuda")
+    perm[at] = by
+    row = torch.full_like(a, -1)
+    row[by] = at
+    assert torch.equal(r.perm.long(), perm) and torch.equal(r.row.reshape(-1).long(), row)
+    ops.check()
+
+
 @pytest.mark.parametrize("t", [10, 9000, 140000])
 def test_route_order_reports_bad_indices(ops, t):
     idx = choices(1, t, 2, 8, "even")
@@ -470,6 +494,24 @@ def test_gemm_keeps_nan_and_large_scales_in_their_rows(ops):
     product_close(c[torch.from_numpy(keep).cuda()], R.value8(a)[keep], R.value8(b), torch.float32, 300)
 
 
+@pytest.mark.parametrize("sa,sb", [(127, 127), (1, 127), (0, 127), (254, 1), (254, 0), (64, 64), (200, 60), (255, 127)])
+def test_gemm_extreme_scale_bytes(ops, sa, sb):
+    """Scale bytes over their whole range, where the sum is a normal fp32 number;
+    zero times any finite scale is zero, and 255 is NaN."""
+    a, b = ops.empty8(128, 128), ops.empty8(64, 128)
+    a.codes.fill_(0x38)
+    a.codes[64:] = 0
+    b.codes.fill_(0x38)
+    a.scales.fill_(sa)
+    b.scales.fill_(sb)
+    c = ops.gemm8(a, b, dtype=torch.float32)
+    if sa == 255:
+        assert torch.isnan(c).all()
+    else:
+        assert (c[:64].double() == 128 * 2.0 ** (sa + sb - 254)).all() and (c[64:] == 0).all()
+    ops.check()
+
+
 def test_bad_segment_starts_stay_in_bounds(ops):
     """Starts that no routing makes are cut to block boundaries inside the
     operands: no access leaves a buffer, whatever they hold."""
@@ -541,6 +583,28 @@ def test_swiglu_backward(ops, rows, width, dt):
         for got, ref, mag in ((dgu[:, :width], d * u * s * (1 + g * (1 - s)), np.abs(d * u) * (s + np.abs(g) * s)),
                               (dgu[:, width:], d * g * s, np.abs(d * g * s)), (act, g * s * u, np.abs(g * s * u))):
             close(got, ref, rel * mag + tiny + HALF_STEP[dtype] * np.abs(ref) * (1 + 1e-2))
+
+
+@pytest.mark.parametrize("width", [128, 264, 512])
+def test_swiglu_with_infinities_and_nan(ops, width):
+    """An infinity or NaN spoils its own elements alone: the rest of its block is
+    as without it."""
+    x = gu_values(40, width, torch.float32)
+    bad = x.clone()
+    bad[7, 3], bad[9, width + 5], bad[11, 0], bad[11, width] = float("nan"), float("inf"), float("-inf"), 0.0
+    bad[20] = float("inf")
+    saved = ops.empty8(40, 2 * width, halves=True)
+    act = ops.swiglu8(bad, saved=saved)
+    codes_equal(saved, R.quant(R.as64(bad), halves=True), "saved")
+    v = R.value8(act)
+    clean = x.clone()                              # what the others see: zeros in the spoilt places
+    clean[7, 3] = clean[9, width + 5] = clean[11, 0] = clean[11, width] = 0.0
+    clean[20] = 0.0
+    w = R.value8(ops.swiglu8(clean))
+    spoilt = np.zeros((40, width), bool)
+    spoilt[7, 3] = spoilt[9, 5] = spoilt[11, 0] = True
+    spoilt[20] = True
+    assert np.isnan(v[spoilt]).all() and np.array_equal(v[~spoilt], w[~spoilt])
 
 
 def test_swiglu_backward_by_differences(ops):
@@ -654,6 +718,51 @@ def test_two_streams_at_once(ops):
             chain(ops, *two)
     torch.cuda.synchronize()
     assert torch.equal(one[6][5], w1) and torch.equal(two[6][5], w2)
+    ops.check()
+
+
+def test_streams_joined_by_events(ops):
+    """Each step on a stream of its own, ordered by events alone, gives the
+    result of one stream."""
+    r, idx, x, w8, wd8, w, bufs = chain_inputs(ops, 3, t=3000)
+    want = chain(ops, r, idx, x, w8, wd8, w, bufs).clone()
+    xs8, gu, act8, saved, y, out = bufs
+    torch.cuda.synchronize()
+    steps = (lambda: r.order(idx), lambda: r.dispatch8(x, out=xs8), lambda: ops.gemm8(xs8, w8, out=gu, offs=r.offs),
+             lambda: ops.swiglu8(gu, act=act8, saved=saved, n_rows=r.offs[-1:]),
+             lambda: ops.gemm8(act8, wd8, out=y, offs=r.offs), lambda: r.combine(y, w, out=out))
+    streams = [torch.cuda.Stream() for _ in steps]
+    for _ in range(5):
+        for t in (r.row, gu, y, out, xs8.codes, act8.codes):
+            t.zero_()
+        done = torch.cuda.current_stream().record_event()
+        for s, f in zip(streams, steps):
+            s.wait_event(done)
+            with torch.cuda.stream(s):
+                f()
+                done = s.record_event()
+        torch.cuda.current_stream().wait_event(done)
+        assert torch.equal(out, want)
+    ops.check()
+
+
+def test_steps_mixed_with_other_kernels(ops):
+    """Operators between plain tensor kernels that write what they read and
+    read what they write, many in a row without waiting: no step starts on old
+    data."""
+    t, k, e, d = 4096, 2, 8, 512
+    r = ops.Route(t, k, e)
+    idx = torch.from_numpy(choices(1, t, k, e, "even")).cuda()
+    r.order(idx)
+    x, xs, back = torch.zeros(t, d, device="cuda"), torch.zeros(r.rows, d, device="cuda"), torch.zeros(t, d, device="cuda")
+    for i in range(40):
+        x.fill_(i + 1.0)
+        r.dispatch(x, out=xs)
+        xs.mul_(2.0)
+        r.combine(xs, out=back)
+        assert_later = back.sum() if i % 8 == 7 else None
+        if assert_later is not None:
+            assert float(assert_later) == float(t * d) * k * 2.0 * (i + 1.0)
     ops.check()
 
 

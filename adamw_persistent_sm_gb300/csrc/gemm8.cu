@@ -238,6 +238,53 @@ __device__ __forceinline__ void g8_put<__nv_bfloat16>(uint32_t win, int lane, co
   }
 }
 
+// A window's rows to global memory at any alignment: lane `lane` takes word `lane`
+// of each row.  Element i of row r lies at r * 128 + (((chunk of i) ^ (r & 7)) << 4);
+// rows come by eights, so r & 7 is known and an address costs one exclusive or.
+__device__ __forceinline__ void g8_store_rows(const char* w, float* dst, long long ldc, int rows, int n, int lane,
+                                              int accumulate) {
+  const char* a = w + (lane & 3) * 4;
+  const int q = lane >> 2;
+  float* p = dst + lane;
+  for (int r0 = 0; r0 < rows; r0 += 8, a += 1024) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const float*>(a + j * 128 + ((q ^ j) << 4));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (lane < n && r0 + j < rows) *p = accumulate ? *p + v[j] : v[j];
+      p += ldc;
+    }
+  }
+}
+// bf16: words start at even elements, so a row at an odd address has its first
+// element apart and words one element on; with an odd ldc that is every other row.
+__device__ __forceinline__ void g8_store_rows(const char* w, __nv_bfloat16* dst, long long ldc, int rows, int n,
+                                              int lane, int) {
+  const int odd0 = (int)((uintptr_t)dst >> 1) & 1, odd1 = odd0 ^ (int)(ldc & 1);
+  const char* a = w;
+  uint16_t* p = reinterpret_cast<uint16_t*>(dst) + 2 * lane;
+  for (int r0 = 0; r0 < rows; r0 += 8, a += 1024) {
+    uint32_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int x = 2 * lane + (j & 1 ? odd1 : odd0), y = x < 63 ? x + 1 : 63;
+      v[j] = *reinterpret_cast<const uint16_t*>(a + j * 128 + (((x >> 3) ^ j) << 4) + (x & 7) * 2) |
+             (uint32_t)*reinterpret_cast<const uint16_t*>(a + j * 128 + (((y >> 3) ^ j) << 4) + (y & 7) * 2) << 16;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int odd = j & 1 ? odd1 : odd0, x = 2 * lane + odd;
+      if (r0 + j < rows) {
+        if (x + 1 < n && x < 63) *reinterpret_cast<uint32_t*>(p + odd) = v[j];
+        else if (x < n) p[odd] = (uint16_t)v[j];
+        if (odd && lane == 0) *p = *reinterpret_cast<const uint16_t*>(a + j * 128 + (j << 4));
+      }
+      p += ldc;
+    }
+  }
+}
+
 // BN: columns of a tile.  BCOL: B has a scale per row (column of C) instead of
 // one per 128.  CT: type of C.
 template <int BN, bool BCOL, class CT>
@@ -544,22 +591,12 @@ __global__ void __launch_bounds__(G8_THREADS, 1) gemm8_k(const __grid_constant__
             bulk_commit();
           }
         } else {
-          // rows of any alignment: the window is read back a row at a time
+          // rows of any alignment: the window is read back eight rows at a time and
+          // leaves in 4-byte words
           __syncwarp();
           const int rows = g.M - row0 < 32 ? g.M - row0 : 32;
-          const char* w = gen + (win - base);
-          for (int r = 0; r < rows; ++r) {
-            CT* dst = reinterpret_cast<CT*>(g.out) + ((long long)z * g.M + row0 + r) * g.ldc + col + c;
-#pragma unroll
-            for (int i = 0; i < CW; i += 32) {
-              const int x = i + lane, off = x * (int)sizeof(CT);
-              if (col + c + x < g.N) {
-                const CT e = *reinterpret_cast<const CT*>(w + r * 128 + ((((off >> 4) ^ (r & 7))) << 4) + (off & 15));
-                if constexpr (sizeof(CT) == 4) dst[x] = g.accumulate ? dst[x] + e : e;
-                else dst[x] = e;
-              }
-            }
-          }
+          g8_store_rows(gen + (win - base), reinterpret_cast<CT*>(g.out) + ((long long)z * g.M + row0) * g.ldc + col + c,
+                        g.ldc, rows, g.N - col - c, lane, g.accumulate);
           __syncwarp();
         }
       }

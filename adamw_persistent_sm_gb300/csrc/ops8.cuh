@@ -50,8 +50,10 @@ __device__ __forceinline__ void ops_ld8(const float* p, int c, int n, float* v) 
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     return;
   }
+  if constexpr (VEC != 2) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = c + i < n ? p[c + i] : 0.f;
+    for (int i = 0; i < 8; ++i) v[i] = c + i < n ? p[c + i] : 0.f;
+  }
 }
 __device__ __forceinline__ float ops_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float ops_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
@@ -63,8 +65,10 @@ __device__ __forceinline__ void ops_ld8(const __nv_bfloat16* p, int c, int n, fl
     v[4] = ops_lo(u.z); v[5] = ops_hi(u.z); v[6] = ops_lo(u.w); v[7] = ops_hi(u.w);
     return;
   }
+  if constexpr (VEC != 2) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = c + i < n ? __bfloat162float(p[c + i]) : 0.f;
+    for (int i = 0; i < 8; ++i) v[i] = c + i < n ? __bfloat162float(p[c + i]) : 0.f;
+  }
 }
 __device__ __forceinline__ uint32_t ops_bf2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -83,9 +87,11 @@ __device__ __forceinline__ void ops_st8(float* p, int c, int n, const float* v) 
     *reinterpret_cast<float4*>(p + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
     return;
   }
+  if constexpr (VEC != 2) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (c + i < n) p[c + i] = v[i];
+    for (int i = 0; i < 8; ++i)
+      if (c + i < n) p[c + i] = v[i];
+  }
 }
 template <int VEC>
 __device__ __forceinline__ void ops_st8(__nv_bfloat16* p, int c, int n, const float* v) {
@@ -94,9 +100,11 @@ __device__ __forceinline__ void ops_st8(__nv_bfloat16* p, int c, int n, const fl
         make_uint4(ops_bf2(v[0], v[1]), ops_bf2(v[2], v[3]), ops_bf2(v[4], v[5]), ops_bf2(v[6], v[7]));
     return;
   }
+  if constexpr (VEC != 2) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (c + i < n) p[c + i] = __float2bfloat16_rn(v[i]);
+    for (int i = 0; i < 8; ++i)
+      if (c + i < n) p[c + i] = __float2bfloat16_rn(v[i]);
+  }
 }
 // Eight codes; `v8`: the address is 8-byte aligned.
 template <int VEC>
@@ -105,19 +113,24 @@ __device__ __forceinline__ void ops_st_codes(uint8_t* p, int c, int n, uint2 q, 
     *reinterpret_cast<uint2*>(p + c) = q;
     return;
   }
+  if constexpr (VEC != 2) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (c + i < n) p[c + i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+    for (int i = 0; i < 8; ++i)
+      if (c + i < n) p[c + i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+  }
 }
 template <int VEC>
 __device__ __forceinline__ uint2 ops_ld_codes(const uint8_t* p, int c, int n, bool v8) {
-  if (VEC == 2 || (v8 && c + 8 <= n)) return *reinterpret_cast<const uint2*>(p + c);
   uint2 q = make_uint2(0, 0);
+  if (VEC == 2 || (v8 && c + 8 <= n)) {
+    q = *reinterpret_cast<const uint2*>(p + c);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t b = c + i < n ? p[c + i] : 0;
-    if (i < 4) q.x |= b << (8 * i);
-    else q.y |= b << (8 * (i - 4));
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t b = c + i < n ? p[c + i] : 0;
+      if (i < 4) q.x |= b << (8 * i);
+      else q.y |= b << (8 * (i - 4));
+    }
   }
   return q;
 }
@@ -201,10 +214,12 @@ struct Raw8<__nv_bfloat16> {
       u = *reinterpret_cast<const uint4*>(p + c);
       return;
     }
-    uint32_t h[8];
+    if constexpr (VEC != 2) {
+      uint32_t h[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = c + i < n ? reinterpret_cast<const uint16_t*>(p)[c + i] : 0;
-    u = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+      for (int i = 0; i < 8; ++i) h[i] = c + i < n ? reinterpret_cast<const uint16_t*>(p)[c + i] : 0;
+      u = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    }
   }
   template <int VEC>
   __device__ __forceinline__ void store(__nv_bfloat16* p, int c, int n) const {
@@ -212,10 +227,12 @@ struct Raw8<__nv_bfloat16> {
       *reinterpret_cast<uint4*>(p + c) = u;
       return;
     }
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if constexpr (VEC != 2) {
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < n) reinterpret_cast<uint16_t*>(p)[c + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+      for (int i = 0; i < 8; ++i)
+        if (c + i < n) reinterpret_cast<uint16_t*>(p)[c + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    }
   }
   // bits (fp32) of the largest magnitude
   __device__ __forceinline__ uint32_t top() const {

@@ -36,15 +36,8 @@ _current = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _call(what: str, fn, dev: int, *args) -> None:
-    """One call of the C ABI with the device's current stream, on that device."""
-    if _current() == dev:
-        st = fn(*args, _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, _raw_stream(dev))
-    if st:
-        raise _error(what, st)
+# Every operator makes its device current around the call of the C ABI (a
+# no-op in the usual case) and passes that device's current stream.
 
 
 def _status_word(dev: int) -> int:
@@ -82,15 +75,17 @@ def _device(device) -> torch.device:
 def _mat(t: torch.Tensor, what: str, dev: int, rows: int | None = None, cols: int | None = None,
          dtype=None) -> int:
     """Checks a [rows, cols] matrix with contiguous rows on a device; its row stride."""
-    shape, strides = t.shape, t.stride()
+    shape = t.shape
     if len(shape) != 2 or t.get_device() != dev or dev < 0:
         raise ValueError(f"{what}: expected a matrix on cuda:{dev}, got {tuple(shape)} on {t.device}")
-    if t.dtype not in _DTYPES or (dtype is not None and t.dtype is not dtype):
+    if dtype is not None and t.dtype is not dtype or dtype is None and t.dtype not in _DTYPES:
         raise TypeError(f"{what}: {t.dtype} where {dtype or 'float32 or bfloat16'} is needed")
     r, c = shape
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError(f"{what}: expected [{rows}, {cols}], got [{r}, {c}]")
-    s0, s1 = strides
+    if t.is_contiguous():
+        return c
+    s0, s1 = t.stride()
     if (s1 != 1 and c > 1) or (s0 < c and r > 1):
         raise ValueError(f"{what}: rows must be contiguous and may not overlap (strides {s0}, {s1})")
     return s0 if s0 >= c else c
@@ -207,7 +202,14 @@ def quant8(x: torch.Tensor, block_rows: int = 1, out: Tensor8 | None = None, n_r
         raise ValueError(f"out: expected {tuple(x.shape)} on cuda:{dev}, got {out.shape} on {out.device}")
     if batch == 0:
         return out
-    _call("mt_quant8", B.load().mt_quant8, dev, x.data_ptr(), _DTYPES[x.dtype], ldx, _limit(n_rows, dev), out._ref)
+    here = _current()
+    if here != dev:
+        torch.cuda.set_device(dev)
+    st = B.load().mt_quant8(x.data_ptr(), _DTYPES[x.dtype], ldx, _limit(n_rows, dev), out._ref, _raw_stream(dev))
+    if here != dev:
+        torch.cuda.set_device(here)
+    if st:
+        raise _error("mt_quant8", st)
     return out
 
 
@@ -230,7 +232,14 @@ def quant8_t(x, block_rows: int = 1, out: Tensor8 | None = None, n_rows: torch.T
         raise ValueError(f"out: expected {(*lead, cols, rows)} on cuda:{dev}, got {out.shape} on {out.device}")
     if lead and lead[0] == 0:
         return out
-    _call("mt_quant8_t", B.load().mt_quant8_t, dev, ptr, dt, ldx, src, _limit(n_rows, dev), out._ref)
+    here = _current()
+    if here != dev:
+        torch.cuda.set_device(dev)
+    st = B.load().mt_quant8_t(ptr, dt, ldx, src, _limit(n_rows, dev), out._ref, _raw_stream(dev))
+    if here != dev:
+        torch.cuda.set_device(here)
+    if st:
+        raise _error("mt_quant8_t", st)
     return out
 
 
@@ -241,8 +250,14 @@ def dequant8(a: Tensor8, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor 
     if out is None:
         out = torch.empty(a.shape, dtype=dtype, device=dev)
     ldo = _mat(out, "out", dev, a.rows, a.cols)
-    _call("mt_dequant8", B.load().mt_dequant8, dev, a._ref, _limit(n_rows, dev), out.data_ptr(), _DTYPES[out.dtype],
-          ldo)
+    here = _current()
+    if here != dev:
+        torch.cuda.set_device(dev)
+    st = B.load().mt_dequant8(a._ref, _limit(n_rows, dev), out.data_ptr(), _DTYPES[out.dtype], ldo, _raw_stream(dev))
+    if here != dev:
+        torch.cuda.set_device(here)
+    if st:
+        raise _error("mt_dequant8", st)
     return out
 
 
@@ -259,8 +274,15 @@ def gemm8(a: Tensor8, b: Tensor8, out: torch.Tensor | None = None, offs: torch.T
         out = torch.empty((a.rows, b.rows), dtype=dtype, device=dev)
     ldc = _mat(out, "out", dev, a.rows, b.rows)
     po = 0 if offs is None else _ints(offs, "offs", dev, (seg + 1,))
-    _call("mt_gemm8", B.load().mt_gemm8, dev, a._ref, b._ref, po, seg, out.data_ptr(), _DTYPES[out.dtype], ldc,
-          int(accumulate), _status_word(dev))
+    here = _current()
+    if here != dev:
+        torch.cuda.set_device(dev)
+    st = B.load().mt_gemm8(a._ref, b._ref, po, seg, out.data_ptr(), _DTYPES[out.dtype], ldc, int(accumulate),
+                           _status_word(dev), _raw_stream(dev))
+    if here != dev:
+        torch.cuda.set_device(here)
+    if st:
+        raise _error("mt_gemm8", st)
     return out
 
 
@@ -278,8 +300,15 @@ def gemm8_reduce(a: Tensor8, b: Tensor8, offs: torch.Tensor, out: torch.Tensor |
     if out.dim() != 3 or out.dtype != torch.float32 or tuple(out.shape) != (seg, a.rows, b.rows):
         raise ValueError(f"out: expected float32 {(seg, a.rows, b.rows)}, got {out.dtype} {tuple(out.shape)}")
     _, ldc = _as_matrix(out, "out", dev)
-    _call("mt_gemm8_reduce", B.load().mt_gemm8_reduce, dev, a._ref, b._ref, _ints(offs, "offs", dev, (seg + 1,)),
-          seg, out.data_ptr(), ldc, int(accumulate), _status_word(dev))
+    here = _current()
+    if here != dev:
+        torch.cuda.set_device(dev)
+    st = B.load().mt_gemm8_reduce(a._ref, b._ref, _ints(offs, "offs", dev, (seg + 1,)), seg, out.data_ptr(), ldc,
+                                  int(accumulate), _status_word(dev), _raw_stream(dev))
+    if here != dev:
+        torch.cuda.set_device(here)
+    if st:
+        raise _error("mt_gemm8_reduce", st)
     return out
 
 
@@ -296,8 +325,15 @@ def swiglu8(gu: torch.Tensor, act: Tensor8 | None = None, saved: Tensor8 | None 
         act = empty8(rows, cols // 2, dev)
     if act.shape != (rows, cols // 2) or act._dev != dev or (saved is not None and saved._dev != dev):
         raise ValueError(f"act: expected {(rows, cols // 2)} on cuda:{dev}, got {act.shape} on {act.device}")
-    _call("mt_swiglu8", B.load().mt_swiglu8, dev, gu.data_ptr(), _DTYPES[gu.dtype], ld, _limit(n_rows, dev),
-          act._ref, saved._ref if saved is not None else None)
+    here = _current()
+    if here != dev:
+        torch.cuda.set_device(dev)
+    st = B.load().mt_swiglu8(gu.data_ptr(), _DTYPES[gu.dtype], ld, _limit(n_rows, dev), act._ref,
+                             saved._ref if saved is not None else None, _raw_stream(dev))
+    if here != dev:
+        torch.cuda.set_device(here)
+    if st:
+        raise _error("mt_swiglu8", st)
     return act
 
 
@@ -313,8 +349,15 @@ def swiglu8_bwd(dact: torch.Tensor, saved: Tensor8, dgu: torch.Tensor | None = N
         dgu = torch.empty(saved.shape, dtype=dact.dtype, device=dev)
     ldg = _mat(dgu, "dgu", dev, saved.rows, saved.cols, dact.dtype)
     lda = 0 if act is None else _mat(act, "act", dev, *dact.shape, dact.dtype)
-    _call("mt_swiglu8_bwd", B.load().mt_swiglu8_bwd, dev, dact.data_ptr(), _DTYPES[dact.dtype], ldd, saved._ref,
-          _limit(n_rows, dev), dgu.data_ptr(), ldg, 0 if act is None else act.data_ptr(), lda)
+    here = _current()
+    if here != dev:
+        torch.cuda.set_device(dev)
+    st = B.load().mt_swiglu8_bwd(dact.data_ptr(), _DTYPES[dact.dtype], ldd, saved._ref, _limit(n_rows, dev),
+                                 dgu.data_ptr(), ldg, 0 if act is None else act.data_ptr(), lda, _raw_stream(dev))
+    if here != dev:
+        torch.cuda.set_device(here)
+    if st:
+        raise _error("mt_swiglu8_bwd", st)
     return dgu
 
 
@@ -325,7 +368,8 @@ class Route:
     """Buffers of a routing of ``n_tokens`` x ``top_k`` assignments over
     ``n_experts``, refilled by :meth:`order`: ``offs`` [E+1] segment starts,
     ``perm`` [rows] the assignment at each row, ``row`` [n_tokens, top_k] the
-    row of each assignment (all int32, -1 for none)."""
+    row of each assignment (all int32, -1 for none).  Calls that refill or read
+    one Route, captured ones too, have to be ordered by the caller."""
 
     def __init__(self, n_tokens: int, top_k: int, n_experts: int, device="cuda"):
         dev = _device(device)
@@ -335,7 +379,12 @@ class Route:
         self._set(torch.empty(n_experts + 1, dtype=torch.int32, device=dev),
                   torch.empty(rows, dtype=torch.int32, device=dev),
                   torch.empty((n_tokens, top_k), dtype=torch.int32, device=dev))
-        self.ws = torch.empty(B.load().mt_route_ws_bytes(n_tokens, top_k, n_experts), dtype=torch.uint8, device=dev)
+        self._workspace()
+
+    def _workspace(self) -> None:
+        self.ws = torch.empty(B.load().mt_route_ws_bytes(self.n_tokens, self.top_k, self.n_experts),
+                              dtype=torch.uint8, device=self.device)
+        self._ws = (self.ws.data_ptr(), self.ws.numel())
 
     @classmethod
     def of(cls, offs: torch.Tensor, perm: torch.Tensor, row: torch.Tensor) -> "Route":
@@ -367,11 +416,17 @@ class Route:
         """Sort idx int32 [n_tokens, top_k] (-1: no expert)."""
         dev = self._dev
         if self.ws is None:
-            self.ws = torch.empty(B.load().mt_route_ws_bytes(self.n_tokens, self.top_k, self.n_experts),
-                                  dtype=torch.uint8, device=dev)
+            self._workspace()
         p = _ints(idx, "idx", dev, self.row.shape)
-        _call("mt_route_order", B.load().mt_route_order, dev, p, self.n_tokens, self.top_k, self.n_experts,
-              *self._ptrs, self.ws.data_ptr(), self.ws.numel(), _status_word(dev))
+        here = _current()
+        if here != dev:
+            torch.cuda.set_device(dev)
+        st = B.load().mt_route_order(p, self.n_tokens, self.top_k, self.n_experts, *self._ptrs, *self._ws,
+                                     _status_word(dev), _raw_stream(dev))
+        if here != dev:
+            torch.cuda.set_device(here)
+        if st:
+            raise _error("mt_route_order", st)
         return self
 
     def dispatch(self, x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
@@ -382,8 +437,15 @@ class Route:
         if out is None:
             out = torch.empty((self.rows, x.shape[1]), dtype=x.dtype, device=dev)
         ldo = _mat(out, "out", dev, self.rows, x.shape[1], x.dtype)
-        _call("mt_dispatch", B.load().mt_dispatch, dev, x.data_ptr(), _DTYPES[x.dtype], ldx, self.n_tokens,
-              x.shape[1], self.top_k, self.n_experts, *self._ptrs, self.rows, out.data_ptr(), ldo)
+        here = _current()
+        if here != dev:
+            torch.cuda.set_device(dev)
+        st = B.load().mt_dispatch(x.data_ptr(), _DTYPES[x.dtype], ldx, self.n_tokens, x.shape[1], self.top_k,
+                                  self.n_experts, *self._ptrs, self.rows, out.data_ptr(), ldo, _raw_stream(dev))
+        if here != dev:
+            torch.cuda.set_device(here)
+        if st:
+            raise _error("mt_dispatch", st)
         return out
 
     def dispatch8(self, x: torch.Tensor, out: Tensor8 | None = None) -> Tensor8:
@@ -394,8 +456,15 @@ class Route:
             out = empty8(self.rows, x.shape[1], dev)
         if out.shape != (self.rows, x.shape[1]) or out._dev != dev:
             raise ValueError(f"out: expected {(self.rows, x.shape[1])} on cuda:{dev}, got {out.shape} on {out.device}")
-        _call("mt_dispatch8", B.load().mt_dispatch8, dev, x.data_ptr(), _DTYPES[x.dtype], ldx, self.n_tokens,
-              self.top_k, self.n_experts, *self._ptrs, out._ref)
+        here = _current()
+        if here != dev:
+            torch.cuda.set_device(dev)
+        st = B.load().mt_dispatch8(x.data_ptr(), _DTYPES[x.dtype], ldx, self.n_tokens, self.top_k, self.n_experts,
+                                   *self._ptrs, out._ref, _raw_stream(dev))
+        if here != dev:
+            torch.cuda.set_device(here)
+        if st:
+            raise _error("mt_dispatch8", st)
         return out
 
     def _weights(self, w: torch.Tensor, what: str) -> int:
@@ -413,8 +482,15 @@ class Route:
             out = torch.empty((self.n_tokens, y.shape[1]), dtype=y.dtype, device=dev)
         ldo = _mat(out, "out", dev, self.n_tokens, y.shape[1], y.dtype)
         pw = 0 if w is None else self._weights(w, "w")
-        _call("mt_combine", B.load().mt_combine, dev, y.data_ptr(), _DTYPES[y.dtype], ldy, self.rows, self._ptrs[2],
-              pw, self.n_tokens, self.top_k, y.shape[1], out.data_ptr(), ldo)
+        here = _current()
+        if here != dev:
+            torch.cuda.set_device(dev)
+        st = B.load().mt_combine(y.data_ptr(), _DTYPES[y.dtype], ldy, self.rows, self._ptrs[2], pw, self.n_tokens,
+                                 self.top_k, y.shape[1], out.data_ptr(), ldo, _raw_stream(dev))
+        if here != dev:
+            torch.cuda.set_device(here)
+        if st:
+            raise _error("mt_combine", st)
         return out
 
     def dispatch_bwd(self, dxs: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
@@ -434,7 +510,14 @@ class Route:
         if dw is None:
             dw = torch.empty(self.row.shape, dtype=torch.float32, device=dev)
         ldg = _mat(dy, "dy", dev, self.rows, width, dout.dtype)
-        _call("mt_combine_bwd", B.load().mt_combine_bwd, dev, dout.data_ptr(), _DTYPES[dout.dtype], ldd,
-              y.data_ptr(), ldy, *self._ptrs, self.rows, self._weights(w, "w"), self.n_tokens, self.top_k,
-              self.n_experts, width, dy.data_ptr(), ldg, self._weights(dw, "dw"))
+        here = _current()
+        if here != dev:
+            torch.cuda.set_device(dev)
+        st = B.load().mt_combine_bwd(dout.data_ptr(), _DTYPES[dout.dtype], ldd, y.data_ptr(), ldy, *self._ptrs,
+                                     self.rows, self._weights(w, "w"), self.n_tokens, self.top_k, self.n_experts,
+                                     width, dy.data_ptr(), ldg, self._weights(dw, "dw"), _raw_stream(dev))
+        if here != dev:
+            torch.cuda.set_device(here)
+        if st:
+            raise _error("mt_combine_bwd", st)
         return dy, dw

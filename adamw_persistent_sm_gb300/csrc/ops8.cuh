@@ -31,13 +31,15 @@ __device__ __forceinline__ int ops_row_limit(const int* p, int rows) {
   return v < 0 ? 0 : v < rows ? v : rows;
 }
 
-// Elements c..c+7 of a row, zeros from column n on.  VEC 0: any alignment; 1: row
+// Elements c..c+7 of a row, zeros from column n on.  VEC 0: any alignment (S: the
+// step between a lane's elements; 32 makes neighbouring lanes take neighbours, where
+// it does not matter which lane has which); 1: row
 // start and c are 16-byte aligned; 2: and every lane's eight lie inside the row
 // and (fp32) on 32-byte boundaries, which the launch knows from the sizes: no test
 // per access, the loads of a loop stay together, and fp32 lanes move whole sectors
 // (two 16-byte halves each left every sector written twice: 27 against 20 us for
 // 4096 x 8 rows of 768).
-template <int VEC>
+template <int VEC, int S = 1>
 __device__ __forceinline__ void ops_ld8(const float* p, int c, int n, float* v) {
   if constexpr (VEC == 2) {
     asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -52,12 +54,12 @@ __device__ __forceinline__ void ops_ld8(const float* p, int c, int n, float* v) 
   }
   if constexpr (VEC != 2) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < n ? p[c + i] : 0.f;
+    for (int i = 0; i < 8; ++i) v[i] = c + i * (VEC ? 1 : S) < n ? p[c + i * (VEC ? 1 : S)] : 0.f;
   }
 }
 __device__ __forceinline__ float ops_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float ops_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
-template <int VEC>
+template <int VEC, int S = 1>
 __device__ __forceinline__ void ops_ld8(const __nv_bfloat16* p, int c, int n, float* v) {
   if (VEC == 2 || (VEC && c + 8 <= n)) {
     const uint4 u = *reinterpret_cast<const uint4*>(p + c);
@@ -67,14 +69,14 @@ __device__ __forceinline__ void ops_ld8(const __nv_bfloat16* p, int c, int n, fl
   }
   if constexpr (VEC != 2) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < n ? __bfloat162float(p[c + i]) : 0.f;
+    for (int i = 0; i < 8; ++i) v[i] = c + i * (VEC ? 1 : S) < n ? __bfloat162float(p[c + i * (VEC ? 1 : S)]) : 0.f;
   }
 }
 __device__ __forceinline__ uint32_t ops_bf2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-template <int VEC>
+template <int VEC, int S = 1>
 __device__ __forceinline__ void ops_st8(float* p, int c, int n, const float* v) {
   if constexpr (VEC == 2) {
     asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + c), "f"(v[0]), "f"(v[1]),
@@ -90,10 +92,10 @@ __device__ __forceinline__ void ops_st8(float* p, int c, int n, const float* v) 
   if constexpr (VEC != 2) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (c + i < n) p[c + i] = v[i];
+      if (c + i * (VEC ? 1 : S) < n) p[c + i * (VEC ? 1 : S)] = v[i];
   }
 }
-template <int VEC>
+template <int VEC, int S = 1>
 __device__ __forceinline__ void ops_st8(__nv_bfloat16* p, int c, int n, const float* v) {
   if (VEC == 2 || (VEC && c + 8 <= n)) {
     *reinterpret_cast<uint4*>(p + c) =
@@ -103,7 +105,7 @@ __device__ __forceinline__ void ops_st8(__nv_bfloat16* p, int c, int n, const fl
   if constexpr (VEC != 2) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (c + i < n) p[c + i] = __float2bfloat16_rn(v[i]);
+      if (c + i * (VEC ? 1 : S) < n) p[c + i * (VEC ? 1 : S)] = __float2bfloat16_rn(v[i]);
   }
 }
 // Eight codes; `v8`: the address is 8-byte aligned.
@@ -208,7 +210,7 @@ struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
   uint4 u;
-  template <int VEC>
+  template <int VEC, int S = 1>
   __device__ __forceinline__ void load(const __nv_bfloat16* p, int c, int n) {
     if (VEC == 2 || (VEC && c + 8 <= n)) {
       u = *reinterpret_cast<const uint4*>(p + c);
@@ -217,11 +219,11 @@ struct Raw8<__nv_bfloat16> {
     if constexpr (VEC != 2) {
       uint32_t h[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = c + i < n ? reinterpret_cast<const uint16_t*>(p)[c + i] : 0;
+      for (int i = 0; i < 8; ++i) h[i] = c + i * (VEC ? 1 : S) < n ? reinterpret_cast<const uint16_t*>(p)[c + i * (VEC ? 1 : S)] : 0;
       u = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
     }
   }
-  template <int VEC>
+  template <int VEC, int S = 1>
   __device__ __forceinline__ void store(__nv_bfloat16* p, int c, int n) const {
     if (VEC == 2 || (VEC && c + 8 <= n)) {
       *reinterpret_cast<uint4*>(p + c) = u;
@@ -231,7 +233,7 @@ struct Raw8<__nv_bfloat16> {
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (c + i < n) reinterpret_cast<uint16_t*>(p)[c + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+        if (c + i * (VEC ? 1 : S) < n) reinterpret_cast<uint16_t*>(p)[c + i * (VEC ? 1 : S)] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
     }
   }
   // bits (fp32) of the largest magnitude
@@ -248,18 +250,18 @@ struct Raw8<__nv_bfloat16> {
 template <>
 struct Raw8<float> {
   float4 a, b;
-  template <int VEC>
+  template <int VEC, int S = 1>
   __device__ __forceinline__ void load(const float* p, int c, int n) {
     float v[8];
-    ops_ld8<VEC>(p, c, n, v);
+    ops_ld8<VEC, S>(p, c, n, v);
     a = make_float4(v[0], v[1], v[2], v[3]);
     b = make_float4(v[4], v[5], v[6], v[7]);
   }
-  template <int VEC>
+  template <int VEC, int S = 1>
   __device__ __forceinline__ void store(float* p, int c, int n) const {
     float v[8];
     values(v);
-    ops_st8<VEC>(p, c, n, v);
+    ops_st8<VEC, S>(p, c, n, v);
   }
   __device__ __forceinline__ uint32_t top() const {
     const float m = ops_max3(ops_max3(a.x, a.y, a.z), ops_max3(a.w, b.x, b.y), b.z);

@@ -240,6 +240,11 @@ __device__ __forceinline__ long long pad_row(long long i, int E, const int* offs
   return perm[r] < 0 ? r : -1;
 }
 
+// A lane's part of a chunk of 256 columns: eight neighbours, or in rows of any
+// alignment every 32nd element, so that each access of the warp is one segment.
+constexpr int MOVE_STEP = 32;
+#define MOVE_COL(VEC) ((VEC) ? lane * 8 : lane)
+
 // A warp holds one token's chunk of 256 columns (8 per lane) and writes it to
 // the token's rows: x is read once however many experts take it, which leaves
 // the write of the copies as the bound.  The CTAs behind the tokens' write the
@@ -254,19 +259,20 @@ __global__ void __launch_bounds__(256) dispatch_k(const T* x, long long ldx, lon
   if (blockIdx.x >= tok_ctas) {
     const long long r = pad_row((blockIdx.x - tok_ctas) * 8 + warp, E, offs, perm, rows);
     if (r < 0) return;
-    for (int c = lane * 8 + 256 * (int)blockIdx.y; c < width; c += 256 * (int)gridDim.y)
-      ops_st8<VEC>(out + r * ldo, c, width, zero);
+    for (int c0 = 256 * (int)blockIdx.y; c0 < width; c0 += 256 * (int)gridDim.y)
+      ops_st8<VEC, MOVE_STEP>(out + r * ldo, c0 + MOVE_COL(VEC), width, zero);
     return;
   }
   const long long t = (long long)blockIdx.x * 8 + warp;
   if (t >= tokens) return;
   const int mine = lane < K ? row[t * K + lane] : -1;
-  for (int c = lane * 8 + 256 * (int)blockIdx.y; c - lane * 8 < width; c += 256 * (int)gridDim.y) {
+  for (int c0 = 256 * (int)blockIdx.y; c0 < width; c0 += 256 * (int)gridDim.y) {
+    const int c = c0 + MOVE_COL(VEC);
     Raw8<T> v;
-    v.template load<VEC>(x + t * ldx, c, width);
+    v.template load<VEC, MOVE_STEP>(x + t * ldx, c, width);
     for (int k = 0; k < K; ++k) {
       const long long r = __shfl_sync(0xffffffffu, mine, k);
-      if (r >= 0 && r < rows) v.template store<VEC>(out + r * ldo, c, width);
+      if (r >= 0 && r < rows) v.template store<VEC, MOVE_STEP>(out + r * ldo, c, width);
     }
   }
 }
@@ -339,7 +345,7 @@ __global__ void __launch_bounds__(256) combine_k(const T* y, long long ldy, long
       const long long r = __shfl_sync(0xffffffffu, mine, k);
 #pragma unroll
       for (int h = 0; h < CH; ++h)
-        if (r >= 0 && c0 + 256 * h < width) v[k][h].template load<VEC>(y + r * ldy, c0 + 256 * h + lane * 8, width);
+        if (r >= 0 && c0 + 256 * h < width) v[k][h].template load<VEC, MOVE_STEP>(y + r * ldy, c0 + 256 * h + MOVE_COL(VEC), width);
     }
 #pragma unroll
     for (int h = 0; h < CH; ++h) {
@@ -355,7 +361,7 @@ __global__ void __launch_bounds__(256) combine_k(const T* y, long long ldy, long
           for (int i = 0; i < 8; ++i) s[i] = fmaf(wk, x[i], s[i]);
         }
       }
-      ops_st8<VEC>(out + t * ldo, c0 + 256 * h + lane * 8, width, s);
+      ops_st8<VEC, MOVE_STEP>(out + t * ldo, c0 + 256 * h + MOVE_COL(VEC), width, s);
     }
   }
 }
@@ -374,7 +380,7 @@ __global__ void __launch_bounds__(256) combine_bwd_k(const T* dout, long long ld
   if (blockIdx.x >= tok_ctas) {
     const long long r = pad_row((blockIdx.x - tok_ctas) * 8 + warp, E, offs, perm, rows);
     if (r < 0) return;
-    for (int c = lane * 8; c < width; c += 256) ops_st8<VEC>(dy + r * lddy, c, width, zero);
+    for (int c0 = 0; c0 < width; c0 += 256) ops_st8<VEC, MOVE_STEP>(dy + r * lddy, c0 + MOVE_COL(VEC), width, zero);
     return;
   }
   const long long t = (long long)blockIdx.x * 8 + warp;
@@ -387,13 +393,13 @@ __global__ void __launch_bounds__(256) combine_bwd_k(const T* dout, long long ld
     Raw8<T> d8[CH], v8[KM][CH];
 #pragma unroll
     for (int h = 0; h < CH; ++h)
-      if (c0 + 256 * h < width) d8[h].template load<VEC>(dout + t * lddo, c0 + 256 * h + lane * 8, width);
+      if (c0 + 256 * h < width) d8[h].template load<VEC, MOVE_STEP>(dout + t * lddo, c0 + 256 * h + MOVE_COL(VEC), width);
 #pragma unroll
     for (int k = 0; k < KM; ++k) {
       const long long r = __shfl_sync(0xffffffffu, mine, k);
 #pragma unroll
       for (int h = 0; h < CH; ++h)
-        if (r >= 0 && c0 + 256 * h < width) v8[k][h].template load<VEC>(y + r * ldy, c0 + 256 * h + lane * 8, width);
+        if (r >= 0 && c0 + 256 * h < width) v8[k][h].template load<VEC, MOVE_STEP>(y + r * ldy, c0 + 256 * h + MOVE_COL(VEC), width);
     }
 #pragma unroll
     for (int h = 0; h < CH; ++h) {
@@ -412,7 +418,7 @@ __global__ void __launch_bounds__(256) combine_bwd_k(const T* dout, long long ld
           o[i] = wk * d[i];
           dot[k] = fmaf(d[i], v[i], dot[k]);
         }
-        ops_st8<VEC>(dy + r * lddy, c0 + 256 * h + lane * 8, width, o);
+        ops_st8<VEC, MOVE_STEP>(dy + r * lddy, c0 + 256 * h + MOVE_COL(VEC), width, o);
       }
     }
   }

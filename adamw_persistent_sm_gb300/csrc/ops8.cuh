@@ -142,13 +142,15 @@ __device__ __forceinline__ uint2 ops_ld_codes(const uint8_t* p, int c, int n, bo
 __device__ __forceinline__ float ops_finite(float x) {
   return fabsf(x) <= 3.402823466e38f ? x : __int_as_float(0x7fffffff);
 }
-// Least e >= -126 with amax <= 448 * 2^e = 1.75 * 2^(e + 8); 0 for amax = 0.
-// With amax = 1.f * 2^x that is x - 8, one more where 1.f > 1.75.
-__device__ __forceinline__ int ops_exponent(float amax) {
-  const uint32_t b = __float_as_uint(amax);
-  if (b == 0) return 0;
-  const int e = (int)(b >> 23) - 135 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return e < -126 ? -126 : e;
+// The block's scale from the bits of its largest magnitude 1.f * 2^x: e, the least
+// with amax <= 448 * 2^e = 1.75 * 2^(e + 8), is x - 8, one more where 1.f > 1.75 -
+// where adding 0x1fffff carries into the exponent.  At least -126, 0 for amax = 0.
+// `byte` e + 127; the result 2^-e.
+__device__ __forceinline__ float ops_scale(uint32_t top, uint32_t* byte) {
+  uint32_t x = (top + 0x1fffffu) >> 23;
+  x = top ? max(x, 9u) : 135u;
+  *byte = x - 8;
+  return __uint_as_float((262u - x) << 23);
 }
 __device__ __forceinline__ float ops_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 // four e4m3 codes of v * s (round to nearest even; |v * s| <= 448 or NaN); the
@@ -283,8 +285,8 @@ __device__ __forceinline__ uint32_t ops_max16(uint32_t a) {
   return a;
 }
 // Codes of eight elements v of a block whose largest magnitude (over 16 lanes)
-// has the bits `top`, and the block's exponent.  The whole warp calls it.
-__device__ __forceinline__ uint2 ops_quantise(float* v, uint32_t top, int* e) {
+// has the bits `top`, and the block's scale byte.  The whole warp calls it.
+__device__ __forceinline__ uint2 ops_quantise(float* v, uint32_t top, uint32_t* byte) {
   if (__any_sync(0xffffffffu, top >= OPS_INF)) {
     uint32_t m = 0;
 #pragma unroll
@@ -294,8 +296,7 @@ __device__ __forceinline__ uint2 ops_quantise(float* v, uint32_t top, int* e) {
     }
     top = ops_max16(m);
   }
-  *e = ops_exponent(__uint_as_float(top));
-  return ops_codes8(v, ops_pow2(-*e));
+  return ops_codes8(v, ops_scale(top, byte));
 }
 
 // ---------------------------------------------------------------------------

@@ -51,11 +51,11 @@ __global__ void __launch_bounds__(256) quant_rows_k(const T* x, long long ldx, c
     for (int i = 0; i < R; ++i) {
       if (r0 + i >= lim) break;
       float v[8];
-      int e;
+      uint32_t e;
       x8[i].values(v);
       const uint2 q = ops_quantise(v, top[i], &e);
       ops_st_codes<VEC>(o.q + (long long)(r0 + i) * o.ld + base, c, pcols, q, v8 || parts == 1);
-      if ((lane & 15) == 0 && c < pcols) o.s[(long long)(r0 + i) * o.lds + part * pblocks + (c >> 7)] = (uint8_t)(e + 127);
+      if ((lane & 15) == 0 && c < pcols) o.s[(long long)(r0 + i) * o.lds + part * pblocks + (c >> 7)] = (uint8_t)e;
     }
   }
 }
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 1 ? 3 : 2) quant_tile_k(cons
   // three CTAs without reading ahead take 30 us where two that do take 35
   constexpr bool PRE = sizeof(T) == 2;
   __shared__ uint32_t part[8][128];
-  __shared__ int ex[128];
+  __shared__ float inv[128];
   __shared__ __align__(16) uint2 tile[MODE == T_BLOCK ? 1 : 128 * 16];
   ops_begin();
   typedef typename Tile8<T>::Raw Raw;
@@ -249,22 +249,22 @@ __global__ void __launch_bounds__(256, sizeof(T) == 1 ? 3 : 2) quant_tile_k(cons
           for (int s = 16; s > 0; s >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, s));
           if ((tid & 31) == 0) part[0][tid] = a;      // read by this thread's own warp alone so far
         } else {
-          const int e = ops_exponent(__uint_as_float(a));
-          ex[tid] = e;
-          if (ct * 128 + tid < cols) o.s[(long long)(b * cols + ct * 128 + tid) * o.lds + rt] = (uint8_t)(e + 127);
+          uint32_t e;
+          inv[tid] = ops_scale(a, &e);
+          if (ct * 128 + tid < cols) o.s[(long long)(b * cols + ct * 128 + tid) * o.lds + rt] = (uint8_t)e;
         }
       }
       __syncthreads();
-      int e0 = 0;
+      float s0 = 1.f;
       if (MODE != T_COLS_T) {
-        e0 = ops_exponent(__uint_as_float(max(max(part[0][0], part[0][32]), max(part[0][64], part[0][96]))));
+        uint32_t e0;
+        s0 = ops_scale(max(max(part[0][0], part[0][32]), max(part[0][64], part[0][96])), &e0);
         if (tid == 0) {
-          if (MODE == T_BLOCK) o.s[(long long)(b * ((rows + 127) / 128) + rt) * o.lds + ct] = (uint8_t)(e0 + 127);
-          else o.s[(long long)(b * ((cols + 127) / 128) + ct) * o.lds + rt] = (uint8_t)(e0 + 127);
+          if (MODE == T_BLOCK) o.s[(long long)(b * ((rows + 127) / 128) + rt) * o.lds + ct] = (uint8_t)e0;
+          else o.s[(long long)(b * ((cols + 127) / 128) + ct) * o.lds + rt] = (uint8_t)e0;
         }
       }
       if (MODE == T_BLOCK) {
-        const float s = ops_pow2(-e0);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float v[8];
@@ -273,12 +273,12 @@ __global__ void __launch_bounds__(256, sizeof(T) == 1 ? 3 : 2) quant_tile_k(cons
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = ops_finite(v[j]);
           }
-          if (r0 + i < rows) ops_st_codes<VEC>(o.q + (long long)(b * rows + r0 + i) * o.ld, c0, cols, ops_codes8(v, s), true);
+          if (r0 + i < rows) ops_st_codes<VEC>(o.q + (long long)(b * rows + r0 + i) * o.ld, c0, cols, ops_codes8(v, s0), true);
         }
       } else {
         float sc[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sc[j] = ops_pow2(-(MODE == T_COLS_T ? ex[tc * 8 + j] : e0));
+        for (int j = 0; j < 8; ++j) sc[j] = MODE == T_COLS_T ? inv[tc * 8 + j] : s0;
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
           float v[4][8];
@@ -357,12 +357,12 @@ __global__ void __launch_bounds__(256, SAVE ? 4 : 1) swiglu_k(const T* gu, long 
       u8[i].values(u);
 #pragma unroll
       for (int j = 0; j < 8; ++j) a[j] = g[j] * sigmoid_f(g[j]) * u[j];
-      int e;
+      uint32_t e;
       const uint2 q = ops_quantise(a, ops_max16(ops_top8(a)), &e);
       ops_st_codes<VEC>(act.q + r * act.ld, c, F, q, true);
-      if (first) act.s[r * act.lds + (c >> 7)] = (uint8_t)(e + 127);
+      if (first) act.s[r * act.lds + (c >> 7)] = (uint8_t)e;
       if (SAVE) {
-        int eg, eu;
+        uint32_t eg, eu;
         uint32_t tg = g8[i].top(), tu = u8[i].top();
         if (sizeof(T) == 2) {            // 16 bits each: one word goes round
           uint32_t t = (tg >> 16) | tu;
@@ -378,8 +378,8 @@ __global__ void __launch_bounds__(256, SAVE ? 4 : 1) swiglu_k(const T* gu, long 
         ops_st_codes<VEC>(sv.q + r * sv.ld, c, F, qg, true);
         ops_st_codes<VEC>(sv.q + r * sv.ld + F, c, F, qu, v8);
         if (first) {
-          sv.s[r * sv.lds + (c >> 7)] = (uint8_t)(eg + 127);
-          sv.s[r * sv.lds + nb + (c >> 7)] = (uint8_t)(eu + 127);
+          sv.s[r * sv.lds + (c >> 7)] = (uint8_t)eg;
+          sv.s[r * sv.lds + nb + (c >> 7)] = (uint8_t)eu;
         }
       }
     }

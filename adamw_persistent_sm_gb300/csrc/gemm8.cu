@@ -177,7 +177,11 @@ __device__ __forceinline__ void g8_ld_wait(uint32_t* r) {
 struct G8Tile {
   int m0, n0, seg, k0, nkb;      // first row and column of C, segment, first element and blocks of K
 };
-// Tiles in use: all of them, or those before the end of the last segment.
+// Tiles in use: all of them, or those from the first segment's start to the last
+// one's end.
+__device__ __forceinline__ int g8_first(const G8Args& g, const int* offs) {
+  return g.mode == G8_ROWS ? (offs[0] >> 7) * g.nt : 0;
+}
 __device__ __forceinline__ int g8_tiles(const G8Args& g, const int* offs) {
   if (g.mode != G8_ROWS) return g.ntiles;
   const int n = ((offs[g.nseg] + 127) >> 7) * g.nt;
@@ -336,17 +340,15 @@ __global__ void __launch_bounds__(G8_THREADS, 1) gemm8_k(const __grid_constant__
   // segment starts, kept inside the operands and on block boundaries whatever
   // they hold (a TMA coordinate has to be a multiple of 16)
   if (g.mode != G8_DENSE && tid <= g.nseg) {
-    const int lim = g.mode == G8_ROWS ? (g.M + 127) & ~127 : g.K;
-    int v = g.offs[tid] & ~127;
-    v = v < 0 ? 0 : v > lim ? lim : v;
-    offs[tid] = v & ~127;
+    const int lim = ((g.mode == G8_ROWS ? g.M : g.K) + 127) & ~127, v = g.offs[tid] & ~127;
+    offs[tid] = v < 0 ? 0 : v > lim ? lim : v;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gen + G8_TMEM);
 
-  const int ntiles = g8_tiles(g, offs);
+  const int ntiles = g8_tiles(g, offs), first = g8_first(g, offs) + (int)blockIdx.x;
   // The loading warps need few registers, the storing ones 128 for their part
   // of the tile: the split gives away only what the launch has.
   if (warp < 4) {
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(G8_THREADS, 1) gemm8_k(const __grid_constant__
     if (warp == 0 && lane == 0) {
       int it = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+      for (int t = first; t < ntiles && ok; t += gridDim.x) {
         const G8Tile ti = g8_tile<BN>(g, offs, t);
         const int by = (g.mode == G8_ROWS ? ti.seg * g.N : 0) + ti.n0;
         for (int kb = 0; kb < ti.nkb; ++kb, ++it) {
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(G8_THREADS, 1) gemm8_k(const __grid_constant__
       const uint64_t ad0 = sdesc(stages, 16, 1024), bd0 = sdesc(stages + G8_A_BYTES, 16, 1024);
       uint64_t ad = ad0, bd = bd0;
       bool ok = true;
-      for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+      for (int t = first; t < ntiles && ok; t += gridDim.x) {
         const int nkb = g8_blocks(g, offs, t);
         for (int kc = 0; kc < nkb && ok; kc += G8_CHUNK) {
           const int end = nkb - kc < G8_CHUNK ? nkb : kc + G8_CHUNK;
@@ -439,7 +441,7 @@ __global__ void __launch_bounds__(G8_THREADS, 1) gemm8_k(const __grid_constant__
       const bool isa = warp == 2, words = isa ? g.words_a : g.words_b;
       G8Tile ti;
       ti.nkb = 0;
-      int t = (int)blockIdx.x - (int)gridDim.x, kb = -4;
+      int t = first - (int)gridDim.x, kb = -4;
       auto advance = [&]() {
         kb += 4;
         while (kb >= ti.nkb) {
@@ -540,7 +542,7 @@ __global__ void __launch_bounds__(G8_THREADS, 1) gemm8_k(const __grid_constant__
     const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16) + half * HALF;
     int nt = 0;
     bool ok = true;
-    for (int t = ew < EW ? (int)blockIdx.x : ntiles; t < ntiles && ok; t += gridDim.x) {
+    for (int t = ew < EW ? first : ntiles; t < ntiles && ok; t += gridDim.x) {
       const G8Tile ti = g8_tile<BN>(g, offs, t);
       const int col = ti.n0 + half * HALF;
       uint32_t acc[HALF];

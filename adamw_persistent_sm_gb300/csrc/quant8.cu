@@ -321,7 +321,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 1 ? 3 : 2) quant_tile_k(cons
 // SwiGLU
 // ---------------------------------------------------------------------------
 // 1 / (1 + 2^(-g log2 e)) on the two approximate instructions (2 and 1 ulp): the
-// product's rounding adds |g| 2^-24, far inside the 8-bit results' steps.
+// product's rounding adds |g| 2^-24, far inside the 8-bit results' steps.  Below
+// g = -87.3, where it is under 2^-126, it is 0.
 __device__ __forceinline__ float sigmoid_f(float g) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));

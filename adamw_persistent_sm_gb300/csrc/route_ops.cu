@@ -501,7 +501,7 @@ int moves_ok(int64_t tokens, int32_t K, int32_t E, int64_t rows, int64_t width, 
   if (st) return st;
   if (rows < 0 || width < 1) return MT_ERR_ARG;
   if (rows > OPS_MAX_ROWS || width > OPS_MAX_ROWS) return MT_ERR_UNSUPPORTED;
-  if (!offs || !perm || !row || !ops_aligned(offs, 4) || !ops_aligned(perm, 4) || !ops_aligned(row, 4))
+  if (!offs || !perm || (tokens && !row) || !ops_aligned(offs, 4) || !ops_aligned(perm, 4) || !ops_aligned(row, 4))
     return MT_ERR_ARG;
   // perm and offs were made for this many rows
   return rows == route_rows(tokens, K, E) ? MT_OK : MT_ERR_ARG;

@@ -37,7 +37,8 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 # Every operator makes its device current around the call of the C ABI (a
-# no-op in the usual case) and passes that device's current stream.
+# no-op in the usual case) and passes that device's current stream.  Nothing
+# between the two changes of device may raise: arguments are checked before.
 
 
 def _status_word(dev: int) -> int:
@@ -193,7 +194,8 @@ def _as_matrix(x: torch.Tensor, what: str, dev) -> tuple[int, int]:
 def quant8(x: torch.Tensor, block_rows: int = 1, out: Tensor8 | None = None, n_rows: torch.Tensor | None = None,
            halves: bool = False) -> Tensor8:
     """x [rows, cols] or [batch, rows, cols] in 8 bits.  ``n_rows`` (device
-    int32 [1]): only rows below it are written."""
+    int32 [1]): only rows below it are written.  ``out`` brings its own
+    block_rows and halves."""
     dev = x.get_device()
     batch, ldx = _as_matrix(x, "x", dev)
     if out is None:
@@ -202,10 +204,11 @@ def quant8(x: torch.Tensor, block_rows: int = 1, out: Tensor8 | None = None, n_r
         raise ValueError(f"out: expected {tuple(x.shape)} on cuda:{dev}, got {out.shape} on {out.device}")
     if batch == 0:
         return out
+    lim = _limit(n_rows, dev)
     here = _current()
     if here != dev:
         torch.cuda.set_device(dev)
-    st = B.load().mt_quant8(x.data_ptr(), _DTYPES[x.dtype], ldx, _limit(n_rows, dev), out._ref, _raw_stream(dev))
+    st = B.load().mt_quant8(x.data_ptr(), _DTYPES[x.dtype], ldx, lim, out._ref, _raw_stream(dev))
     if here != dev:
         torch.cuda.set_device(here)
     if st:
@@ -232,10 +235,11 @@ def quant8_t(x, block_rows: int = 1, out: Tensor8 | None = None, n_rows: torch.T
         raise ValueError(f"out: expected {(*lead, cols, rows)} on cuda:{dev}, got {out.shape} on {out.device}")
     if lead and lead[0] == 0:
         return out
+    lim = _limit(n_rows, dev)
     here = _current()
     if here != dev:
         torch.cuda.set_device(dev)
-    st = B.load().mt_quant8_t(ptr, dt, ldx, src, _limit(n_rows, dev), out._ref, _raw_stream(dev))
+    st = B.load().mt_quant8_t(ptr, dt, ldx, src, lim, out._ref, _raw_stream(dev))
     if here != dev:
         torch.cuda.set_device(here)
     if st:
@@ -249,11 +253,11 @@ def dequant8(a: Tensor8, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor 
     dev = a._dev
     if out is None:
         out = torch.empty(a.shape, dtype=dtype, device=dev)
-    ldo = _mat(out, "out", dev, a.rows, a.cols)
+    ldo, lim = _mat(out, "out", dev, a.rows, a.cols), _limit(n_rows, dev)
     here = _current()
     if here != dev:
         torch.cuda.set_device(dev)
-    st = B.load().mt_dequant8(a._ref, _limit(n_rows, dev), out.data_ptr(), _DTYPES[out.dtype], ldo, _raw_stream(dev))
+    st = B.load().mt_dequant8(a._ref, lim, out.data_ptr(), _DTYPES[out.dtype], ldo, _raw_stream(dev))
     if here != dev:
         torch.cuda.set_device(here)
     if st:
@@ -263,7 +267,9 @@ def dequant8(a: Tensor8, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor 
 
 def gemm8(a: Tensor8, b: Tensor8, out: torch.Tensor | None = None, offs: torch.Tensor | None = None,
           dtype: torch.dtype = torch.bfloat16, accumulate: bool = False) -> torch.Tensor:
-    """a b^T: a [M, K]; b [N, K], or with ``offs`` (int32 [E+1] row starts) [E, N, K]."""
+    """a b^T: a [M, K]; b [N, K], or with ``offs`` (int32 [E+1] row starts, also a
+    run of consecutive experts of a routing) [E, N, K]; rows outside the segments
+    are left as they were."""
     dev = a._dev
     if b._dev != dev:
         raise ValueError(f"b is on {b.device}, a on cuda:{dev}")
@@ -300,10 +306,11 @@ def gemm8_reduce(a: Tensor8, b: Tensor8, offs: torch.Tensor, out: torch.Tensor |
     if out.dim() != 3 or out.dtype != torch.float32 or tuple(out.shape) != (seg, a.rows, b.rows):
         raise ValueError(f"out: expected float32 {(seg, a.rows, b.rows)}, got {out.dtype} {tuple(out.shape)}")
     _, ldc = _as_matrix(out, "out", dev)
+    po = _ints(offs, "offs", dev, (seg + 1,))
     here = _current()
     if here != dev:
         torch.cuda.set_device(dev)
-    st = B.load().mt_gemm8_reduce(a._ref, b._ref, _ints(offs, "offs", dev, (seg + 1,)), seg, out.data_ptr(), ldc,
+    st = B.load().mt_gemm8_reduce(a._ref, b._ref, po, seg, out.data_ptr(), ldc,
                                   int(accumulate), _status_word(dev), _raw_stream(dev))
     if here != dev:
         torch.cuda.set_device(here)
@@ -325,10 +332,11 @@ def swiglu8(gu: torch.Tensor, act: Tensor8 | None = None, saved: Tensor8 | None 
         act = empty8(rows, cols // 2, dev)
     if act.shape != (rows, cols // 2) or act._dev != dev or (saved is not None and saved._dev != dev):
         raise ValueError(f"act: expected {(rows, cols // 2)} on cuda:{dev}, got {act.shape} on {act.device}")
+    lim = _limit(n_rows, dev)
     here = _current()
     if here != dev:
         torch.cuda.set_device(dev)
-    st = B.load().mt_swiglu8(gu.data_ptr(), _DTYPES[gu.dtype], ld, _limit(n_rows, dev), act._ref,
+    st = B.load().mt_swiglu8(gu.data_ptr(), _DTYPES[gu.dtype], ld, lim, act._ref,
                              saved._ref if saved is not None else None, _raw_stream(dev))
     if here != dev:
         torch.cuda.set_device(here)
@@ -349,10 +357,11 @@ def swiglu8_bwd(dact: torch.Tensor, saved: Tensor8, dgu: torch.Tensor | None = N
         dgu = torch.empty(saved.shape, dtype=dact.dtype, device=dev)
     ldg = _mat(dgu, "dgu", dev, saved.rows, saved.cols, dact.dtype)
     lda = 0 if act is None else _mat(act, "act", dev, *dact.shape, dact.dtype)
+    lim = _limit(n_rows, dev)
     here = _current()
     if here != dev:
         torch.cuda.set_device(dev)
-    st = B.load().mt_swiglu8_bwd(dact.data_ptr(), _DTYPES[dact.dtype], ldd, saved._ref, _limit(n_rows, dev),
+    st = B.load().mt_swiglu8_bwd(dact.data_ptr(), _DTYPES[dact.dtype], ldd, saved._ref, lim,
                                  dgu.data_ptr(), ldg, 0 if act is None else act.data_ptr(), lda, _raw_stream(dev))
     if here != dev:
         torch.cuda.set_device(here)
@@ -510,12 +519,13 @@ class Route:
         if dw is None:
             dw = torch.empty(self.row.shape, dtype=torch.float32, device=dev)
         ldg = _mat(dy, "dy", dev, self.rows, width, dout.dtype)
+        pw, pdw = self._weights(w, "w"), self._weights(dw, "dw")
         here = _current()
         if here != dev:
             torch.cuda.set_device(dev)
         st = B.load().mt_combine_bwd(dout.data_ptr(), _DTYPES[dout.dtype], ldd, y.data_ptr(), ldy, *self._ptrs,
-                                     self.rows, self._weights(w, "w"), self.n_tokens, self.top_k, self.n_experts,
-                                     width, dy.data_ptr(), ldg, self._weights(dw, "dw"), _raw_stream(dev))
+                                     self.rows, pw, self.n_tokens, self.top_k, self.n_experts,
+                                     width, dy.data_ptr(), ldg, pdw, _raw_stream(dev))
         if here != dev:
             torch.cuda.set_device(here)
         if st:

@@ -59,14 +59,15 @@ class ExpertLayer8:
         """sum_k w[t, k] expert[idx[t, k]](x[t]) for x [n_tokens, d], idx int32
         and w float32 [n_tokens, top_k] (idx -1: no expert).  ``save`` False
         keeps nothing for :meth:`backward`."""
-        r = self.route
+        r, self.w = self.route, None        # a forward that fails leaves nothing to go back through
         r.order(idx)
         r.dispatch8(x, out=self.xs8)
         ops.gemm8(self.xs8, self.w_gu, out=self.gu, offs=r.offs)
         ops.swiglu8(self.gu, act=self.act8, saved=self.saved if save else None, n_rows=r.offs[-1:])
         ops.gemm8(self.act8, self.w_down, out=self.y, offs=r.offs)
+        out = r.combine(self.y, w, out=out)
         self.w = w if save else None
-        return r.combine(self.y, w, out=out)
+        return out
 
     def backward(self, dout: torch.Tensor, grads: tuple[torch.Tensor, torch.Tensor, torch.Tensor] | None = None,
                  accumulate: bool = False) -> tuple[torch.Tensor, torch.Tensor, tuple]:

@@ -409,7 +409,7 @@ int32_t mt_debug_gemm(const void* A, int32_t a_mn, const void* B, int32_t b_mn, 
  *    all the buffers must be.  No call allocates, synchronises or keeps
  *    anything; every launch can be captured into a CUDA graph.
  *  - Outputs may not overlap inputs or one another.  Calls that share an
- *    output, a workspace or a status word must be ordered by the caller.
+ *    output or a workspace must be ordered by the caller.
  *  - `status` (device int32[2], zeroed by the caller once) receives an
  *    mt_status and an error site when a device-side check fails; the first
  *    failure stays.  It may be shared by any number of calls.
@@ -516,16 +516,19 @@ int32_t mt_dequant8(const mt_mat8* a, const int32_t* n_rows, void* out, int32_t 
 /* C = A B^T on the tensor cores with fp32 sums: A [M, K] (batch 1, block_rows
  * 1, halves 0), B [N, K] or, by expert, [n_seg][N][K] (block_rows 1 or 128), C
  * [M, N] of dtype.  offs NULL: dense (n_seg 0, B batch 1).  Otherwise offs is
- * device int32 [n_seg+1] of multiples of 128 as mt_route_order makes them, and
- * rows offs[e]..offs[e+1]-1 of C are A's times B[e]; rows from offs[n_seg] on
- * are left as they were.  accumulate 1: C += (fp32 C only).  A scale byte of
- * 255 is NaN (the quantisers write none). */
+ * device int32 [n_seg+1], ascending multiples of 128 as mt_route_order makes
+ * them or a part of those, and rows offs[e]..offs[e+1]-1 of C are A's times
+ * B[e]; rows before offs[0] and from offs[n_seg] on are left as they were.  A
+ * last segment may end at M rounded up to 128; other starts are cut to block
+ * boundaries inside the operands.  accumulate 1: C += (fp32 C only; sums below
+ * 2^-126 may become zero).  A scale byte of 255 is NaN (the quantisers write
+ * none). */
 int32_t mt_gemm8(const mt_mat8* a, const mt_mat8* b, const int32_t* offs, int32_t n_seg, void* c, int32_t dtype,
                  int64_t ldc, int32_t accumulate, int32_t* status, void* stream);
 /* C[e] = A[:, offs[e]..offs[e+1]) B[:, same)^T: the reduction split into
  * segments, as the experts' weight gradients are (A [M, P], B [N, P], both
- * block_rows 1; C fp32 [n_seg][M][N], matrices M*ldc apart).  An empty segment
- * gives zeros (with accumulate: changes nothing). */
+ * block_rows 1; C fp32 [n_seg][M][N], matrices M*ldc apart).  offs as in
+ * mt_gemm8, P in M's place.  An empty segment gives zeros (with accumulate: changes nothing). */
 int32_t mt_gemm8_reduce(const mt_mat8* a, const mt_mat8* b, const int32_t* offs, int32_t n_seg, float* c, int64_t ldc,
                         int32_t accumulate, int32_t* status, void* stream);
 

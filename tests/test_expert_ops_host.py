@@ -168,3 +168,13 @@ def test_reference_quantiser_pins():
     want = torch.from_numpy(x).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
     assert np.array_equal(R.e4m3_code(x.astype(np.float64)), want)
     assert [R.scale_exponent(a) for a in (0.0, 448.0, 448.0001, 1.75, 1.7500001, 1e-300)] == [0, 0, 1, -8, -7, -126]
+
+
+def test_moves_of_no_tokens_need_no_rows(lib):
+    """The row numbers of no assignments have no storage; the other two do."""
+    r0 = lib.mt_route_rows(0, 2, 4)
+    assert lib.mt_dispatch(0, F32, 8, 0, 8, 2, 4, P, P, 0, r0, P, 8, 0) == B.MT_OK
+    assert lib.mt_dispatch8(0, F32, 8, 0, 2, 4, P, P, 0, mat(r0, 8), 0) == B.MT_OK
+    assert lib.mt_combine_bwd(0, F32, 8, P, 8, P, P, 0, r0, 0, 0, 2, 4, 8, P, 8, 0, 0) == B.MT_OK
+    assert lib.mt_dispatch(0, F32, 8, 0, 8, 2, 4, P, 0, 0, r0, P, 8, 0) == BAD
+    assert lib.mt_dispatch(0, F32, 8, 0, 8, 2, 4, 0, P, 0, r0, P, 8, 0) == BAD

@@ -387,6 +387,37 @@ def test_gemm_reduce(ops, offs, m, n):
     ops.check()
 
 
+@pytest.mark.parametrize("p", [1, 100, 300, 1263])
+def test_gemm_reduce_of_lengths_off_blocks(ops, p):
+    """The last segment ends at the length rounded up to 128: its last block is
+    a part of one."""
+    end = -(-p // 128) * 128
+    a, b = ops.quant8_t(rnd(1, p, 70)), ops.quant8_t(rnd(2, p, 200))
+    av, bv = R.value8(a), R.value8(b)
+    for offs in ([0, end], [0, end - 128, end], [0, 0, end, end]):
+        out = ops.gemm8_reduce(a, b, torch.tensor(offs, dtype=torch.int32, device="cuda"))
+        for i in range(len(offs) - 1):
+            s = slice(offs[i], min(offs[i + 1], p))
+            product_close(out[i], av[:, s], bv[:, s], torch.float32, max(s.stop - s.start, 0))
+    ops.check()
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("lo,hi", [(0, 2), (1, 3), (2, 5), (4, 5), (1, 2)])
+def test_gemm_by_some_of_the_experts(ops, lo, hi, dt):
+    """A run of consecutive experts of a routing: their rows alone are written."""
+    offs, n, k = [0, 256, 256, 640, 1152, 1280], 264, 200
+    a, b = ops.quant8(rnd(1, 1300, k)), ops.quant8(rnd(2, 5, n, k, std=0.02), 128)
+    o = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    some = ops.Tensor8(b.codes[lo:hi], b.scales[lo:hi], k, 128)
+    out = torch.full((1300, n), 7.0, dtype=DT[dt], device="cuda")
+    ops.gemm8(a, some, out=out, offs=o[lo:hi + 1])
+    want = ops.gemm8(a, b, dtype=DT[dt], offs=o)
+    s = slice(offs[lo], offs[hi])
+    assert torch.equal(out[s], want[s]) and (out[:s.start] == 7).all() and (out[s.stop:] == 7).all()
+    ops.check()
+
+
 def product64(got, a, b, k, dtype, before=None):
     """product_close on the device, for sizes that the host takes too long for."""
     av, bv = (torch.from_numpy(R.value8(t)).cuda() for t in (a, b))
@@ -798,3 +829,37 @@ def test_wrapper_refusals(ops):
         ops.dequant8(ops.quant8(x, block_rows=128))
     with pytest.raises(ValueError):
         ops.Tensor8(a.codes[:, :48], a.scales, 48)
+
+
+def test_no_tokens(ops):
+    """A routing of no tokens: every move runs and writes nothing."""
+    r = ops.Route(0, 2, 4).order(torch.empty(0, 2, dtype=torch.int32, device="cuda"))
+    assert (r.offs == 0).all() and (r.perm == -1).all()
+    x, w = torch.empty(0, 64, device="cuda"), torch.empty(0, 2, device="cuda")
+    xs = torch.full((r.rows, 64), 7.0, device="cuda")
+    assert r.dispatch(x, out=xs) is xs and (xs == 7).all()
+    r.dispatch8(x)
+    assert r.combine(xs, w).shape == (0, 64)
+    dy, dw = r.combine_bwd(x, xs, w)
+    assert dy.shape == (r.rows, 64) and dw.shape == (0, 2)
+    ops.check()
+
+
+def test_refusals_leave_the_device_as_it_was(ops, monkeypatch):
+    """With another device current, a refused argument raises before the device
+    changes, or changes it back."""
+    x, r = rnd(1, 128, 64), ops.Route(128, 2, 4)
+    a, saved, bad = ops.quant8(x), ops.quant8(x, halves=True), torch.zeros(2, dtype=torch.int32, device="cuda")
+    xs, w, t = torch.zeros(r.rows, 64, device="cuda"), torch.zeros(128, 2, device="cuda"), ops.quant8_t(x)
+    now = [7]
+    monkeypatch.setattr(ops, "_current", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "set_device", lambda d: now.__setitem__(0, d))
+    for call in (lambda: ops.quant8(x, n_rows=bad), lambda: ops.quant8_t(x, n_rows=bad),
+                 lambda: ops.dequant8(a, n_rows=bad), lambda: ops.gemm8_reduce(t, t, bad.view(1, 2)),
+                 lambda: ops.gemm8(a, a, offs=bad[:1]), lambda: ops.swiglu8(x, n_rows=bad),
+                 lambda: ops.swiglu8_bwd(x[:, :32], saved, n_rows=bad), lambda: r.order(bad),
+                 lambda: r.combine(xs, w.half()), lambda: r.combine_bwd(x, xs, w.half()),
+                 lambda: r.combine_bwd(x, xs, w, dw=w.half())):
+        with pytest.raises(ValueError):
+            call()
+        assert now == [7]

@@ -208,3 +208,28 @@ def test_layer_captured_while_an_eager_result_lives():
         torch.cuda.synchronize()
         for a, b in zip((o2, dx2, dw2, *gr2), (out, dx, dw, *grads)):
             assert torch.equal(a, b)
+
+
+def test_failed_forward_leaves_nothing_to_go_back_through():
+    """A forward that is refused halfway has changed the buffers of the one
+    before: backward asks for a new one.  (A layer of no
+    tokens runs too.)"""
+    from adamw_persistent_sm_gb300 import ExpertLayer8
+    t, k, e, d, f = 20, 2, 4, 64, 48
+    wg, wu, wd = rnd(1, e, f, d, std=0.05), rnd(2, e, f, d, std=0.05), rnd(3, e, d, f, std=0.05)
+    layer = ExpertLayer8(wg, wu, wd, t, k, torch.float32)
+    idx, w = torch.from_numpy(routing(t, k, e, 4)).cuda(), torch.softmax(rnd(7, t, k), 1)
+    x = rnd(5, t, d)
+    want = layer.forward(x, idx, w).clone()
+    for bad in (lambda: layer.forward(x[:, :32], idx, w), lambda: layer.forward(x, idx, w.bfloat16())):
+        layer.forward(x, idx, w)
+        with pytest.raises(ValueError):
+            bad()
+        with pytest.raises(RuntimeError):
+            layer.backward(x)
+    assert torch.equal(layer.forward(x, idx, w), want)
+    layer.backward(x)
+    none = ExpertLayer8(wg, wu, wd, 0, k, torch.float32)
+    assert none.forward(x[:0], idx[:0], w[:0]).shape == (0, d)
+    dx, dw, grads = none.backward(x[:0])
+    assert dx.shape == (0, d) and all((g == 0).all() for g in grads)

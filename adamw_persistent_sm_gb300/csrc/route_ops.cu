@@ -6,7 +6,7 @@ namespace {
 
 constexpr int RO_E = MT_MAX_EXPERTS;
 constexpr int RO_SMALL = 4096;        // assignments that one CTA sorts alone,
-constexpr int RO_CLUSTER = 1 << 18;   // that a cluster of sixteen sorts (65536: 13 us with eight, 9.4 with sixteen),
+constexpr int RO_CLUSTER = 1 << 16;   // that a cluster of sixteen sorts (65536: 6.3 us, a grid 7.5; 131072: 17 to 21, 15 to 17),
 constexpr int RO_CTAS = 16;
 constexpr int RO_CHUNK = 2048;        // and per CTA of a grid otherwise, or more:
 constexpr int RO_GRID = 1024;         // its CTAs each add up the counts of all
@@ -46,8 +46,8 @@ __device__ __forceinline__ unsigned ro_peers(int e) { return __match_any_sync(0x
 
 // Counting sort of assignments [a0, a1) by a CTA of NW warps, each warp taking
 // `span` consecutive ones (a multiple of 32): wh[warp][e] counts, then holds the
-// next row of expert e for the warp, so rows ascend with the assignment.  Two
-// reads of idx (the second from cache) instead of keeping choices in registers.
+// next row of expert e for the warp, so rows ascend with the assignment.  Chunks
+// of a grid may be long: two reads of idx, the second from cache.
 template <int NW>
 struct RoSmem {
   int wh[NW][RO_E];
@@ -106,10 +106,8 @@ __device__ __forceinline__ void ro_pads(const int* cnt, const int* offs, int E, 
   for (long long r = offs[E] + t; r < rows; r += nt) perm[r] = -1;
 }
 
-__device__ __forceinline__ void ro_cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void ro_cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void ro_cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ int ro_remote(const int* p, int cta) {
   uint32_t a;
   int v;
@@ -119,18 +117,38 @@ __device__ __forceinline__ int ro_remote(const int* p, int cta) {
 }
 
 // Up to RO_SMALL assignments one CTA, up to RO_CLUSTER a cluster of sixteen whose
-// CTAs read one another's counts in shared memory: one launch, bound by the two
-// trips to idx (a counting and a placing launch over the whole grid took 20 us
-// for 65536 assignments).
+// CTAs read one another's counts in shared memory: one launch.  A lane keeps its
+// choices and their places among the warp's equal ones in registers: idx is read
+// once, all loads in flight, and the counts grow one time (65536 assignments 6.3
+// us, 7.5 with a counting and a placing pass; 1024: 2.8 and 4.2).  Bound by
+// latency: the choices' trip, the barriers, the serial counts of a warp.
 template <int NC>
 __global__ void __launch_bounds__(1024) ro_sort(const int* idx, int n, int E, long long rows, int* offs, int* perm,
                                                 int* row, int* status) {
   ops_begin();
+  constexpr int PER = (NC > 1 ? RO_CLUSTER : RO_SMALL) / (NC * 1024);   // choices of a lane, at most
   __shared__ RoSmem<32> s;
-  const int tid = threadIdx.x, warp = tid >> 5, cta = blockIdx.x;
+  __shared__ int start[RO_E];            // first row of this CTA's part of each segment
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
   const int span = ((n + 32 * NC - 1) / (32 * NC) + 31) & ~31;
   const int w0 = min((cta * 32 + warp) * span, n), w1 = min(w0 + span, n);
-  ro_count(s, idx, w0, w1, E, status);
+  int mine[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) mine[j] = w0 + 32 * j + lane < w1 ? idx[w0 + 32 * j + lane] : -1;
+  for (int e = lane; e < RO_E; e += 32) s.wh[warp][e] = 0;
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    if (32 * j >= span) break;
+    const int e = ro_expert(mine[j], E, status);
+    const unsigned peers = ro_peers(e);
+    int c = 0;
+    if (e >= 0) c = s.wh[warp][e];
+    __syncwarp();
+    if (e >= 0 && lane == __ffs(peers) - 1) s.wh[warp][e] = c + __popc(peers);
+    __syncwarp();
+    mine[j] = e < 0 ? -1 : (c + __popc(peers & ((1u << lane) - 1u))) * RO_E + e;
+  }
   __syncthreads();
   if (tid < RO_E) {
     int c = 0;
@@ -144,7 +162,8 @@ __global__ void __launch_bounds__(1024) ro_sort(const int* idx, int n, int E, lo
   }
   int base = 0;
   if (NC > 1) {
-    ro_cluster_sync();
+    ro_cluster_arrive();
+    ro_cluster_wait();
     if (tid < RO_E) {
       int all = 0;
 #pragma unroll
@@ -155,6 +174,8 @@ __global__ void __launch_bounds__(1024) ro_sort(const int* idx, int n, int E, lo
       }
       s.cnt[tid] = all;
     }
+    __syncwarp();
+    ro_cluster_arrive();                 // the counts have been read
   } else if (tid < RO_E) {
     s.cnt[tid] = s.before[tid];
   }
@@ -162,14 +183,23 @@ __global__ void __launch_bounds__(1024) ro_sort(const int* idx, int n, int E, lo
   ro_offsets(s.cnt, E, s.offs);
   __syncthreads();
   if (cta == 0 && tid <= E) offs[tid] = s.offs[tid];
-  if (NC > 1) ro_cluster_sync();         // the counts have been read
-  if (tid < E) s.before[tid] = s.offs[tid] + base;
+  if (tid < E) start[tid] = s.offs[tid] + base;
   __syncthreads();
-  for (int i = tid; i < 32 * RO_E; i += 1024)
-    if ((i & (RO_E - 1)) < E) s.wh[i / RO_E][i & (RO_E - 1)] += s.before[i & (RO_E - 1)];
-  __syncthreads();
-  ro_place(s, idx, w0, w1, E, status, perm, row);
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int a = w0 + 32 * j + lane;
+    if (a < w1) {
+      const int e = mine[j] & (RO_E - 1);
+      int r = -1;
+      if (mine[j] >= 0) {
+        r = start[e] + s.wh[warp][e] + mine[j] / RO_E;
+        perm[r] = a;
+      }
+      row[a] = r;
+    }
+  }
   ro_pads(s.cnt, s.offs, E, rows, perm, cta * 1024 + tid, NC * 1024);
+  if (NC > 1) ro_cluster_wait();         // no CTA's shared memory goes while another may read it
 }
 
 // Many: every CTA counts its chunk, then every CTA sums the counts before its
@@ -191,24 +221,38 @@ __global__ void __launch_bounds__(256) ro_scatter(const int* idx, long long n, i
                                                   int* offs, int* perm, int* row, int* status) {
   ops_begin();
   __shared__ RoSmem<8> s;
-  __shared__ int part[2][4][RO_E];
-  const int tid = threadIdx.x, e = tid & (RO_E - 1), p = tid / RO_E;
+  // counts come four experts per load: a thread adds up every sixteenth CTA's
+  __shared__ __align__(16) int part[2][16][RO_E];
+  const int tid = threadIdx.x, e = (tid & 15) * 4, p = tid >> 4;
   const long long a0 = (long long)blockIdx.x * chunk + (tid >> 5) * (chunk / 8);
   const long long a1 = a0 + chunk / 8 < n ? a0 + chunk / 8 : n;
-  int all = 0, mine = 0;
-#pragma unroll 8
-  for (int c = p; c < (int)gridDim.x; c += 4) {
-    const int h = hist[(long long)c * RO_E + e];
-    all += h;
-    if (c < (int)blockIdx.x) mine += h;
+  int4 all = make_int4(0, 0, 0, 0), mine = all;
+  for (int c0 = p; c0 < (int)gridDim.x; c0 += 128) {
+    int4 h[8];                           // eight loads in flight, for any number of CTAs
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      h[j] = c0 + 16 * j < (int)gridDim.x ? *reinterpret_cast<const int4*>(hist + (long long)(c0 + 16 * j) * RO_E + e)
+                                          : make_int4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int m = c0 + 16 * j < (int)blockIdx.x ? -1 : 0;
+      all.x += h[j].x; all.y += h[j].y; all.z += h[j].z; all.w += h[j].w;
+      mine.x += h[j].x & m; mine.y += h[j].y & m; mine.z += h[j].z & m; mine.w += h[j].w & m;
+    }
   }
-  part[0][p][e] = all;
-  part[1][p][e] = mine;
+  *reinterpret_cast<int4*>(&part[0][p][e]) = all;
+  *reinterpret_cast<int4*>(&part[1][p][e]) = mine;
   ro_count(s, idx, a0, a1, E, status);
   __syncthreads();
   if (tid < RO_E) {
-    s.cnt[tid] = part[0][0][tid] + part[0][1][tid] + part[0][2][tid] + part[0][3][tid];
-    s.before[tid] = part[1][0][tid] + part[1][1][tid] + part[1][2][tid] + part[1][3][tid];
+    int a = 0, b = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      a += part[0][i][tid];
+      b += part[1][i][tid];
+    }
+    s.cnt[tid] = a;
+    s.before[tid] = b;
   }
   __syncthreads();
   ro_offsets(s.cnt, E, s.offs);

@@ -81,6 +81,13 @@ def test_route_order(ops, t, k, e, how):
     ops.check()
 
 
+@pytest.mark.parametrize("n", [31, 33, 1023, 4095, 4096, 4097, 16385, 65535, 65536, 65537, 98305, 262145])
+@pytest.mark.parametrize("how", ["dropped", "one"])
+def test_route_order_at_the_kernels_limits(ops, n, how):
+    """Sizes around those where one CTA, a cluster and a grid take over."""
+    test_route_order(ops, n, 1, 5, how)
+
+
 def test_route_order_of_many_tokens(ops):
     """Three million assignments (a grid of CTAs with long chunks), against a
     stable sort on the device."""

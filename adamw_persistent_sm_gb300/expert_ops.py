@@ -148,9 +148,12 @@ class Tensor8:
         self.device, self._dev = codes.device, codes.get_device()
         _status_word(self._dev)
         self.rows, self.batch, self.shape = rows, batch, (*codes.shape[:-1], cols)
-        # an empty tensor has no storage: any address stands in for it
-        self._mat = B.mt_mat8(codes.data_ptr() or 16, scales.data_ptr() or 16, rows, cols, ld, lds, block_rows,
-                              max(batch, 1), int(halves), 0)
+        # Matrices of no rows have no storage and nothing reads them: any address
+        # stands in.  A stack of no matrices keeps its batch of 0, which every
+        # entry point refuses: its rows would be read at that address.
+        none = 16 if rows == 0 else 0
+        self._mat = B.mt_mat8(codes.data_ptr() or none, scales.data_ptr() or none, rows, cols, ld, lds, block_rows,
+                              batch, int(halves), 0)
         self._ref = C.byref(self._mat)
 
     def __getitem__(self, i: int) -> "Tensor8":

@@ -178,3 +178,51 @@ def test_moves_of_no_tokens_need_no_rows(lib):
     assert lib.mt_combine_bwd(0, F32, 8, P, 8, P, P, 0, r0, 0, 0, 2, 4, 8, P, 8, 0, 0) == B.MT_OK
     assert lib.mt_dispatch(0, F32, 8, 0, 8, 2, 4, P, 0, 0, r0, P, 8, 0) == BAD
     assert lib.mt_dispatch(0, F32, 8, 0, 8, 2, 4, 0, P, 0, r0, P, 8, 0) == BAD
+
+
+class OnDevice:
+    """A host tensor that says it lies on cuda:0, for the arguments a wrapper passes on."""
+
+    def __init__(self, t):
+        self._t, self.device = t, torch.device("cuda", 0)
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+    def get_device(self):
+        return 0
+
+
+def described(monkeypatch, codes, scales, cols, **kw):
+    """Tensor8's description of host buffers of these shapes."""
+    monkeypatch.setattr(ops, "_status_word", lambda dev: P)
+    return ops.Tensor8(OnDevice(torch.zeros(codes, dtype=torch.uint8)), OnDevice(torch.zeros(scales, dtype=torch.uint8)),
+                       cols, **kw)
+
+
+def test_empty_stacks_have_no_address(lib, monkeypatch):
+    """A stack of no matrices has no storage: whatever takes or fills one is
+    refused on the host, and no address stands in for it.  (A matrix of no rows
+    is valid and nothing reads it.)"""
+    rows = lib.mt_route_rows(4, 2, 4)
+    a = described(monkeypatch, (0, 64, 256), (0, 64, 2), 256)
+    b = described(monkeypatch, (0, 64, 256), (0, 1, 2), 256, block_rows=128)
+    s = described(monkeypatch, (0, 64, 512), (0, 64, 4), 512, halves=True)
+    x = described(monkeypatch, (0, rows, 16), (0, rows, 1), 8)
+    for t in (a, b, s, x):
+        assert t._mat.batch == 0 and not t._mat.codes and not t._mat.scales
+    full, held = mat(), mat(64, 512, halves=1)
+    for st in (lib.mt_gemm8(a._ref, full, 0, 0, P, F32, 64, 0, P, 0), lib.mt_gemm8(full, a._ref, 0, 0, P, F32, 64, 0, P, 0),
+               lib.mt_gemm8(full, b._ref, 0, 0, P, F32, 64, 0, P, 0), lib.mt_gemm8(full, b._ref, P, 1, P, F32, 64, 0, P, 0),
+               lib.mt_gemm8(full, b._ref, P, 0, P, F32, 64, 0, P, 0),
+               lib.mt_gemm8_reduce(a._ref, full, P, 1, P, 64, 0, P, 0), lib.mt_gemm8_reduce(full, a._ref, P, 1, P, 64, 0, P, 0),
+               lib.mt_quant8(P, F32, 256, 0, a._ref, 0), lib.mt_quant8(P, F32, 256, 0, b._ref, 0),
+               lib.mt_quant8_t(0, 0, 0, a._ref, 0, mat(256, 64), 0), lib.mt_quant8_t(P, F32, 64, None, 0, a._ref, 0),
+               lib.mt_dequant8(a._ref, 0, P, F32, 256, 0), lib.mt_swiglu8(P, F32, 512, 0, full, s._ref, 0),
+               lib.mt_swiglu8(P, F32, 512, 0, a._ref, held, 0), lib.mt_swiglu8_bwd(P, F32, 256, s._ref, 0, P, 512, 0, 0, 0),
+               lib.mt_dispatch8(P, F32, 8, 4, 2, 4, P, P, P, x._ref, 0)):
+        assert st == BAD
+    none = described(monkeypatch, (0, 256), (0, 2), 256)
+    assert none._mat.batch == 1 and none._mat.codes and none._mat.scales
+    assert lib.mt_gemm8(none._ref, full, 0, 0, 0, F32, 64, 0, P, 0) == B.MT_OK
+    assert lib.mt_quant8(0, F32, 256, 0, none._ref, 0) == B.MT_OK

@@ -18,6 +18,7 @@ Matrices may be views whose rows are contiguous (any row stride).
 from __future__ import annotations
 
 import ctypes as C
+import threading
 
 import torch
 
@@ -25,6 +26,7 @@ from . import binding as B
 
 _DTYPES = {torch.float32: B.MT_DT_FP32, torch.bfloat16: B.MT_DT_BF16}
 _status: dict = {}          # device index -> (int32 [2] status words, their address)
+_status_lock = threading.Lock()
 
 
 def _error(what: str, st: int) -> Exception:
@@ -47,9 +49,12 @@ def _status_word(dev: int) -> int:
     if t is None:
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("the first operator, Route or Tensor8 on a device comes before a stream capture")
-        t = torch.zeros(2, dtype=torch.int32, device=f"cuda:{dev}")
-        torch.cuda.synchronize(dev)         # once per device: zeroed before any other stream uses it
-        t = _status[dev] = (t, t.data_ptr())
+        with _status_lock:                      # one pair, however many threads come first
+            t = _status.get(dev)
+            if t is None:
+                t = torch.zeros(2, dtype=torch.int32, device=f"cuda:{dev}")
+                torch.cuda.synchronize(dev)     # once per device: zeroed before any other stream uses it
+                t = _status[dev] = (t, t.data_ptr())
     return t[1]
 
 

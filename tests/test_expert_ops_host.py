@@ -226,3 +226,33 @@ def test_empty_stacks_have_no_address(lib, monkeypatch):
     assert none._mat.batch == 1 and none._mat.codes and none._mat.scales
     assert lib.mt_gemm8(none._ref, full, 0, 0, 0, F32, 64, 0, P, 0) == B.MT_OK
     assert lib.mt_quant8(0, F32, 256, 0, none._ref, 0) == B.MT_OK
+
+
+def test_status_words_are_made_once_by_any_number_of_threads(monkeypatch):
+    """Threads that use a device for the first time together get the same
+    status words: a second pair would leave the first address, which a launch
+    may already have, to the allocator."""
+    import threading
+    made, inside = [], threading.Event()
+
+    def zeros(*args, **kw):
+        made.append(torch.empty(2, dtype=torch.int32))
+        return made[-1]
+
+    def synchronize(dev):                  # lets the other threads run, as the real one does
+        inside.set()
+        threading.Event().wait(0.2)
+
+    monkeypatch.setattr(ops, "_status", {})
+    monkeypatch.setattr(ops.torch, "zeros", zeros)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "synchronize", synchronize)
+    got = []
+    threads = [threading.Thread(target=lambda: got.append(ops._status_word(0))) for _ in range(4)]
+    threads[0].start()
+    assert inside.wait(10)
+    for t in threads[1:]:
+        t.start()
+    for t in threads:
+        t.join(10)
+    assert len(made) == 1 and got == [made[0].data_ptr()] * 4

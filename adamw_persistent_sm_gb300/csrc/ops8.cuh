@@ -152,7 +152,11 @@ __device__ __forceinline__ float ops_scale(uint32_t top, uint32_t* byte) {
   *byte = x - 8;
   return __uint_as_float((262u - x) << 23);
 }
-__device__ __forceinline__ float ops_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// What a scale byte stands for, as the products read it: 2^(byte - 127), subnormal
+// for 0, and NaN for 255 - the two whose bits need more than the exponent's place.
+__device__ __forceinline__ float ops_byte_scale(uint32_t byte) {
+  return __uint_as_float(byte << 23 | (((byte + 1) & 0xff) <= 1 ? 0x400000u : 0u));
+}
 // four e4m3 codes of v * s (round to nearest even; |v * s| <= 448 or NaN); the
 // products two at a time (one issue slot for both)
 __device__ __forceinline__ uint32_t ops_codes4(float v0, float v1, float v2, float v3, float s) {

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(256) dequant_k(Mat8 a, const int* n_rows, int 
     const int part = ch / chunks, c = (ch - part * chunks) * 256 + lane * 8, base = part * pcols;
     if (c >= pcols) continue;
     uint2 q[4];
-    int s[4];
+    uint32_t s[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const long long r = min(r0 + i, lim - 1);
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(256) dequant_k(Mat8 a, const int* n_rows, int 
     for (int i = 0; i < 4; ++i)
       if (r0 + i < lim) {
         float v[8];
-        ops_values8(q[i], ops_pow2(s[i] - 127), v);
+        ops_values8(q[i], ops_byte_scale(s[i]), v);
         ops_st8<VEC>(out + (long long)(r0 + i) * ldo + base, c, pcols, v);
       }
   }
@@ -128,7 +128,7 @@ struct Tile8<uint8_t> {
     w.s = 1.f;
     if (VEC != 2 && c >= n) return;
     w.q = ops_ld_codes<VEC>(a.q + r * a.ld, c, n, true);
-    w.s = ops_pow2((int)a.s[r * a.lds + (c >> 7)] - 127);
+    w.s = ops_byte_scale(a.s[r * a.lds + (c >> 7)]);
   }
   static __device__ __forceinline__ void zero(Raw& w) {
     w.q = make_uint2(0, 0);
@@ -401,9 +401,9 @@ __global__ void __launch_bounds__(256) swiglu_bwd_k(const T* da, long long ldda,
     ops_ld8<VEC>(da + r * ldda, c, F, d);
     const uint2 qg = ops_ld_codes<VEC>(sv.q + r * sv.ld, c, F, true);
     const uint2 qu = ops_ld_codes<VEC>(sv.q + r * sv.ld + F, c, F, v8);
-    const int eg = sv.s[r * sv.lds + (c >> 7)], eu = sv.s[r * sv.lds + nb + (c >> 7)];
-    ops_values8(qg, ops_pow2(eg - 127), g);
-    ops_values8(qu, ops_pow2(eu - 127), u);
+    const uint32_t eg = sv.s[r * sv.lds + (c >> 7)], eu = sv.s[r * sv.lds + nb + (c >> 7)];
+    ops_values8(qg, ops_byte_scale(eg), g);
+    ops_values8(qu, ops_byte_scale(eu), u);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float s = sigmoid_f(g[j]), gs = g[j] * s, x = d[j];

@@ -423,8 +423,9 @@ enum { MT_DT_FP32 = 0, MT_DT_BF16 = 1 };   /* element types, numbered as MT_PREC
  * A matrix held in 8 bits: e4m3 codes and one power-of-two scale per block of
  * 128 elements (host struct, copied at call time; the buffers are the
  * caller's device memory).  Element (b, r, c) is
- *   e4m3(codes[(b*rows + r)*ld + c]) * 2^(scale byte - 127),
- * its scale byte lying at
+ *   e4m3(codes[(b*rows + r)*ld + c]) * 2^(scale byte - 127)
+ * for bytes 0 to 254, NaN for 255 (the quantisers below write 1 to 247), its
+ * scale byte lying at
  *   scales[(b*rows + r)*lds + c/128]                    block_rows == 1
  *   scales[(b*ceil(rows/128) + r/128)*lds + c/128]      block_rows == 128.
  * halves == 1 (block_rows 1, cols even): the columns are two parts of cols/2,
@@ -521,8 +522,7 @@ int32_t mt_dequant8(const mt_mat8* a, const int32_t* n_rows, void* out, int32_t 
  * B[e]; rows before offs[0] and from offs[n_seg] on are left as they were.  A
  * last segment may end at M rounded up to 128; other starts are cut to block
  * boundaries inside the operands.  accumulate 1: C += (fp32 C only; sums below
- * 2^-126 may become zero).  A scale byte of 255 is NaN (the quantisers write
- * none). */
+ * 2^-126 may become zero). */
 int32_t mt_gemm8(const mt_mat8* a, const mt_mat8* b, const int32_t* offs, int32_t n_seg, void* c, int32_t dtype,
                  int64_t ldc, int32_t accumulate, int32_t* status, void* stream);
 /* C[e] = A[:, offs[e]..offs[e+1]) B[:, same)^T: the reduction split into

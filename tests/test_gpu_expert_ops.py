@@ -870,3 +870,59 @@ def test_refusals_leave_the_device_as_it_was(ops, monkeypatch):
         with pytest.raises(ValueError):
             call()
         assert now == [7]
+
+
+def with_bytes(ops, rows, cols, byte, halves=False, below=0x40):
+    """Codes over the positive and negative ones below `below`, all scales one byte."""
+    t = ops.empty8(rows, cols, halves=halves)
+    g = torch.Generator().manual_seed(byte + 1)
+    q = torch.randint(0, below, t.codes.shape, generator=g) + 128 * torch.randint(0, 2, t.codes.shape, generator=g)
+    t.codes.copy_(q.to(torch.uint8).cuda())
+    t.scales.fill_(byte)
+    return t
+
+
+@pytest.mark.parametrize("byte", [0, 1, 127, 254, 255])
+def test_scale_bytes_mean_the_same_everywhere(ops, byte):
+    """Bytes over their whole range stand for 2^(byte - 127), 255 for NaN, in
+    every operator that reads codes as they do in products: restored values
+    are exact (0 gives numbers down to 2^-136, subnormal in fp32), and so are
+    the codes of their transpose."""
+    rows, cols = 130, 200
+    t = with_bytes(ops, rows, cols, byte)
+    val = R.value8(t) if byte < 255 else np.full((rows, cols), np.nan)
+    for dtype in (torch.float32, torch.bfloat16):
+        assert np.array_equal(R.as64(ops.dequant8(t, dtype)), R.rounded(val, dtype), equal_nan=True)
+    codes_equal(ops.quant8_t(t), R.quant(val.T), "columns")
+    codes_equal(ops.quant8_t(t, block_rows=128), R.quant(val.T, 128), "blocks")
+    h = with_bytes(ops, rows, cols, byte, halves=True)
+    val = R.value8(h) if byte < 255 else np.full((rows, cols), np.nan)
+    assert np.array_equal(R.as64(ops.dequant8(h, torch.float32)), R.rounded(val, torch.float32), equal_nan=True)
+    eye = ops.quant8(torch.eye(cols, device="cuda"))
+    c = R.as64(ops.gemm8(t, eye, dtype=torch.float32))
+    if byte == 255:
+        assert np.isnan(c).all()
+    elif byte > 0:                       # a product's sums are normal numbers
+        assert np.array_equal(c, R.value8(t))
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("bg,bu", [(0, 127), (127, 0), (0, 0), (1, 1), (255, 127), (127, 255)])
+def test_swiglu_backward_reads_every_scale_byte(ops, bg, bu, dt):
+    """g or u under the least scales, with gradients large enough that the
+    results are normal numbers: the bound of test_swiglu_backward, and half a
+    step of the subnormal products on the way (2^-150 each, times dact)."""
+    rows, width, dtype = 20, 136, DT[dt]
+    saved = with_bytes(ops, rows, 2 * width, 0, halves=True)
+    saved.scales[:, :2], saved.scales[:, 2:] = bg, bu
+    da = rnd(3, rows, width, std=2.0 ** 60, dtype=dtype)
+    act = torch.zeros(rows, width, dtype=dtype, device="cuda")
+    dgu = ops.swiglu8_bwd(da, saved, act=act)
+    g, u = np.split(R.value8(saved), 2, axis=1)
+    g, u = (np.full_like(v, np.nan) if b == 255 else v for v, b in ((g, bg), (u, bu)))
+    d, s = R.as64(da), R.sigmoid(g)
+    rel = (np.abs(g) + 8) * 2.0 ** -22
+    sub = 2.0 ** -149 * (1 + np.abs(d)) * (1 + np.abs(u)) + (0 if dt == "fp32" else 2.0 ** -134)
+    for got, ref, mag in ((dgu[:, :width], d * u * s * (1 + g * (1 - s)), np.abs(d * u) * (s + np.abs(g) * s)),
+                          (dgu[:, width:], d * g * s, np.abs(d * g * s)), (act, g * s * u, np.abs(g * s * u))):
+        close(got, ref, rel * mag + sub + HALF_STEP[dtype] * np.abs(ref) * (1 + 1e-2))

@@ -5,10 +5,11 @@ saved activations.
 
 Between forward and backward the layer keeps, per expert row, d + 2 F bytes of
 codes (its input, and g and u) and the down product's rows for the routing
-weights' gradient.  Every product takes e4m3 operands with a scale per block of
-128: along the features for outputs and input gradients (weights in 128 x 128
-blocks, quantised once per :meth:`ExpertLayer8.refresh` in both orientations),
-along the tokens for weight gradients.  Weight gradients are fp32.
+weights' gradient, and a copy of the routing weights.  Every product takes e4m3
+operands with a scale per block of 128: along the features for outputs and input
+gradients (weights in 128 x 128 blocks, quantised once per
+:meth:`ExpertLayer8.refresh` in both orientations), along the tokens for weight
+gradients.  Weight gradients are fp32.
 """
 from __future__ import annotations
 
@@ -39,6 +40,7 @@ class ExpertLayer8:
         # kept from forward to backward
         self.xs8, self.saved = ops.empty8(rows, d, dev), ops.empty8(rows, 2 * f, dev, halves=True)
         self.y = torch.empty((rows, d), dtype=dtype, device=dev)
+        self._w = torch.empty((n_tokens, top_k), dtype=torch.float32, device=dev)
         # passing buffers
         self.act8 = ops.empty8(rows, f, dev)
         self.gu = torch.empty((rows, 2 * f), dtype=dtype, device=dev)
@@ -66,7 +68,8 @@ class ExpertLayer8:
         ops.swiglu8(self.gu, act=self.act8, saved=self.saved if save else None, n_rows=r.offs[-1:])
         ops.gemm8(self.act8, self.w_down, out=self.y, offs=r.offs)
         out = r.combine(self.y, w, out=out)
-        self.w = w if save else None
+        if save:                            # a copy: the caller's may hold the next microbatch's by then
+            self.w = self._w.copy_(w.detach())
         return out
 
     def backward(self, dout: torch.Tensor, grads: tuple[torch.Tensor, torch.Tensor, torch.Tensor] | None = None,

@@ -233,3 +233,32 @@ def test_failed_forward_leaves_nothing_to_go_back_through():
     assert none.forward(x[:0], idx[:0], w[:0]).shape == (0, d)
     dx, dw, grads = none.backward(x[:0])
     assert dx.shape == (0, d) and all((g == 0).all() for g in grads)
+
+
+def small_layer(dtype=torch.float32, t=60, k=2, e=4, d=64, f=48):
+    from adamw_persistent_sm_gb300 import ExpertLayer8
+    weights = rnd(1, e, f, d, std=0.05), rnd(2, e, f, d, std=0.05), rnd(3, e, d, f, std=0.05)
+    layer = ExpertLayer8(*weights, t, k, dtype)
+    idx, w = torch.from_numpy(routing(t, k, e, 4)).cuda(), torch.softmax(rnd(7, t, k), 1)
+    return layer, weights, rnd(5, t, d, dtype=dtype), idx, w, rnd(6, t, d, dtype=dtype)
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_weights_rewritten_between_the_passes(captured):
+    """backward goes through the routing weights that forward applied, also
+    where the caller has put the next microbatch's into the same tensor."""
+    layer, _, x, idx, w, dout = small_layer(torch.bfloat16)
+    layer.forward(x, idx, w)
+    dx, dw, grads = layer.backward(dout)
+    layer.forward(x, idx, w.clone().requires_grad_())
+    assert not layer.w.requires_grad and torch.equal(layer.w, w)       # and no history grows with the passes
+    layer.forward(x, idx, w)
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            layer.forward(x, idx, w)
+        g.replay()
+    w.fill_(float("nan"))
+    dx2, dw2, grads2 = layer.backward(dout)
+    assert torch.equal(dw, dw2)
+    assert torch.equal(dx, dx2) and all(torch.equal(a, b) for a, b in zip(grads, grads2))

@@ -26,12 +26,11 @@ class ExpertLayer8:
 
     def __init__(self, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, n_tokens: int, top_k: int,
                  dtype: torch.dtype = torch.bfloat16):
-        if w_gate.dim() != 3 or w_up.shape != w_gate.shape or \
-                tuple(w_down.shape) != (w_gate.shape[0], w_gate.shape[2], w_gate.shape[1]):
-            raise ValueError(f"expected [E, F, d], [E, F, d] and [E, d, F], got {tuple(w_gate.shape)}, "
-                             f"{tuple(w_up.shape)} and {tuple(w_down.shape)}")
+        if w_gate.dim() != 3:
+            raise ValueError(f"w_gate: expected [E, F, d], got {tuple(w_gate.shape)}")
         self.n_experts, self.width, self.d = w_gate.shape
         self.device, self.dtype = w_gate.device, dtype
+        self._check_weights(w_gate, w_up, w_down)
         e, f, d, dev = self.n_experts, self.width, self.d, self.device
         self.route = ops.Route(n_tokens, top_k, e, dev)
         rows = self.route.rows
@@ -48,9 +47,21 @@ class ExpertLayer8:
         self._bwd = None
         self.refresh(w_gate, w_up, w_down)
 
+    def _check_weights(self, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor) -> None:
+        e, f, d = self.n_experts, self.width, self.d
+        for t, what, shape in ((w_gate, "w_gate", (e, f, d)), (w_up, "w_up", (e, f, d)), (w_down, "w_down", (e, d, f))):
+            if tuple(t.shape) != shape or t.device != self.device or t.dtype not in (torch.float32, torch.bfloat16):
+                raise ValueError(f"{what}: expected float32 or bfloat16 {shape} on {self.device}, got {t.dtype} "
+                                 f"{tuple(t.shape)} on {t.device}")
+        # read where it lies; gate and up are copied together first
+        ops._as_matrix(w_down, "w_down", w_down.get_device())
+
     def refresh(self, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor) -> None:
-        """Quantise the weights (again, after an optimizer step)."""
-        gu = torch.cat([w_gate, w_up], 1)
+        """Quantise the weights (again, after an optimizer step).  Weights of other
+        shapes than the layer was made with, or of another device or type, are
+        refused before any of them is written."""
+        self._check_weights(w_gate, w_up, w_down)
+        gu = torch.cat([w_gate.detach(), w_up.detach()], 1)
         ops.quant8(gu, 128, out=self.w_gu)
         ops.quant8_t(gu, 128, out=self.w_gu_t)
         ops.quant8(w_down, 128, out=self.w_down)

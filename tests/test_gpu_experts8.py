@@ -262,3 +262,25 @@ def test_weights_rewritten_between_the_passes(captured):
     dx2, dw2, grads2 = layer.backward(dout)
     assert torch.equal(dw, dw2)
     assert torch.equal(dx, dx2) and all(torch.equal(a, b) for a, b in zip(grads, grads2))
+
+
+def test_refused_refresh_leaves_the_weights_alone():
+    """Weights of other shapes, types or devices are refused before any is
+    quantised - also a gate and an up projection whose rows add up to the same
+    number - and the layer goes on with those it has."""
+    layer, (wg, wu, wd), x, idx, w, _ = small_layer()
+    want = layer.forward(x, idx, w).clone()
+    more, less = torch.cat([wg, wg[:, :1]], 1) * 2, wu[:, 1:] * 2
+    for bad in ((more, less, wd), (wg * 2, wu * 2, wd[:, :, :-1]), (wg * 2, wu * 2, wd.double()), (wg * 2, wu.half(), wd),
+                (wg * 2, wu * 2, wd.cpu()), (wg.cpu(), wu.cpu(), wd), (wg * 2, wu * 2, wd.transpose(1, 2)),
+                (wg * 2, wu * 2, wd[:2]), (wg[0], wu[0], wd[0])):
+        with pytest.raises((ValueError, TypeError)):
+            layer.refresh(*bad)
+        assert torch.equal(layer.forward(x, idx, w), want)
+    both = torch.cat([wg, wu], 1)          # two views of one tensor are as good as two tensors
+    layer.refresh(both[:, :48], both[:, 48:], wd)
+    assert torch.equal(layer.forward(x, idx, w), want)
+    layer.refresh(wg * 2, wu * 2, wd.bfloat16())
+    assert not torch.equal(layer.forward(x, idx, w), want)
+    layer.refresh(wg, wu, wd)
+    assert torch.equal(layer.forward(x, idx, w), want)

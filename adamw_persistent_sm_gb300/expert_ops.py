@@ -300,6 +300,13 @@ def gemm8(a: Tensor8, b: Tensor8, out: torch.Tensor | None = None, offs: torch.T
     return out
 
 
+def _sums(out: torch.Tensor, what: str, dev: int, shape: tuple) -> int:
+    """Checks an output of :func:`gemm8_reduce`; its row stride."""
+    if out.dim() != 3 or out.dtype != torch.float32 or tuple(out.shape) != shape:
+        raise ValueError(f"{what}: expected float32 {shape}, got {out.dtype} {tuple(out.shape)}")
+    return _as_matrix(out, what, dev)[1]
+
+
 def gemm8_reduce(a: Tensor8, b: Tensor8, offs: torch.Tensor, out: torch.Tensor | None = None,
                  accumulate: bool = False) -> torch.Tensor:
     """out[e] = a[:, offs[e]:offs[e+1]] b[:, same]^T in fp32: a [M, P], b [N, P]."""
@@ -311,9 +318,7 @@ def gemm8_reduce(a: Tensor8, b: Tensor8, offs: torch.Tensor, out: torch.Tensor |
         if accumulate:
             raise ValueError("accumulate needs out")
         out = torch.empty((max(seg, 0), a.rows, b.rows), dtype=torch.float32, device=dev)
-    if out.dim() != 3 or out.dtype != torch.float32 or tuple(out.shape) != (seg, a.rows, b.rows):
-        raise ValueError(f"out: expected float32 {(seg, a.rows, b.rows)}, got {out.dtype} {tuple(out.shape)}")
-    _, ldc = _as_matrix(out, "out", dev)
+    ldc = _sums(out, "out", dev, (seg, a.rows, b.rows))
     po = _ints(offs, "offs", dev, (seg + 1,))
     here = _current()
     if here != dev:

@@ -87,14 +87,20 @@ class ExpertLayer8:
                  accumulate: bool = False) -> tuple[torch.Tensor, torch.Tensor, tuple]:
         """Gradients after a saving :meth:`forward`: dx [n_tokens, d], dw
         [n_tokens, top_k] and (w_gate's, w_up's, w_down's), float32 in the
-        weights' shapes - written into ``grads``, or added with ``accumulate``."""
+        weights' shapes - written into ``grads``, or added with ``accumulate``.
+        A refused call has written none of them."""
         if self.w is None:
             raise RuntimeError("backward needs a forward with save=True before it")
         r, f, d, e, dev = self.route, self.width, self.d, self.n_experts, self.device
+        shapes = ((e, f, d), (e, f, d), (e, d, f))
         if grads is None:
             if accumulate:
                 raise ValueError("accumulate needs grads")
-            grads = tuple(torch.empty(s, dtype=torch.float32, device=dev) for s in ((e, f, d), (e, f, d), (e, d, f)))
+            grads = tuple(torch.empty(s, dtype=torch.float32, device=dev) for s in shapes)
+        if len(grads) != 3:
+            raise ValueError(f"grads: expected w_gate's, w_up's and w_down's, got {len(grads)}")
+        for g, what, s in zip(grads, ("w_gate's gradient", "w_up's gradient", "w_down's gradient"), shapes):
+            ops._sums(g, what, r._dev, s)
         if self._bwd is None:
             rows = r.rows
             like = lambda c: torch.empty((rows, c), dtype=self.dtype, device=dev)  # noqa: E731

@@ -284,3 +284,31 @@ def test_refused_refresh_leaves_the_weights_alone():
     assert not torch.equal(layer.forward(x, idx, w), want)
     layer.refresh(wg, wu, wd)
     assert torch.equal(layer.forward(x, idx, w), want)
+
+def test_refused_backward_leaves_gradients_alone():
+    """Gradient buffers are looked at before any of them grows: a refused
+    backward may be called again without counting anything twice."""
+    layer, _, x, idx, w, dout = small_layer()
+    layer.forward(x, idx, w)
+    e, f, d = layer.n_experts, layer.width, layer.d
+    make = lambda: [rnd(8 + i, *s) for i, s in enumerate(((e, f, d), (e, f, d), (e, d, f)))]  # noqa: E731
+    want = layer.backward(dout, tuple(make()), accumulate=True)[2]
+    for i in range(3):
+        for spoil in (lambda g: g[:, :-1], lambda g: g.double(), lambda g: g.cpu(), lambda g: g.transpose(1, 2),
+                      lambda g: g[0], lambda g: g.bfloat16()):
+            grads = make()
+            before = [g.clone() for g in grads]
+            grads[i] = spoil(grads[i])
+            with pytest.raises((ValueError, TypeError)):
+                layer.backward(dout, tuple(grads), accumulate=True)
+            assert all(j == i or torch.equal(g, b) for j, (g, b) in enumerate(zip(grads, before)))
+    grads = make()
+    before = [g.clone() for g in grads]
+    for bad in (lambda: layer.backward(dout, tuple(grads[:2]), accumulate=True),
+                lambda: layer.backward(dout[:-1], tuple(grads), accumulate=True),
+                lambda: layer.backward(dout.bfloat16(), tuple(grads), accumulate=True)):
+        with pytest.raises((ValueError, TypeError)):
+            bad()
+        assert all(torch.equal(g, b) for g, b in zip(grads, before))
+    got = layer.backward(dout, tuple(grads), accumulate=True)[2]
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

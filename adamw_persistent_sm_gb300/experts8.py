@@ -59,8 +59,10 @@ class ExpertLayer8:
     def refresh(self, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor) -> None:
         """Quantise the weights (again, after an optimizer step).  Weights of other
         shapes than the layer was made with, or of another device or type, are
-        refused before any of them is written."""
+        refused before any of them is written.  A :meth:`backward` after it needs a
+        new :meth:`forward`: the old one went through other weights."""
         self._check_weights(w_gate, w_up, w_down)
+        self.w = None
         gu = torch.cat([w_gate.detach(), w_up.detach()], 1)
         ops.quant8(gu, 128, out=self.w_gu)
         ops.quant8_t(gu, 128, out=self.w_gu_t)

@@ -312,3 +312,21 @@ def test_refused_backward_leaves_gradients_alone():
         assert all(torch.equal(g, b) for g, b in zip(grads, before))
     got = layer.backward(dout, tuple(grads), accumulate=True)[2]
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_weights_refreshed_between_the_passes():
+    """A backward would go through other weights than its forward did: it asks
+    for a new forward.  A refused refresh changes nothing and asks for none."""
+    layer, weights, x, idx, w, dout = small_layer()
+    layer.forward(x, idx, w)
+    want = layer.backward(dout)[0]
+    layer.forward(x, idx, w)
+    with pytest.raises(ValueError):
+        layer.refresh(weights[0][:1], *weights[1:])
+    assert torch.equal(layer.backward(dout)[0], want)
+    layer.refresh(*(v * 2 for v in weights))
+    with pytest.raises(RuntimeError):
+        layer.backward(dout)
+    layer.refresh(*weights)
+    layer.forward(x, idx, w)
+    assert torch.equal(layer.backward(dout)[0], want)

@@ -68,6 +68,7 @@ def check(device: str | torch.device = "cuda") -> None:
     st, site = t.tolist()
     if st != B.MT_OK:
         t.zero_()
+        torch.cuda.synchronize(dev)             # cleared before another stream can report again
         raise _error(f"device-side check (site {site})", st)
 
 

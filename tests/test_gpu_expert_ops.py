@@ -926,3 +926,31 @@ def test_swiglu_backward_reads_every_scale_byte(ops, bg, bu, dt):
     for got, ref, mag in ((dgu[:, :width], d * u * s * (1 + g * (1 - s)), np.abs(d * u) * (s + np.abs(g) * s)),
                           (dgu[:, width:], d * g * s, np.abs(d * g * s)), (act, g * s * u, np.abs(g * s * u))):
         close(got, ref, rel * mag + sub + HALF_STEP[dtype] * np.abs(ref) * (1 + 1e-2))
+
+
+def test_check_clears_before_it_returns(ops, monkeypatch):
+    """The words are zero on the device when check() raises: a failure that
+    another stream reports from then on stays."""
+    r = ops.Route(1, 1, 2)
+    r.order(torch.full((1, 1), 5, dtype=torch.int32, device="cuda"))
+    s, busy = torch.cuda.Stream(), torch.zeros(1 << 26, device="cuda")
+    from adamw_persistent_sm_gb300.trainer import StatusError
+    torch.cuda.synchronize()
+    words = ops._status[r._dev][0]
+    real = torch.Tensor.zero_
+
+    def late(t):                             # work of another thread on the stream that clears
+        if t is words:
+            for _ in range(50):
+                busy.add_(1.0)
+        return real(t)
+
+    monkeypatch.setattr(torch.Tensor, "zero_", late)
+    with pytest.raises(StatusError):
+        ops.check()
+    monkeypatch.undo()
+    with torch.cuda.stream(s):
+        r.order(torch.full((1, 1), 7, dtype=torch.int32, device="cuda"))
+    with pytest.raises(StatusError):
+        ops.check()
+    ops.check()

@@ -109,3 +109,41 @@ def sigmoid(g):
 def rounded(x, dtype):
     """float64 -> dtype -> float64 through torch (one rounding)."""
     return torch.from_numpy(np.ascontiguousarray(x)).to(dtype).double().numpy()
+
+
+def power_t(e):
+    """2^e as float64, exactly, for whole e (a device's pow is not exact)."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
+def quant_t(x, block_rows=1, halves=False):
+    """:func:`quant` on a float64 tensor where it lies, for sizes that take the loop above too long."""
+    rows, cols = x.shape
+    if halves:
+        parts = [quant_t(p) for p in x.split(cols // 2, 1)]
+        return tuple(torch.cat(p, 1) for p in zip(*parts))
+    b = torch.nn.functional.pad(x, (0, -cols % BLOCK, 0, -rows % block_rows))
+    b = b.unflatten(1, (-1, BLOCK)).unflatten(0, (-1, block_rows))
+    top = torch.where(torch.isfinite(b), b.abs(), 0.0).amax((1, 3))
+    m, ex = torch.frexp(top)                     # 448 = 0.875 * 2^9
+    e = torch.where(top > 0, (ex - 9 + (m > 0.875).int()).clamp(min=-126), 0)
+    v = b * power_t(-e)[:, None, :, None]
+    v = v.flatten(2).flatten(0, 1)[:rows, :cols]
+    pos = torch.from_numpy(_POS).to(x.device)
+    a = v.abs().nan_to_num(0.0, 0.0).contiguous()
+    hi = torch.searchsorted(pos, a).clamp(0, 126)
+    lo = (hi - 1).clamp(min=0)
+    dl, dh = a - pos[lo], pos[hi] - a
+    c = torch.where((dl < dh) | ((dl == dh) & (lo % 2 == 0)), lo, hi)
+    c = torch.where(a == pos[hi], hi, c) + 128 * torch.signbit(v).int()
+    return torch.where(torch.isfinite(v), c, 127).to(torch.uint8), (e + 127).to(torch.uint8)
+
+
+def value_t(codes, scales, cols, block_rows=1, halves=False):
+    """:func:`value` on tensors where they lie."""
+    v = torch.from_numpy(TABLE).to(codes.device)[codes[:, :cols].long()]
+    r = torch.arange(codes.shape[0], device=codes.device) // block_rows
+    c = torch.arange(cols, device=codes.device)
+    nb = -(-(cols // 2) // BLOCK)
+    blk = torch.where(c < cols // 2, c // BLOCK, nb + (c - cols // 2) // BLOCK) if halves else c // BLOCK
+    return v * power_t(scales[r][:, blk].long() - 127)

@@ -256,3 +256,19 @@ def test_status_words_are_made_once_by_any_number_of_threads(monkeypatch):
     for t in threads:
         t.join(10)
     assert len(made) == 1 and got == [made[0].data_ptr()] * 4
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 2), (7, 100), (130, 264), (257, 300)])
+def test_reference_quantiser_on_tensors(rows, cols):
+    """The vectorised definition gives the block by block one's codes, scales and values."""
+    g = np.random.default_rng(rows)
+    x = g.normal(size=(rows, cols)) * 2.0 ** g.integers(-140, 120, (rows, 1))
+    x[0] = 0
+    if rows > 5:
+        x[1], x[2, ::2], x[3, 5], x[4, 7], x[5] = 448.0, 448.0 * (1 + 2.0 ** -40), np.nan, -np.inf, np.inf
+    for kw in ({}, dict(block_rows=128), dict(halves=True)):
+        want = R.quant(x, **kw)
+        got = R.quant_t(torch.from_numpy(x), **kw)
+        assert all(np.array_equal(a.numpy(), b) for a, b in zip(got, want))
+        val = R.value_t(*got, cols, **kw)
+        assert np.array_equal(val.numpy(), R.value(*want, cols, **kw), equal_nan=True)

@@ -954,3 +954,119 @@ def test_check_clears_before_it_returns(ops, monkeypatch):
     with pytest.raises(StatusError):
         ops.check()
     ops.check()
+
+
+def test_chain_captured_over_several_streams(ops):
+    """Each step of a chain captured on a stream of its own, joined by events,
+    with a copy between two of them: replays give one stream's result."""
+    r, idx, x, w8, wd8, w, bufs = chain_inputs(ops, 4, t=3000)
+    want = chain(ops, r, idx, x, w8, wd8, w, bufs).clone()
+    xs8, gu, act8, saved, y, out = bufs
+    x2 = x.clone()
+    steps = (lambda: r.order(idx), lambda: (x2.copy_(x), r.dispatch8(x2, out=xs8)),
+             lambda: ops.gemm8(xs8, w8, out=gu, offs=r.offs),
+             lambda: ops.swiglu8(gu, act=act8, saved=saved, n_rows=r.offs[-1:]),
+             lambda: ops.gemm8(act8, wd8, out=y, offs=r.offs), lambda: r.combine(y, w, out=out))
+    streams = [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        done = main.record_event()
+        for s, f in zip(streams, steps):
+            s.wait_event(done)
+            with torch.cuda.stream(s):
+                f()
+                done = s.record_event()
+        main.wait_event(done)
+    for _ in range(4):
+        for t in (r.row, r.perm, x2, gu, y, out, xs8.codes, act8.codes):
+            t.zero_()
+        g.replay()
+        assert torch.equal(out, want)
+    ops.check()
+
+
+def test_threads_on_streams_of_their_own(ops):
+    """Host threads that launch at once, each on its own stream and buffers, get what one gets."""
+    import threading
+    chains = [chain_inputs(ops, 10 + i, t=500 + 700 * i) for i in range(4)]
+    want = [chain(ops, *c).clone() for c in chains]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(c):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    chain(ops, *c)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:               # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(c,)) for c in chains]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    assert all(torch.equal(c[6][5], v) for c, v in zip(chains, want))
+    ops.check()
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+def test_matrices_of_no_rows(ops, dt):
+    x = torch.empty(0, 64, dtype=DT[dt], device="cuda")
+    a = ops.quant8(x)
+    assert a.shape == (0, 64) and ops.quant8(x, 128).shape == (0, 64) and ops.quant8(x, halves=True).shape == (0, 64)
+    assert ops.dequant8(a).shape == (0, 64)
+    b = ops.quant8(rnd(1, 30, 64))
+    assert ops.gemm8(a, b).shape == (0, 30) and ops.gemm8(b, a).shape == (30, 0)
+    saved = ops.empty8(0, 64, halves=True)
+    assert ops.swiglu8(x, saved=saved).shape == (0, 32) and ops.swiglu8_bwd(x[:, :32], saved).shape == (0, 64)
+    offs = torch.zeros(3, dtype=torch.int32, device="cuda")
+    assert ops.gemm8(a, ops.quant8(rnd(2, 2, 30, 64), 128), offs=offs).shape == (0, 30)
+    assert ops.quant8(torch.empty(0, 30, 64, device="cuda"), 128).shape == (0, 30, 64)
+    assert ops.quant8_t(torch.empty(0, 30, 64, device="cuda")).shape == (0, 64, 30)
+    ops.check()
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("n,k", [(72, 130), (1024, 100), (1001, 256)])
+def test_gemm_by_expert_adds_to_its_rows(ops, n, k, block_rows):
+    """accumulate by expert: rows of the segments grow, all others stay."""
+    offs, rows, e = [128, 128, 384, 1024], 1300, 3
+    a, b = ops.quant8(rnd(1, rows, k)), ops.quant8(rnd(2, e, n, k, std=0.02), block_rows=block_rows)
+    o = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    for pad, shift in ((0, 0), (3, 1)):
+        out = strided(rnd(3, rows, n), pad, shift)
+        before = R.as64(out)
+        ops.gemm8(a, b, out=out, offs=o, accumulate=True)
+        av, bv = R.value8(a), R.value8(b)
+        for i in range(e):
+            s = slice(offs[i], offs[i + 1])
+            product_close(out[s], av[s], bv[i], torch.float32, k, before[s])
+        after = R.as64(out)
+        assert np.array_equal(after[:128], before[:128]) and np.array_equal(after[1024:], before[1024:])
+    ops.check()
+
+
+@pytest.mark.parametrize("t", [500, 40000, 90000])
+def test_route_of_tensors_ordered_again(ops, t):
+    """A Route made of a routing's tensors sorts into them, in a capture too
+    (its workspace is then the graph's)."""
+    k, e = 2, 6
+    a = ops.Route(t, k, e)
+    r = ops.Route.of(a.offs, a.perm, a.row)
+    idx = torch.from_numpy(choices(1, t, k, e, "dropped")).cuda()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r.order(idx)
+    for seed in (2, 3):
+        new = choices(seed, t, k, e, "dropped")
+        idx.copy_(torch.from_numpy(new))
+        g.replay()
+        for got, want in zip((a.offs, a.perm, a.row), R.order(new, e)):
+            assert np.array_equal(got.cpu().numpy(), want)
+    ops.check()

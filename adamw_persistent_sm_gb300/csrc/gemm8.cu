@@ -299,8 +299,9 @@ __global__ void __launch_bounds__(G8_THREADS, 1) gemm8_k(const __grid_constant__
   constexpr int HALF = BN == 64 ? 64 : BN / 2;        // columns per epilogue warp (a window holds 64 of bf16)
   constexpr int EW = 4 * (BN / HALF);                 // epilogue warps
   constexpr int CW = 128 / (int)sizeof(CT);           // columns of a window
-  constexpr int ND = BN == 256 ? 1 : 2;               // accumulators (TMEM has 512 columns, scales take 24)
+  constexpr int ND = BN == 256 ? 1 : 2;               // accumulators (TMEM has 512 columns, scales take 48)
   constexpr int SF = ND * BN;                         // TMEM columns of the scales: slots of 4 (A) + 8 (B)
+  static_assert(SF + 12 * G8_SLOTS <= 512, "accumulators and scales exceed TMEM");
   const uint32_t base = smem_u32(gen);
   if (base & 1023) {                                  // swizzled tiles start on 1024-byte boundaries
     if (threadIdx.x == 0 && atomicCAS(g.status, 0, (int)MT_ERR_LAUNCH) == 0) g.status[1] = SITE_TC_ALIGN;

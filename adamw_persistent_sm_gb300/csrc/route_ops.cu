@@ -412,7 +412,13 @@ __global__ void __launch_bounds__(256) combine_k(const T* y, long long ldy, long
 
 // A warp takes one token's whole row: dout is read once for its slots, each
 // slot's y row is read for the dot product and its dy row written; CH chunks at
-// once as above.
+// once as above.  For up to two slots of bf16 that is three, the most that 64
+// registers hold (four CTAs on an SM; a fourth chunk takes 78 and leaves three).
+// 1 / 2 / 3 / 4 chunks, us for 32768 tokens x 2 of 768 columns and as many bytes
+// of others: 256 columns 41 / 50 / 50 / 60, 512: 38.6 / 38.7 / 38.7 / 43, 768: 39.0 /
+// 39.5 / 38.3 / 39.1, 1024: 39.2 / 38.4 / 38.9 / 38.3, 2048: 39.6 / 39.1 / 39.0 / 38.7,
+// 4096: 41.4 / 39.9 / 40.0 / 39.1.  Up to four slots 2 against 1 or 3: 35.5, 36.8, 38.0
+// at 1024; fp32 with two slots 2 against 1 or 3: 38.4, 38.6, 39.4.
 template <class T, int VEC, int KM, int CH>
 __global__ void __launch_bounds__(256) combine_bwd_k(const T* dout, long long lddo, const T* y, long long ldy,
                                                      const int* offs, const int* perm, const int* row, long long rows,

@@ -13,7 +13,9 @@ a stream capture: a device-side failure is reported by :func:`check`.
   power-of-two scale per block of 128;
 * :func:`swiglu8`, :func:`swiglu8_bwd` - SwiGLU that saves its inputs in 8 bits.
 
-Matrices may be views whose rows are contiguous (any row stride).
+Matrices may be views whose rows are contiguous (any row stride).  The
+functions record no autograd history, whatever their arguments require: each
+gradient is an operator of its own, called in the backward pass.
 """
 from __future__ import annotations
 

@@ -9,7 +9,8 @@ weights' gradient, and a copy of the routing weights.  Every product takes e4m3
 operands with a scale per block of 128: along the features for outputs and input
 gradients (weights in 128 x 128 blocks, quantised once per
 :meth:`ExpertLayer8.refresh` in both orientations), along the tokens for weight
-gradients.  Weight gradients are fp32.
+gradients.  Weight gradients are fp32.  Neither pass records autograd history:
+backward is called by the training program.
 """
 from __future__ import annotations
 

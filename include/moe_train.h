@@ -406,8 +406,9 @@ int32_t mt_debug_gemm(const void* A, int32_t a_mn, const void* B, int32_t b_mn, 
  *    a buffer and of its row stride selects vector accesses (same results).
  *    mt_mat8.codes is 16-byte aligned and mt_mat8.ld a multiple of 16.
  *  - Work is enqueued on `stream`, which belongs to the current device, where
- *    all the buffers must be.  No call allocates, synchronises or keeps
- *    anything; every launch can be captured into a CUDA graph.
+ *    all the buffers must be.  No call allocates or synchronises, or keeps
+ *    anything of its arguments (a kernel's shared-memory limit is set once per
+ *    device); every launch can be captured into a CUDA graph.
  *  - Outputs may not overlap inputs or one another.  Calls that share an
  *    output or a workspace must be ordered by the caller.
  *  - `status` (device int32[2], zeroed by the caller once) receives an
@@ -470,7 +471,9 @@ int64_t mt_route_ws_bytes(int64_t n_tokens, int32_t top_k, int32_t n_experts);
  *                             segment, -1 in padding and past offs[n_experts]
  *                             (rows = mt_route_rows(...));
  *   row  int32 [n_tokens, top_k]  row of each assignment, -1 for none.
- * All outputs are written whole also for n_tokens == 0. */
+ * All outputs are written whole also for n_tokens == 0.  4,097 to 65,536
+ * assignments take one cluster of 16 CTAs: where the device has no place for
+ * one (a part of a GPU) the call is MT_ERR_LAUNCH. */
 int32_t mt_route_order(const int32_t* idx, int64_t n_tokens, int32_t top_k, int32_t n_experts, int32_t* offs,
                        int32_t* perm, int32_t* row, void* ws, int64_t ws_bytes, int32_t* status, void* stream);
 
@@ -511,7 +514,8 @@ int32_t mt_quant8(const void* x, int32_t dtype, int64_t ldx, const int32_t* n_ro
  * 128; batch 1) only the blocks below it are written. */
 int32_t mt_quant8_t(const void* x, int32_t dtype, int64_t ldx, const mt_mat8* x8, const int32_t* n_rows,
                     const mt_mat8* out, void* stream);
-/* Values of an 8-bit matrix (block_rows 1, batch 1): out [rows, cols]. */
+/* Values of an 8-bit matrix (block_rows 1, batch 1): out [rows, cols], rounded
+ * to dtype; infinite where they are beyond its range. */
 int32_t mt_dequant8(const mt_mat8* a, const int32_t* n_rows, void* out, int32_t dtype, int64_t ldo, void* stream);
 
 /* C = A B^T on the tensor cores with fp32 sums: A [M, K] (batch 1, block_rows
@@ -534,7 +538,9 @@ int32_t mt_gemm8_reduce(const mt_mat8* a, const mt_mat8* b, const int32_t* offs,
 
 /* act = quantised silu(g) * u of gu [rows, 2*width] = [g | u]; act->cols =
  * width.  saved: NULL, or an 8-bit matrix [rows, 2*width] with halves 1 that
- * keeps g and u for the backward pass.  n_rows as in mt_quant8. */
+ * keeps g and u for the backward pass.  n_rows as in mt_quant8.  Here and in the
+ * backward pass sigmoid(g) is off by up to (|g| + 8) 2^-22 of its value, and 0
+ * below g = -87.3, where it is no normal fp32 number. */
 int32_t mt_swiglu8(const void* gu, int32_t dtype, int64_t ldgu, const int32_t* n_rows, const mt_mat8* act,
                    const mt_mat8* saved, void* stream);
 /* Backward from the saved 8-bit g and u: with s = sigmoid(g),

@@ -54,7 +54,8 @@ def _status_word(dev: int) -> int:
         with _status_lock:                      # one pair, however many threads come first
             t = _status.get(dev)
             if t is None:
-                t = torch.zeros(2, dtype=torch.int32, device=f"cuda:{dev}")
+                with torch.inference_mode(False):       # check() clears them in any mode
+                    t = torch.zeros(2, dtype=torch.int32, device=f"cuda:{dev}")
                 torch.cuda.synchronize(dev)     # once per device: zeroed before any other stream uses it
                 t = _status[dev] = (t, t.data_ptr())
     return t[1]

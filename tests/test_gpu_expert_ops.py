@@ -1070,3 +1070,16 @@ def test_route_of_tensors_ordered_again(ops, t):
         for got, want in zip((a.offs, a.perm, a.row), R.order(new, e)):
             assert np.array_equal(got.cpu().numpy(), want)
     ops.check()
+
+
+def test_failure_found_outside_inference_mode(ops, monkeypatch):
+    """Status words made in inference mode can be read and cleared outside it."""
+    monkeypatch.setattr(ops, "_status", {})
+    with torch.inference_mode():
+        r = ops.Route(1, 1, 2)
+        idx = torch.full((1, 1), 5, dtype=torch.int32, device="cuda")
+    r.order(idx)
+    from adamw_persistent_sm_gb300.trainer import StatusError
+    with pytest.raises(StatusError, match="out of range"):
+        ops.check()
+    ops.check()

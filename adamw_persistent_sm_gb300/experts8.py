@@ -40,7 +40,8 @@ class ExpertLayer8:
         # kept from forward to backward
         self.xs8, self.saved = ops.empty8(rows, d, dev), ops.empty8(rows, 2 * f, dev, halves=True)
         self.y = torch.empty((rows, d), dtype=dtype, device=dev)
-        self._w = torch.empty((n_tokens, top_k), dtype=torch.float32, device=dev)
+        with torch.inference_mode(False):       # torch itself copies into it, in any mode
+            self._w = torch.empty((n_tokens, top_k), dtype=torch.float32, device=dev)
         # passing buffers
         self.act8 = ops.empty8(rows, f, dev)
         self.gu = torch.empty((rows, 2 * f), dtype=dtype, device=dev)

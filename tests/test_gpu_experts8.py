@@ -330,3 +330,14 @@ def test_weights_refreshed_between_the_passes():
     layer.refresh(*weights)
     layer.forward(x, idx, w)
     assert torch.equal(layer.backward(dout)[0], want)
+
+
+def test_layer_made_in_inference_mode_trains_outside_it():
+    layer, _, x, idx, w, dout = small_layer()
+    layer.forward(x, idx, w)
+    want = layer.backward(dout)[0]
+    with torch.inference_mode():
+        other = small_layer()[0]
+        assert torch.equal(other.forward(x, idx, w), layer.forward(x, idx, w))
+    other.forward(x, idx, w)
+    assert torch.equal(other.backward(dout)[0], want)

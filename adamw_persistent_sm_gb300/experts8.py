@@ -46,6 +46,7 @@ class ExpertLayer8:
         self.act8 = ops.empty8(rows, f, dev)
         self.gu = torch.empty((rows, 2 * f), dtype=dtype, device=dev)
         self.w = None
+        self._captured = False              # a saving forward is part of a graph
         self._bwd = None
         self.refresh(w_gate, w_up, w_down)
 
@@ -62,9 +63,11 @@ class ExpertLayer8:
         """Quantise the weights (again, after an optimizer step).  Weights of other
         shapes than the layer was made with, or of another device or type, are
         refused before any of them is written.  A :meth:`backward` after it needs a
-        new :meth:`forward`: the old one went through other weights."""
+        new :meth:`forward`: the old one went through other weights (replays of a
+        captured forward are not seen here: their order is the caller's)."""
         self._check_weights(w_gate, w_up, w_down)
-        self.w = None
+        if not self._captured:
+            self.w = None
         gu = torch.cat([w_gate.detach(), w_up.detach()], 1)
         ops.quant8(gu, 128, out=self.w_gu)
         ops.quant8_t(gu, 128, out=self.w_gu_t)
@@ -85,6 +88,7 @@ class ExpertLayer8:
         out = r.combine(self.y, w, out=out)
         if save:                            # a copy: the caller's may hold the next microbatch's by then
             self.w = self._w.copy_(w.detach())
+            self._captured = self._captured or torch.cuda.is_current_stream_capturing()
         return out
 
     def backward(self, dout: torch.Tensor, grads: tuple[torch.Tensor, torch.Tensor, torch.Tensor] | None = None,

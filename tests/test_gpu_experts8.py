@@ -341,3 +341,24 @@ def test_layer_made_in_inference_mode_trains_outside_it():
         assert torch.equal(other.forward(x, idx, w), layer.forward(x, idx, w))
     other.forward(x, idx, w)
     assert torch.equal(other.backward(dout)[0], want)
+
+
+def test_captured_forward_replayed_after_a_refresh():
+    """A replay is a new forward that the layer does not see: a refresh before
+    it does not keep the backward behind it from running."""
+    layer, weights, x, idx, w, dout = small_layer()
+    layer.forward(x, idx, w)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = layer.forward(x, idx, w)
+    other = small_layer()[0]
+    for scale in (1.0, 2.0, 3.0):
+        new = [v * scale for v in weights]
+        layer.refresh(*new)
+        g.replay()
+        other.refresh(*new)
+        assert torch.equal(out, other.forward(x, idx, w))
+        dx, dw, grads = layer.backward(dout)
+        dx2, dw2, grads2 = other.backward(dout)
+        assert torch.equal(dx, dx2) and torch.equal(dw, dw2) and all(torch.equal(a, b) for a, b in zip(grads, grads2))

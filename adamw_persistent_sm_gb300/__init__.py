@@ -6,11 +6,13 @@ The compute path is the CUDA library built from ``csrc/`` (C ABI in
 ``include/moe_train.h``); :mod:`.binding` marshals arguments to it and
 :mod:`.trainer` allocates device buffers through torch.  :mod:`.expert_ops` and
 :mod:`.experts8` offer the expert layer's steps as stand-alone operators, with
-8-bit products.
+8-bit products; :mod:`.block_ops` what a training step needs around them:
+block norms with gate and residual, the router's choice with its balance loss,
+and the gradient norm with clipping.
 """
 from . import binding  # noqa: F401
 
-__all__ = ["binding", "build", "MoETrainer", "ExpertLayer8", "expert_ops"]
+__all__ = ["binding", "build", "MoETrainer", "ExpertLayer8", "expert_ops", "block_ops"]
 
 
 def build(force: bool = False) -> str:
@@ -25,7 +27,7 @@ def __getattr__(name):
     if name == "ExpertLayer8":
         from .experts8 import ExpertLayer8
         return ExpertLayer8
-    if name == "expert_ops":
+    if name in ("expert_ops", "block_ops"):
         import importlib
-        return importlib.import_module(".expert_ops", __name__)
+        return importlib.import_module("." + name, __name__)
     raise AttributeError(name)

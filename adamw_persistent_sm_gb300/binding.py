@@ -64,6 +64,11 @@ MT_VIEW_DX = 19
 MT_DT_FP32 = 0
 MT_DT_BF16 = 1
 
+MT_GATE_NONE = 0
+MT_GATE_CHANNEL = 1
+MT_GATE_TOKEN = 2
+MT_GATE_FULL = 3
+
 MT_OP_ATTN_FWD = 1
 MT_OP_ATTN_BWD = 2
 MT_OP_ROUTER = 3
@@ -111,6 +116,18 @@ class mt_mat8(C.Structure):
                 ("halves", C.c_int32), ("reserved0", C.c_int32)]
 
 
+class mt_joint(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("width", C.c_int64), ("stream_dtype", C.c_int32), ("dtype", C.c_int32),
+                ("after", C.c_void_p), ("before", C.c_void_p), ("gate", C.c_void_p), ("ldgate", C.c_int64),
+                ("n_rows", C.c_void_p), ("gate_kind", C.c_int32), ("res_scale", C.c_float),
+                ("out_scale", C.c_float), ("eps", C.c_float), ("reserved0", C.c_int32)]
+
+
+class mt_span(C.Structure):
+    _fields_ = [("grad", C.c_void_p), ("out", C.c_void_p), ("numel", C.c_int64), ("dtype", C.c_int32),
+                ("reserved0", C.c_int32)]
+
+
 _P = C.c_void_p
 _I, _L, _M8 = C.c_int32, C.c_int64, C.POINTER(mt_mat8)
 _SIGNATURES = {
@@ -144,6 +161,17 @@ _SIGNATURES = {
     "mt_gemm8_reduce": (_I, [_M8, _M8, _P, _I, _P, _L, _I, _P, _P]),
     "mt_swiglu8": (_I, [_P, _I, _L, _P, _M8, _M8, _P]),
     "mt_swiglu8_bwd": (_I, [_P, _I, _L, _M8, _P, _P, _L, _P, _L, _P]),
+    # stand-alone operators around the expert layer
+    "mt_block_norm": (_I, [C.POINTER(mt_joint), _P, _L, _P, _L, _P, _L, _P, _L, _P]),
+    "mt_block_norm_ws_bytes": (_L, [_L, _L]),
+    "mt_block_norm_bwd": (_I, [C.POINTER(mt_joint), _P, _L, _P, _L, _P, _L, _P, _L, _P, _L, _P, _L, _P, _L, _P, _P,
+                               _I, _P, _L, _P]),
+    "mt_choose_ws_bytes": (_L, [_L, _I, _I]),
+    "mt_choose": (_I, [_P, _I, _L, _L, _I, _I, _P, _I, _P, _P, _P, _P, _P, _L, _P]),
+    "mt_choose_bwd": (_I, [_P, _I, _L, _L, _I, _I, _P, _I, _P, _P, _P, _P, _P, _L, _P]),
+    "mt_grad_ws_bytes": (_L, [_I]),
+    "mt_grad_norm": (_I, [C.POINTER(mt_span), _I, C.c_double, _P, _P, _L, _P]),
+    "mt_grad_clip": (_I, [C.POINTER(mt_span), _I, C.c_double, C.c_double, C.c_double, _P, _P, _L, _P]),
 }
 
 _lib = None

@@ -1,0 +1,435 @@
+"""Stand-alone operators around the expert layer, on torch tensors.
+
+What a training step needs between, before and after the operators of
+:mod:`.expert_ops`, with the same conventions (``include/moe_train.h`` has each
+operator's definition): arguments are checked on the host, work is enqueued on
+the tensors' device and its current stream, outputs may be given and are
+allocated through torch otherwise, nothing synchronises or records autograd
+history.
+
+* :func:`block_norm`, :func:`block_norm_bwd` - the joint between two blocks: the
+  norm after a block, its gate, the scaled residual sum, the norm before the next;
+* :func:`choose`, :func:`choose_bwd` - the experts of each token from the router's
+  logits, counts, a balance loss and a loss on the logits' size;
+* :class:`GradSet`, :func:`grad_norm`, :func:`clip_grads` - the global norm of many
+  gradient tensors, and their clipping.
+
+Matrices may be views whose rows are contiguous (any row stride).
+"""
+from __future__ import annotations
+
+import ctypes as C
+from typing import NamedTuple, Sequence
+
+import torch
+
+from . import binding as B
+from .expert_ops import _DTYPES, _current, _error, _limit, _mat, _raw_stream
+
+__all__ = ["block_norm", "block_norm_bwd", "BlockGrads", "choose", "choose_bwd", "Choice", "GradSet", "grad_norm",
+           "clip_grads"]
+
+
+def _vec(t: torch.Tensor | None, what: str, dev: int, n: int) -> int | None:
+    """Address of a contiguous fp32 vector [n], None for none."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.get_device() != dev or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what}: expected contiguous float32 [{n}] on cuda:{dev}, got {t.dtype} {tuple(t.shape)} "
+                         f"on {t.device}")
+    return t.data_ptr()
+
+
+# ---------------------------------------------------------------------------
+# the joint between two blocks
+# ---------------------------------------------------------------------------
+class BlockGrads(NamedTuple):
+    """Gradients of :func:`block_norm`; None where there is no such input."""
+    dx: torch.Tensor
+    dy: torch.Tensor | None
+    dafter: torch.Tensor | None
+    dgate: torch.Tensor | None
+    dbefore: torch.Tensor | None
+
+
+def _gate(gate, dev: int, rows: int, width: int, dtype, what: str = "gate") -> tuple[int, int]:
+    """Kind and row stride of a gate [width], [rows, 1] or [rows, width]."""
+    if gate is None:
+        return B.MT_GATE_NONE, 0
+    if gate.dim() == 1:
+        _vec(gate, what, dev, width)
+        return B.MT_GATE_CHANNEL, 0
+    if gate.dim() == 2 and gate.shape[1] == 1 and (width > 1 or gate.dtype is torch.float32):
+        return B.MT_GATE_TOKEN, _mat(gate, what, dev, rows, 1, torch.float32)
+    return B.MT_GATE_FULL, _mat(gate, what, dev, rows, width, dtype)
+
+
+def _joint(stream: torch.Tensor, dtype, after, gate, before, res_scale, out_scale, eps, n_rows, dev):
+    rows, width = stream.shape
+    kind, ldgate = _gate(gate, dev, rows, width, dtype)
+    return B.mt_joint(rows, width, _DTYPES[stream.dtype], _DTYPES[dtype], _vec(after, "after", dev, width),
+                      _vec(before, "before", dev, width), None if gate is None else gate.data_ptr() or 16, ldgate,
+                      _limit(n_rows, dev) or None, kind, res_scale, out_scale, eps, 0)
+
+
+def _alone(after, gate, res_scale) -> None:
+    if after is not None or gate is not None or res_scale != 1.0:
+        raise ValueError("after, gate and res_scale belong to a block's output y")
+
+
+def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, after: torch.Tensor | None = None,
+               gate: torch.Tensor | None = None, before: torch.Tensor | None = None, res_scale: float = 1.0,
+               out_scale: float = 1.0, eps: float = 1e-5, h: torch.Tensor | None = None,
+               r: torch.Tensor | None = None, n_rows: torch.Tensor | None = None,
+               dtype: torch.dtype | None = None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """The joint between two blocks, in one pass: with rms(v) = sqrt(mean(v^2) +
+    eps) over the columns,
+
+        h = res_scale * x + out_scale * gate * (y / rms(y) * after)
+        r = h / rms(h) * before
+
+    x [rows, width] is the residual stream (float32 or bfloat16, as h), y the
+    block's output.  ``after`` and ``before`` are float32 [width]; without
+    ``after`` y is taken as it is, without ``before`` r is None.  ``gate`` is
+    float32 [width], float32 [rows, 1], or [rows, width] of y's type.  Without y
+    the call is the norm before the first block: h is x itself.  y and r have
+    one type, the stream's or bfloat16 (``dtype`` gives r's where there is no y).
+    ``h`` may be x (in place).  ``n_rows`` (device int32 [1]): rows from it on are
+    left as they were.  Up to 8192 columns.  Returns (h, r)."""
+    dev = x.get_device()
+    ldx = _mat(x, "x", dev)
+    rows, width = x.shape
+    if y is None:
+        _alone(after, gate, res_scale)
+        if before is None or h is not None:
+            raise ValueError("without y there is no h to write, and before is needed")
+        dtype = r.dtype if r is not None else dtype or x.dtype
+        if dtype not in _DTYPES:
+            raise TypeError(f"r: {dtype} where float32 or bfloat16 is needed")
+        ldy = ldh = 0
+    else:
+        ldy = _mat(y, "y", dev, rows, width)
+        if dtype is not None and dtype is not y.dtype:
+            raise TypeError(f"r has y's type {y.dtype}, not {dtype}")
+        dtype = y.dtype
+        if h is None:
+            h = torch.empty((rows, width), dtype=x.dtype, device=dev)
+        ldh = _mat(h, "h", dev, rows, width, x.dtype)
+    if before is None:
+        if r is not None:
+            raise ValueError("r needs before")
+        ldr = 0
+    else:
+        if r is None:
+            r = torch.empty((rows, width), dtype=dtype, device=dev)
+        ldr = _mat(r, "r", dev, rows, width, dtype)
+    j = _joint(x, dtype, after, gate, before, res_scale, out_scale, eps, n_rows, dev)
+    lib, here = B.load(), _current()
+    if here != dev:
+        torch.cuda.set_device(dev)
+    st = lib.mt_block_norm(j, x.data_ptr(), ldx, None if y is None else y.data_ptr(), ldy,
+                           None if y is None else h.data_ptr(), ldh, None if r is None else r.data_ptr(), ldr,
+                           _raw_stream(dev))
+    if here != dev:
+        torch.cuda.set_device(here)
+    if st:
+        raise _error("mt_block_norm", st)
+    return (x if y is None else h), r
+
+
+def block_norm_bwd(dr: torch.Tensor | None, dh: torch.Tensor | None, h: torch.Tensor, y: torch.Tensor | None = None, *,
+                   after: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                   before: torch.Tensor | None = None, res_scale: float = 1.0, out_scale: float = 1.0,
+                   eps: float = 1e-5, dx: torch.Tensor | None = None, dy: torch.Tensor | None = None,
+                   dgate: torch.Tensor | None = None, dafter: torch.Tensor | None = None,
+                   dbefore: torch.Tensor | None = None, accumulate: bool = False,
+                   n_rows: torch.Tensor | None = None) -> BlockGrads:
+    """Gradients of :func:`block_norm` from those of r and h, at the h and y that
+    it left (nothing else is kept).  ``dh`` is what reaches h along the residual
+    stream, of h's type (None: nothing); ``dr`` has y's type (None exactly where
+    ``before`` is).  ``dx`` may be dh (in place).  ``dafter``, ``dbefore`` and the
+    gradient of a gate [width] are sums over the rows, float32; with
+    ``accumulate`` they are added to what the given tensors hold."""
+    dev = h.get_device()
+    ldh = _mat(h, "h", dev)
+    rows, width = h.shape
+    if dr is None and dh is None:
+        raise ValueError("a gradient of r or of h is needed")
+    if (dr is None) != (before is None):
+        raise ValueError("dr and before come together")
+    if y is None:
+        _alone(after, gate, res_scale)
+        if dy is not None:
+            raise ValueError("dy needs y")
+    dtype = y.dtype if y is not None else dr.dtype if dr is not None else h.dtype
+    lddr = 0 if dr is None else _mat(dr, "dr", dev, rows, width, dtype)
+    lddh = 0 if dh is None else _mat(dh, "dh", dev, rows, width, h.dtype)
+    ldy = 0 if y is None else _mat(y, "y", dev, rows, width)
+    sums = ((after, dafter, "dafter"), (before, dbefore, "dbefore"),
+            (gate if gate is not None and gate.dim() == 1 else None, dgate if gate is None or gate.dim() == 1 else None, "dgate"))
+    for given, grad, what in sums:
+        if given is None and grad is not None:
+            raise ValueError(f"{what} of nothing")
+        if accumulate and given is not None and grad is None:
+            raise ValueError(f"accumulate needs {what}")
+        _vec(grad, what, dev, width)
+    j = _joint(h, dtype, after, gate, before, res_scale, out_scale, eps, n_rows, dev)
+    if dx is None:
+        dx = torch.empty((rows, width), dtype=h.dtype, device=dev)
+    lddx = _mat(dx, "dx", dev, rows, width, h.dtype)
+    if y is not None and dy is None:
+        dy = torch.empty((rows, width), dtype=dtype, device=dev)
+    lddy = 0 if dy is None else _mat(dy, "dy", dev, rows, width, dtype)
+    if after is not None and dafter is None:
+        dafter = torch.empty(width, dtype=torch.float32, device=dev)
+    if before is not None and dbefore is None:
+        dbefore = torch.empty(width, dtype=torch.float32, device=dev)
+    lddgate = 0
+    if gate is not None:
+        if dgate is None:
+            dgate = torch.empty(gate.shape, dtype=gate.dtype, device=dev)
+        if gate.dim() == 2:
+            lddgate = _mat(dgate, "dgate", dev, rows, gate.shape[1], gate.dtype)
+    lib = B.load()
+    nbytes = lib.mt_block_norm_ws_bytes(rows, width)
+    if nbytes < 0:
+        raise _error("mt_block_norm_bwd", -nbytes)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    here = _current()
+    if here != dev:
+        torch.cuda.set_device(dev)
+    ptr = lambda t: None if t is None else t.data_ptr()                          # noqa: E731
+    st = lib.mt_block_norm_bwd(j, ptr(h), ldh, ptr(y), ldy, ptr(dr), lddr, ptr(dh), lddh, ptr(dx), lddx, ptr(dy), lddy,
+                               ptr(dgate), lddgate, ptr(dafter), ptr(dbefore), int(accumulate), ptr(ws), nbytes,
+                               _raw_stream(dev))
+    if here != dev:
+        torch.cuda.set_device(here)
+    if st:
+        raise _error("mt_block_norm_bwd", st)
+    return BlockGrads(dx, dy, dafter, dgate, dbefore)
+
+
+# ---------------------------------------------------------------------------
+# the router's choice
+# ---------------------------------------------------------------------------
+class Choice(NamedTuple):
+    """The experts of a batch of tokens, as :func:`choose` leaves them."""
+    idx: torch.Tensor       # int32 [tokens, top_k], best first, -1: none
+    w: torch.Tensor         # float32 [tokens, top_k]
+    counts: torch.Tensor    # int32 [experts + 1]: tokens that chose each, and the number that take part
+    losses: torch.Tensor    # float32 [2]: balance, mean squared log of the sum of exponentials
+    ws: torch.Tensor        # workspace
+
+
+def _logits(z: torch.Tensor, top_k: int, mask) -> tuple[int, int]:
+    dev = z.get_device()
+    ldz = _mat(z, "logits", dev)
+    if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or mask.get_device() != dev
+                             or mask.shape != z.shape[:1] or not mask.is_contiguous()):
+        raise ValueError(f"mask: expected contiguous bool [{z.shape[0]}] on cuda:{dev}, got {mask.dtype} "
+                         f"{tuple(mask.shape)} on {mask.device}")
+    return dev, ldz
+
+
+def _plain(t: torch.Tensor, what: str, dev: int, shape, dtype) -> int:
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: expected contiguous {dtype} {tuple(shape)} on cuda:{dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def choose(logits: torch.Tensor, top_k: int, mask: torch.Tensor | None = None, renormalize: bool = True,
+           out: Choice | None = None) -> Choice:
+    """The ``top_k`` experts of each token by its logits [tokens, experts]
+    (float32 or bfloat16; equal logits: the lowest expert first), their weights
+    (softmax, divided by the chosen ones' sum with ``renormalize``), the tokens
+    that chose each expert, and two losses: the balance loss experts * sum_e f_e
+    P_e of the shares f and the mean probabilities P, and the mean squared
+    logsumexp.  ``mask`` (bool [tokens]): False takes no part and goes nowhere.
+    An expert whose logit is -inf is never chosen.  ``out`` is refilled; calls
+    that refill or read one Choice, captured ones too, have to be ordered by the
+    caller."""
+    dev, ldz = _logits(logits, top_k, mask)
+    t, e = logits.shape
+    lib = B.load()
+    nbytes = lib.mt_choose_ws_bytes(t, top_k, e)
+    if nbytes < 0:
+        raise _error("mt_choose", -nbytes)
+    if out is None:
+        out = Choice(torch.empty((t, top_k), dtype=torch.int32, device=dev),
+                     torch.empty((t, top_k), dtype=torch.float32, device=dev),
+                     torch.empty(e + 1, dtype=torch.int32, device=dev),
+                     torch.empty(2, dtype=torch.float32, device=dev),
+                     torch.empty(nbytes, dtype=torch.uint8, device=dev))
+    idx, w, counts, losses, ws = out
+    args = (_plain(idx, "idx", dev, (t, top_k), torch.int32), _plain(w, "w", dev, (t, top_k), torch.float32),
+            _plain(counts, "counts", dev, (e + 1,), torch.int32), _plain(losses, "losses", dev, (2,), torch.float32),
+            _plain(ws, "ws", dev, (nbytes,), torch.uint8))
+    here = _current()
+    if here != dev:
+        torch.cuda.set_device(dev)
+    st = lib.mt_choose(logits.data_ptr(), _DTYPES[logits.dtype], ldz, t, e, top_k,
+                       None if mask is None else mask.data_ptr(), int(renormalize), *args, nbytes, _raw_stream(dev))
+    if here != dev:
+        torch.cuda.set_device(here)
+    if st:
+        raise _error("mt_choose", st)
+    return out
+
+
+def choose_bwd(logits: torch.Tensor, idx: torch.Tensor, counts: torch.Tensor | None = None,
+               dw: torch.Tensor | None = None, dlosses: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+               renormalize: bool = True, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient for the logits, of their type: through the weights of the
+    chosen (``dw`` float32 [tokens, top_k]) and through the two losses
+    (``dlosses`` float32 [2] on the device, with the ``counts`` of the choice);
+    either may be None."""
+    dev, ldz = _logits(logits, 0, mask)
+    t, e = logits.shape
+    if dw is None and dlosses is None:
+        raise ValueError("dw or dlosses is needed")
+    if idx.dim() != 2:
+        raise ValueError(f"idx: expected [tokens, top_k], got {tuple(idx.shape)}")
+    k = idx.shape[1]
+    pi = _plain(idx, "idx", dev, (t, k), torch.int32)
+    pw = None if dw is None else _plain(dw, "dw", dev, (t, k), torch.float32)
+    pl = pc = None
+    if dlosses is not None:
+        if counts is None:
+            raise ValueError("dlosses needs counts")
+        pl, pc = _plain(dlosses, "dlosses", dev, (2,), torch.float32), _plain(counts, "counts", dev, (e + 1,), torch.int32)
+    if out is None:
+        out = torch.empty((t, e), dtype=logits.dtype, device=dev)
+    ldo = _mat(out, "out", dev, t, e, logits.dtype)
+    lib, here = B.load(), _current()
+    if here != dev:
+        torch.cuda.set_device(dev)
+    st = lib.mt_choose_bwd(logits.data_ptr(), _DTYPES[logits.dtype], ldz, t, e, k,
+                           None if mask is None else mask.data_ptr(), int(renormalize), pi, pc, pw, pl,
+                           out.data_ptr(), ldo, _raw_stream(dev))
+    if here != dev:
+        torch.cuda.set_device(here)
+    if st:
+        raise _error("mt_choose_bwd", st)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# the gradient norm and clipping
+# ---------------------------------------------------------------------------
+def _dense(t: torch.Tensor) -> bool:
+    """Whether a tensor's elements fill one run of memory (in any order of dimensions)."""
+    if t.is_contiguous():
+        return True
+    run = 1
+    for step, n in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1):
+        if step != run:
+            return False
+        run *= n
+    return True
+
+
+class GradSet:
+    """A set of gradient tensors on one device (float32 or bfloat16, mixed as
+    they come) for :meth:`norm` and :meth:`clip`; ``out``: tensors that receive
+    the clipped ones (default: in place).  Tensors are dense (contiguous, or a
+    permutation of that) and do not overlap; an output is its gradient itself, or
+    has its type, shape and strides and overlaps no tensor of the set.  The set
+    holds the tensors, not their values: each call takes what they hold then (and
+    looks where they lie, so that ``t.data = ...`` is seen).  The results are new
+    at each call, and so is the workspace: a set may be used on several streams."""
+
+    def __init__(self, tensors: Sequence[torch.Tensor], out: Sequence[torch.Tensor] | None = None,
+                 device: str | torch.device | None = None):
+        self.tensors = list(tensors)
+        self.out = self.tensors if out is None else list(out)
+        if len(self.out) != len(self.tensors):
+            raise ValueError(f"{len(self.out)} outputs for {len(self.tensors)} tensors")
+        if device is None:
+            device = self.tensors[0].device if self.tensors else "cuda"
+        self.device = torch.device(device)
+        if self.device.type != "cuda":
+            raise ValueError(f"expected tensors on a CUDA device, got {self.device}")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self._dev = self.device.index
+        self._bytes = B.load().mt_grad_ws_bytes(len(self.tensors))
+        self._look()
+
+    def _where(self) -> list[int]:
+        """Where everything lies now."""
+        at = [t.data_ptr() for t in self.tensors]
+        return at if self.out is self.tensors else at + [t.data_ptr() for t in self.out]
+
+    def _look(self) -> None:
+        dev, spans, runs = self._dev, [], []
+        for i, (t, o) in enumerate(zip(self.tensors, self.out)):
+            if t.dtype not in _DTYPES or t.get_device() != dev or t.is_sparse or not _dense(t):
+                raise ValueError(f"tensor {i}: expected dense float32 or bfloat16 on cuda:{dev}, got {t.dtype} "
+                                 f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+            if o is not t and (o.dtype is not t.dtype or o.get_device() != dev or o.shape != t.shape
+                               or o.stride() != t.stride()):
+                raise ValueError(f"output {i}: expected {t.dtype} {tuple(t.shape)} with strides {t.stride()} on "
+                                 f"cuda:{dev}, got {o.dtype} {tuple(o.shape)} with strides {o.stride()} on {o.device}")
+            n = t.numel()
+            a, b, size = t.data_ptr(), o.data_ptr(), n * t.element_size()
+            if n:
+                runs.append((a, a + size, i))
+                if a != b:
+                    runs.append((b, b + size, i))
+            spans.append((a, b, n, _DTYPES[t.dtype], 0))
+        runs.sort()
+        for (_, end, i), (start, _, k) in zip(runs, runs[1:]):
+            if start < end:
+                raise ValueError(f"tensors or outputs {i} and {k} overlap")
+        self._spans = (B.mt_span * max(1, len(spans)))(*spans)
+        self._at = self._where()
+
+    def _ready(self) -> torch.Tensor:
+        if self._where() != self._at:
+            self._look()
+        return torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
+
+    def norm(self, scale: float = 1.0) -> torch.Tensor:
+        """|scale| times the square root of the sum of all squares, float32 [1]."""
+        ws = self._ready()
+        norm = torch.empty(1, dtype=torch.float32, device=self.device)
+        dev, lib, here = self._dev, B.load(), _current()
+        if here != dev:
+            torch.cuda.set_device(dev)
+        st = lib.mt_grad_norm(self._spans, len(self.tensors), scale, norm.data_ptr(), ws.data_ptr(), self._bytes,
+                              _raw_stream(dev))
+        if here != dev:
+            torch.cuda.set_device(here)
+        if st:
+            raise _error("mt_grad_norm", st)
+        return norm
+
+    def clip(self, max_norm: float, eps: float = 1e-6, scale: float = 1.0) -> torch.Tensor:
+        """The tensors times scale * c, c = min(1, max_norm / (norm + eps)) with
+        the norm of the scaled tensors (NaN where that is NaN).  ``scale`` turns
+        a sum over microbatches or of scaled losses into the gradient.  Returns
+        (norm, c), float32 [2]."""
+        ws = self._ready()
+        stats = torch.empty(2, dtype=torch.float32, device=self.device)
+        dev, lib, here = self._dev, B.load(), _current()
+        if here != dev:
+            torch.cuda.set_device(dev)
+        st = lib.mt_grad_clip(self._spans, len(self.tensors), max_norm, eps, scale, stats.data_ptr(), ws.data_ptr(),
+                              self._bytes, _raw_stream(dev))
+        if here != dev:
+            torch.cuda.set_device(here)
+        if st:
+            raise _error("mt_grad_clip", st)
+        return stats
+
+
+def grad_norm(tensors: Sequence[torch.Tensor], scale: float = 1.0) -> torch.Tensor:
+    """:meth:`GradSet.norm` of tensors taken together once."""
+    return GradSet(tensors).norm(scale)
+
+
+def clip_grads(tensors: Sequence[torch.Tensor], max_norm: float, eps: float = 1e-6, scale: float = 1.0,
+               out: Sequence[torch.Tensor] | None = None) -> torch.Tensor:
+    """:meth:`GradSet.clip` of tensors taken together once."""
+    return GradSet(tensors, out).clip(max_norm, eps, scale)

@@ -550,6 +550,126 @@ int32_t mt_swiglu8(const void* gu, int32_t dtype, int64_t ldgu, const int32_t* n
 int32_t mt_swiglu8_bwd(const void* dact, int32_t dtype, int64_t ldda, const mt_mat8* saved, const int32_t* n_rows,
                        void* dgu, int64_t lddgu, void* act, int64_t ldact, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators around the expert layer: what a training step needs between,
+ * before and after the operators above.
+ *   joint  - mt_block_norm, mt_block_norm_bwd: the norm after a block, its gate,
+ *            the scaled residual sum and the norm before the next block;
+ *   router - mt_choose, mt_choose_bwd: the experts of each token from the
+ *            router's logits, counts, a balance loss and a loss on the logits'
+ *            size;
+ *   clip   - mt_grad_norm, mt_grad_clip: the global norm of many gradient
+ *            tensors, and their clipping.
+ * Conventions as above.  Sums are fp32 or wider in a fixed order: results are
+ * bitwise reproducible on one kind of device.
+ */
+enum {
+  MT_GATE_NONE = 0,
+  MT_GATE_CHANNEL = 1,   /* fp32 [width]: one gate per column */
+  MT_GATE_TOKEN = 2,     /* fp32 [rows, 1], row stride ldgate: one per row */
+  MT_GATE_FULL = 3       /* [rows, width] of dtype, row stride ldgate */
+};
+
+/*
+ * The joint between two blocks (host struct, copied at call time).  With
+ * rms(v) = sqrt(mean(v^2) + eps) over the columns of a row:
+ *   n = y / rms(y) * after          (after NULL: n = y)
+ *   h = res_scale * x + out_scale * gate * n
+ *   r = h / rms(h) * before         (of h before its rounding)
+ * x and h are of stream_dtype, y, r and a full gate of dtype: both the same, or
+ * fp32 and bf16.  after, before: fp32 [width] or NULL.  n_rows: device int32 or
+ * NULL; rows from it on are neither read nor written.  res_scale and out_scale
+ * finite, eps finite and > 0, rows <= 2^30, width <= 8192.
+ */
+typedef struct mt_joint {
+  int64_t rows, width;
+  int32_t stream_dtype, dtype;
+  const float* after;
+  const float* before;
+  const void* gate;
+  int64_t ldgate;
+  const int32_t* n_rows;
+  int32_t gate_kind;       /* MT_GATE_*; gate is NULL exactly for MT_GATE_NONE */
+  float res_scale, out_scale, eps;
+  int32_t reserved0;       /* must be 0 */
+} mt_joint;
+
+/* h and r of x and y.  y NULL: h = x, and h is NULL (no after, gate; res_scale
+ * 1).  before NULL: r is NULL.  Not both.  h may be x itself (ldh == ldx). */
+int32_t mt_block_norm(const mt_joint* j, const void* x, int64_t ldx, const void* y, int64_t ldy, void* h, int64_t ldh,
+                      void* r, int64_t ldr, void* stream);
+/* Bytes of device workspace (16-byte aligned) for mt_block_norm_bwd. */
+int64_t mt_block_norm_ws_bytes(int64_t rows, int64_t width);
+/* Gradients at h and y as they are stored; nothing else is kept from forward.
+ * dr [rows, width] of dtype (NULL exactly where before is), dh of stream_dtype:
+ * what reaches h along the residual stream (NULL: nothing; not both NULL).
+ *   dx = res_scale * G, G = dh + d(r)/d(h) dr      of stream_dtype
+ *   dy, dgate of the types of y and gate; dafter, dbefore and a channel gate's
+ *   gradient are sums over the rows, fp32, added to what is there with
+ *   accumulate 1.
+ * Outputs are NULL exactly where their input is; h may be NULL without before.
+ * dx may be dh itself (lddx == lddh).  rows == 0 and n_rows of 0 write sums of
+ * nothing. */
+int32_t mt_block_norm_bwd(const mt_joint* j, const void* h, int64_t ldh, const void* y, int64_t ldy, const void* dr,
+                          int64_t lddr, const void* dh, int64_t lddh, void* dx, int64_t lddx, void* dy, int64_t lddy,
+                          void* dgate, int64_t lddgate, float* dafter, float* dbefore, int32_t accumulate, void* ws,
+                          int64_t ws_bytes, void* stream);
+
+/* Bytes of device workspace (16-byte aligned) for mt_choose. */
+int64_t mt_choose_ws_bytes(int64_t n_tokens, int32_t top_k, int32_t n_experts);
+/* The experts of each token.  With p = softmax(z) over the n_experts logits z of
+ * a token (row stride ldz, dtype fp32 or bf16):
+ *   idx int32 [n_tokens, top_k]  the largest logits, descending, the lowest
+ *       expert among equals (as mt_route_order takes them);
+ *   w fp32 [n_tokens, top_k]     p of the chosen, divided by their sum with
+ *       renormalize 1;
+ *   counts int32 [n_experts + 1] tokens that chose each expert, and N, the
+ *       number of tokens that take part;
+ *   losses fp32 [2]              balance = n_experts * sum_e f_e P_e with f_e =
+ *       counts_e / (top_k N) and P_e the mean of p_e (1 for an even load), and
+ *       the mean of logsumexp(z)^2; zeros for N = 0.
+ * mask (one byte per token, or NULL): a token whose byte is 0, and one whose
+ * logits are all -infinity, takes no part: idx -1, w 0.  An expert whose logit is
+ * -infinity is never chosen (its slot: -1 and 0).  A row that holds NaN or
+ * +infinity takes part and chooses nothing: idx -1, w NaN, and the losses are
+ * NaN.  Limits as mt_route_order's.  counts and losses are written for n_tokens
+ * == 0 too. */
+int32_t mt_choose(const void* logits, int32_t dtype, int64_t ldz, int64_t n_tokens, int32_t n_experts, int32_t top_k,
+                  const uint8_t* mask, int32_t renormalize, int32_t* idx, float* w, int32_t* counts, float* losses,
+                  void* ws, int64_t ws_bytes, void* stream);
+/* The gradient for the logits, of their dtype: from dw fp32 [n_tokens, top_k]
+ * (NULL: none) through the weights at idx (entries outside [0, n_experts) add
+ * nothing), and from dlosses fp32 [2] (NULL: none) through the losses, whose
+ * counts (as mt_choose left them) are constants.  Zeros for tokens that take no
+ * part and for logits of -infinity, NaN where the row holds NaN or +infinity. */
+int32_t mt_choose_bwd(const void* logits, int32_t dtype, int64_t ldz, int64_t n_tokens, int32_t n_experts,
+                      int32_t top_k, const uint8_t* mask, int32_t renormalize, const int32_t* idx,
+                      const int32_t* counts, const float* dw, const float* dlosses, void* dlogits, int64_t lddz,
+                      void* stream);
+
+/* One tensor of a set (host struct, copied at call time): numel elements in a
+ * row, of MT_DT_FP32 or MT_DT_BF16, aligned to their size.  out: where the
+ * clipped tensor goes, grad itself or memory that no tensor of the set overlaps. */
+typedef struct mt_span {
+  const void* grad;
+  void* out;
+  int64_t numel;           /* up to 2^40 */
+  int32_t dtype;
+  int32_t reserved0;       /* must be 0 */
+} mt_span;
+/* Bytes of device workspace (16-byte aligned) for the calls below on n tensors. */
+int64_t mt_grad_ws_bytes(int32_t n);
+/* norm[0] = |scale| * sqrt(sum of the squares of all elements of all n tensors).
+ * Squares and sums neither overflow nor vanish: the norm is infinite only where
+ * an element is, or where it is beyond fp32 itself. */
+int32_t mt_grad_norm(const mt_span* spans, int32_t n, double scale, float* norm, void* ws, int64_t ws_bytes,
+                     void* stream);
+/* stats[0] = that norm, stats[1] = c = min(1, max_norm / (norm + eps)) (NaN where
+ * the norm is), and out = grad * (scale * c), rounded once.  Elements stay as they
+ * are where out is grad and scale * c is 1.  max_norm > 0, eps >= 0, all finite. */
+int32_t mt_grad_clip(const mt_span* spans, int32_t n, double max_norm, double eps, double scale, float* stats, void* ws,
+                     int64_t ws_bytes, void* stream);
+
 /* Stable text for a status code. */
 const char* mt_status_string(int32_t status);
 

@@ -361,9 +361,13 @@ __global__ void __launch_bounds__(256) column_sums_k(Sums s) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane, k = blockIdx.y;
   const long long step = (long long)s.sums * s.width;
   float v = 0.f;
-  if (c < s.width) {
-#pragma unroll 8
-    for (int p = w; p < s.parts; p += 8) v += s.ws[p * step + (long long)k * s.width + c];
+  constexpr int U = 20;                       // all in flight: 152 parts by eight warps
+  for (int p0 = w; p0 < s.parts && c < s.width; p0 += 8 * U) {
+    float x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = p0 + 8 * u < s.parts ? s.ws[(p0 + 8 * u) * step + (long long)k * s.width + c] : 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) v += x[u];
   }
   red[w][lane] = v;
   __syncthreads();

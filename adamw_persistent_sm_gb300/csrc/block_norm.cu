@@ -10,6 +10,9 @@ namespace {
 
 #define BN_MAX_WIDTH 8192
 #define BN_MAX_PARTS 256          // CTAs that leave partial column sums
+#define BN_WARPS 16               // of a CTA of the backward pass
+#define BN_SMEM (226 * 1024)      // its shared memory
+#define BN_STAGES 2               // of its ring, at most (three: 79.9 against 77.3 us)
 
 struct Joint {
   const float *after, *before;
@@ -30,7 +33,9 @@ struct Bwd {
   const void *h, *y, *dr, *dh;
   void *dx, *dy, *dgate;
   long long ldh, ldy, lddr, lddh, lddx, lddy, lddgate;
-  float* ws;                      // [CTAs][sums][width]: dbefore, dafter, dgate where there are such sums
+  float* ws;                      // [CTAs][sums][width], see column_sums_k
+  // elements from a group's row to its next
+  long long hop_dh, hop_h, hop_dr, hop_y, hop_gate, hop_dx, hop_dy, hop_dgate;
 };
 
 // Columns of a lane within a chunk of 256: eight neighbours, or (no alignment)
@@ -160,29 +165,131 @@ __global__ void __launch_bounds__(256) block_norm_k(Fwd f) {
 // ---------------------------------------------------------------------------
 // gradients
 // ---------------------------------------------------------------------------
-// Sums of K values over a group of `warps` warps (named barrier `bar`); every
-// lane gets them.  red: two buffers of the group, taken in turn: whoever writes one
-// again has passed the other's barrier, and with it every warp's reads of this one.
-template <int K>
-__device__ __forceinline__ void bn_group_sum(float (&s)[K], float* red, int warps, int w, int lane, int bar, int& turn) {
+// two fp32 numbers in a register pair: one issue slot for both
+typedef unsigned long long bn2;
+__device__ __forceinline__ bn2 bn_pair(float x, float y) {
+  bn2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ void bn_split(bn2 v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ bn2 bn_mul(bn2 a, bn2 b) {
+  bn2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ bn2 bn_fma(bn2 a, bn2 b, bn2 c) {
+  bn2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float bn_both(bn2 v) {
+  float x, y;
+  bn_split(v, x, y);
+  return x + y;
+}
+__device__ __forceinline__ void bn_pairs(const float* v, bn2* p) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) s[k] = bn_sum(s[k]);
-  if (warps == 1) return;
-  red += turn * warps * 4;
-  turn ^= 1;
-  if (lane == 0) {
+  for (int e = 0; e < 4; ++e) p[e] = bn_pair(v[2 * e], v[2 * e + 1]);
+}
+template <class T>
+__device__ __forceinline__ void bn_pairs(const Raw8<T>& r, bn2* p) {
+  float v[8];
+  r.values(v);
+  bn_pairs(v, p);
+}
+template <int VEC, class T>
+__device__ __forceinline__ void bn_store(T* p, int c, int n, const bn2* v) {
+  float x[8];
 #pragma unroll
-    for (int k = 0; k < K; ++k) red[w * K + k] = s[k];
-  }
-  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(32 * warps) : "memory");
-#pragma unroll
-  for (int k = 0; k < K; ++k) s[k] = 0.f;
-  for (int i = 0; i < warps; ++i) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) s[k] += red[i * K + k];
-  }
+  for (int e = 0; e < 4; ++e) bn_split(v[e], x[2 * e], x[2 * e + 1]);
+  bn_store<VEC>(p, c, n, x);
 }
 
+// Sums over a group of `warps` warps (named barrier `bar`), for every lane.  red:
+// two buffers of four words a warp, taken in turn: whoever writes one again has
+// passed the other's barrier, and with it every warp's reads of this one.
+struct Group {
+  float* red;
+  int warps, w, lane, bar, turn;
+  __device__ __forceinline__ float* mine() const { return red + (turn * warps + w) * 4; }
+  __device__ __forceinline__ const float* meet() {
+    const float* r = red + turn * warps * 4;
+    turn ^= 1;
+    if (warps == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(32 * warps) : "memory");
+    return r;
+  }
+  __device__ __forceinline__ float sum(float a) {
+    a = bn_sum(a);
+    if (lane == 0) *mine() = a;
+    const float* r = meet();
+    a = 0.f;
+    for (int i = 0; i < warps; ++i) a += r[i * 4];
+    return a;
+  }
+  // three at once, in 6 shuffles instead of 15: after two exchanges a lane has one of
+  // them only - first, second, third, second by eights of lanes
+  __device__ __forceinline__ void sum(float& a, float& b, float& c) {
+    const bool h16 = lane & 16, h8 = lane & 8;
+    float x = (h16 ? c : a) + __shfl_xor_sync(0xffffffffu, h16 ? a : c, 16);
+    const float y = b + __shfl_xor_sync(0xffffffffu, b, 16);
+    x = (h8 ? y : x) + __shfl_xor_sync(0xffffffffu, h8 ? x : y, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if ((lane & 7) == 0) mine()[lane >> 3] = x;
+    const float* r = meet();
+    a = b = c = 0.f;
+    for (int i = 0; i < warps; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(r + i * 4);
+      a += v.x;
+      b += v.y;
+      c += v.z;
+    }
+  }
+};
+
+// Rows of whole eights go through a ring in shared memory that a warp has to itself,
+// copied there 16 bytes at a time while it works on the rows before: no registers
+// hold them.  An array's eights of a warp take 32 pieces of 16 bytes (bf16; a lane
+// copies its own) or 64 (fp32; lane l copies pieces l and 32 + l, so that a copy
+// instruction takes whole sectors: a lane's own two would ask L2 for every sector
+// twice, 104 against 88 us at 32,768 x 768).  fp32 piece p lies at p ^ (p >> 3 & 1):
+// neither the copies nor the lanes' reads of pieces 2 l and 2 l + 1 meet a bank twice.
+template <class T>
+struct Piece {
+  static constexpr int N = (int)sizeof(T) / 2;          // pieces of eight elements
+  // a lane's first copy: its column within the warp's 256, its place in the array's part
+  __device__ __forceinline__ static int column(int lane) { return N == 2 ? lane * 4 : lane * 8; }
+  __device__ __forceinline__ static uint32_t place(int wid, int lane) {
+    return (uint32_t)(N == 2 ? wid * 64 + (lane ^ (lane >> 3 & 1)) : wid * 32 + lane) * 16;
+  }
+};
+__device__ __forceinline__ void bn_copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+// columns c (and c + 128) of the row at p, as far as it has them
+template <class T>
+__device__ __forceinline__ void bn_copy(uint32_t to, const T* p, int c, int n) {
+  if (c < n) bn_copy16(to, p);
+  if (Piece<T>::N == 2 && c + 128 < n) bn_copy16(to + 512, p + 128);
+}
+// eight elements of this lane as four pairs
+__device__ __forceinline__ void bn_take(const __nv_bfloat16*, uint32_t at, int wid, int lane, bn2* p) {
+  Raw8<__nv_bfloat16> v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.u.x), "=r"(v.u.y), "=r"(v.u.z), "=r"(v.u.w)
+               : "r"(at + (wid * 32 + lane) * 16)
+               : "memory");
+  bn_pairs(v, p);
+}
+__device__ __forceinline__ void bn_take(const float*, uint32_t at, int wid, int lane, bn2* p) {
+  const uint32_t a = at + (uint32_t)(wid * 64 + (2 * lane ^ (lane >> 2 & 1))) * 16;
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(p[0]), "=l"(p[1]) : "r"(a) : "memory");
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(p[2]), "=l"(p[3]) : "r"(a ^ 16) : "memory");
+}
 template <class S, class T>
 struct BwdRow {
   Raw8<S> h, dh;
@@ -199,160 +306,298 @@ __device__ __forceinline__ void bn_row(BwdRow<S, T>& v, const Bwd& f, long long 
   if (f.y) bn_load<VEC>(v.y, (const T*)f.y + row * f.ldy, c, n);
   if (f.j.gate_kind == MT_GATE_FULL) bn_load<VEC>(v.gate, (const T*)f.j.gate + row * f.j.ldgate, c, n);
 }
+// bytes of the groups' sums, below the ring, which starts on a line of all banks (80.9
+// us off one where 76.1 on one)
+__host__ __device__ constexpr int bn_red(int warps) { return (warps * 32 + 127) / 128 * 128; }
 
 // Persistent CTAs of G groups; a group of W warps takes a row, a lane 8 C fixed
 // columns of it, so the gains and the column sums stay in registers from row to
-// row.  With rh = 1 / rms(h), u = dr * before:
-//   G = dh + rh u - h rh^3 mean(u h)          dx = a G, dbefore += dr h rh
-//   g = b G, n = y ry after, v = g gate       dgate += g n, dafter += v y ry
-//   dy = ry w - y ry^3 mean(w y), w = v after
-// Two sums over the row: (h^2, u h, y^2), then (w y, g n).  The next row is on
-// its way while this one is computed (C 1).
-template <class S, class T, int VEC, int C>
-__global__ void __launch_bounds__(512, 1) block_norm_bwd_k(Bwd f, int W, int G) {
+// row.  With rh = 1 / rms(h), u = dr * before, t the token's gate (1 without one):
+//   G = dh + rh u - h rh^3 mean(u h)              dx = a G, dbefore += dr h rh
+//   x = b G (full gate: times the gate), p = x * after * channel gate
+//   s = sum(p y)                                  dgate of a token = s ry
+//   dy = t (p ry - y ry^3 s / width)              q += t x y ry
+// and after the last row dafter = q * channel gate, a channel gate's gradient q *
+// after: one sum for both.  A full gate's gradient is b G y ry after.  Two sums over
+// after: one sum for both.  A full gate's gradient is b G y ry after.  Two sums over
+// after: one sum for both.  A full gate's gradient is b G y ry after.  Two sums over
+// the row: (h^2, u h, y^2) and s.  VEC: the next stages - 1 rows are on their way in
+// the ring, and what a phase needs of a row is read from there again.  Otherwise the
+// next row is on its way in registers (C 1).
+// 32,768 x 768 (fp32 stream, bf16, a channel gate), us with the column sums: 77, 86 %
+// of the copy rate; rows in registers 109, two rows at once 87 to 90, a warp to a row
+// of three chunks 83 and more, 20 warps 86, 8 warps 138.
+template <class S, class T, int VEC, int C, bool ALL>
+__global__ void __launch_bounds__(32 * BN_WARPS, 1) block_norm_bwd_k(Bwd f, int W, int G, int stages, int pieces) {
   ops_begin();
-  extern __shared__ float sh[];
+  extern __shared__ __align__(128) float sh[];
+  constexpr int NS = Piece<S>::N, NT = Piece<T>::N;
   const Joint& j = f.j;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, g = wid / W, w = wid - g * W, n = j.width;
-  float* red = sh + g * W * 8;              // two buffers of four values per warp
-  int turn = 0;
-  const int bar = 1 + g;
+  Group grp = {sh + g * W * 8, W, w, lane, 1 + g, 0};
   const int lim = ops_row_limit(j.n_rows, j.rows), step = (int)gridDim.x * G;
   const float mean = 1.f / (float)n;
+  // ALL: every part but a gate is there, known when this was compiled
+  const bool has_b = ALL || j.before, has_a = ALL || j.after, has_y = ALL || f.y, has_dh = ALL || f.dh;
   const bool channel = j.gate_kind == MT_GATE_CHANNEL, token = j.gate_kind == MT_GATE_TOKEN,
              full = j.gate_kind == MT_GATE_FULL;
-  float kb[C][8], ka[C][8], kg[C][8], sb[C][8], sa[C][8], sg[C][8];
+  // gains of a lane's columns: kept for C 1, fetched where they are used for C 2
+  constexpr bool KEEP = C == 1;
+  bn2 kb[C][4], kw[C][4], sb[C][4], sq[C][4];
+  auto before = [&](int i) {
+    float v[8];
+    bn_vec<VEC>(j.before, bn_col<VEC>(w + i * W, lane), n, v);
+    bn_pairs(v, kb[i]);
+  };
+  auto behind = [&](int i) {
+    const int c = bn_col<VEC>(w + i * W, lane);
+    float v[8], u[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 1.f;
+    if (has_a) bn_vec<VEC>(j.after, c, n, v);
+    if (channel) {
+      bn_vec<VEC>((const float*)j.gate, c, n, u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= u[e];
+    }
+    bn_pairs(v, kw[i]);
+  };
 #pragma unroll
   for (int i = 0; i < C; ++i) {
-    const int c = bn_col<VEC>(w + i * W, lane);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) kb[i][e] = ka[i][e] = kg[i][e] = 1.f, sb[i][e] = sa[i][e] = sg[i][e] = 0.f;
-    if (j.before) bn_vec<VEC>(j.before, c, n, kb[i]);
-    if (j.after) bn_vec<VEC>(j.after, c, n, ka[i]);
-    if (channel) bn_vec<VEC>((const float*)j.gate, c, n, kg[i]);
+    for (int e = 0; e < 4; ++e) sb[i][e] = sq[i][e] = 0;
+    if (KEEP && has_b) before(i);
+    if (KEEP && has_y) behind(i);
   }
   BwdRow<S, T> cur[C];
   long long row = (long long)blockIdx.x * G + g;
-  if (C == 1 && row < lim) bn_row<VEC>(cur[0], f, row, bn_col<VEC>(w, lane));
+  const uint32_t hop = blockDim.x * 16, unit = hop * pieces, slot = unit * C;   // a piece; a lane's eight; a stage
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sh) + bn_red(G * W);
+  uint32_t put = 0, get = 0;
+  // where the next row to send lies, for a lane's first copies; a row's hop is a
+  // parameter of its own
+  const int cs = w * 256 + Piece<S>::column(lane), ct = w * 256 + Piece<T>::column(lane);
+  const uint32_t at_s = Piece<S>::place(wid, lane), at_t = Piece<T>::place(wid, lane);
+  int ahead = (int)row;
+  const S *p_dh = nullptr, *p_h = nullptr;
+  const T *p_dr = nullptr, *p_y = nullptr, *p_gate = nullptr;
+  if (has_dh) p_dh = (const S*)f.dh + row * f.lddh + cs;
+  if (has_b) p_h = (const S*)f.h + row * f.ldh + cs;
+  if (has_b) p_dr = (const T*)f.dr + row * f.lddr + ct;
+  if (has_y) p_y = (const T*)f.y + row * f.ldy + ct;
+  if (full) p_gate = (const T*)j.gate + row * j.ldgate + ct;
+  auto send = [&]() {
+    if (ahead < lim) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const uint32_t to = ring + put + i * unit;
+        const int c = i * W * 256;
+        if (has_dh) bn_copy(to + at_s, p_dh + c, cs + c, n);
+        if (has_b) {
+          bn_copy(to + NS * hop + at_s, p_h + c, cs + c, n);
+          bn_copy(to + 2 * NS * hop + at_t, p_dr + c, ct + c, n);
+        }
+        if (has_y) bn_copy(to + (2 * NS + NT) * hop + at_t, p_y + c, ct + c, n);
+        if (full) bn_copy(to + (2 * NS + 2 * NT) * hop + at_t, p_gate + c, ct + c, n);
+      }
+      ahead += step;
+      p_dh += f.hop_dh;
+      p_h += f.hop_h;
+      p_dr += f.hop_dr;
+      p_y += f.hop_y;
+      if (full) p_gate += f.hop_gate;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    put = put + slot == slot * stages ? 0 : put + slot;
+  };
+  // a row's inputs as pairs, of chunk i and row q
+  auto in_h = [&](int i, bn2* p) {
+    if constexpr (VEC) bn_take((const S*)nullptr, ring + get + i * unit + NS * hop, wid, lane, p);
+    else bn_pairs(cur[i].h, p);
+  };
+  auto in_dh = [&](int i, bn2* p) {
+    if constexpr (VEC) bn_take((const S*)nullptr, ring + get + i * unit, wid, lane, p);
+    else bn_pairs(cur[i].dh, p);
+  };
+  auto in_dr = [&](int i, bn2* p) {
+    if constexpr (VEC) bn_take((const T*)nullptr, ring + get + i * unit + 2 * NS * hop, wid, lane, p);
+    else bn_pairs(cur[i].dr, p);
+  };
+  auto in_y = [&](int i, bn2* p) {
+    if constexpr (VEC) bn_take((const T*)nullptr, ring + get + i * unit + (2 * NS + NT) * hop, wid, lane, p);
+    else bn_pairs(cur[i].y, p);
+  };
+  auto in_gate = [&](int i, bn2* p) {
+    if constexpr (VEC) bn_take((const T*)nullptr, ring + get + i * unit + (2 * NS + 2 * NT) * hop, wid, lane, p);
+    else bn_pairs(cur[i].gate, p);
+  };
+  if constexpr (VEC) {
+    // columns behind the row stay zeros in every stage
+    if (n < 256 * C * W) {
+      for (uint32_t at = threadIdx.x * 16; at < slot * stages; at += hop)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(ring + at), "r"(0) : "memory");
+      __syncthreads();
+    }
+    for (int k = 0; k < stages - 1; ++k) send();
+  } else if (C == 1 && row < lim) {
+    bn_row<VEC>(cur[0], f, row, bn_col<VEC>(w, lane));
+  }
+  S* o_dx = (S*)f.dx + row * f.lddx;
+  T *o_dy = nullptr, *o_dgate = nullptr;
+  if (has_y) o_dy = (T*)f.dy + row * f.lddy;
+  if (full) o_dgate = (T*)f.dgate + row * f.lddgate;
+  const bn2 a2 = bn_pair(j.a, j.a), b2 = bn_pair(j.b, j.b);
   for (; row < lim; row += step) {
     BwdRow<S, T> next;
-    if (C > 1) {
+    if constexpr (VEC) {
+      if (row != (long long)blockIdx.x * G + g) __syncwarp();    // the stage that this fills has been read
+      send();
+      // all but the newest stages - 1 copies have landed
+      if (stages == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
+      else asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();                                             // by every lane
+    } else if constexpr (C > 1) {
 #pragma unroll
       for (int i = 0; i < C; ++i) bn_row<VEC>(cur[i], f, row, bn_col<VEC>(w + i * W, lane));
     } else if (row + step < lim) {
       bn_row<VEC>(next, f, row + step, bn_col<VEC>(w, lane));
     }
     const float tg = token ? ((const float*)j.gate)[row * j.ldgate] : 1.f;
-    float s1[3] = {0.f, 0.f, 0.f};
+    bn2 hh = 0, uh = 0, yy = 0;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      float h[8], v[8];
-      if (j.before) {
-        cur[i].h.values(h);
-        cur[i].dr.values(v);
+      bn2 h[4], v[4];
+      if (has_b) {
+        if (!KEEP) before(i);
+        in_h(i, h);
+        in_dr(i, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s1[0] = fmaf(h[e], h[e], s1[0]);
-          s1[1] = fmaf(v[e] * kb[i][e], h[e], s1[1]);
+        for (int e = 0; e < 4; ++e) {
+          hh = bn_fma(h[e], h[e], hh);
+          uh = bn_fma(bn_mul(v[e], kb[i][e]), h[e], uh);
         }
       }
-      if (j.after) {
-        cur[i].y.values(v);
+      if (has_a) {
+        in_y(i, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s1[2] = fmaf(v[e], v[e], s1[2]);
+        for (int e = 0; e < 4; ++e) yy = bn_fma(v[e], v[e], yy);
       }
     }
-    bn_group_sum(s1, red, W, w, lane, bar, turn);
-    const float rh = j.before ? __frsqrt_rn(fmaf(s1[0], mean, j.eps)) : 0.f;
-    const float ry = j.after ? __frsqrt_rn(fmaf(s1[2], mean, j.eps)) : 1.f;
-    const float qh = rh * rh * rh * (s1[1] * mean);
-    float s2[2] = {0.f, 0.f}, gr[C][8];
+    float s0 = bn_both(hh), s1 = bn_both(uh), s2 = bn_both(yy);
+    grp.sum(s0, s1, s2);
+    const float rh = rsqrtf(fmaf(s0, mean, j.eps)), qh = -(rh * rh * rh * (s1 * mean));
+    const float ry = has_a ? rsqrtf(fmaf(s2, mean, j.eps)) : 1.f, rt = ry * tg;
+    const bn2 rh2 = bn_pair(rh, rh), qh2 = bn_pair(qh, qh), rt2 = bn_pair(rt, rt);
+    bn2 gr[C][4], py = 0;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int c = bn_col<VEC>(w + i * W, lane);
-      float h[8], v[8], o[8];
-      if (f.dh) cur[i].dh.values(gr[i]);
-      else
+      bn2 h[4], v[4], o[4], (&x)[4] = gr[i];
+      if (has_dh) {
+        in_dh(i, x);
+      } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) gr[i][e] = 0.f;
-      if (j.before) {
-        cur[i].h.values(h);
-        cur[i].dr.values(v);
+        for (int e = 0; e < 4; ++e) x[e] = 0;
+      }
+      if (has_b) {
+        if (!KEEP) before(i);
+        in_h(i, h);
+        in_dr(i, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float t = v[e] * rh;
-          sb[i][e] = fmaf(t, h[e], sb[i][e]);
-          gr[i][e] += fmaf(t, kb[i][e], -h[e] * qh);
+        for (int e = 0; e < 4; ++e) {
+          const bn2 t = bn_mul(v[e], rh2);
+          sb[i][e] = bn_fma(t, h[e], sb[i][e]);
+          x[e] = bn_fma(t, kb[i][e], bn_fma(h[e], qh2, x[e]));
         }
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = j.a * gr[i][e];
-      bn_store<VEC>((S*)f.dx + row * f.lddx, c, n, o);
-      if (!f.y) continue;
-      cur[i].y.values(v);
-      float gt[8];
-      if (full) cur[i].gate.values(gt);
+      for (int e = 0; e < 4; ++e) o[e] = bn_mul(a2, x[e]);
+      bn_store<VEC>(o_dx, c, n, o);
+      if (!has_y) continue;
+      if (!KEEP) behind(i);
+      in_y(i, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float t = j.b * gr[i][e], yn = v[e] * ry, gn = t * (yn * ka[i][e]);
-        if (channel) sg[i][e] += gn;
-        if (token) s2[1] += gn;
-        if (full) o[e] = gn;
-        const float u = t * (full ? gt[e] : channel ? kg[i][e] : tg);
-        sa[i][e] = fmaf(u, yn, sa[i][e]);
-        gr[i][e] = u * ka[i][e];
-        s2[0] = fmaf(gr[i][e], v[e], s2[0]);
+      for (int e = 0; e < 4; ++e) x[e] = bn_mul(b2, x[e]);
+      if (full) {
+        in_gate(i, h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[e] = bn_mul(bn_mul(x[e], kw[i][e]), bn_mul(v[e], rt2));
+          x[e] = bn_mul(x[e], h[e]);
+        }
+        bn_store<VEC>(o_dgate, c, n, o);
       }
-      if (full) bn_store<VEC>((T*)f.dgate + row * f.lddgate, c, n, o);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sq[i][e] = bn_fma(x[e], bn_mul(v[e], rt2), sq[i][e]);
+        x[e] = bn_mul(x[e], kw[i][e]);
+        py = bn_fma(x[e], v[e], py);
+      }
     }
-    if (f.y) {
-      if (j.after || token) bn_group_sum(s2, red, W, w, lane, bar, turn);
-      if (token && w == 0 && lane == 0) ((float*)f.dgate)[row * f.lddgate] = s2[1];
-      const float qy = j.after ? ry * ry * ry * (s2[0] * mean) : 0.f;
+    o_dx += f.hop_dx;
+    if (full) o_dgate += f.hop_dgate;
+    if (has_y) {
+      float s = 0.f;
+      if (has_a || token) s = grp.sum(bn_both(py));
+      if (token && w == 0 && lane == 0) ((float*)f.dgate)[row * f.lddgate] = s * ry;
+      const float qy = has_a ? -(ry * ry * rt * (s * mean)) : 0.f;
+      const bn2 qy2 = bn_pair(qy, qy);
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        float v[8];
-        cur[i].y.values(v);
+        bn2 v[4];
+        in_y(i, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = fmaf(gr[i][e], ry, -v[e] * qy);
-        bn_store<VEC>((T*)f.dy + row * f.lddy, bn_col<VEC>(w + i * W, lane), n, v);
+        for (int e = 0; e < 4; ++e) v[e] = bn_fma(gr[i][e], rt2, bn_mul(v[e], qy2));
+        bn_store<VEC>(o_dy, bn_col<VEC>(w + i * W, lane), n, v);
       }
+      o_dy += f.hop_dy;
     }
-    if (C == 1) cur[0] = next;
+    if (VEC) get = get + slot == slot * stages ? 0 : get + slot;
+    if (!VEC && C == 1) cur[0] = next;
   }
-  // the groups' column sums, in the groups' order
-  const int nb = j.before ? 1 : 0, na = j.after ? 1 : 0, ns = nb + na + (channel ? 1 : 0);
+  // the groups' column sums side by side, then joined in the groups' order
+  const int nb = has_b ? 1 : 0, nq = has_a || channel ? 1 : 0, ns = nb + nq;
   if (!ns) return;
   float* part = f.ws + (long long)blockIdx.x * ns * n;
-  float* to = G > 1 ? sh : part;
-  for (int gg = 0; gg < G; ++gg) {
-    __syncthreads();                        // the row sums' buffers, then the group before
-    if (g != gg) continue;
+  float* to = G > 1 ? sh + (long long)g * ns * n : part;
+  if (G > 1) __syncthreads();               // the rows' use of shared memory
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
+  for (int i = 0; i < C; ++i) {
+    const int c = bn_col<VEC>(w + i * W, lane);
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        if (k == 0 ? !nb : k == 1 ? !na : !channel) continue;
-        const float* v = k == 0 ? sb[i] : k == 1 ? sa[i] : sg[i];
-        float* p = to + (long long)(k == 0 ? 0 : k == 1 ? nb : nb + na) * n;
+    for (int k = 0; k < 2; ++k) {
+      if (k == 0 ? !nb : !nq) continue;
+      float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int c = bn_col<VEC>(w + i * W, lane) + (VEC ? e : 32 * e);
-          if (c < n) p[c] = gg ? p[c] + v[e] : v[e];
+      for (int e = 0; e < 4; ++e) bn_split(k == 0 ? sb[i][e] : sq[i][e], v[2 * e], v[2 * e + 1]);
+      float* p = to + (long long)(k ? nb : 0) * n;
+      if constexpr (VEC) {
+        if (c < n) {
+          *reinterpret_cast<float4*>(p + c) = make_float4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<float4*>(p + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
         }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + 32 * e < n) p[c + 32 * e] = v[e];
       }
     }
   }
   if (G == 1) return;
   __syncthreads();
-  for (int c = threadIdx.x; c < ns * n; c += blockDim.x) part[c] = sh[c];
+  for (int c = threadIdx.x; c < ns * n; c += blockDim.x) {
+    float v = 0.f;
+    for (int i = 0; i < G; ++i) v += sh[i * ns * n + c];
+    part[c] = v;
+  }
 }
 
 // Column sums of the CTAs' parts: eight warps take every eighth part of 32
-// columns, joined in order.
+// columns, joined in order.  Of the two sums (or one) the first is dbefore's, the
+// second q.
 struct Sums {
-  const float* ws;
-  float* out[3];
+  const float *ws, *after, *gate;
+  float *dbefore, *dafter, *dgate;
   int parts, width, sums, accumulate;
 };
 __global__ void __launch_bounds__(256) column_sums_k(Sums s) {
@@ -375,8 +620,18 @@ __global__ void __launch_bounds__(256) column_sums_k(Sums s) {
   v = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) v += red[i][lane];
-  float* out = k == 0 ? s.out[0] : k == 1 ? s.out[1] : s.out[2];
-  out[c] = s.accumulate ? out[c] + v : v;
+  if (k == 0 && s.dbefore) {
+    s.dbefore[c] = s.accumulate ? s.dbefore[c] + v : v;
+    return;
+  }
+  if (s.dafter) {
+    const float x = s.gate ? v * s.gate[c] : v;
+    s.dafter[c] = s.accumulate ? s.dafter[c] + x : x;
+  }
+  if (s.dgate) {
+    const float x = s.after ? v * s.after[c] : v;
+    s.dgate[c] = s.accumulate ? s.dgate[c] + x : x;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -421,21 +676,30 @@ int fwd_t(const Fwd& f, cudaStream_t st) {
   return ops_launch(block_norm_k<S, T, VEC, 4, true>, (unsigned)f.j.rows, 32u * (unsigned)((chunks + 3) / 4), 0, st, 1, f);
 }
 
-// warps of a row, and rows at once of a CTA of up to 16 warps
-int bwd_warps(int64_t width) {
-  const int chunks = (int)((width + 255) / 256);
-  return chunks <= 16 ? chunks : (chunks + 1) / 2;
-}
 template <class S, class T, int VEC>
-int bwd_t(const Bwd& f, int sms, int* parts, cudaStream_t st) {
-  const int W = bwd_warps(f.j.width), most = ops_least(sms, BN_MAX_PARTS);
+int bwd_t(Bwd f, int sms, int* parts, cudaStream_t st) {
+  // a warp to 256 columns of a row up to 4096, to 512 beyond
+  const int chunks = (f.j.width + 255) / 256, C = chunks <= BN_WARPS ? 1 : 2, W = (chunks + C - 1) / C;
+  const int pieces = 2 * Piece<S>::N + (f.j.gate_kind == MT_GATE_FULL ? 3 : 2) * Piece<T>::N;
   // rows are spread over the CTAs before any takes two at once
-  const int per = (f.j.rows + most - 1) / most, G = ops_least(16 / W, per);
+  const int most = ops_least(sms, BN_MAX_PARTS), G = ops_least(BN_WARPS / W, (f.j.rows + most - 1) / most);
   *parts = ops_least((f.j.rows + G - 1) / G, most);
-  size_t smem = (size_t)G * W * 8 * 4, sums = G > 1 ? (size_t)3 * f.j.width * 4 : 0;
+  const size_t red = bn_red(G * W), stage = VEC ? (size_t)C * pieces * 512 * W * G : 0;
+  int stages = BN_STAGES;
+  while (stages > 1 && red + stages * stage > BN_SMEM) --stages;
+  size_t smem = red + stages * stage, sums = G > 1 ? (size_t)G * 2 * f.j.width * 4 : 0;
   if (smem < sums) smem = sums;
-  auto k = W * 256 >= f.j.width ? block_norm_bwd_k<S, T, VEC, 1> : block_norm_bwd_k<S, T, VEC, 2>;
-  return ops_launch(k, (unsigned)*parts, 32u * W * G, smem, st, 1, f, W, G);
+  const long long step = (long long)*parts * G;
+  f.hop_dh = step * f.lddh, f.hop_h = step * f.ldh, f.hop_dr = step * f.lddr, f.hop_y = step * f.ldy;
+  f.hop_gate = step * f.j.ldgate, f.hop_dx = step * f.lddx, f.hop_dy = step * f.lddy, f.hop_dgate = step * f.lddgate;
+  const bool whole = VEC && f.j.before && f.j.after && f.y && f.dh;
+  auto k = C == 2 ? block_norm_bwd_k<S, T, VEC, 2, false>
+           : whole ? block_norm_bwd_k<S, T, VEC, 1, VEC> : block_norm_bwd_k<S, T, VEC, 1, false>;
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+    cudaGetLastError();
+    return MT_ERR_CUDA;
+  }
+  return ops_launch(k, (unsigned)*parts, 32u * W * G, smem, st, 1, f, W, G, stages, pieces);
 }
 
 }  // namespace
@@ -465,7 +729,7 @@ int32_t mt_block_norm(const mt_joint* j, const void* x, int64_t ldx, const void*
 int64_t mt_block_norm_ws_bytes(int64_t rows, int64_t width) {
   if (rows < 0 || width < 1) return -MT_ERR_ARG;
   if (rows > OPS_MAX_ROWS || width > BN_MAX_WIDTH) return -MT_ERR_UNSUPPORTED;
-  return (rows < 1 ? 1 : rows < BN_MAX_PARTS ? rows : BN_MAX_PARTS) * 3 * width * 4;
+  return ((rows < 1 ? 1 : rows < BN_MAX_PARTS ? rows : BN_MAX_PARTS) * 2 * width * 4 + 15) / 16 * 16;
 }
 
 int32_t mt_block_norm_bwd(const mt_joint* j, const void* h, int64_t ldh, const void* y, int64_t ldy, const void* dr,
@@ -492,7 +756,7 @@ int32_t mt_block_norm_bwd(const mt_joint* j, const void* h, int64_t ldh, const v
     if (j->gate_kind == MT_GATE_TOKEN && !ops_mat_ok(dgate, MT_DT_FP32, lddgate, 1)) return MT_ERR_ARG;
     if (j->gate_kind == MT_GATE_FULL && !ops_mat_ok(dgate, od, lddgate, n)) return MT_ERR_ARG;
   }
-  const int sums = (dbefore ? 1 : 0) + (dafter ? 1 : 0) + (channel ? 1 : 0);
+  const int sums = (dbefore ? 1 : 0) + (dafter || channel ? 1 : 0);
   if (sums && (!ws || !ops_aligned(ws, 16))) return MT_ERR_ARG;
   if (sums && ws_bytes < mt_block_norm_ws_bytes(j->rows, j->width)) return MT_ERR_ARENA_SMALL;
   cudaStream_t s = (cudaStream_t)stream;
@@ -515,11 +779,8 @@ int32_t mt_block_norm_bwd(const mt_joint* j, const void* h, int64_t ldh, const v
     if (rc) return rc;
   }
   if (!sums) return MT_OK;
-  Sums c = {(const float*)ws, {}, parts, (int)j->width, sums, accumulate};
-  int k = 0;
-  if (dbefore) c.out[k++] = dbefore;
-  if (dafter) c.out[k++] = dafter;
-  if (channel) c.out[k++] = (float*)dgate;
+  const Sums c = {(const float*)ws, j->after, channel ? (const float*)j->gate : nullptr, dbefore, dafter,
+                  channel ? (float*)dgate : nullptr, parts, (int)j->width, sums, accumulate};
   return ops_launch(column_sums_k, dim3((unsigned)((j->width + 31) / 32), (unsigned)sums), 256, 0, s, 1, c);
 }
 

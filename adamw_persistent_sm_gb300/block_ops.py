@@ -72,6 +72,17 @@ def _joint(stream: torch.Tensor, dtype, after, gate, before, res_scale, out_scal
                       _limit(n_rows, dev) or None, kind, res_scale, out_scale, eps, 0)
 
 
+def _summed(given, grad, what: str, dev: int, width: int, accumulate: bool) -> int | None:
+    """Address of the gradient of a vector that rows share, None where there is none yet."""
+    if grad is None:
+        if accumulate and given is not None:
+            raise ValueError(f"accumulate needs {what}")
+        return None
+    if given is None:
+        raise ValueError(f"{what} of nothing")
+    return _vec(grad, what, dev, width)
+
+
 def _alone(after, gate, res_scale) -> None:
     if after is not None or gate is not None or res_scale != 1.0:
         raise ValueError("after, gate and res_scale belong to a block's output y")
@@ -165,30 +176,29 @@ def block_norm_bwd(dr: torch.Tensor | None, dh: torch.Tensor | None, h: torch.Te
     lddr = 0 if dr is None else _mat(dr, "dr", dev, rows, width, dtype)
     lddh = 0 if dh is None else _mat(dh, "dh", dev, rows, width, h.dtype)
     ldy = 0 if y is None else _mat(y, "y", dev, rows, width)
-    sums = ((after, dafter, "dafter"), (before, dbefore, "dbefore"),
-            (gate if gate is not None and gate.dim() == 1 else None, dgate if gate is None or gate.dim() == 1 else None, "dgate"))
-    for given, grad, what in sums:
-        if given is None and grad is not None:
-            raise ValueError(f"{what} of nothing")
-        if accumulate and given is not None and grad is None:
-            raise ValueError(f"accumulate needs {what}")
-        _vec(grad, what, dev, width)
+    channel = gate is not None and gate.dim() == 1
     j = _joint(h, dtype, after, gate, before, res_scale, out_scale, eps, n_rows, dev)
     if dx is None:
         dx = torch.empty((rows, width), dtype=h.dtype, device=dev)
     lddx = _mat(dx, "dx", dev, rows, width, h.dtype)
     if y is not None and dy is None:
         dy = torch.empty((rows, width), dtype=dtype, device=dev)
-    lddy = 0 if dy is None else _mat(dy, "dy", dev, rows, width, dtype)
+    lddy = 0 if y is None else _mat(dy, "dy", dev, rows, width, dtype)
+    pa = _summed(after, dafter, "dafter", dev, width, accumulate)
     if after is not None and dafter is None:
         dafter = torch.empty(width, dtype=torch.float32, device=dev)
+        pa = dafter.data_ptr()
+    pb = _summed(before, dbefore, "dbefore", dev, width, accumulate)
     if before is not None and dbefore is None:
         dbefore = torch.empty(width, dtype=torch.float32, device=dev)
+        pb = dbefore.data_ptr()
     lddgate = 0
+    if channel or gate is None:
+        _summed(gate, dgate, "dgate", dev, width, accumulate)
     if gate is not None:
         if dgate is None:
             dgate = torch.empty(gate.shape, dtype=gate.dtype, device=dev)
-        if gate.dim() == 2:
+        if not channel:
             lddgate = _mat(dgate, "dgate", dev, rows, gate.shape[1], gate.dtype)
     lib = B.load()
     nbytes = lib.mt_block_norm_ws_bytes(rows, width)
@@ -198,10 +208,11 @@ def block_norm_bwd(dr: torch.Tensor | None, dh: torch.Tensor | None, h: torch.Te
     here = _current()
     if here != dev:
         torch.cuda.set_device(dev)
-    ptr = lambda t: None if t is None else t.data_ptr()                          # noqa: E731
-    st = lib.mt_block_norm_bwd(j, ptr(h), ldh, ptr(y), ldy, ptr(dr), lddr, ptr(dh), lddh, ptr(dx), lddx, ptr(dy), lddy,
-                               ptr(dgate), lddgate, ptr(dafter), ptr(dbefore), int(accumulate), ptr(ws), nbytes,
-                               _raw_stream(dev))
+    st = lib.mt_block_norm_bwd(j, h.data_ptr(), ldh, None if y is None else y.data_ptr(), ldy,
+                               None if dr is None else dr.data_ptr(), lddr, None if dh is None else dh.data_ptr(),
+                               lddh, dx.data_ptr(), lddx, None if dy is None else dy.data_ptr(), lddy,
+                               None if dgate is None else dgate.data_ptr(), lddgate, pa, pb, int(accumulate),
+                               ws.data_ptr(), nbytes, _raw_stream(dev))
     if here != dev:
         torch.cuda.set_device(here)
     if st:
@@ -334,70 +345,61 @@ class GradSet:
     they come) for :meth:`norm` and :meth:`clip`; ``out``: tensors that receive
     the clipped ones (default: in place).  Tensors are dense (contiguous, or a
     permutation of that) and do not overlap; an output is its gradient itself, or
-    has its type, shape and strides and overlaps no tensor of the set.  The set
-    holds the tensors, not their values: each call takes what they hold then (and
-    looks where they lie, so that ``t.data = ...`` is seen).  The results are new
-    at each call, and so is the workspace: a set may be used on several streams."""
+    has its type, shape and strides and overlaps no tensor of the set.
+
+    The set is of the memory that the tensors have when it is made, which it keeps
+    alive: each call takes the values that are there then, and looks at no tensor
+    again (500 of them would take 110 us).  Tensors that were given other memory
+    since (``t.data = ...``, a new ``.grad``) need a new set; memory may not be
+    taken from under it (a storage resized).  Results and workspaces are new at
+    each call."""
 
     def __init__(self, tensors: Sequence[torch.Tensor], out: Sequence[torch.Tensor] | None = None,
                  device: str | torch.device | None = None):
-        self.tensors = list(tensors)
-        self.out = self.tensors if out is None else list(out)
-        if len(self.out) != len(self.tensors):
-            raise ValueError(f"{len(self.out)} outputs for {len(self.tensors)} tensors")
+        tensors = list(tensors)
+        out = tensors if out is None else list(out)
+        if len(out) != len(tensors):
+            raise ValueError(f"{len(out)} outputs for {len(tensors)} tensors")
         if device is None:
-            device = self.tensors[0].device if self.tensors else "cuda"
+            device = tensors[0].device if tensors else "cuda"
         self.device = torch.device(device)
         if self.device.type != "cuda":
             raise ValueError(f"expected tensors on a CUDA device, got {self.device}")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
-        self._dev = self.device.index
-        self._bytes = B.load().mt_grad_ws_bytes(len(self.tensors))
-        self._look()
-
-    def _where(self) -> list[int]:
-        """Where everything lies now."""
-        at = [t.data_ptr() for t in self.tensors]
-        return at if self.out is self.tensors else at + [t.data_ptr() for t in self.out]
-
-    def _look(self) -> None:
-        dev, spans, runs = self._dev, [], []
-        for i, (t, o) in enumerate(zip(self.tensors, self.out)):
-            if t.dtype not in _DTYPES or t.get_device() != dev or t.is_sparse or not _dense(t):
+        self._dev = dev = self.device.index
+        spans, runs = [], []
+        for i, (t, o) in enumerate(zip(tensors, out)):
+            if t.dtype not in _DTYPES or t.get_device() != dev or t.layout is not torch.strided or not _dense(t):
                 raise ValueError(f"tensor {i}: expected dense float32 or bfloat16 on cuda:{dev}, got {t.dtype} "
-                                 f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+                                 f"{tuple(t.shape)} on {t.device}")
             if o is not t and (o.dtype is not t.dtype or o.get_device() != dev or o.shape != t.shape
                                or o.stride() != t.stride()):
                 raise ValueError(f"output {i}: expected {t.dtype} {tuple(t.shape)} with strides {t.stride()} on "
                                  f"cuda:{dev}, got {o.dtype} {tuple(o.shape)} with strides {o.stride()} on {o.device}")
-            n = t.numel()
-            a, b, size = t.data_ptr(), o.data_ptr(), n * t.element_size()
+            n, a, b = t.numel(), t.data_ptr(), o.data_ptr()
             if n:
-                runs.append((a, a + size, i))
+                runs.append((a, a + n * t.element_size(), i))
                 if a != b:
-                    runs.append((b, b + size, i))
+                    runs.append((b, b + n * t.element_size(), i))
             spans.append((a, b, n, _DTYPES[t.dtype], 0))
         runs.sort()
         for (_, end, i), (start, _, k) in zip(runs, runs[1:]):
             if start < end:
                 raise ValueError(f"tensors or outputs {i} and {k} overlap")
+        self._n = len(spans)
         self._spans = (B.mt_span * max(1, len(spans)))(*spans)
-        self._at = self._where()
-
-    def _ready(self) -> torch.Tensor:
-        if self._where() != self._at:
-            self._look()
-        return torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
+        self._bytes = B.load().mt_grad_ws_bytes(len(spans))
+        self._kept = {s.data_ptr(): s for s in (t.untyped_storage() for t in (*tensors, *out))}
 
     def norm(self, scale: float = 1.0) -> torch.Tensor:
         """|scale| times the square root of the sum of all squares, float32 [1]."""
-        ws = self._ready()
+        ws = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
         norm = torch.empty(1, dtype=torch.float32, device=self.device)
         dev, lib, here = self._dev, B.load(), _current()
         if here != dev:
             torch.cuda.set_device(dev)
-        st = lib.mt_grad_norm(self._spans, len(self.tensors), scale, norm.data_ptr(), ws.data_ptr(), self._bytes,
+        st = lib.mt_grad_norm(self._spans, self._n, scale, norm.data_ptr(), ws.data_ptr(), self._bytes,
                               _raw_stream(dev))
         if here != dev:
             torch.cuda.set_device(here)
@@ -410,12 +412,12 @@ class GradSet:
         the norm of the scaled tensors (NaN where that is NaN).  ``scale`` turns
         a sum over microbatches or of scaled losses into the gradient.  Returns
         (norm, c), float32 [2]."""
-        ws = self._ready()
+        ws = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
         stats = torch.empty(2, dtype=torch.float32, device=self.device)
         dev, lib, here = self._dev, B.load(), _current()
         if here != dev:
             torch.cuda.set_device(dev)
-        st = lib.mt_grad_clip(self._spans, len(self.tensors), max_norm, eps, scale, stats.data_ptr(), ws.data_ptr(),
+        st = lib.mt_grad_clip(self._spans, self._n, max_norm, eps, scale, stats.data_ptr(), ws.data_ptr(),
                               self._bytes, _raw_stream(dev))
         if here != dev:
             torch.cuda.set_device(here)

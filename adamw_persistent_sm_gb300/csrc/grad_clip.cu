@@ -6,9 +6,10 @@
 
 namespace {
 
-#define GC_THREADS 512
+#define GC_THREADS 256
+#define GC_CTAS 3                 // of an SM (219M fp32 elements: 399 us, with four 408)
 #define GC_UNIT 8192              // elements: what work is dealt out in
-#define GC_PARTS 512              // partial sums of one launch, at most
+#define GC_PARTS 1024              // partial sums of one launch, at most
 #define GC_TABLE 1024             // tensors of one launch, at most
 
 // The tensors of a launch, by value: nothing is copied to the device ahead of a
@@ -47,84 +48,115 @@ __device__ __forceinline__ int gc_head(const T* p, long long n) {
 __device__ __forceinline__ float gc_f(float v) { return v; }
 __device__ __forceinline__ float gc_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// Squares of n elements.  Sums of 32 bits over at most 64 squares in each of
-// eight places, joined in 64; eights whose largest magnitude is over 2^52 or
-// under 2^-48, where squares or their sums leave the normal numbers, are squared
-// in 64 bits at once (infinities and NaN among them).
-template <class T>
-__device__ __forceinline__ double gc_squares(const T* p, long long n) {
-  double d = 0.0;
-  const int head = gc_head(p, n);
-  if ((int)threadIdx.x < head) {
-    const double v = gc_f(p[threadIdx.x]);
-    d = v * v;
+// A thread's sum of squares.  In 32 bits over at most 64 squares in each of eight
+// places, then joined in 64; eights whose largest magnitude is over 2^52 or under
+// 2^-48, where squares or their sums leave the normal numbers, are squared in 64 bits
+// at once (infinities and NaN among them).  Sixty-four-bit instructions are some
+// thirty times slower here: with eight of them for every run of a tensor and a
+// reduction of all threads in 64 bits, 16 MB of 500 tensors took 34 us.
+#define GC_JOIN 64
+struct Squares {
+  float s[8];
+  double d;
+  int n;
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = 0.f;
+    d = 0.0;
+    n = 0;
   }
-  const long long vecs = (n - head) / 8;
-  const T* q = p + head;
-  const int tail = (int)(n - head - vecs * 8);
-  if ((int)threadIdx.x < tail) {
-    const double v = gc_f(q[vecs * 8 + threadIdx.x]);
-    d += v * v;
+  __device__ __forceinline__ float places() {
+    const float t = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = 0.f;
+    n = 0;
+    return t;
   }
-  constexpr int U = 4;
-  for (long long i0 = threadIdx.x; i0 < vecs; i0 += 16 * U * GC_THREADS) {
-    float s[8] = {};
-    for (int k = 0; k < 16; ++k) {
-      const long long i = i0 + (long long)k * U * GC_THREADS;
-      if (i >= vecs) break;
-      Raw8<T> v[U];
+  __device__ __forceinline__ void room(int more) {
+    if (n + more > GC_JOIN) d += (double)places();
+    n += more;
+  }
+  __device__ __forceinline__ static bool plain(uint32_t top) { return top - 0x27800000u < 0x59800000u - 0x27800000u; }
+  __device__ __forceinline__ void one(float x) {
+    const uint32_t top = __float_as_uint(x) & 0x7fffffffu;
+    if (plain(top)) s[0] = fmaf(x, x, s[0]);
+    else if (top) d += (double)x * (double)x;
+  }
+  template <class T>
+  __device__ __forceinline__ void eight(const Raw8<T>& v) {
+    float x[8];
+    v.values(x);
+    const uint32_t top = v.top();
+    if (plain(top)) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i + u * GC_THREADS < vecs) v[u].template load<2>(q + (i + u * GC_THREADS) * 8, 0, 8);
+      for (int e = 0; e < 8; ++e) s[e] = fmaf(x[e], x[e], s[e]);
+    } else if (top) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (i + u * GC_THREADS >= vecs) break;
-        float x[8];
-        v[u].values(x);
-        const uint32_t top = v[u].top();
-        if (top - 0x27800000u < 0x59800000u - 0x27800000u) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s[e] = fmaf(x[e], x[e], s[e]);
-        } else if (top) {
-          for (int e = 0; e < 8; ++e) d += (double)x[e] * (double)x[e];
-        }
-      }
+      for (int e = 0; e < 8; ++e) d += (double)x[e] * (double)x[e];
     }
-    d += (((double)s[0] + s[1]) + ((double)s[2] + s[3])) + (((double)s[4] + s[5]) + ((double)s[6] + s[7]));
   }
-  return d;
-}
+};
 
-// sum over the CTA, in a fixed order; every thread gets it
-__device__ __forceinline__ double gc_cta_sum(double d) {
-  __shared__ double red[GC_THREADS / 32];
-  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = d;
-  __syncthreads();
-  d = 0.0;
-  for (int i = 0; i < GC_THREADS / 32; ++i) d += red[i];
-  return d;
+#define GC_FLIGHT 4               // eights of a thread on their way at once
+// n elements at p
+template <class T>
+__device__ __forceinline__ void gc_squares(Squares& q, const T* p, long long n) {
+  const int head = gc_head(p, n);
+  const long long vecs = (n - head) / 8;
+  const int tail = (int)(n - head - vecs * 8);
+  q.room(2);
+  if ((int)threadIdx.x < head) q.one(gc_f(p[threadIdx.x]));
+  p += head;
+  if ((int)threadIdx.x < tail) q.one(gc_f(p[vecs * 8 + threadIdx.x]));
+  for (long long i = threadIdx.x; i < vecs; i += GC_FLIGHT * GC_THREADS) {
+    Raw8<T> v[GC_FLIGHT];
+#pragma unroll
+    for (int u = 0; u < GC_FLIGHT; ++u)
+      if (i + u * GC_THREADS < vecs) v[u].template load<2>(p + (i + u * GC_THREADS) * 8, 0, 8);
+    q.room(GC_FLIGHT);
+#pragma unroll
+    for (int u = 0; u < GC_FLIGHT; ++u)
+      if (i + u * GC_THREADS < vecs) q.eight(v[u]);
+  }
 }
 
 template <int N>
-__global__ void __launch_bounds__(GC_THREADS, 2) squares_k(const __grid_constant__ Table<N> t, double* parts) {
+__global__ void __launch_bounds__(GC_THREADS, GC_CTAS) squares_k(const __grid_constant__ Table<N> t, double* parts) {
   ops_begin();
+  __shared__ double red[GC_THREADS / 32];
   const uint32_t units = t.start[t.n];
   uint32_t u = gc_share(units, blockIdx.x);
   const uint32_t end = gc_share(units, blockIdx.x + 1);
-  double d = 0.0;
+  Squares q;
+  q.clear();
   if (u < end) {
     for (int s = gc_find(t, u); u < end; ++s) {
       const uint32_t first = t.start[s], last = t.start[s + 1] < end ? t.start[s + 1] : end;
       if (last <= u) continue;
       const long long lo = (long long)(u - first) * GC_UNIT, to = (long long)(last - first) * GC_UNIT;
       const long long n = (to < t.numel[s] ? to : t.numel[s]) - lo;
-      d += t.bf16[s] ? gc_squares((const __nv_bfloat16*)t.in[s] + lo, n) : gc_squares((const float*)t.in[s] + lo, n);
+      if (t.bf16[s]) gc_squares(q, (const __nv_bfloat16*)t.in[s] + lo, n);
+      else gc_squares(q, (const float*)t.in[s] + lo, n);
       u = last;
     }
   }
-  d = gc_cta_sum(d);
-  if (threadIdx.x == 0) parts[blockIdx.x] = d;
+  // the CTA's threads, in 32 bits where no thread has more, then its warps
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (__syncthreads_or(q.d != 0.0)) {
+    double d = q.d + (double)q.places();
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if (lane == 0) red[warp] = d;
+  } else {
+    float f = q.places();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+    if (lane == 0) red[warp] = (double)f;
+  }
+  __syncthreads();
+  if (warp) return;
+  double d = lane < GC_THREADS / 32 ? red[lane] : 0.0;
+  for (int o = GC_THREADS / 64; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  if (lane == 0) parts[blockIdx.x] = d;
 }
 
 struct Clip {
@@ -133,19 +165,44 @@ struct Clip {
   double scale, max_norm, eps;
   int n_parts, clip;
 };
-// the norm from the parts, in their order, and the factor of the clipped tensors
+// The norm from the parts, in their order, and the factor of the clipped tensors: by
+// one warp, for the CTA.  In 32 bits where they hold the sum and its root.
 __device__ __forceinline__ float gc_factor(const Clip& c, bool write) {
-  double d = 0.0;
-  for (int i = threadIdx.x; i < c.n_parts; i += GC_THREADS) d += c.parts[i];
-  const double norm = fabs(c.scale) * sqrt(gc_cta_sum(d));
-  const double r = c.max_norm / (norm + c.eps), coef = r >= 1.0 ? 1.0 : r;          // NaN stays
-  if (write && threadIdx.x == 0) {
-    c.stats[0] = (float)norm;
-    if (c.clip) c.stats[1] = (float)coef;
+  __shared__ float factor;
+  if (threadIdx.x < 32) {
+    double d = 0.0;
+    for (int i0 = 0; i0 < c.n_parts; i0 += 512) {
+      double v[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) v[u] = i0 + u * 32 + (int)threadIdx.x < c.n_parts ? c.parts[i0 + u * 32 + threadIdx.x] : 0.0;
+#pragma unroll
+      for (int u = 0; u < 16; ++u)
+        if (i0 + u * 32 < c.n_parts) d += v[u];
+    }
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if (threadIdx.x == 0) {
+      const float f = (float)d, sc = (float)c.scale, top = (float)c.max_norm, eps = (float)c.eps;
+      float norm = fabsf(sc) * sqrtf(f), coef = top / (norm + eps), by;
+      if (f > 1e-24f && f < 1e36f && norm > 1e-12f && norm < 1e18f && top > 1e-12f && top < 1e18f) {
+        coef = coef >= 1.f ? 1.f : coef;
+        by = sc * coef;
+      } else {
+        const double nd = fabs(c.scale) * sqrt(d), r = c.max_norm / (nd + c.eps), cd = r >= 1.0 ? 1.0 : r;     // NaN stays
+        norm = (float)nd;
+        coef = (float)cd;
+        by = (float)(c.scale * cd);
+      }
+      if (write) {
+        c.stats[0] = norm;
+        if (c.clip) c.stats[1] = coef;
+      }
+      factor = by;
+    }
   }
-  return (float)(c.scale * coef);
+  __syncthreads();
+  return factor;
 }
-__global__ void __launch_bounds__(GC_THREADS) norm_k(Clip c) {
+__global__ void __launch_bounds__(32) norm_k(Clip c) {
   ops_begin();
   gc_factor(c, true);
 }
@@ -170,38 +227,37 @@ __device__ __forceinline__ void gc_scale(const T* p, T* o, long long n, float f)
   p += head;
   o += head;
   if ((int)threadIdx.x < tail) o[vecs * 8 + threadIdx.x] = gc_t<T>(gc_f(p[vecs * 8 + threadIdx.x]) * f);
-  constexpr int U = 4;
-  for (long long i = threadIdx.x; i < vecs; i += U * GC_THREADS) {
-    Raw8<T> v[U];
+  // from the end: what the squares read last is the likeliest to be in L2 still
+  for (long long i = vecs - 1 - threadIdx.x; i >= 0; i -= GC_FLIGHT * GC_THREADS) {
+    Raw8<T> v[GC_FLIGHT];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + u * GC_THREADS < vecs) v[u].template load<2>(p + (i + u * GC_THREADS) * 8, 0, 8);
+    for (int u = 0; u < GC_FLIGHT; ++u)
+      if (i - u * GC_THREADS >= 0) v[u].template load<2>(p + (i - u * GC_THREADS) * 8, 0, 8);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (i + u * GC_THREADS >= vecs) break;
+    for (int u = 0; u < GC_FLIGHT; ++u) {
+      if (i - u * GC_THREADS < 0) break;
       float x[8];
       v[u].values(x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] *= f;
-      ops_st8<2>(o + (i + u * GC_THREADS) * 8, 0, 8, x);
+      ops_st8<2>(o + (i - u * GC_THREADS) * 8, 0, 8, x);
     }
   }
 }
 
 template <int N>
-__global__ void __launch_bounds__(GC_THREADS, 2) scale_k(const __grid_constant__ Table<N> t, Clip c, int first) {
+__global__ void __launch_bounds__(GC_THREADS, GC_CTAS) scale_k(const __grid_constant__ Table<N> t, Clip c, int first) {
   ops_begin();
   const float f = gc_factor(c, first && blockIdx.x == 0);
-  const uint32_t units = t.start[t.n];
-  uint32_t u = gc_share(units, blockIdx.x);
-  const uint32_t end = gc_share(units, blockIdx.x + 1);
-  if (u >= end) return;
-  for (int s = gc_find(t, u); u < end; ++s) {
-    const uint32_t from = t.start[s], last = t.start[s + 1] < end ? t.start[s + 1] : end;
-    if (last <= u) continue;
-    const long long lo = (long long)(u - from) * GC_UNIT, to = (long long)(last - from) * GC_UNIT;
+  const uint32_t units = t.start[t.n], begin = gc_share(units, blockIdx.x);
+  uint32_t u = gc_share(units, blockIdx.x + 1);
+  if (u <= begin) return;
+  for (int s = gc_find(t, u - 1); u > begin; --s) {
+    const uint32_t from = t.start[s], low = from > begin ? from : begin;
+    if (low >= u) continue;
+    const long long lo = (long long)(low - from) * GC_UNIT, to = (long long)(u - from) * GC_UNIT;
     const long long n = (to < t.numel[s] ? to : t.numel[s]) - lo;
-    u = last;
+    u = low;
     if (f == 1.f && t.in[s] == t.out[s]) continue;          // in place and nothing to clip
     if (t.bf16[s]) gc_scale((const __nv_bfloat16*)t.in[s] + lo, (__nv_bfloat16*)t.out[s] + lo, n, f);
     else gc_scale((const float*)t.in[s] + lo, (float*)t.out[s] + lo, n, f);
@@ -234,7 +290,7 @@ void fill(Table<N>& t, const mt_span* s, int n) {
   t.n = n;
 }
 unsigned gc_grid(uint32_t units, int sms) {
-  const uint32_t most = (uint32_t)ops_least(2 * sms, GC_PARTS);
+  const uint32_t most = (uint32_t)ops_least(GC_CTAS * sms, GC_PARTS);
   return units < 1 ? 1 : units < most ? units : most;
 }
 // one launch over up to N tensors: squares into parts, or scaled into out
@@ -273,7 +329,7 @@ int all(const mt_span* s, int32_t n, const Clip& c0, void* ws, int64_t ws_bytes,
     if (rc) return rc;
     c.n_parts += used;
   }
-  if (!c.clip || n == 0) return ops_launch(norm_k, 1, GC_THREADS, 0, st, 1, c);
+  if (!c.clip || n == 0) return ops_launch(norm_k, 1, 32, 0, st, 1, c);
   for (int i = 0; i < n; i += GC_TABLE) {
     int used = 0;
     const int rc = launch_any(s + i, ops_least(n - i, GC_TABLE), sms, nullptr, &c, i == 0, &used, st);

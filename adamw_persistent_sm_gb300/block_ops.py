@@ -396,6 +396,7 @@ class GradSet:
         """|scale| times the square root of the sum of all squares, float32 [1]."""
         ws = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
         norm = torch.empty(1, dtype=torch.float32, device=self.device)
+        scale = float(scale)
         dev, lib, here = self._dev, B.load(), _current()
         if here != dev:
             torch.cuda.set_device(dev)
@@ -414,6 +415,7 @@ class GradSet:
         (norm, c), float32 [2]."""
         ws = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
         stats = torch.empty(2, dtype=torch.float32, device=self.device)
+        max_norm, eps, scale = float(max_norm), float(eps), float(scale)
         dev, lib, here = self._dev, B.load(), _current()
         if here != dev:
             torch.cuda.set_device(dev)

@@ -131,6 +131,16 @@ class MoETrainer:
         """The gradient buffer's w_gate, w_up and w_down of a weight slot."""
         return tuple(self.view(self.grads, n)[slot] for n in ("w_gate", "w_up", "w_down"))
 
+    def clip_grads(self, max_norm: float | None = None, scale: float = 1.0) -> torch.Tensor:
+        """Scale the gradient buffer in place and clip it to the configuration's
+        norm (or ``max_norm``), as the update's optimizer step would: for steps of
+        an optimizer of the caller's after launches with MT_FLAG_NO_OPTIMIZER, or
+        where :meth:`expert_layer8` added gradients.  Returns (norm, coefficient),
+        float32 [2] on the device."""
+        from .block_ops import clip_grads
+        return clip_grads(list(self.named(self.grads).values()), self.cfg.clip_norm if max_norm is None else max_norm,
+                          self.cfg.clip_eps, scale)
+
     def outputs(self) -> B.mt_outputs:
         return B.mt_read_outputs(self.arena.data_ptr(), self.stream)
 

@@ -34,10 +34,21 @@ def _vec(t: torch.Tensor | None, what: str, dev: int, n: int) -> int | None:
     """Address of a contiguous fp32 vector [n], None for none."""
     if t is None:
         return None
-    if t.dtype is not torch.float32 or t.get_device() != dev or t.shape != (n,) or not t.is_contiguous():
+    if t.dtype is not _F32 or t.get_device() != dev or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what}: expected contiguous float32 [{n}] on cuda:{dev}, got {t.dtype} {tuple(t.shape)} "
                          f"on {t.device}")
     return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, what: str, dev: int, shape, dtype) -> int:
+    """:func:`_mat` of a matrix of this shape and type, quicker where it is contiguous."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return shape[1]
+    return _mat(t, what, dev, shape[0], shape[1], dtype)
+
+
+_F32 = torch.float32
+_load = B.load
 
 
 # ---------------------------------------------------------------------------
@@ -52,35 +63,34 @@ class BlockGrads(NamedTuple):
     dbefore: torch.Tensor | None
 
 
-def _gate(gate, dev: int, rows: int, width: int, dtype, what: str = "gate") -> tuple[int, int]:
-    """Kind and row stride of a gate [width], [rows, 1] or [rows, width]."""
-    if gate is None:
-        return B.MT_GATE_NONE, 0
-    if gate.dim() == 1:
-        _vec(gate, what, dev, width)
-        return B.MT_GATE_CHANNEL, 0
-    if gate.dim() == 2 and gate.shape[1] == 1 and (width > 1 or gate.dtype is torch.float32):
-        return B.MT_GATE_TOKEN, _mat(gate, what, dev, rows, 1, torch.float32)
-    return B.MT_GATE_FULL, _mat(gate, what, dev, rows, width, dtype)
+def _joint(shape, stream, dtype, after, gate, before, res_scale, out_scale, eps, n_rows, dev):
+    """The C ABI's description of a joint."""
+    rows, width = shape
+    kind = ldgate = 0
+    pg = None
+    if gate is not None:
+        if gate.dim() == 1:
+            kind, pg = B.MT_GATE_CHANNEL, _vec(gate, "gate", dev, width)
+        elif gate.dim() == 2 and gate.shape[1] == 1 and (width > 1 or gate.dtype is _F32):
+            kind, ldgate = B.MT_GATE_TOKEN, _mat(gate, "gate", dev, rows, 1, _F32)
+        else:
+            kind, ldgate = B.MT_GATE_FULL, _rows(gate, "gate", dev, shape, dtype)
+        pg = gate.data_ptr() or 16          # of no rows: present, and read by nothing
+    return B.mt_joint(rows, width, _DTYPES[stream], _DTYPES[dtype], _vec(after, "after", dev, width),
+                      _vec(before, "before", dev, width), pg, ldgate, None if n_rows is None else _limit(n_rows, dev),
+                      kind, res_scale, out_scale, eps, 0)
 
 
-def _joint(stream: torch.Tensor, dtype, after, gate, before, res_scale, out_scale, eps, n_rows, dev):
-    rows, width = stream.shape
-    kind, ldgate = _gate(gate, dev, rows, width, dtype)
-    return B.mt_joint(rows, width, _DTYPES[stream.dtype], _DTYPES[dtype], _vec(after, "after", dev, width),
-                      _vec(before, "before", dev, width), None if gate is None else gate.data_ptr() or 16, ldgate,
-                      _limit(n_rows, dev) or None, kind, res_scale, out_scale, eps, 0)
-
-
-def _summed(given, grad, what: str, dev: int, width: int, accumulate: bool) -> int | None:
-    """Address of the gradient of a vector that rows share, None where there is none yet."""
-    if grad is None:
-        if accumulate and given is not None:
-            raise ValueError(f"accumulate needs {what}")
-        return None
+def _summed(given, grad, what: str, dev: int, width: int, accumulate: bool):
+    """The gradient of a vector that rows share, and its address."""
     if given is None:
         raise ValueError(f"{what} of nothing")
-    return _vec(grad, what, dev, width)
+    if grad is None:
+        if accumulate:
+            raise ValueError(f"accumulate needs {what}")
+        grad = torch.empty(width, dtype=_F32, device=dev)
+        return grad, grad.data_ptr()
+    return grad, _vec(grad, what, dev, width)
 
 
 def _alone(after, gate, res_scale) -> None:
@@ -107,40 +117,40 @@ def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, after: torch.T
     one type, the stream's or bfloat16 (``dtype`` gives r's where there is no y).
     ``h`` may be x (in place).  ``n_rows`` (device int32 [1]): rows from it on are
     left as they were.  Up to 8192 columns.  Returns (h, r)."""
-    dev = x.get_device()
+    dev, shape, stream = x.get_device(), x.shape, x.dtype
     ldx = _mat(x, "x", dev)
-    rows, width = x.shape
+    ldy = ldh = ldr = 0
+    py = ph = pr = None
     if y is None:
         _alone(after, gate, res_scale)
         if before is None or h is not None:
             raise ValueError("without y there is no h to write, and before is needed")
-        dtype = r.dtype if r is not None else dtype or x.dtype
+        dtype = r.dtype if r is not None else dtype or stream
         if dtype not in _DTYPES:
             raise TypeError(f"r: {dtype} where float32 or bfloat16 is needed")
-        ldy = ldh = 0
     else:
-        ldy = _mat(y, "y", dev, rows, width)
         if dtype is not None and dtype is not y.dtype:
             raise TypeError(f"r has y's type {y.dtype}, not {dtype}")
         dtype = y.dtype
+        if dtype not in _DTYPES:
+            raise TypeError(f"y: {dtype} where float32 or bfloat16 is needed")
+        ldy = _rows(y, "y", dev, shape, dtype)
         if h is None:
-            h = torch.empty((rows, width), dtype=x.dtype, device=dev)
-        ldh = _mat(h, "h", dev, rows, width, x.dtype)
-    if before is None:
-        if r is not None:
-            raise ValueError("r needs before")
-        ldr = 0
-    else:
+            h = torch.empty(shape, dtype=stream, device=dev)
+        ldh = _rows(h, "h", dev, shape, stream)
+        py, ph = y.data_ptr(), h.data_ptr()
+    if before is not None:
         if r is None:
-            r = torch.empty((rows, width), dtype=dtype, device=dev)
-        ldr = _mat(r, "r", dev, rows, width, dtype)
-    j = _joint(x, dtype, after, gate, before, res_scale, out_scale, eps, n_rows, dev)
-    lib, here = B.load(), _current()
+            r = torch.empty(shape, dtype=dtype, device=dev)
+        ldr = _rows(r, "r", dev, shape, dtype)
+        pr = r.data_ptr()
+    elif r is not None:
+        raise ValueError("r needs before")
+    j = _joint(shape, stream, dtype, after, gate, before, res_scale, out_scale, eps, n_rows, dev)
+    lib, px, here = _load(), x.data_ptr(), _current()
     if here != dev:
         torch.cuda.set_device(dev)
-    st = lib.mt_block_norm(j, x.data_ptr(), ldx, None if y is None else y.data_ptr(), ldy,
-                           None if y is None else h.data_ptr(), ldh, None if r is None else r.data_ptr(), ldr,
-                           _raw_stream(dev))
+    st = lib.mt_block_norm(j, px, ldx, py, ldy, ph, ldh, pr, ldr, _raw_stream(dev))
     if here != dev:
         torch.cuda.set_device(here)
     if st:
@@ -161,58 +171,61 @@ def block_norm_bwd(dr: torch.Tensor | None, dh: torch.Tensor | None, h: torch.Te
     ``before`` is).  ``dx`` may be dh (in place).  ``dafter``, ``dbefore`` and the
     gradient of a gate [width] are sums over the rows, float32; with
     ``accumulate`` they are added to what the given tensors hold."""
-    dev = h.get_device()
+    accumulate = int(bool(accumulate))
+    dev, shape, stream = h.get_device(), h.shape, h.dtype
     ldh = _mat(h, "h", dev)
-    rows, width = h.shape
+    rows, width = shape
     if dr is None and dh is None:
         raise ValueError("a gradient of r or of h is needed")
     if (dr is None) != (before is None):
         raise ValueError("dr and before come together")
+    dtype = y.dtype if y is not None else dr.dtype if dr is not None else stream
+    if dtype not in _DTYPES:
+        raise TypeError(f"y or dr: {dtype} where float32 or bfloat16 is needed")
+    lddr = lddh = ldy = lddy = lddgate = 0
+    pdr = pdh = py = pdy = pdg = pda = pdb = None
+    if dr is not None:
+        lddr, pdr = _rows(dr, "dr", dev, shape, dtype), dr.data_ptr()
+    if dh is not None:
+        lddh, pdh = _rows(dh, "dh", dev, shape, stream), dh.data_ptr()
     if y is None:
         _alone(after, gate, res_scale)
         if dy is not None:
             raise ValueError("dy needs y")
-    dtype = y.dtype if y is not None else dr.dtype if dr is not None else h.dtype
-    lddr = 0 if dr is None else _mat(dr, "dr", dev, rows, width, dtype)
-    lddh = 0 if dh is None else _mat(dh, "dh", dev, rows, width, h.dtype)
-    ldy = 0 if y is None else _mat(y, "y", dev, rows, width)
-    channel = gate is not None and gate.dim() == 1
-    j = _joint(h, dtype, after, gate, before, res_scale, out_scale, eps, n_rows, dev)
+    else:
+        ldy, py = _rows(y, "y", dev, shape, dtype), y.data_ptr()
+    j = _joint(shape, stream, dtype, after, gate, before, res_scale, out_scale, eps, n_rows, dev)
     if dx is None:
-        dx = torch.empty((rows, width), dtype=h.dtype, device=dev)
-    lddx = _mat(dx, "dx", dev, rows, width, h.dtype)
-    if y is not None and dy is None:
-        dy = torch.empty((rows, width), dtype=dtype, device=dev)
-    lddy = 0 if y is None else _mat(dy, "dy", dev, rows, width, dtype)
-    pa = _summed(after, dafter, "dafter", dev, width, accumulate)
-    if after is not None and dafter is None:
-        dafter = torch.empty(width, dtype=torch.float32, device=dev)
-        pa = dafter.data_ptr()
-    pb = _summed(before, dbefore, "dbefore", dev, width, accumulate)
-    if before is not None and dbefore is None:
-        dbefore = torch.empty(width, dtype=torch.float32, device=dev)
-        pb = dbefore.data_ptr()
-    lddgate = 0
-    if channel or gate is None:
-        _summed(gate, dgate, "dgate", dev, width, accumulate)
-    if gate is not None:
+        dx = torch.empty(shape, dtype=stream, device=dev)
+    lddx = _rows(dx, "dx", dev, shape, stream)
+    if y is not None:
+        if dy is None:
+            dy = torch.empty(shape, dtype=dtype, device=dev)
+        lddy, pdy = _rows(dy, "dy", dev, shape, dtype), dy.data_ptr()
+    if after is not None or dafter is not None:
+        dafter, pda = _summed(after, dafter, "dafter", dev, width, accumulate)
+    if before is not None or dbefore is not None:
+        dbefore, pdb = _summed(before, dbefore, "dbefore", dev, width, accumulate)
+    channel = gate is not None and gate.dim() == 1
+    if channel or gate is None and dgate is not None:
+        dgate, pdg = _summed(gate, dgate, "dgate", dev, width, accumulate)
+    elif gate is not None:
         if dgate is None:
             dgate = torch.empty(gate.shape, dtype=gate.dtype, device=dev)
-        if not channel:
-            lddgate = _mat(dgate, "dgate", dev, rows, gate.shape[1], gate.dtype)
-    lib = B.load()
-    nbytes = lib.mt_block_norm_ws_bytes(rows, width)
-    if nbytes < 0:
-        raise _error("mt_block_norm_bwd", -nbytes)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    here = _current()
+        lddgate = _mat(dgate, "dgate", dev, rows, gate.shape[1], gate.dtype)
+        pdg = dgate.data_ptr()
+    lib, px, nbytes, pws = _load(), dx.data_ptr(), 0, None
+    if after is not None or before is not None or channel:
+        nbytes = lib.mt_block_norm_ws_bytes(rows, width)
+        if nbytes < 0:
+            raise _error("mt_block_norm_bwd", -nbytes)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)     # held until the launch
+        pws = ws.data_ptr()
+    ph, here = h.data_ptr(), _current()
     if here != dev:
         torch.cuda.set_device(dev)
-    st = lib.mt_block_norm_bwd(j, h.data_ptr(), ldh, None if y is None else y.data_ptr(), ldy,
-                               None if dr is None else dr.data_ptr(), lddr, None if dh is None else dh.data_ptr(),
-                               lddh, dx.data_ptr(), lddx, None if dy is None else dy.data_ptr(), lddy,
-                               None if dgate is None else dgate.data_ptr(), lddgate, pa, pb, int(accumulate),
-                               ws.data_ptr(), nbytes, _raw_stream(dev))
+    st = lib.mt_block_norm_bwd(j, ph, ldh, py, ldy, pdr, lddr, pdh, lddh, px, lddx, pdy, lddy, pdg, lddgate, pda, pdb,
+                               accumulate, pws, nbytes, _raw_stream(dev))
     if here != dev:
         torch.cuda.set_device(here)
     if st:

@@ -9,8 +9,9 @@
 namespace {
 
 #define BN_MAX_WIDTH 8192
-#define BN_MAX_PARTS 256          // CTAs that leave partial column sums
+#define BN_MAX_PARTS 160          // CTAs that leave partial column sums
 #define BN_WARPS 16               // of a CTA of the backward pass
+#define BN_ALONE 2                // rounds of one CTA
 #define BN_SMEM (226 * 1024)      // its shared memory
 #define BN_STAGES 2               // of its ring, at most (three: 79.9 against 77.3 us)
 
@@ -33,7 +34,9 @@ struct Bwd {
   const void *h, *y, *dr, *dh;
   void *dx, *dy, *dgate;
   long long ldh, ldy, lddr, lddh, lddx, lddy, lddgate;
-  float* ws;                      // [CTAs][sums][width], see column_sums_k
+  float* ws;                      // [CTAs][sums][width], see bn_finish
+  float *dafter, *dbefore;
+  int accumulate;
   // elements from a group's row to its next
   long long hop_dh, hop_h, hop_dr, hop_y, hop_gate, hop_dx, hop_dy, hop_dgate;
 };
@@ -306,6 +309,41 @@ __device__ __forceinline__ void bn_row(BwdRow<S, T>& v, const Bwd& f, long long 
   if (f.y) bn_load<VEC>(v.y, (const T*)f.y + row * f.ldy, c, n);
   if (f.j.gate_kind == MT_GATE_FULL) bn_load<VEC>(v.gate, (const T*)f.j.gate + row * f.j.ldgate, c, n);
 }
+// What a sum over all rows gives: the first (of two, or the only one, with `before`) is
+// dbefore, the other q.  The factors and what is added to are read before any of U
+// columns is written.
+template <int U>
+__device__ __forceinline__ void bn_finish(const Bwd& f, const int (&k)[U], const int (&c)[U], const float (&v)[U]) {
+  const bool channel = f.j.gate_kind == MT_GATE_CHANNEL;
+  const float* gate = (const float*)f.j.gate;
+  float* dgate = (float*)f.dgate;
+  float ga[U], af[U], o1[U], o2[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    ga[u] = af[u] = 1.f;
+    o1[u] = o2[u] = 0.f;
+    if (c[u] >= f.j.width) continue;
+    if (k[u] == 0 && f.j.before) {
+      if (f.accumulate) o1[u] = f.dbefore[c[u]];
+      continue;
+    }
+    if (channel && f.j.after) ga[u] = gate[c[u]], af[u] = f.j.after[c[u]];
+    if (f.accumulate && f.j.after) o1[u] = f.dafter[c[u]];
+    if (f.accumulate && channel) o2[u] = dgate[c[u]];
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (c[u] >= f.j.width) continue;
+    if (k[u] == 0 && f.j.before) {
+      f.dbefore[c[u]] = o1[u] + v[u];
+      continue;
+    }
+    // rounded before it is added: a gradient added is the gradient alone, added
+    if (f.j.after) f.dafter[c[u]] = o1[u] + __fmul_rn(v[u], ga[u]);
+    if (channel) dgate[c[u]] = o2[u] + __fmul_rn(v[u], af[u]);
+  }
+}
+
 // bytes of the groups' sums, below the ring, which starts on a line of all banks (80.9
 // us off one where 76.1 on one)
 __host__ __device__ constexpr int bn_red(int warps) { return (warps * 32 + 127) / 128 * 128; }
@@ -341,8 +379,8 @@ __global__ void __launch_bounds__(32 * BN_WARPS, 1) block_norm_bwd_k(Bwd f, int 
   const bool has_b = ALL || j.before, has_a = ALL || j.after, has_y = ALL || f.y, has_dh = ALL || f.dh;
   const bool channel = j.gate_kind == MT_GATE_CHANNEL, token = j.gate_kind == MT_GATE_TOKEN,
              full = j.gate_kind == MT_GATE_FULL;
-  // gains of a lane's columns: kept for C 1, fetched where they are used for C 2
-  constexpr bool KEEP = C == 1;
+  // gains of a lane's columns: kept, but by element and C 2 fetched where they are used
+  constexpr bool KEEP = VEC || C == 1;
   bn2 kb[C][4], kw[C][4], sb[C][4], sq[C][4];
   auto before = [&](int i) {
     float v[8];
@@ -448,7 +486,7 @@ __global__ void __launch_bounds__(32 * BN_WARPS, 1) block_norm_bwd_k(Bwd f, int 
   if (full) o_dgate = (T*)f.dgate + row * f.lddgate;
   const bn2 a2 = bn_pair(j.a, j.a), b2 = bn_pair(j.b, j.b);
   for (; row < lim; row += step) {
-    BwdRow<S, T> next;
+    BwdRow<S, T> next = cur[0];
     if constexpr (VEC) {
       if (row != (long long)blockIdx.x * G + g) __syncwarp();    // the stage that this fills has been read
       send();
@@ -485,7 +523,8 @@ __global__ void __launch_bounds__(32 * BN_WARPS, 1) block_norm_bwd_k(Bwd f, int 
     }
     float s0 = bn_both(hh), s1 = bn_both(uh), s2 = bn_both(yy);
     grp.sum(s0, s1, s2);
-    const float rh = rsqrtf(fmaf(s0, mean, j.eps)), qh = -(rh * rh * rh * (s1 * mean));
+    // rh^3 alone may be beyond fp32 for a small eps
+    const float rh = rsqrtf(fmaf(s0, mean, j.eps)), qh = -(rh * (rh * (rh * (s1 * mean))));
     const float ry = has_a ? rsqrtf(fmaf(s2, mean, j.eps)) : 1.f, rt = ry * tg;
     const bn2 rh2 = bn_pair(rh, rh), qh2 = bn_pair(qh, qh), rt2 = bn_pair(rt, rt);
     bn2 gr[C][4], py = 0;
@@ -540,7 +579,7 @@ __global__ void __launch_bounds__(32 * BN_WARPS, 1) block_norm_bwd_k(Bwd f, int 
       float s = 0.f;
       if (has_a || token) s = grp.sum(bn_both(py));
       if (token && w == 0 && lane == 0) ((float*)f.dgate)[row * f.lddgate] = s * ry;
-      const float qy = has_a ? -(ry * ry * rt * (s * mean)) : 0.f;
+      const float qy = has_a ? -(rt * (ry * (ry * (s * mean)))) : 0.f;
       const bn2 qy2 = bn_pair(qy, qy);
 #pragma unroll
       for (int i = 0; i < C; ++i) {
@@ -558,9 +597,8 @@ __global__ void __launch_bounds__(32 * BN_WARPS, 1) block_norm_bwd_k(Bwd f, int 
   // the groups' column sums side by side, then joined in the groups' order
   const int nb = has_b ? 1 : 0, nq = has_a || channel ? 1 : 0, ns = nb + nq;
   if (!ns) return;
-  float* part = f.ws + (long long)blockIdx.x * ns * n;
-  float* to = G > 1 ? sh + (long long)g * ns * n : part;
-  if (G > 1) __syncthreads();               // the rows' use of shared memory
+  float* to = sh + (long long)g * ns * n;
+  __syncthreads();                          // the rows' use of shared memory
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int c = bn_col<VEC>(w + i * W, lane);
@@ -583,55 +621,49 @@ __global__ void __launch_bounds__(32 * BN_WARPS, 1) block_norm_bwd_k(Bwd f, int 
       }
     }
   }
-  if (G == 1) return;
   __syncthreads();
-  for (int c = threadIdx.x; c < ns * n; c += blockDim.x) {
-    float v = 0.f;
-    for (int i = 0; i < G; ++i) v += sh[i * ns * n + c];
-    part[c] = v;
+  constexpr int U = 4;
+  for (int c0 = threadIdx.x; c0 < ns * n; c0 += U * blockDim.x) {
+    int k[U], c[U];
+    float v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = c0 + u * (int)blockDim.x;
+      k[u] = at >= n;
+      c[u] = at < ns * n ? at - k[u] * n : n;
+      v[u] = 0.f;
+      for (int i = 0; i < G && c[u] < n; ++i) v[u] += sh[i * ns * n + at];
+      if (gridDim.x > 1 && c[u] < n) f.ws[(long long)blockIdx.x * ns * n + at] = v[u];
+    }
+    if (gridDim.x == 1) bn_finish(f, k, c, v);
   }
 }
 
-// Column sums of the CTAs' parts: eight warps take every eighth part of 32
-// columns, joined in order.  Of the two sums (or one) the first is dbefore's, the
-// second q.
-struct Sums {
-  const float *ws, *after, *gate;
-  float *dbefore, *dafter, *dgate;
-  int parts, width, sums, accumulate;
-};
-__global__ void __launch_bounds__(256) column_sums_k(Sums s) {
+// Sums of the CTAs' parts: eight warps take every eighth part of 32 columns, joined
+// in order.
+__global__ void __launch_bounds__(256) column_sums_k(Bwd f, int parts, int sums) {
   ops_begin();
   __shared__ float red[8][32];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane, k = blockIdx.y;
-  const long long step = (long long)s.sums * s.width;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane, k = blockIdx.y, n = f.j.width;
+  const float* at = f.ws + (long long)k * n + c;
   float v = 0.f;
   constexpr int U = 20;                       // all in flight: 152 parts by eight warps
-  for (int p0 = w; p0 < s.parts && c < s.width; p0 += 8 * U) {
+  for (int p0 = w; p0 < parts && c < n; p0 += 8 * U) {
     float x[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) x[u] = p0 + 8 * u < s.parts ? s.ws[(p0 + 8 * u) * step + (long long)k * s.width + c] : 0.f;
+    for (int u = 0; u < U; ++u) x[u] = p0 + 8 * u < parts ? at[(long long)(p0 + 8 * u) * sums * n] : 0.f;
 #pragma unroll
     for (int u = 0; u < U; ++u) v += x[u];
   }
   red[w][lane] = v;
   __syncthreads();
-  if (w || c >= s.width) return;
+  if (w || c >= n) return;
   v = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) v += red[i][lane];
-  if (k == 0 && s.dbefore) {
-    s.dbefore[c] = s.accumulate ? s.dbefore[c] + v : v;
-    return;
-  }
-  if (s.dafter) {
-    const float x = s.gate ? v * s.gate[c] : v;
-    s.dafter[c] = s.accumulate ? s.dafter[c] + x : x;
-  }
-  if (s.dgate) {
-    const float x = s.after ? v * s.after[c] : v;
-    s.dgate[c] = s.accumulate ? s.dgate[c] + x : x;
-  }
+  const int ks[1] = {k}, cs[1] = {c};
+  const float vs[1] = {v};
+  bn_finish(f, ks, cs, vs);
 }
 
 // ---------------------------------------------------------------------------
@@ -677,17 +709,20 @@ int fwd_t(const Fwd& f, cudaStream_t st) {
 }
 
 template <class S, class T, int VEC>
-int bwd_t(Bwd f, int sms, int* parts, cudaStream_t st) {
+int bwd_t(Bwd f, int dev, int sms, int* parts, cudaStream_t st) {
   // a warp to 256 columns of a row up to 4096, to 512 beyond
   const int chunks = (f.j.width + 255) / 256, C = chunks <= BN_WARPS ? 1 : 2, W = (chunks + C - 1) / C;
   const int pieces = 2 * Piece<S>::N + (f.j.gate_kind == MT_GATE_FULL ? 3 : 2) * Piece<T>::N;
-  // rows are spread over the CTAs before any takes two at once
-  const int most = ops_least(sms, BN_MAX_PARTS), G = ops_least(BN_WARPS / W, (f.j.rows + most - 1) / most);
-  *parts = ops_least((f.j.rows + G - 1) / G, most);
+  // A few rows stay in one CTA, which needs no sums of parts (BN_ALONE rounds of its
+  // groups cost less than those); more are spread over the CTAs before any takes two.
+  const int most = ops_least(sms, BN_MAX_PARTS), room = BN_WARPS / W;
+  const bool alone = f.j.rows <= BN_ALONE * room;
+  const int G = alone ? room : ops_least(room, (f.j.rows + most - 1) / most);
+  *parts = alone ? 1 : ops_least((f.j.rows + G - 1) / G, most);
   const size_t red = bn_red(G * W), stage = VEC ? (size_t)C * pieces * 512 * W * G : 0;
   int stages = BN_STAGES;
   while (stages > 1 && red + stages * stage > BN_SMEM) --stages;
-  size_t smem = red + stages * stage, sums = G > 1 ? (size_t)G * 2 * f.j.width * 4 : 0;
+  size_t smem = red + stages * stage, sums = (size_t)G * 2 * f.j.width * 4;
   if (smem < sums) smem = sums;
   const long long step = (long long)*parts * G;
   f.hop_dh = step * f.lddh, f.hop_h = step * f.ldh, f.hop_dr = step * f.lddr, f.hop_y = step * f.ldy;
@@ -695,11 +730,7 @@ int bwd_t(Bwd f, int sms, int* parts, cudaStream_t st) {
   const bool whole = VEC && f.j.before && f.j.after && f.y && f.dh;
   auto k = C == 2 ? block_norm_bwd_k<S, T, VEC, 2, false>
            : whole ? block_norm_bwd_k<S, T, VEC, 1, VEC> : block_norm_bwd_k<S, T, VEC, 1, false>;
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-    cudaGetLastError();
-    return MT_ERR_CUDA;
-  }
-  return ops_launch(k, (unsigned)*parts, 32u * W * G, smem, st, 1, f, W, G, stages, pieces);
+  return ops_launch_wide(k, dev, BN_SMEM, (unsigned)*parts, 32u * W * G, smem, st, f, W, G, stages, pieces);
 }
 
 }  // namespace
@@ -761,13 +792,11 @@ int32_t mt_block_norm_bwd(const mt_joint* j, const void* h, int64_t ldh, const v
   if (sums && ws_bytes < mt_block_norm_ws_bytes(j->rows, j->width)) return MT_ERR_ARENA_SMALL;
   cudaStream_t s = (cudaStream_t)stream;
   int parts = 0;
+  const Bwd f = {joint(j), dr ? h : nullptr, y, dr, dh, dx, dy, dgate, ldh, ldy, lddr, lddh, lddx, lddy, lddgate, (float*)ws,
+                 dafter, dbefore, accumulate};
   if (j->rows) {
     int dev, sms;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-      cudaGetLastError();
-      return MT_ERR_CUDA;
-    }
-    const Bwd f = {joint(j), dr ? h : nullptr, y, dr, dh, dx, dy, dgate, ldh, ldy, lddr, lddh, lddx, lddy, lddgate, (float*)ws};
+    if (!ops_device(&dev, &sms)) return MT_ERR_CUDA;
     const bool vec = joint_vec(j) && mat_vec(f.h, j->stream_dtype, ldh) && mat_vec(y, j->dtype, ldy) &&
                      mat_vec(dr, j->dtype, lddr) && mat_vec(dh, j->stream_dtype, lddh) &&
                      mat_vec(dx, j->stream_dtype, lddx) && mat_vec(dy, j->dtype, lddy) &&
@@ -775,13 +804,11 @@ int32_t mt_block_norm_bwd(const mt_joint* j, const void* h, int64_t ldh, const v
     auto k = j->stream_dtype == MT_DT_BF16 ? (vec ? bwd_t<__nv_bfloat16, __nv_bfloat16, 1> : bwd_t<__nv_bfloat16, __nv_bfloat16, 0>)
              : j->dtype == MT_DT_BF16      ? (vec ? bwd_t<float, __nv_bfloat16, 1> : bwd_t<float, __nv_bfloat16, 0>)
                                            : (vec ? bwd_t<float, float, 1> : bwd_t<float, float, 0>);
-    const int rc = k(f, sms, &parts, s);
-    if (rc) return rc;
+    const int rc = k(f, dev, sms, &parts, s);
+    if (rc || parts == 1) return rc;
   }
   if (!sums) return MT_OK;
-  const Sums c = {(const float*)ws, j->after, channel ? (const float*)j->gate : nullptr, dbefore, dafter,
-                  channel ? (float*)dgate : nullptr, parts, (int)j->width, sums, accumulate};
-  return ops_launch(column_sums_k, dim3((unsigned)((j->width + 31) / 32), (unsigned)sums), 256, 0, s, 1, c);
+  return ops_launch(column_sums_k, dim3((unsigned)((j->width + 31) / 32), (unsigned)sums), 256, 0, s, 1, f, parts, sums);
 }
 
 }  // extern "C"

@@ -316,10 +316,7 @@ int all(const mt_span* s, int32_t n, const Clip& c0, void* ws, int64_t ws_bytes,
   for (int i = 0; i < n; ++i) units += (s[i].numel + GC_UNIT - 1) / GC_UNIT;
   if (units >= (1LL << 31)) return MT_ERR_UNSUPPORTED;
   int dev, sms;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return MT_ERR_CUDA;
-  }
+  if (!ops_device(&dev, &sms)) return MT_ERR_CUDA;
   cudaStream_t st = (cudaStream_t)stream;
   c.parts = (const double*)ws;
   c.n_parts = 0;

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "../../include/moe_train.h"
 
 #define OPS_MAX_ROWS (1LL << 30)
@@ -359,4 +361,43 @@ static int ops_launch(void (*k)(P...), dim3 grid, unsigned block, size_t smem, c
     return MT_ERR_LAUNCH;
   }
   return MT_OK;
+}
+// The current device and its number of SMs; false on an error.
+static inline bool ops_device(int* dev, int* sms) {
+  if (cudaGetDevice(dev) == cudaSuccess && *dev >= 0 && *dev < 64 &&
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev) == cudaSuccess)
+    return true;
+  cudaGetLastError();
+  return false;
+}
+// The same launch with more shared memory than a kernel has by itself: its limit is
+// raised to `most` at its first launch on a device (2 us that later ones save).
+template <class... P, class... A>
+static int ops_launch_wide(void (*k)(P...), int dev, size_t most, dim3 grid, unsigned block, size_t smem,
+                           cudaStream_t st, A... args) {
+  static std::mutex mu;                       // of all kernels with these parameters
+  static struct {
+    const void* kernel;
+    uint64_t devices;
+  } seen[32];
+  bool raised = false;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    int i = 0;
+    while (i < 31 && seen[i].kernel && seen[i].kernel != (const void*)k) ++i;
+    if (seen[i].kernel != (const void*)k) seen[i] = {(const void*)k, 0};
+    if (!(seen[i].devices >> dev & 1)) {
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess) {
+        cudaGetLastError();
+        return MT_ERR_LAUNCH;
+      }
+      seen[i].devices |= 1ull << dev;
+      raised = true;
+    }
+  }
+  int rc = ops_launch(k, grid, block, smem, st, 1, args...);
+  // a device that was reset since has the limit it came with
+  if (rc && !raised && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) == cudaSuccess)
+    rc = ops_launch(k, grid, block, smem, st, 1, args...);
+  return rc;
 }

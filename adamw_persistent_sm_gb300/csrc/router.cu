@@ -692,11 +692,9 @@ int choose_t(const Choose& c, const Plan& plan, cudaStream_t st) {
   if (plan.tiles) {
     const size_t smem = (size_t)plan.warps * 32 * (c.E <= 32 ? 32 : 64) * 4;
     auto k = c.E <= 32 ? choose_tiles_k<Z, VEC, false> : choose_tiles_k<Z, VEC, true>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-      cudaGetLastError();
-      return MT_ERR_CUDA;
-    }
-    rc = ops_launch(k, (unsigned)plan.parts, 32u * plan.warps, smem, st, 1, c);
+    int dev, sms;
+    if (!ops_device(&dev, &sms)) return MT_ERR_CUDA;
+    rc = ops_launch_wide(k, dev, (size_t)RT_WARPS * 8192, (unsigned)plan.parts, 32u * plan.warps, smem, st, c);
   } else {
     auto k = c.K <= 2 ? (c.E <= 8    ? choose_lanes_k<Z, 4, 2, 2, VEC>
                          : c.E <= 16 ? choose_lanes_k<Z, 4, 4, 2, VEC>

@@ -268,6 +268,53 @@ def test_joint_rows_that_are_zero_or_not_finite(ops):
     assert g.dx[ok].isfinite().all() and g.dy[ok].isfinite().all() and g.dbefore.isnan().any()
 
 
+def test_joint_of_tiny_rows_and_eps(ops):
+    """Rows of zeros and of 1e-12 under an eps of 1e-26: the cube of 1 / rms is beyond
+    fp32, the gradients are not."""
+    t, d = 12, 768
+    x = rnd(1, t, d) * 1e-12
+    x[3] = 0.0
+    w = rnd(4, d, std=0.1, mean=1.0)
+    _, r = ops.block_norm(x, before=w, eps=1e-26)
+    _, want, _, bound = R.joint(as64(x), None, None, None, as_row(w), 1.0, 1.0, 1e-26)
+    close(r, want, bound)
+    dr = rnd(5, t, d)
+    got = ops.block_norm_bwd(dr, None, x, before=w, eps=1e-26)
+    ref = R.joint_grad(as64(dr), None, as64(x), None, None, None, as_row(w), 1.0, 1.0, 1e-26)
+    close(got.dx, *ref["dx"])
+    close(got.dbefore, *R.row_sum(*ref["dbefore"]))
+    y = x.clone()
+    got = ops.block_norm_bwd(None, dr, x, y, after=w, eps=1e-26)
+    ref = R.joint_grad(None, as64(dr), as64(x), as64(y), as_row(w), None, None, 1.0, 1.0, 1e-26)
+    close(got.dy, *ref["dy"])
+
+
+def test_rows_far_apart(ops):
+    """Row strides of 2^26 elements: offsets beyond 32 bits."""
+    t, d = 40, 264
+    far = lambda dt: torch.empty(t << 26, dtype=dt, device="cuda").view(t, 1 << 26)[:, :d]      # noqa: E731
+    p = joint_inputs(t, d, "fp32", "bf16", "full")
+    x, h = far(torch.float32), far(torch.float32)
+    y = far(torch.bfloat16)
+    x.copy_(p["x"])
+    y.copy_(p["y"])
+    q = dict(p, x=x, y=y)
+    check_joint(ops, q, 1.0, 0.5, h=h)
+    want = ops.block_norm(p["x"], p["y"], after=p["after"], gate=p["gate"], before=p["before"], out_scale=0.5)
+    assert torch.equal(h, want[0])
+    dr, dh = rnd(5, t, d, dtype=torch.bfloat16), rnd(6, t, d)
+    a = ops.block_norm_bwd(dr, dh, want[0], p["y"], after=p["after"], gate=p["gate"], before=p["before"])
+    x.copy_(dh)
+    b = ops.block_norm_bwd(dr, x, h, y, after=p["after"], gate=p["gate"], before=p["before"], dx=x)
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+    z = rnd(7, t, 16)
+    h[:, :16] = z
+    c, c2 = ops.choose(z, 2), ops.choose(h[:, :16], 2)
+    assert all(torch.equal(u, v) for u, v in zip(c[:4], c2[:4]))
+    want = ops.choose_bwd(z, c.idx, c.counts, c.w, c.losses)
+    assert torch.equal(ops.choose_bwd(h[:, :16], c.idx, c.counts, c.w, c.losses, out=x[:, :16]), want)
+
+
 def test_joint_refusals(ops):
     p = joint_inputs(6, 64, "fp32", "bf16", "channel")
     x, y, w = p["x"], p["y"], p["after"]
@@ -409,6 +456,56 @@ def test_choice_over_many_tokens(ops, t, e, k):
     dw, dl = rnd(8, t, k), torch.tensor([0.7, 0.03], device="cuda")
     want, mag = R.choose_grad(as64(z), c.idx.cpu().numpy(), c.counts.cpu().numpy().astype(np.int64), as64(dw), as64(dl), mask.cpu().numpy(), True)
     close(ops.choose_bwd(z, c.idx, c.counts, dw, dl, mask), want, (3 * rel + 30 * U) * mag + 1e-36)
+
+
+TILED = [(50000, 17, 8), (60000, 24, 6), (45000, 32, 8), (101000, 33, 3), (38000, 63, 8), (40000, 64, 8)]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("how", ["plain", "ties", "equal", "closed", "lowest", "wide", "zeros", "bad"])
+@pytest.mark.parametrize("t,e,k", TILED)
+def test_choice_by_tiles(ops, t, e, k, how, dtype):
+    """More choices than the lanes' kernel takes: the same as its own, which the
+    other tests hold to the definition, over slices that it takes."""
+    z = logits(t, t, e, how, DT[dtype])
+    mask = torch.rand(t, generator=torch.Generator().manual_seed(5)).cuda() < 0.8
+    for renormalize, m in ((True, mask), (False, None)):
+        assert t * k > 300000
+        c = ops.choose(z, k, m, renormalize)
+        n = 300000 // k
+        parts = [ops.choose(z[i:i + n], k, None if m is None else m[i:i + n], renormalize) for i in range(0, t, n)]
+        assert torch.equal(c.idx, torch.cat([p.idx for p in parts]))
+        assert torch.equal(c.counts, sum(p.counts for p in parts))
+        w = torch.cat([p.w for p in parts])
+        # sums of up to 64 exponentials in another order
+        assert torch.equal(c.w.isnan(), w.isnan())       # NaN meets no bound: compared apart
+        w = w.nan_to_num(0.0)
+        assert ((c.w.nan_to_num(0.0) - w).abs() <= 130 * U * w).all()
+        spoiled = ~(z < float("inf")).all(1)
+        if m is not None:
+            spoiled &= m                         # a masked row spoils nothing
+        assert bool(c.losses.isnan().all()) == bool(spoiled.any()) == bool(c.losses.isnan().any())
+        if spoiled.any():
+            continue
+        if how == "lowest":                      # squares of the lowest logit: beyond fp32
+            assert c.losses[1] == float("inf")
+        many = torch.stack([p.counts[-1] for p in parts]).double()
+        size = float((torch.stack([p.losses[1] for p in parts]).double() * many).sum() / many.sum())
+        assert how == "lowest" or abs(float(c.losses[1]) - size) <= 1000 * U * size
+        live = torch.ones(t, dtype=torch.bool, device="cuda") if m is None else m
+        live = live & (z.float().amax(1) > -float("inf"))
+        p = torch.softmax(z[live].double(), 1).mean(0)
+        balance = float(e * (c.counts[:-1].double() / (k * int(c.counts[-1])) * p).sum())
+        assert abs(float(c.losses[0]) - balance) <= 1000 * U * balance
+        again = ops.choose(z, k, m, renormalize)
+        assert all(torch.equal(a, b) for a, b in zip(c[:3], again[:3])) and torch.equal(c.losses, again.losses)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_choice_by_tiles_against_the_definition(ops, dtype):
+    z = logits(3, 40000, 64, "closed", DT[dtype])
+    check_choice(ops, z, 8, torch.rand(40000, generator=torch.Generator().manual_seed(5)).cuda() < 0.8, True)
+    check_choice(ops, strided(z[:, :61].contiguous(), 3, 1), 8, None, False)
 
 
 def test_choice_of_views_and_given_outputs(ops):
@@ -591,6 +688,21 @@ def test_clip_refusals(ops):
         with pytest.raises(RuntimeError):
             ops.clip_grads([a], **kw)
         assert torch.equal(a, before)
+
+
+def test_clip_of_a_tensor_beyond_32_bits(ops):
+    """2^31 and some elements in one tensor, and a few behind it."""
+    n = (1 << 31) + 4099
+    big, small = torch.zeros(n, dtype=torch.bfloat16, device="cuda"), torch.ones(1001, device="cuda")
+    for i in (0, 12345, (1 << 31) - 1, 1 << 31, n - 1):
+        big[i] = 3.0
+    s = ops.clip_grads([big, small], 1.0)
+    norm = math.sqrt(5 * 9 + 1001)
+    assert abs(float(s[0]) - norm) <= NORM * norm
+    want = torch.tensor(3.0 * (1.0 / (norm + 1e-6))).bfloat16()
+    for i in (0, 12345, (1 << 31) - 1, 1 << 31, n - 1):
+        assert float((big[i].float() - want.float()).abs()) <= 2.0 ** -8 * float(want)
+    assert int(torch.count_nonzero(big)) == 5
 
 
 def test_norm_of_a_large_set(ops):

@@ -219,8 +219,9 @@ def block_norm_bwd(dr: torch.Tensor | None, dh: torch.Tensor | None, h: torch.Te
         nbytes = lib.mt_block_norm_ws_bytes(rows, width)
         if nbytes < 0:
             raise _error("mt_block_norm_bwd", -nbytes)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)     # held until the launch
-        pws = ws.data_ptr()
+        if nbytes:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)     # held until the launch
+            pws = ws.data_ptr()
     ph, here = h.data_ptr(), _current()
     if here != dev:
         torch.cuda.set_device(dev)
@@ -245,7 +246,7 @@ class Choice(NamedTuple):
     ws: torch.Tensor        # workspace
 
 
-def _logits(z: torch.Tensor, top_k: int, mask) -> tuple[int, int]:
+def _logits(z: torch.Tensor, mask) -> tuple[int, int]:
     dev = z.get_device()
     ldz = _mat(z, "logits", dev)
     if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or mask.get_device() != dev
@@ -273,27 +274,26 @@ def choose(logits: torch.Tensor, top_k: int, mask: torch.Tensor | None = None, r
     An expert whose logit is -inf is never chosen.  ``out`` is refilled; calls
     that refill or read one Choice, captured ones too, have to be ordered by the
     caller."""
-    dev, ldz = _logits(logits, top_k, mask)
+    dev, ldz = _logits(logits, mask)
     t, e = logits.shape
-    lib = B.load()
-    nbytes = lib.mt_choose_ws_bytes(t, top_k, e)
-    if nbytes < 0:
-        raise _error("mt_choose", -nbytes)
+    lib, picked = _load(), (t, top_k)
     if out is None:
-        out = Choice(torch.empty((t, top_k), dtype=torch.int32, device=dev),
-                     torch.empty((t, top_k), dtype=torch.float32, device=dev),
-                     torch.empty(e + 1, dtype=torch.int32, device=dev),
-                     torch.empty(2, dtype=torch.float32, device=dev),
+        nbytes = lib.mt_choose_ws_bytes(t, top_k, e)
+        if nbytes < 0:
+            raise _error("mt_choose", -nbytes)
+        out = Choice(torch.empty(picked, dtype=torch.int32, device=dev), torch.empty(picked, dtype=_F32, device=dev),
+                     torch.empty(e + 1, dtype=torch.int32, device=dev), torch.empty(2, dtype=_F32, device=dev),
                      torch.empty(nbytes, dtype=torch.uint8, device=dev))
     idx, w, counts, losses, ws = out
-    args = (_plain(idx, "idx", dev, (t, top_k), torch.int32), _plain(w, "w", dev, (t, top_k), torch.float32),
-            _plain(counts, "counts", dev, (e + 1,), torch.int32), _plain(losses, "losses", dev, (2,), torch.float32),
+    nbytes = ws.numel()
+    args = (_plain(idx, "idx", dev, picked, torch.int32), _plain(w, "w", dev, picked, _F32),
+            _plain(counts, "counts", dev, (e + 1,), torch.int32), _plain(losses, "losses", dev, (2,), _F32),
             _plain(ws, "ws", dev, (nbytes,), torch.uint8))
+    what, pm, keep = (logits.data_ptr(), _DTYPES[logits.dtype], ldz, t, e), None if mask is None else mask.data_ptr(), int(renormalize)
     here = _current()
     if here != dev:
         torch.cuda.set_device(dev)
-    st = lib.mt_choose(logits.data_ptr(), _DTYPES[logits.dtype], ldz, t, e, top_k,
-                       None if mask is None else mask.data_ptr(), int(renormalize), *args, nbytes, _raw_stream(dev))
+    st = lib.mt_choose(*what, top_k, pm, keep, *args, nbytes, _raw_stream(dev))
     if here != dev:
         torch.cuda.set_device(here)
     if st:
@@ -308,7 +308,7 @@ def choose_bwd(logits: torch.Tensor, idx: torch.Tensor, counts: torch.Tensor | N
     chosen (``dw`` float32 [tokens, top_k]) and through the two losses
     (``dlosses`` float32 [2] on the device, with the ``counts`` of the choice);
     either may be None."""
-    dev, ldz = _logits(logits, 0, mask)
+    dev, ldz = _logits(logits, mask)
     t, e = logits.shape
     if dw is None and dlosses is None:
         raise ValueError("dw or dlosses is needed")
@@ -324,13 +324,13 @@ def choose_bwd(logits: torch.Tensor, idx: torch.Tensor, counts: torch.Tensor | N
         pl, pc = _plain(dlosses, "dlosses", dev, (2,), torch.float32), _plain(counts, "counts", dev, (e + 1,), torch.int32)
     if out is None:
         out = torch.empty((t, e), dtype=logits.dtype, device=dev)
-    ldo = _mat(out, "out", dev, t, e, logits.dtype)
-    lib, here = B.load(), _current()
+    ldo = _rows(out, "out", dev, logits.shape, logits.dtype)
+    keep, po = int(renormalize), out.data_ptr()
+    lib, here = _load(), _current()
     if here != dev:
         torch.cuda.set_device(dev)
     st = lib.mt_choose_bwd(logits.data_ptr(), _DTYPES[logits.dtype], ldz, t, e, k,
-                           None if mask is None else mask.data_ptr(), int(renormalize), pi, pc, pw, pl,
-                           out.data_ptr(), ldo, _raw_stream(dev))
+                           None if mask is None else mask.data_ptr(), keep, pi, pc, pw, pl, po, ldo, _raw_stream(dev))
     if here != dev:
         torch.cuda.set_device(here)
     if st:

@@ -11,7 +11,6 @@ namespace {
 #define BN_MAX_WIDTH 8192
 #define BN_MAX_PARTS 160          // CTAs that leave partial column sums
 #define BN_WARPS 16               // of a CTA of the backward pass
-#define BN_ALONE 2                // rounds of one CTA
 #define BN_SMEM (226 * 1024)      // its shared memory
 #define BN_STAGES 2               // of its ring, at most (three: 79.9 against 77.3 us)
 
@@ -708,15 +707,23 @@ int fwd_t(const Fwd& f, cudaStream_t st) {
   return ops_launch(block_norm_k<S, T, VEC, 4, true>, (unsigned)f.j.rows, 32u * (unsigned)((chunks + 3) / 4), 0, st, 1, f);
 }
 
+// Warps of a row in the backward pass: one to 256 columns up to 4096, to 512 beyond.
+int bn_width(int64_t width) {
+  const int chunks = (int)((width + 255) / 256), C = chunks <= BN_WARPS ? 1 : 2;
+  return (chunks + C - 1) / C;
+}
+// A few rows stay in one CTA, which leaves no parts: two rounds of its groups cost less
+// than their sums (8 rows of 768: 6.0 against 6.4 us and a launch of the host's; three
+// rounds: 7.3 against 6.4).
+bool bn_alone(int64_t rows, int64_t width) { return rows <= 2 * (BN_WARPS / bn_width(width)); }
+
 template <class S, class T, int VEC>
 int bwd_t(Bwd f, int dev, int sms, int* parts, cudaStream_t st) {
-  // a warp to 256 columns of a row up to 4096, to 512 beyond
-  const int chunks = (f.j.width + 255) / 256, C = chunks <= BN_WARPS ? 1 : 2, W = (chunks + C - 1) / C;
+  const int W = bn_width(f.j.width), C = W * 256 < f.j.width ? 2 : 1;
   const int pieces = 2 * Piece<S>::N + (f.j.gate_kind == MT_GATE_FULL ? 3 : 2) * Piece<T>::N;
-  // A few rows stay in one CTA, which needs no sums of parts (BN_ALONE rounds of its
-  // groups cost less than those); more are spread over the CTAs before any takes two.
+  // rows are spread over the CTAs before any takes two at once
   const int most = ops_least(sms, BN_MAX_PARTS), room = BN_WARPS / W;
-  const bool alone = f.j.rows <= BN_ALONE * room;
+  const bool alone = bn_alone(f.j.rows, f.j.width);
   const int G = alone ? room : ops_least(room, (f.j.rows + most - 1) / most);
   *parts = alone ? 1 : ops_least((f.j.rows + G - 1) / G, most);
   const size_t red = bn_red(G * W), stage = VEC ? (size_t)C * pieces * 512 * W * G : 0;
@@ -760,7 +767,8 @@ int32_t mt_block_norm(const mt_joint* j, const void* x, int64_t ldx, const void*
 int64_t mt_block_norm_ws_bytes(int64_t rows, int64_t width) {
   if (rows < 0 || width < 1) return -MT_ERR_ARG;
   if (rows > OPS_MAX_ROWS || width > BN_MAX_WIDTH) return -MT_ERR_UNSUPPORTED;
-  return ((rows < 1 ? 1 : rows < BN_MAX_PARTS ? rows : BN_MAX_PARTS) * 2 * width * 4 + 15) / 16 * 16;
+  if (bn_alone(rows, width)) return 0;
+  return ((rows < BN_MAX_PARTS ? rows : BN_MAX_PARTS) * 2 * width * 4 + 15) / 16 * 16;
 }
 
 int32_t mt_block_norm_bwd(const mt_joint* j, const void* h, int64_t ldh, const void* y, int64_t ldy, const void* dr,
@@ -788,8 +796,9 @@ int32_t mt_block_norm_bwd(const mt_joint* j, const void* h, int64_t ldh, const v
     if (j->gate_kind == MT_GATE_FULL && !ops_mat_ok(dgate, od, lddgate, n)) return MT_ERR_ARG;
   }
   const int sums = (dbefore ? 1 : 0) + (dafter || channel ? 1 : 0);
-  if (sums && (!ws || !ops_aligned(ws, 16))) return MT_ERR_ARG;
-  if (sums && ws_bytes < mt_block_norm_ws_bytes(j->rows, j->width)) return MT_ERR_ARENA_SMALL;
+  const int64_t need = sums ? mt_block_norm_ws_bytes(j->rows, j->width) : 0;
+  if (need && (!ws || !ops_aligned(ws, 16))) return MT_ERR_ARG;
+  if (ws_bytes < need) return MT_ERR_ARENA_SMALL;
   cudaStream_t s = (cudaStream_t)stream;
   int parts = 0;
   const Bwd f = {joint(j), dr ? h : nullptr, y, dr, dh, dx, dy, dgate, ldh, ldy, lddr, lddh, lddx, lddy, lddgate, (float*)ws,

@@ -598,7 +598,7 @@ typedef struct mt_joint {
  * 1).  before NULL: r is NULL.  Not both.  h may be x itself (ldh == ldx). */
 int32_t mt_block_norm(const mt_joint* j, const void* x, int64_t ldx, const void* y, int64_t ldy, void* h, int64_t ldh,
                       void* r, int64_t ldr, void* stream);
-/* Bytes of device workspace (16-byte aligned) for mt_block_norm_bwd. */
+/* Bytes of device workspace (16-byte aligned) for mt_block_norm_bwd; 0: none. */
 int64_t mt_block_norm_ws_bytes(int64_t rows, int64_t width);
 /* Gradients at h and y as they are stored; nothing else is kept from forward.
  * dr [rows, width] of dtype (NULL exactly where before is), dh of stream_dtype:

@@ -127,7 +127,7 @@ def test_joint_limits(lib):
         assert lib.mt_block_norm(joint(**kw), *FWD.values(), 0) == UNS
         assert lib.mt_block_norm_bwd(joint(**kw), *BWD.values(), 0) == UNS
     assert lib.mt_block_norm_ws_bytes(4, 8193) == -UNS and lib.mt_block_norm_ws_bytes(-1, 8) == -BAD
-    assert lib.mt_block_norm_ws_bytes(0, 8) > 0
+    assert lib.mt_block_norm_ws_bytes(0, 8) == 0 and lib.mt_block_norm_ws_bytes(4, 16) == 0 and lib.mt_block_norm_ws_bytes(400, 16) > 0
     assert lib.mt_block_norm(None, *FWD.values(), 0) == BAD
     assert lib.mt_block_norm(joint(rows=0), *FWD.values(), 0) == OK
 
@@ -146,10 +146,12 @@ def test_block_norm_refusals(lib):
 def test_block_norm_bwd_refusals(lib):
     for kw in (dict(h=0), dict(ldh=15), dict(y=0), dict(ldy=15), dict(dr=0), dict(lddr=15), dict(dh=P + 2),
                dict(lddh=15), dict(dx=0), dict(lddx=15), dict(dy=0), dict(lddy=15), dict(dgate=0), dict(dgate=P + 2),
-               dict(dafter=0), dict(dafter=P + 2), dict(dbefore=0), dict(accumulate=2), dict(ws=0), dict(ws=P + 8)):
+               dict(dafter=0), dict(dafter=P + 2), dict(dbefore=0), dict(accumulate=2)):
         assert lib.mt_block_norm_bwd(joint(), *{**BWD, **kw}.values(), 0) == BAD, kw
-    need = lib.mt_block_norm_ws_bytes(4, 16)
-    assert lib.mt_block_norm_bwd(joint(), *{**BWD, "ws_bytes": need - 1}.values(), 0) == SMALL
+    for kw in (dict(ws=0), dict(ws=P + 8)):
+        assert lib.mt_block_norm_bwd(joint(rows=400), *{**BWD, **kw}.values(), 0) == BAD, kw
+    need = lib.mt_block_norm_ws_bytes(400, 16)
+    assert lib.mt_block_norm_bwd(joint(rows=400), *{**BWD, "ws_bytes": need - 1}.values(), 0) == SMALL
     for kw in (dict(gate_kind=TOKEN, ldgate=1), dict(gate_kind=FULL, ldgate=16)):
         assert lib.mt_block_norm_bwd(joint(**kw), *{**BWD, "lddgate": 0}.values(), 0) == BAD
     for kw in (dict(after=None), dict(before=None), dict(gate=None, gate_kind=NONE)):

@@ -74,7 +74,9 @@ __device__ __forceinline__ float bn_sum(float s) {
 // One pass over the rows: x and y are read once, kept in registers (8 C columns
 // per lane) over the two sums of squares, and h and r written once.  Up to 1024
 // columns a warp takes a row and nothing is shared; wider rows take a CTA of as
-// many warps as they have 1024 columns.
+// many warps as they have 1024 columns.  Memory bounds it: 47 to 49 us for 25 million
+// elements (fp32 stream, bf16) in rows of 256 to 8192, 91 to 94 % of the copy rate; a
+// warp to 256 columns takes 102 us for rows of 256, 47 for 768 and 85 for 8192.
 template <class S, class T, int VEC, int C, bool WIDE>
 __global__ void __launch_bounds__(256) block_norm_k(Fwd f) {
   ops_begin();
@@ -639,7 +641,8 @@ __global__ void __launch_bounds__(32 * BN_WARPS, 1) block_norm_bwd_k(Bwd f, int 
 }
 
 // Sums of the CTAs' parts: eight warps take every eighth part of 32 columns, joined
-// in order.
+// in order, with every load of a warp on its way at once (eight at a time: 5 us more).
+// About 3 us behind the rows' kernel, of which its launch and one trip to L2 are most.
 __global__ void __launch_bounds__(256) column_sums_k(Bwd f, int parts, int sums) {
   ops_begin();
   __shared__ float red[8][32];

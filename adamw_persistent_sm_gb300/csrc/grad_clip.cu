@@ -97,7 +97,8 @@ struct Squares {
   }
 };
 
-#define GC_FLIGHT 4               // eights of a thread on their way at once
+#define GC_FLIGHT 4               // eights of a thread on their way at once (219M fp32: 404 us, two 425;
+                                  // 500 ragged bf16 tensors: 26 us, three 29)
 // n elements at p
 template <class T>
 __device__ __forceinline__ void gc_squares(Squares& q, const T* p, long long n) {
@@ -120,6 +121,8 @@ __device__ __forceinline__ void gc_squares(Squares& q, const T* p, long long n) 
   }
 }
 
+// A CTA takes a contiguous run of units, over as many tensors as lie in it.  876 MB of
+// fp32: 129 us, the copy rate.
 template <int N>
 __global__ void __launch_bounds__(GC_THREADS, GC_CTAS) squares_k(const __grid_constant__ Table<N> t, double* parts) {
   ops_begin();
@@ -245,6 +248,9 @@ __device__ __forceinline__ void gc_scale(const T* p, T* o, long long n, float f)
   }
 }
 
+// The same runs, from their ends.  876 MB of fp32 into as many: 270 us, 95 % of the copy
+// rate; a unit to each CTA in turn instead of a run takes as long there, and 45 us
+// instead of 26 for 500 ragged tensors.
 template <int N>
 __global__ void __launch_bounds__(GC_THREADS, GC_CTAS) scale_k(const __grid_constant__ Table<N> t, Clip c, int first) {
   ops_begin();

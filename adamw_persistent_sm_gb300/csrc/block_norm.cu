@@ -358,8 +358,6 @@ __host__ __device__ constexpr int bn_red(int warps) { return (warps * 32 + 127) 
 //   dy = t (p ry - y ry^3 s / width)              q += t x y ry
 // and after the last row dafter = q * channel gate, a channel gate's gradient q *
 // after: one sum for both.  A full gate's gradient is b G y ry after.  Two sums over
-// after: one sum for both.  A full gate's gradient is b G y ry after.  Two sums over
-// after: one sum for both.  A full gate's gradient is b G y ry after.  Two sums over
 // the row: (h^2, u h, y^2) and s.  VEC: the next stages - 1 rows are on their way in
 // the ring, and what a phase needs of a row is read from there again.  Otherwise the
 // next row is on its way in registers (C 1).
@@ -449,7 +447,7 @@ __global__ void __launch_bounds__(32 * BN_WARPS, 1) block_norm_bwd_k(Bwd f, int 
     asm volatile("cp.async.commit_group;" ::: "memory");
     put = put + slot == slot * stages ? 0 : put + slot;
   };
-  // a row's inputs as pairs, of chunk i and row q
+  // a row's inputs as pairs, of chunk i
   auto in_h = [&](int i, bn2* p) {
     if constexpr (VEC) bn_take((const S*)nullptr, ring + get + i * unit + NS * hop, wid, lane, p);
     else bn_pairs(cur[i].h, p);

@@ -335,7 +335,8 @@ __global__ void __launch_bounds__(32 * RT_WARPS) choose_tiles_k(Choose c) {
   float* mine = tile + lane * LD;
   const int sw = (lane & (LD / 4 - 1)) * 4;                // word e of this lane's row is at e ^ sw
   for (int e = threadIdx.x; e < RT_E; e += blockDim.x) hist[e] = 0;
-  for (int e = E; e < LD; ++e) mine[e ^ sw] = -INFINITY;   // up to whole eights
+  const int up = (E + 7) & ~7;
+  for (int e = E; e < up; ++e) mine[e ^ sw] = -INFINITY;   // up to whole eights
   __syncthreads();
   float sum[2] = {0.f, 0.f}, size = 0.f;
   int tokens = 0;
@@ -407,18 +408,18 @@ __global__ void __launch_bounds__(32 * RT_WARPS) choose_tiles_k(Choose c) {
     }
     if (!live) reach[0] = reach[1] = 0;
     uint32_t at[2] = {~0u, ~0u}, used = 0;        // a byte per place
-    while (__any_sync(0xffffffffu, reach[0] | reach[1])) {
-      if (!(reach[0] | reach[1])) continue;
-      const int e = reach[0] ? __ffs(reach[0]) - 1 : __ffs(reach[1]) + 31;
-      int k = top.larger(mine[e ^ sw]);
-      k += __ffs(~(used >> k)) - 1;               // equals in the order of their experts
-      if (k < K) {
-        used |= 1u << k;
-        at[k >> 2] ^= (uint32_t)(0xff ^ e) << (8 * (k & 3));
+    for (int half = 0; half < (PAIR ? 2 : 1); ++half) {
+      for (uint32_t left = reach[half]; __any_sync(0xffffffffu, left); left &= left - 1) {
+        const int e = __ffs(left) - 1 + 32 * half;
+        if (left) {
+          int k = top.larger(mine[e ^ sw]);
+          k += __ffs(~(used >> k)) - 1;             // equals in the order of their experts
+          if (k < K) {
+            used |= 1u << k;
+            at[k >> 2] ^= (uint32_t)(0xff ^ e) << (8 * (k & 3));
+          }
+        }
       }
-      if (e < 32) reach[0] &= reach[0] - 1;
-      else reach[1] &= reach[1] - 1;
-      if (used == (1u << K) - 1) reach[0] = reach[1] = 0;
     }
     // exponentials in place of the logits; a row that holds NaN or +inf, which the
     // values above do not show, has a sum that is NaN
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS) choose_tiles_k(Choose c) {
       c.w[r0 * K + i] = tile[at_ + KM];
     }
     __syncwarp();
-    for (int e = E; e < LD; ++e) mine[e ^ sw] = -INFINITY;
+    for (int e = E; e < up; ++e) mine[e ^ sw] = -INFINITY;
   }
   // the tiles are done with: each warp's sums in its own
 #pragma unroll

@@ -235,6 +235,43 @@ def test_joint_accumulates(ops):
         ops.block_norm_bwd(dr, dh, h, p["y"], **kw, dafter=held["dafter"], dbefore=held["dbefore"], accumulate=True)
 
 
+@pytest.mark.parametrize("d", [64, 768, 1001, 4104])
+def test_few_rows_accumulate_and_end_early(ops, d):
+    """As few rows as one CTA takes: sums added to what is there, rows behind the last left as they were."""
+    t = 2
+    p = joint_inputs(t, d, "fp32", "bf16", "channel")
+    kw = dict(after=p["after"], gate=p["gate"], before=p["before"])
+    h, _ = check_joint(ops, p, 1.0, 1.0)
+    dr, dh = rnd(5, t, d, dtype=torch.bfloat16), rnd(6, t, d)
+    once = ops.block_norm_bwd(dr, dh, h, p["y"], **kw)
+    for live in (0, 1, 2, 5):
+        lim = torch.tensor([live], dtype=torch.int32, device="cuda")
+        n = min(live, t)
+        cut = {k: v[:n] if v is not None and v.dim() == 2 else v for k, v in p.items()}
+        want = ops.block_norm_bwd(dr[:n], dh[:n], h[:n], cut["y"], **kw) if n else None
+        held = {k: rnd(20 + i, d) for i, k in enumerate(("dafter", "dgate", "dbefore"))}
+        before = {k: v.clone() for k, v in held.items()}
+        dx, dy = torch.full((t, d), 7.0, device="cuda"), torch.full((t, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        got = ops.block_norm_bwd(dr, dh, h, p["y"], **kw, **held, dx=dx, dy=dy, accumulate=True, n_rows=lim)
+        assert (dx[n:] == 7).all() and (dy[n:] == 7).all() and torch.equal(dx[:n], once.dx[:n]) and torch.equal(dy[:n], once.dy[:n])
+        for k in held:
+            assert torch.equal(getattr(got, k), before[k] + (getattr(want, k) if n else 0.0))
+
+
+def test_joint_of_very_many_narrow_rows(ops):
+    t, d = 300001, 40
+    x, y, w = rnd(1, t, d), rnd(2, t, d, dtype=torch.bfloat16), rnd(3, d, std=0.1, mean=1.0)
+    h, r = ops.block_norm(x, y, after=w, before=w)
+    rms = lambda v: v / torch.sqrt((v * v).mean(1, keepdim=True) + EPS)        # noqa: E731
+    want = x.double() + rms(y.double()) * w.double()
+    assert float((h.double() - want).abs().max()) < 100 * U * float(want.abs().max())
+    assert float((r.double() - rms(want) * w.double()).abs().max()) < 2.0 ** -8 * 1.1 * float(r.abs().max())
+    g = ops.block_norm_bwd(r, x, h, y, after=w, before=w)
+    hn = rms(h.double())
+    ref = (r.double() * hn).sum(0)
+    assert float((g.dbefore.double() - ref).abs().max()) <= (t / 100 + 200) * U * float((r.double() * hn).abs().sum(0).max())
+
+
 def test_joint_in_place(ops):
     for d in (768, 101, 4104):
         t = 300
@@ -529,6 +566,32 @@ def test_choice_gradient_of_strange_indices(ops):
     for renormalize in (True, False):
         want, mag = R.choose_grad(as64(z), idx.cpu().numpy(), np.zeros(9, np.int64), as64(dw), None, None, renormalize)
         close(ops.choose_bwd(z, idx, dw=dw, renormalize=renormalize), want, 400 * U * mag + 1e-36)
+
+
+@pytest.mark.parametrize("t,e,k", [(1000003, 16, 2), (300001, 40, 8)])
+def test_choice_over_very_many_tokens(ops, t, e, k):
+    z = rnd(1, t, e)
+    c = ops.choose(z, k)
+    want = torch.sort(z, dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(c.idx.long(), want)
+    load = torch.bincount(want.reshape(-1), minlength=e)
+    assert torch.equal(c.counts[:-1].long(), load) and int(c.counts[-1]) == t
+    p = torch.softmax(z.double(), 1)
+    balance = float(e * (load.double() / (k * t) * p.mean(0)).sum())
+    size = float((torch.logsumexp(z.double(), 1) ** 2).mean())
+    assert abs(float(c.losses[0]) - balance) < 1e-5 and abs(float(c.losses[1]) - size) < 1e-5 * size
+    w = p.gather(1, want)
+    assert float((c.w.double() - w / w.sum(1, keepdim=True)).abs().max()) < 1e-6
+
+
+def test_masks_of_bytes(ops):
+    """Any byte but 0 lets a token take part."""
+    z = rnd(1, 300, 16)
+    m = torch.tensor([0, 1, 2, 255] * 75, dtype=torch.uint8, device="cuda")
+    a, b = ops.choose(z, 2, m), ops.choose(z, 2, m != 0)
+    assert all(torch.equal(u, v) for u, v in zip(a[:4], b[:4]))
+    dw = rnd(2, 300, 2)
+    assert torch.equal(ops.choose_bwd(z, a.idx, a.counts, dw, a.losses, m), ops.choose_bwd(z, a.idx, a.counts, dw, a.losses, m != 0))
 
 
 def test_choice_refusals(ops):

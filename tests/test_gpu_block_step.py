@@ -215,6 +215,58 @@ def test_one_set_and_one_input_on_two_streams(ops):
         assert all(torch.equal(a, b) for a, b in zip(out[:n], want[i // 2][:n]))
 
 
+def test_many_tensors_captured(ops):
+    """More tensors than one launch's table holds, captured and replayed on other values."""
+    ts = [rnd(i, 3 + i % 7) for i in range(1100)]
+    gs = ops.GradSet(ts)
+    gs.norm()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        norm, stats = gs.norm(), gs.clip(2.0)
+    for v in (1.0, 3.0):
+        for i, t in enumerate(ts):
+            t.copy_(rnd(i, t.numel()) * v)
+        want = float(torch.cat(ts).double().norm())
+        g.replay()
+        torch.cuda.synchronize()
+        assert abs(float(norm) - want) < 1e-5 * want and abs(float(stats[0]) - want) < 1e-5 * want
+        assert abs(float(torch.cat(ts).double().norm()) - 2.0) < 1e-5
+
+
+FIRST = """
+import sys
+import torch
+from adamw_persistent_sm_gb300 import block_ops as ops
+torch.manual_seed(0)
+x, w, z = torch.randn(500, 768, device="cuda"), torch.rand(768, device="cuda"), torch.randn(50000, 64, device="cuda")
+y = x.bfloat16()
+g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+def step():
+    h, r = ops.block_norm(x, y, after=w, gate=w, before=w)
+    b = ops.block_norm_bwd(r, h, h, y, after=w, gate=w, before=w)
+    c = ops.choose(z, 8)
+    return (h, r, *b, *c[:4], ops.choose_bwd(z, c.idx, c.counts, c.w, c.losses), ops.GradSet([x]).norm(), ops.GradSet([w], [torch.empty_like(w)]).clip(1.0))
+with torch.cuda.graph(g):
+    out = step()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, step()))
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_captured():
+    """No operator needs a call before the capture that holds its first."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and done.stdout.strip().endswith("same"), done.stderr[-2000:]
+
+
 def test_between_other_kernels(ops):
     """Plain tensor kernels write what the operators read and read what they write, without waiting."""
     t, d = 3000, 512

@@ -47,6 +47,29 @@ def _rows(t: torch.Tensor, what: str, dev: int, shape, dtype) -> int:
     return _mat(t, what, dev, shape[0], shape[1], dtype)
 
 
+class _Space:
+    """Memory of a call's own, on a device and for its current stream, from
+    torch's allocator and back to it when the object goes (a tensor for it would
+    cost a call 5 us more)."""
+
+    __slots__ = ("ptr",)
+
+    def __init__(self, nbytes: int, dev: int):
+        self.ptr = 0
+        here = _current()
+        if here != dev:
+            torch.cuda.set_device(dev)
+        try:
+            self.ptr = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, _raw_stream(dev))
+        finally:
+            if here != dev:
+                torch.cuda.set_device(here)
+
+    def __del__(self):
+        if self.ptr:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(self.ptr)
+
+
 _F32 = torch.float32
 _load = B.load
 
@@ -220,8 +243,8 @@ def block_norm_bwd(dr: torch.Tensor | None, dh: torch.Tensor | None, h: torch.Te
         if nbytes < 0:
             raise _error("mt_block_norm_bwd", -nbytes)
         if nbytes:
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)     # held until the launch
-            pws = ws.data_ptr()
+            ws = _Space(nbytes, dev)        # held until the launches
+            pws = ws.ptr
     ph, here = h.data_ptr(), _current()
     if here != dev:
         torch.cuda.set_device(dev)
@@ -407,13 +430,13 @@ class GradSet:
 
     def norm(self, scale: float = 1.0) -> torch.Tensor:
         """|scale| times the square root of the sum of all squares, float32 [1]."""
-        ws = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
-        norm = torch.empty(1, dtype=torch.float32, device=self.device)
+        ws = _Space(self._bytes, self._dev)
+        norm = torch.empty(1, dtype=_F32, device=self._dev)
         scale = float(scale)
         dev, lib, here = self._dev, B.load(), _current()
         if here != dev:
             torch.cuda.set_device(dev)
-        st = lib.mt_grad_norm(self._spans, self._n, scale, norm.data_ptr(), ws.data_ptr(), self._bytes,
+        st = lib.mt_grad_norm(self._spans, self._n, scale, norm.data_ptr(), ws.ptr, self._bytes,
                               _raw_stream(dev))
         if here != dev:
             torch.cuda.set_device(here)
@@ -426,13 +449,13 @@ class GradSet:
         the norm of the scaled tensors (NaN where that is NaN).  ``scale`` turns
         a sum over microbatches or of scaled losses into the gradient.  Returns
         (norm, c), float32 [2]."""
-        ws = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
-        stats = torch.empty(2, dtype=torch.float32, device=self.device)
+        ws = _Space(self._bytes, self._dev)
+        stats = torch.empty(2, dtype=_F32, device=self._dev)
         max_norm, eps, scale = float(max_norm), float(eps), float(scale)
         dev, lib, here = self._dev, B.load(), _current()
         if here != dev:
             torch.cuda.set_device(dev)
-        st = lib.mt_grad_clip(self._spans, self._n, max_norm, eps, scale, stats.data_ptr(), ws.data_ptr(),
+        st = lib.mt_grad_clip(self._spans, self._n, max_norm, eps, scale, stats.data_ptr(), ws.ptr,
                               self._bytes, _raw_stream(dev))
         if here != dev:
             torch.cuda.set_device(here)

@@ -50,7 +50,8 @@ def close(got, want, bound, what=""):
     # half a step of the output, at the value or at what the bound lets it be
     lim = np.broadcast_to(bound, want.shape)[f] * 1.01 + HALF[dtype] * np.abs(want[f]) * 1.01 + 1e-44
     off = np.abs(got[f] - want[f])
-    assert not (off > lim).any(), (what, int((off > lim).sum()), float(off[off > lim].max()))
+    bad = off > lim
+    assert not bad.any(), (what, int(bad.sum()), float(off[bad].max()), np.argwhere(f)[bad][:4].tolist(), got[f][bad][:4], want[f][bad][:4])
 
 
 # ---------------------------------------------------------------------------

@@ -12,7 +12,7 @@ namespace {
 #define BN_MAX_PARTS 160          // CTAs that leave partial column sums
 #define BN_WARPS 16               // of a CTA of the backward pass
 #define BN_SMEM (226 * 1024)      // its shared memory
-#define BN_STAGES 2               // of its ring, at most (three: 79.9 against 77.3 us)
+#define BN_STAGES 2               // of its ring, at most (three: 83 against 80 us)
 
 struct Joint {
   const float *after, *before;
@@ -361,11 +361,11 @@ __host__ __device__ constexpr int bn_red(int warps) { return (warps * 32 + 127) 
 // the row: (h^2, u h, y^2) and s.  VEC: the next stages - 1 rows are on their way in
 // the ring, and what a phase needs of a row is read from there again.  Otherwise the
 // next row is on its way in registers (C 1).
-// 32,768 x 768 (fp32 stream, bf16, a channel gate), us with the column sums: 77, 86 %
+// 32,768 x 768 (fp32 stream, bf16, a channel gate), us with the column sums: 76, 88 %
 // of the copy rate; rows in registers 109, two rows at once 87 to 90, a warp to a row
 // of three chunks 83 and more, 20 warps 86, 8 warps 138.
-template <class S, class T, int VEC, int C, bool ALL>
-__global__ void __launch_bounds__(32 * BN_WARPS, 1) block_norm_bwd_k(Bwd f, int W, int G, int stages, int pieces) {
+template <class S, class T, int VEC, int C, bool ALL, int WARPS = BN_WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 1) block_norm_bwd_k(Bwd f, int W, int G, int stages, int pieces) {
   ops_begin();
   extern __shared__ __align__(128) float sh[];
   constexpr int NS = Piece<S>::N, NT = Piece<T>::N;
@@ -723,7 +723,7 @@ int bwd_t(Bwd f, int dev, int sms, int* parts, cudaStream_t st) {
   const int W = bn_width(f.j.width), C = W * 256 < f.j.width ? 2 : 1;
   const int pieces = 2 * Piece<S>::N + (f.j.gate_kind == MT_GATE_FULL ? 3 : 2) * Piece<T>::N;
   // rows are spread over the CTAs before any takes two at once
-  const int most = ops_least(sms, BN_MAX_PARTS), room = BN_WARPS / W;
+  const int most = ops_least(sms, BN_MAX_PARTS), room = W == 1 ? BN_WARPS - 1 : BN_WARPS / W;
   const bool alone = bn_alone(f.j.rows, f.j.width);
   const int G = alone ? room : ops_least(room, (f.j.rows + most - 1) / most);
   *parts = alone ? 1 : ops_least((f.j.rows + G - 1) / G, most);
@@ -736,8 +736,12 @@ int bwd_t(Bwd f, int dev, int sms, int* parts, cudaStream_t st) {
   f.hop_dh = step * f.lddh, f.hop_h = step * f.ldh, f.hop_dr = step * f.lddr, f.hop_y = step * f.ldy;
   f.hop_gate = step * f.j.ldgate, f.hop_dx = step * f.lddx, f.hop_dy = step * f.lddy, f.hop_dgate = step * f.lddgate;
   const bool whole = VEC && f.j.before && f.j.after && f.y && f.dh;
-  auto k = C == 2 ? block_norm_bwd_k<S, T, VEC, 2, false>
-           : whole ? block_norm_bwd_k<S, T, VEC, 1, VEC> : block_norm_bwd_k<S, T, VEC, 1, false>;
+  // compiled for a warp less it spills nothing: 75.8 against 80.0 us for 32,768 x 768
+  // (five groups of three warps in both)
+  auto k = C == 2                  ? block_norm_bwd_k<S, T, VEC, 2, false>
+           : !whole                ? block_norm_bwd_k<S, T, VEC, 1, false>
+           : W * G < BN_WARPS      ? block_norm_bwd_k<S, T, VEC, 1, VEC, BN_WARPS - 1>
+                                   : block_norm_bwd_k<S, T, VEC, 1, VEC>;
   return ops_launch_wide(k, dev, BN_SMEM, (unsigned)*parts, 32u * W * G, smem, st, f, W, G, stages, pieces);
 }
 

@@ -177,7 +177,7 @@ __device__ __forceinline__ float gc_factor(const Clip& c, bool write) {
     for (int i0 = 0; i0 < c.n_parts; i0 += 512) {
       double v[16];
 #pragma unroll
-      for (int u = 0; u < 16; ++u) v[u] = i0 + u * 32 + (int)threadIdx.x < c.n_parts ? c.parts[i0 + u * 32 + threadIdx.x] : 0.0;
+      for (int u = 0; u < 16; ++u) v[u] = i0 + u * 32 + (int)threadIdx.x < c.n_parts ? __ldcg(c.parts + i0 + u * 32 + threadIdx.x) : 0.0;
 #pragma unroll
       for (int u = 0; u < 16; ++u)
         if (i0 + u * 32 < c.n_parts) d += v[u];

@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(1024) choose_join_k(Choose c, int parts, int w
   for (int k0 = s; k0 < parts && i < words; k0 += U * slices) {
     uint32_t v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = k0 + u * slices < parts ? c.ws[(long long)(k0 + u * slices) * words + i] : 0u;
+    for (int u = 0; u < U; ++u) v[u] = k0 + u * slices < parts ? __ldcg(c.ws + (long long)(k0 + u * slices) * words + i) : 0u;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (real) a += __uint_as_float(v[u]);

@@ -577,6 +577,9 @@ struct ChooseBwd {
 //   weights  chosen j: w_j (dw_j - sum w dw); without renormalising p_j (dw_j - sum p dw), for every j
 //   balance  E / (K N^2) p_j (counts_j - sum_e counts_e p_e)
 //   size     2 / N lse p_j
+// Logits of -inf, which also stand for experts that there are not and for tokens that
+// take no part, neither take a dw nor get a gradient: by selection, for an infinite
+// factor times their probability of 0 is NaN.
 // 4.1 us for 32,768 tokens with 16 experts (4.7 MB): its launch and latency.
 template <class Z, int V, int L, bool VEC>
 __global__ void __launch_bounds__(256) choose_bwd_k(ChooseBwd c) {
@@ -618,7 +621,7 @@ __global__ void __launch_bounds__(256) choose_bwd_k(ChooseBwd c) {
       const float dk = there && e >= 0 ? c.dw[row * c.K + k] : 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (rt_expert<V, L, VEC>(l, v) == e) {
+        if (rt_expert<V, L, VEC>(l, v) == e && z[v] > -INFINITY) {
           d[v] += dk;
           chosen |= 1u << v;
         }
@@ -657,7 +660,7 @@ __global__ void __launch_bounds__(256) choose_bwd_k(ChooseBwd c) {
     for (int v = 0; v < V; ++v) o[v] += ex[v] * inv * (c0 * (cnt[v] - load) + c1 * lse);
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) o[v] = bad && live ? NAN : o[v];
+  for (int v = 0; v < V; ++v) o[v] = bad && live ? NAN : z[v] > -INFINITY ? o[v] : 0.f;
   if (there) rt_store<Z, V, L, VEC>((Z*)c.dz + row * c.lddz, l, c.E, o);
 }
 

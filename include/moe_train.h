@@ -638,10 +638,12 @@ int32_t mt_choose(const void* logits, int32_t dtype, int64_t ldz, int64_t n_toke
                   const uint8_t* mask, int32_t renormalize, int32_t* idx, float* w, int32_t* counts, float* losses,
                   void* ws, int64_t ws_bytes, void* stream);
 /* The gradient for the logits, of their dtype: from dw fp32 [n_tokens, top_k]
- * (NULL: none) through the weights at idx (entries outside [0, n_experts) add
- * nothing), and from dlosses fp32 [2] (NULL: none) through the losses, whose
- * counts (as mt_choose left them) are constants.  Zeros for tokens that take no
- * part and for logits of -infinity, NaN where the row holds NaN or +infinity. */
+ * (NULL: none) through the weights at idx (entries outside [0, n_experts) and
+ * those of logits of -infinity or of tokens that take no part add nothing,
+ * whatever their dw), and from dlosses fp32 [2] (NULL: none) through the losses,
+ * whose counts (as mt_choose left them) are constants.  Zeros for tokens that
+ * take no part and for logits of -infinity, also where dlosses is not finite; NaN
+ * where the row holds NaN or +infinity. */
 int32_t mt_choose_bwd(const void* logits, int32_t dtype, int64_t ldz, int64_t n_tokens, int32_t n_experts,
                       int32_t top_k, const uint8_t* mask, int32_t renormalize, const int32_t* idx,
                       const int32_t* counts, const float* dw, const float* dlosses, void* dlogits, int64_t lddz,

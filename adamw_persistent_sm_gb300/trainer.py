@@ -33,6 +33,7 @@ class MoETrainer:
         self.device = torch.device(device)
         self.flags = flags
         self.wait_timeout_ns = wait_timeout_ns
+        self._launch = flags, cfg.micro_count - 1       # flags and microbatch that self.grads are of
         hp = B.hparams(cfg, flags=flags)      # MT_FLAG_TRACE adds the trace to the arena
         n = B.mt_param_count(hp)
         if n < 0:
@@ -98,6 +99,7 @@ class MoETrainer:
                                tokens.data_ptr(), hp, self.arena.data_ptr(), self.arena_bytes,
                                self.stream)
         _check(st, "mt_train_update")
+        self._launch = hp.flags, micro_index
 
     def update(self, micro_tokens: list, step: int | None = None, flags: int | None = None) -> None:
         for i, tok in enumerate(micro_tokens):
@@ -131,15 +133,35 @@ class MoETrainer:
         """The gradient buffer's w_gate, w_up and w_down of a weight slot."""
         return tuple(self.view(self.grads, n)[slot] for n in ("w_gate", "w_up", "w_down"))
 
-    def clip_grads(self, max_norm: float | None = None, scale: float = 1.0) -> torch.Tensor:
+    def clip_grads(self, max_norm: float | None = None, scale: float = 1.0, micro_index: int | None = None,
+                   flags: int | None = None) -> torch.Tensor:
         """Scale the gradient buffer in place and clip it to the configuration's
         norm (or ``max_norm``), as the update's optimizer step would: for steps of
         an optimizer of the caller's after launches with MT_FLAG_NO_OPTIMIZER, or
         where :meth:`expert_layer8` added gradients.  Returns (norm, coefficient),
-        float32 [2] on the device."""
+        float32 [2] on the device.
+
+        With MT_FLAG_SELECTIVE_EXPERTS the update steps the shared tensors alone,
+        and after a period's last microbatch the experts' on the mean of their
+        gradients, each with a norm of its own: so does this, and returns [2, 2]
+        (shared, experts) after the last microbatch; before it the experts' sum is
+        left as it is.  ``flags`` and ``micro_index`` are those of the newest
+        :meth:`micro_step` (before any: the trainer's and the last), or as given
+        (where graphs replay other launches than the newest)."""
         from .block_ops import clip_grads
-        return clip_grads(list(self.named(self.grads).values()), self.cfg.clip_norm if max_norm is None else max_norm,
-                          self.cfg.clip_eps, scale)
+        flags = self._launch[0] if flags is None else flags
+        micro_index = self._launch[1] if micro_index is None else micro_index
+        if not 0 <= micro_index < self.cfg.micro_count:
+            raise ValueError(f"micro_index {micro_index} of {self.cfg.micro_count}")
+        max_norm = self.cfg.clip_norm if max_norm is None else max_norm
+        named, eps = self.named(self.grads), self.cfg.clip_eps
+        if not flags & B.MT_FLAG_SELECTIVE_EXPERTS:
+            return clip_grads(list(named.values()), max_norm, eps, scale)
+        experts = [named.pop(n) for n in ("w_gate", "w_up", "w_down")]
+        stats = clip_grads(list(named.values()), max_norm, eps, scale)
+        if micro_index < self.cfg.micro_count - 1:
+            return stats
+        return torch.stack([stats, clip_grads(experts, max_norm, eps, scale / self.cfg.micro_count)])
 
     def outputs(self) -> B.mt_outputs:
         return B.mt_read_outputs(self.arena.data_ptr(), self.stream)

@@ -1,8 +1,10 @@
 """The operators around the expert layer in calls that their definitions allow and
 that are easily answered wrongly: gradients that are not finite beside tokens and
-experts that take no part."""
+experts that take no part, and groups of gradients with norms of their own."""
 import pytest
 import torch
+
+import moe_inputs as mi
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +71,63 @@ def test_weights_gradients_that_belong_to_nothing(ops, e, dtype):
         for v in (1.0, INF, -INF, NAN):
             got = ops.choose_bwd(z, idx, dw=torch.where(nothing, v, dw), mask=mask, renormalize=renormalize)
             assert torch.equal(got, want)
+
+
+# ---------------------------------------------------------------------------
+# the trainer's gradients in two groups
+# ---------------------------------------------------------------------------
+def test_trainer_clips_selective_updates_in_two_groups():
+    """Launches with MT_FLAG_SELECTIVE_EXPERTS: the shared tensors and the mean of
+    the experts' gradients have norms and coefficients of their own, those that
+    the update reports (as 1e-5 holds for one group)."""
+    from adamw_persistent_sm_gb300 import binding as B
+    from adamw_persistent_sm_gb300.trainer import MoETrainer
+    sel, stay = B.MT_FLAG_SELECTIVE_EXPERTS, B.MT_FLAG_SELECTIVE_EXPERTS | B.MT_FLAG_NO_OPTIMIZER
+    experts = ("w_gate", "w_up", "w_down")
+    cfg = mi.get_config("tiny", micro_count=2, clip_norm=0.01)
+    params, toks = mi.make_params(cfg), [torch.as_tensor(v).cuda() for v in mi.make_update_tokens(cfg)]
+    one, two = MoETrainer(cfg, "cuda:0"), MoETrainer(cfg, "cuda:0")
+    for tr, last in ((one, sel), (two, stay)):
+        tr.load_params(params)
+        tr.micro_step(toks[0], 0, flags=stay)
+        if tr is two:                        # a step of the shared tensors alone, the sum of the experts' goes on
+            was = tr.grads.clone()
+            stats = tr.clip_grads()
+            assert stats.shape == (2,) and float(stats[1]) < 1
+            for n in tr.layout:
+                g, w = tr.view(tr.grads, n), tr.view(was, n)
+                assert torch.equal(g, w) if n in experts else torch.allclose(g, w * float(stats[1]), rtol=1e-6, atol=0)
+            total = sum(float((tr.view(was, n).double() ** 2).sum()) for n in tr.layout if n not in experts)
+            assert abs(float(stats[0]) - total ** 0.5) < 1e-5 * total ** 0.5
+        tr.micro_step(toks[1], 1, flags=last)
+        assert tr.outputs().status == B.MT_OK
+    out, was = one.outputs(), two.grads.clone()
+    assert out.experts_updated == 1 and out.clip_coef < 1 and out.expert_clip_coef < 1
+    stats = two.clip_grads()
+    assert stats.shape == (2, 2)
+    for got, want in zip(stats.reshape(-1).tolist(), (out.grad_norm, out.clip_coef, out.expert_grad_norm, out.expert_clip_coef)):
+        assert abs(got - want) < 1e-5 * want
+    for n in two.layout:
+        by = float(stats[1, 1]) / 2 if n in experts else float(stats[0, 1])
+        assert torch.allclose(two.view(two.grads, n), two.view(was, n) * by, rtol=1e-6, atol=0)
+
+
+def test_trainer_takes_the_groups_of_its_flags():
+    """Without a launch the trainer's own flags say which groups there are; a call may say it itself."""
+    from adamw_persistent_sm_gb300 import binding as B
+    from adamw_persistent_sm_gb300.trainer import MoETrainer
+    cfg = mi.get_config("tiny", micro_count=4)
+    tr = MoETrainer(cfg, "cuda:0", flags=B.MT_FLAG_SELECTIVE_EXPERTS)
+    tr.grads.copy_(rnd(1, tr.n_params))
+    was = tr.grads.clone()
+    assert tr.clip_grads(max_norm=1e9).shape == (2, 2)
+    for n in tr.layout:
+        assert torch.equal(tr.view(tr.grads, n), tr.view(was, n) * (0.25 if n in ("w_gate", "w_up", "w_down") else 1.0))
+    tr.grads.copy_(was)
+    assert tr.clip_grads(max_norm=1e9, scale=2.0, micro_index=2).shape == (2,)
+    for n in tr.layout:
+        assert torch.equal(tr.view(tr.grads, n), tr.view(was, n) * (1.0 if n in ("w_gate", "w_up", "w_down") else 2.0))
+    tr.grads.copy_(was)
+    assert tr.clip_grads(max_norm=1e9, scale=2.0, flags=0).shape == (2,) and torch.equal(tr.grads, was * 2.0)
+    with pytest.raises(ValueError):
+        tr.clip_grads(micro_index=4)

@@ -169,7 +169,7 @@ struct Clip {
   int n_parts, clip;
 };
 // The norm from the parts, in their order, and the factor of the clipped tensors: by
-// one warp, for the CTA.  In 32 bits where they hold the sum and its root.
+// one warp, for the CTA.  In 32 bits where they hold the sum, its root, the limit and eps.
 __device__ __forceinline__ float gc_factor(const Clip& c, bool write) {
   __shared__ float factor;
   if (threadIdx.x < 32) {
@@ -186,7 +186,7 @@ __device__ __forceinline__ float gc_factor(const Clip& c, bool write) {
     if (threadIdx.x == 0) {
       const float f = (float)d, sc = (float)c.scale, top = (float)c.max_norm, eps = (float)c.eps;
       float norm = fabsf(sc) * sqrtf(f), coef = top / (norm + eps), by;
-      if (f > 1e-24f && f < 1e36f && norm > 1e-12f && norm < 1e18f && top > 1e-12f && top < 1e18f) {
+      if (f > 1e-24f && f < 1e36f && norm > 1e-12f && norm < 1e18f && top > 1e-12f && top < 1e18f && eps < 1e18f) {
         coef = coef >= 1.f ? 1.f : coef;
         by = sc * coef;
       } else {

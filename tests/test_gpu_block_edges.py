@@ -1,6 +1,7 @@
 """The operators around the expert layer in calls that their definitions allow and
 that are easily answered wrongly: gradients that are not finite beside tokens and
-experts that take no part, and groups of gradients with norms of their own."""
+experts that take no part, groups of gradients with norms of their own, and numbers
+at the ends of the range."""
 import pytest
 import torch
 
@@ -131,3 +132,21 @@ def test_trainer_takes_the_groups_of_its_flags():
     assert tr.clip_grads(max_norm=1e9, scale=2.0, flags=0).shape == (2,) and torch.equal(tr.grads, was * 2.0)
     with pytest.raises(ValueError):
         tr.clip_grads(micro_index=4)
+
+
+# ---------------------------------------------------------------------------
+# the clip factor
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("max_norm,eps,scale", [(1e17, 1e39, 1.0), (1e-6, 1e300, 1.0), (2.0, 1e40, 1e30), (1.0, 1e37, 1.0), (1e-40, 0.0, 1.0)])
+def test_factors_beyond_32_bits(ops, max_norm, eps, scale):
+    """c = max_norm / (norm + eps) where one of them is beyond fp32: off by the
+    roundings of c and of the product, 3 steps of 2^-24, and by half of the least
+    subnormal number of each."""
+    t = rnd(1, 1000)
+    norm = abs(scale) * float((t.double() ** 2).sum().sqrt())
+    c = min(1.0, max_norm / (norm + eps))
+    out = torch.empty_like(t)
+    stats = ops.GradSet([t], [out]).clip(max_norm, eps, scale)
+    assert abs(float(stats[1]) - c) <= 40 * 2.0 ** -24 * c + 1e-45
+    want = t.double() * (scale * c)
+    assert ((out.double() - want).abs() <= 43 * 2.0 ** -24 * want.abs() + 1e-45 * (1 + t.double().abs())).all()

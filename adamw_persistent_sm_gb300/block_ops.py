@@ -19,6 +19,7 @@ Matrices may be views whose rows are contiguous (any row stride).
 from __future__ import annotations
 
 import ctypes as C
+import operator
 from typing import NamedTuple, Sequence
 
 import torch
@@ -299,6 +300,7 @@ def choose(logits: torch.Tensor, top_k: int, mask: torch.Tensor | None = None, r
     caller."""
     dev, ldz = _logits(logits, mask)
     t, e = logits.shape
+    top_k = operator.index(top_k)
     lib, picked = _load(), (t, top_k)
     if out is None:
         nbytes = lib.mt_choose_ws_bytes(t, top_k, e)

@@ -1,7 +1,8 @@
 """The operators around the expert layer in calls that their definitions allow and
 that are easily answered wrongly: gradients that are not finite beside tokens and
-experts that take no part, groups of gradients with norms of their own, and numbers
-at the ends of the range."""
+experts that take no part, groups of gradients with norms of their own, numbers at
+the ends of the range, and arguments of neighbouring types."""
+import numpy as np
 import pytest
 import torch
 
@@ -150,3 +151,21 @@ def test_factors_beyond_32_bits(ops, max_norm, eps, scale):
     assert abs(float(stats[1]) - c) <= 40 * 2.0 ** -24 * c + 1e-45
     want = t.double() * (scale * c)
     assert ((out.double() - want).abs() <= 43 * 2.0 ** -24 * want.abs() + 1e-45 * (1 + t.double().abs())).all()
+
+
+# ---------------------------------------------------------------------------
+# arguments
+# ---------------------------------------------------------------------------
+def test_numbers_of_choices(ops, monkeypatch):
+    """top_k is any whole number; another is refused with the device as it was."""
+    z = rnd(1, 6, 8)
+    c = ops.choose(z, 2)
+    assert all(torch.equal(a, b) for a, b in zip(c[:4], ops.choose(z, np.int64(2))[:4]))
+    assert all(torch.equal(a, b) for a, b in zip(c[:4], ops.choose(z, np.int32(2), out=ops.choose(z + 1, 2))[:4]))
+    now = [7]
+    monkeypatch.setattr(ops, "_current", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "set_device", lambda d: now.__setitem__(0, d))
+    for out in (None, c):
+        with pytest.raises(TypeError):
+            ops.choose(z, 2.0, out=out)
+        assert now == [7]

@@ -18,7 +18,6 @@ Matrices may be views whose rows are contiguous (any row stride).
 """
 from __future__ import annotations
 
-import ctypes as C
 import operator
 from typing import NamedTuple, Sequence
 

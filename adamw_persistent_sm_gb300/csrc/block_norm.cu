@@ -736,13 +736,13 @@ int bwd_t(Bwd f, int dev, int sms, int* parts, cudaStream_t st) {
   const long long step = (long long)*parts * G;
   f.hop_dh = step * f.lddh, f.hop_h = step * f.ldh, f.hop_dr = step * f.lddr, f.hop_y = step * f.ldy;
   f.hop_gate = step * f.j.ldgate, f.hop_dx = step * f.lddx, f.hop_dy = step * f.lddy, f.hop_dgate = step * f.lddgate;
-  const bool whole = VEC && f.j.before && f.j.after && f.y && f.dh;
+  auto k = C == 2 ? block_norm_bwd_k<S, T, VEC, 2, false> : block_norm_bwd_k<S, T, VEC, 1, false>;
   // compiled for a warp less it spills nothing: 75.8 against 80.0 us for 32,768 x 768
   // (five groups of three warps in both)
-  auto k = C == 2                  ? block_norm_bwd_k<S, T, VEC, 2, false>
-           : !whole                ? block_norm_bwd_k<S, T, VEC, 1, false>
-           : W * G < BN_WARPS      ? block_norm_bwd_k<S, T, VEC, 1, VEC, BN_WARPS - 1>
-                                   : block_norm_bwd_k<S, T, VEC, 1, VEC>;
+  if constexpr (VEC) {
+    if (C == 1 && f.j.before && f.j.after && f.y && f.dh)
+      k = W * G < BN_WARPS ? block_norm_bwd_k<S, T, VEC, 1, true, BN_WARPS - 1> : block_norm_bwd_k<S, T, VEC, 1, true>;
+  }
   return ops_launch_wide(k, dev, BN_SMEM, (unsigned)*parts, 32u * W * G, smem, st, f, W, G, stages, pieces);
 }
 

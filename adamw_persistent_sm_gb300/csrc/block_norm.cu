@@ -74,9 +74,11 @@ __device__ __forceinline__ float bn_sum(float s) {
 // One pass over the rows: x and y are read once, kept in registers (8 C columns
 // per lane) over the two sums of squares, and h and r written once.  Up to 1024
 // columns a warp takes a row and nothing is shared; wider rows take a CTA of as
-// many warps as they have 1024 columns.  Memory bounds it: 47 to 49 us for 25 million
-// elements (fp32 stream, bf16) in rows of 256 to 8192, 91 to 94 % of the copy rate; a
-// warp to 256 columns takes 102 us for rows of 256, 47 for 768 and 85 for 8192.
+// many warps as they have 1024 columns.  Memory bounds it: 45 to 50 us for 25 million
+// elements (fp32 stream, bf16) in rows of 256 to 8192, 89 to 98 % of the copy rate, and 53
+// in rows of 8000; a warp to 256 columns takes 102 us for rows of 256, 47 for 768 and 85
+// for 8192.  Shorter rows leave lanes idle (128 columns 66 us, 64 124), rows by element
+// take narrow loads and stores (1001: 86).
 template <class S, class T, int VEC, int C, bool WIDE>
 __global__ void __launch_bounds__(256) block_norm_k(Fwd f) {
   ops_begin();
@@ -363,7 +365,10 @@ __host__ __device__ constexpr int bn_red(int warps) { return (warps * 32 + 127) 
 // next row is on its way in registers (C 1).
 // 32,768 x 768 (fp32 stream, bf16, a channel gate), us with the column sums: 76, 88 %
 // of the copy rate; rows in registers 109, two rows at once 87 to 90, a warp to a row
-// of three chunks 83 and more, 20 warps 86, 8 warps 138.
+// of three chunks 83 and more, 20 warps 86, 8 warps 138.  As many elements in rows of
+// other widths: 64 222 and 128 117 (idle lanes), 2048 84, 2304 106 (nine of sixteen warps
+// run), 4096 97 (one row at a time, its sums over all warps), 5120 118 and 8000 108 (and
+// registers spilled), by element 1001 135 (narrow loads, and in fp32 registers spilled).
 template <class S, class T, int VEC, int C, bool ALL, int WARPS = BN_WARPS>
 __global__ void __launch_bounds__(32 * WARPS, 1) block_norm_bwd_k(Bwd f, int W, int G, int stages, int pieces) {
   ops_begin();

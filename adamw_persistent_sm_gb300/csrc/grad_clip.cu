@@ -7,7 +7,7 @@
 namespace {
 
 #define GC_THREADS 256
-#define GC_CTAS 3                 // of an SM (219M fp32 elements: 399 us, with four 408)
+#define GC_CTAS 3                 // of an SM (219M fp32 elements: 399 us, in the same run four 408)
 #define GC_UNIT 8192              // elements: what work is dealt out in
 #define GC_PARTS 1024              // partial sums of one launch, at most
 #define GC_TABLE 1024             // tensors of one launch, at most
@@ -97,8 +97,8 @@ struct Squares {
   }
 };
 
-#define GC_FLIGHT 4               // eights of a thread on their way at once (219M fp32: 404 us, two 425;
-                                  // 500 ragged bf16 tensors: 26 us, three 29)
+#define GC_FLIGHT 4               // eights of a thread on their way at once (219M fp32: 404 us, in the same
+                                  // run two 425; 500 ragged bf16 tensors: 26 us, three 29)
 // n elements at p
 template <class T>
 __device__ __forceinline__ void gc_squares(Squares& q, const T* p, long long n) {
@@ -122,7 +122,8 @@ __device__ __forceinline__ void gc_squares(Squares& q, const T* p, long long n) 
 }
 
 // A CTA takes a contiguous run of units, over as many tensors as lie in it.  876 MB of
-// fp32: 129 us, the copy rate.
+// fp32: 128 us, the copy rate; 438 MB of bf16, with half the bytes on their way, 75, 86 %
+// of it.
 template <int N>
 __global__ void __launch_bounds__(GC_THREADS, GC_CTAS) squares_k(const __grid_constant__ Table<N> t, double* parts) {
   ops_begin();
@@ -220,7 +221,9 @@ __device__ __forceinline__ __nv_bfloat16 gc_t<__nv_bfloat16>(float v) { return _
 template <class T>
 __device__ __forceinline__ void gc_scale(const T* p, T* o, long long n, float f) {
   const int head = gc_head(p, n);
-  if (head != gc_head(o, n)) {            // the two never reach a boundary together
+  // The two never reach a boundary together: by element, clipping 219M of fp32 takes 1080
+  // us instead of 405, of bf16 952 instead of 207.
+  if (head != gc_head(o, n)) {
     for (long long i = threadIdx.x; i < n; i += GC_THREADS) o[i] = gc_t<T>(gc_f(p[i]) * f);
     return;
   }

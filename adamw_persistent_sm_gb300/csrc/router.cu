@@ -177,6 +177,8 @@ __device__ __forceinline__ float rt_exp(float z, float top) {
 // joined by warp, CTA and part in a fixed order.  Launches and their latency bound it:
 // 2.6 us for a token, 6.0 for 32,768 with 2 of 16 experts (2.6 MB), of which the join
 // takes 1.5 to 2; 1,024 tokens in one CTA took 11, spread over many with a join 4.4.
+// 131,072 tokens take 10.4 us, with 4 of 16 13.4: a warp's next rows are not on their way
+// while it chooses, and each choice is a search over the lanes of a row.
 template <class Z, int V, int L, int KM, bool VEC>
 __global__ void __launch_bounds__(1024) choose_lanes_k(Choose c) {
   ops_begin();
@@ -318,11 +320,13 @@ __global__ void __launch_bounds__(1024) choose_lanes_k(Choose c) {
 // probabilities it sums over the 32 rows and on.  All in a fixed order, as are
 // warps, CTAs and parts.  16-byte piece p of row r lies at p ^ r: accesses of 16
 // bytes by rows and of words by experts meet no bank twice, and 28 warps fit an SM.
-// 131,072 tokens, 8 of 64 experts, bf16: 24 us, lanes 43.  Issue slots bound it (60 %
-// used, the pipe of comparisons 54 %): some 110 instructions a row, of which the
-// network takes 17 (by lanes that share a row it would take 80).  With rows 68 words
-// apart instead, 24 warps to an SM and a second round for an eighth of them: 27 us;
-// that round all in the first CTAs: 43.
+// 131,072 tokens, 8 of 64 experts, bf16: 24 us, lanes 43.  The time of one warp's tile
+// bounds it, from its loads to its last sum: 65,536 tokens, the same tiles on half the
+// warps, take 24 us too, though at 131,072 the issue slots are 60 % used (the pipe of
+// comparisons 54 %).  Some 110 instructions a row, of which the network takes 17 (by
+// lanes that share a row it would take 80).  With rows 68 words apart instead, 24 warps
+// to an SM and a second round for an eighth of them: 27 us; that round all in the first
+// CTAs: 43.
 template <class Z, bool VEC, bool PAIR>
 __global__ void __launch_bounds__(32 * RT_WARPS) choose_tiles_k(Choose c) {
   ops_begin();
@@ -524,8 +528,9 @@ __global__ void __launch_bounds__(32 * RT_WARPS) choose_tiles_k(Choose c) {
 }
 
 // The parts joined: `wide` threads (whole warps) take a word each, of every
-// slices-th part, with every load on its way at once (one after the other the join
-// took 5 us instead of 1.5 to 2).
+// slices-th part, thirteen loads on their way at once: all of 152 parts up to 31
+// experts, which have sixteen slices (16 experts: 1.5 to 2 us, one load after the other
+// 5).  32 experts have ten and 64 six, and take two rounds.
 __global__ void __launch_bounds__(1024) choose_join_k(Choose c, int parts, int wide) {
   ops_begin();
   __shared__ float p[RT_E + 1];
@@ -535,7 +540,7 @@ __global__ void __launch_bounds__(1024) choose_join_k(Choose c, int parts, int w
   const bool real = i <= c.E;
   float a = 0.f;
   int b = 0;
-  constexpr int U = 13;                       // all in flight: 152 parts by 12 slices and less
+  constexpr int U = 13;
   for (int k0 = s; k0 < parts && i < words; k0 += U * slices) {
     uint32_t v[U];
 #pragma unroll
@@ -580,7 +585,9 @@ struct ChooseBwd {
 // Logits of -inf, which also stand for experts that there are not and for tokens that
 // take no part, neither take a dw nor get a gradient: by selection, for an infinite
 // factor times their probability of 0 is NaN.
-// 4.1 us for 32,768 tokens with 16 experts (4.7 MB): its launch and latency.
+// 3.7 to 4.1 us for 32,768 tokens with 16 experts (4.7 MB): its launch and latency.
+// 131,072 tokens: 10 us, and 32 with 8 of 64 experts, fp32 or bf16 (11 and 6 by bytes):
+// every lane of a row reads all its indices and their gradients.
 template <class Z, int V, int L, bool VEC>
 __global__ void __launch_bounds__(256) choose_bwd_k(ChooseBwd c) {
   ops_begin();

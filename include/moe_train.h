@@ -667,8 +667,10 @@ int64_t mt_grad_ws_bytes(int32_t n);
 int32_t mt_grad_norm(const mt_span* spans, int32_t n, double scale, float* norm, void* ws, int64_t ws_bytes,
                      void* stream);
 /* stats[0] = that norm, stats[1] = c = min(1, max_norm / (norm + eps)) (NaN where
- * the norm is), and out = grad * (scale * c), rounded once.  Elements stay as they
- * are where out is grad and scale * c is 1.  max_norm > 0, eps >= 0, all finite. */
+ * the norm is), and out = grad * f, f = scale * c as an fp32 number (scale and c
+ * are rounded to fp32 before it, but where one of the numbers is far from 1); the
+ * product is rounded to fp32, and then to the tensor's type.  Elements stay as they
+ * are where out is grad and f is 1.  max_norm > 0, eps >= 0, all finite. */
 int32_t mt_grad_clip(const mt_span* spans, int32_t n, double max_norm, double eps, double scale, float* stats, void* ws,
                      int64_t ws_bytes, void* stream);
 

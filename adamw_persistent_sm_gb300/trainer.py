@@ -33,7 +33,7 @@ class MoETrainer:
         self.device = torch.device(device)
         self.flags = flags
         self.wait_timeout_ns = wait_timeout_ns
-        self._launch = flags, cfg.micro_count - 1       # flags and microbatch that self.grads are of
+        self._launch = None         # flags and microbatch of the newest launch
         hp = B.hparams(cfg, flags=flags)      # MT_FLAG_TRACE adds the trace to the arena
         n = B.mt_param_count(hp)
         if n < 0:
@@ -149,8 +149,9 @@ class MoETrainer:
         :meth:`micro_step` (before any: the trainer's and the last), or as given
         (where graphs replay other launches than the newest)."""
         from .block_ops import clip_grads
-        flags = self._launch[0] if flags is None else flags
-        micro_index = self._launch[1] if micro_index is None else micro_index
+        newest = self._launch or (self.flags, self.cfg.micro_count - 1)
+        flags = newest[0] if flags is None else flags
+        micro_index = newest[1] if micro_index is None else micro_index
         if not 0 <= micro_index < self.cfg.micro_count:
             raise ValueError(f"micro_index {micro_index} of {self.cfg.micro_count}")
         max_norm = self.cfg.clip_norm if max_norm is None else max_norm

@@ -135,6 +135,21 @@ def test_trainer_takes_the_groups_of_its_flags():
         tr.clip_grads(micro_index=4)
 
 
+def test_trainer_flags_set_later_and_refusals():
+    """Flags that the trainer is given after it was made count as well; a refused call leaves every gradient."""
+    from adamw_persistent_sm_gb300 import binding as B
+    from adamw_persistent_sm_gb300.trainer import MoETrainer
+    tr = MoETrainer(mi.get_config("tiny", micro_count=4), "cuda:0")
+    tr.flags |= B.MT_FLAG_SELECTIVE_EXPERTS
+    tr.grads.copy_(rnd(1, tr.n_params))
+    was = tr.grads.clone()
+    for kw in (dict(max_norm=-1.0), dict(scale=INF), dict(max_norm=NAN)):
+        with pytest.raises(RuntimeError):
+            tr.clip_grads(**kw)
+        assert torch.equal(tr.grads, was)
+    assert tr.clip_grads().shape == (2, 2)
+
+
 # ---------------------------------------------------------------------------
 # the clip factor
 # ---------------------------------------------------------------------------
